@@ -544,6 +544,143 @@ moe_status moe_router_bwd(const moe_dims* d, const void* x, const void* w_r, con
                           const int32_t* idx, const float* prob, const float* dprob, float* dlogits,
                           void* dx, float* dw_r, void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
+/*
+ * Operators around the expert FFN: layer norm, the gated activation, activations kept in 8
+ * bits between forward and backward, and linear layers grouped by expert on dense ragged
+ * rows.  The pages name the grouped linear layer (page "Efficient MoE Training for Biological
+ * Foundation Models", section "GroupedLinear") and the gated activation (section
+ * "MXFP8与融合MLP"); layer norm and the 8-bit checkpoints are interface additions for the
+ * block around the layer.
+ *
+ * Row pitches (ld...) are in elements and at least the row's length.  Rows whose length and
+ * pitches are multiples of 8 take 16-byte loads; all others work, more slowly.  rows = 0 is
+ * valid everywhere.  Base pointers are 16-byte aligned, as everywhere.
+ *
+ * 8-bit checkpoint ("act8") of a [rows][cols] tensor: codes uint8 E4M3 [rows][cols] and scales
+ * uint8 [rows][ceil(cols/32)], both dense row-major; one power-of-two scale per 32
+ * consecutive values of a row (the last block may be short) under the MX rule stated above
+ * for bf16 and f32 input alike.  Unlike an MX tensor it feeds no MMA, so its sizes are free
+ * and its scales are not tiled.
+ */
+typedef struct moe_norm {
+  int64_t rows;         /* >= 0 */
+  int64_t ld_in;        /* row pitch of x, residual (forward) and of dy, x, dres (backward) */
+  int64_t ld_out;       /* row pitch of h, y (forward) and of dx (backward) */
+  int32_t H;            /* 1..16384 */
+  int32_t x_f32;        /* activations: 0 bf16, 1 f32 */
+  int32_t w_f32;        /* gamma, beta and their gradients: 0 bf16, 1 f32 */
+  float eps;            /* >= 0 */
+} moe_norm;
+
+/* Bytes of workspace of moe_layernorm_bwd (256-byte aligned, need not be zeroed); 0 for
+ * invalid sizes.  Host only. */
+size_t moe_layernorm_workspace_size(const moe_norm* n);
+
+/*
+ * moe_layernorm_fwd -- h = x (+ residual), y = (h - mean) * rstd * gamma + beta per row, with
+ * mean and rstd = 1 / sqrt(variance + eps) over the row's H values.
+ *   x, residual   [rows][H] at pitch ld_in; residual may be NULL
+ *   gamma, beta   [H]; beta may be NULL
+ *   h             out [rows][H] at pitch ld_out: the sum, rounded (mean, rstd, y and the
+ *                 checkpoint are those of the unrounded sum); required with residual, else NULL
+ *   y             out [rows][H] at pitch ld_out
+ *   mean, rstd    out f32 [rows], each may be NULL
+ *   codes,scales  both set or both NULL: out act8 of (h - mean) * rstd
+ * h and y must not overlap x and residual, except that h may be x or residual itself when
+ * ld_in = ld_out (each row is read before it is written).
+ */
+moe_status moe_layernorm_fwd(const moe_norm* n, const void* x, const void* residual, const void* gamma,
+                             const void* beta, void* h, void* y, float* mean, float* rstd, uint8_t* codes,
+                             uint8_t* scales, moe_stream_t stream);
+
+/*
+ * moe_layernorm_bwd -- gradients of moe_layernorm_fwd, with n the normalised input:
+ *   dx = rstd * (d - mean(d) - n * mean(d * n)) (+ dres),  d = dy * gamma;
+ *   dgamma = sum over rows of dy * n, dbeta = sum over rows of dy (zeros for rows = 0).
+ *   dy            [rows][H] at pitch ld_in
+ *   either x and mean (what was normalised: x, or h when there was a residual; n is computed
+ *   again) or codes and scales (n as kept in 8 bits; x and mean NULL); rstd always
+ *   dres          [rows][H] at pitch ld_in or NULL: the gradient that reaches h past the norm
+ *   dx            out [rows][H] at pitch ld_out; with a residual it is the gradient of both
+ *                 summands; may be dy or dres itself when ld_in = ld_out
+ *   dgamma        out [H]; dbeta out [H] or NULL; in gamma's type, summed in f32 in a fixed
+ *                 order (results do not depend on timing)
+ */
+moe_status moe_layernorm_bwd(const moe_norm* n, const void* dy, const void* x, const float* mean, const float* rstd,
+                             const uint8_t* codes, const uint8_t* scales, const void* gamma, const void* dres,
+                             void* dx, void* dgamma, void* dbeta, void* workspace, size_t workspace_bytes,
+                             moe_stream_t stream);
+
+/* moe_act8_pack -- act8 of src [rows][cols] (bf16, or f32 with src_f32) at pitch ld; cols >= 1. */
+moe_status moe_act8_pack(const void* src, int32_t src_f32, int64_t rows, int32_t cols, int64_t ld, uint8_t* codes,
+                         uint8_t* scales, moe_stream_t stream);
+
+/* moe_act8_unpack -- dst [rows][cols] (bf16, or f32 with dst_f32) at pitch ld = the kept values,
+ * times gamma plus beta per column where given ([cols], bf16 or f32 with w_f32; beta only with
+ * gamma): with a layer norm's checkpoint and weights that is the norm's output again. */
+moe_status moe_act8_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols, const void* gamma,
+                           const void* beta, int32_t w_f32, void* dst, int32_t dst_f32, int64_t ld,
+                           moe_stream_t stream);
+
+/*
+ * moe_swiglu_fwd -- a = silu(g) * u * prob[row] with g = gu[row][0..I-1], u = gu[row][I..2I-1].
+ *   gu bf16 [rows][2I] at pitch ld_gu; prob f32 [rows] or NULL (1); a out bf16 [rows][I] at
+ *   pitch ld_a; codes [rows][2I], scales [rows][2*ceil(I/32)] both set or both NULL: out act8 of
+ *   g and of u, side by side (a block never spans both).  I >= 1.
+ */
+moe_status moe_swiglu_fwd(int64_t rows, int32_t I, const void* gu, int64_t ld_gu, const float* prob, void* a,
+                          int64_t ld_a, uint8_t* codes, uint8_t* scales, moe_stream_t stream);
+
+/*
+ * moe_swiglu_bwd -- from da bf16 [rows][I] (pitch ld_da) and g, u either as gu (bf16, pitch
+ * ld_gu) or as kept by moe_swiglu_fwd in codes and scales (gu NULL):
+ *   dgu   out bf16 [rows][2I] (pitch ld_dgu): da*p*u*silu'(g) | da*p*silu(g)
+ *   dprob out f32 [rows] or NULL: sum of da * silu(g) * u (NULL without prob)
+ *   a     out bf16 [rows][I] (pitch ld_a) or NULL: the activation again, for the weight
+ *         gradient of the layer behind it
+ * da and a may be the same tensor.
+ */
+moe_status moe_swiglu_bwd(int64_t rows, int32_t I, const void* gu, int64_t ld_gu, const uint8_t* codes,
+                          const uint8_t* scales, const float* prob, const void* da, int64_t ld_da, void* dgu,
+                          int64_t ld_dgu, float* dprob, void* a, int64_t ld_a, moe_stream_t stream);
+
+typedef struct moe_grouped {
+  int64_t rows;         /* rows of x, y, dx, dy: 0..2^30 */
+  int32_t K;            /* input features, a multiple of 8 */
+  int32_t N;            /* output features, a multiple of 8 */
+  int32_t E;            /* experts, 1..256 */
+} moe_grouped;
+
+/* Bytes of workspace of the grouped linear calls (256-byte aligned, zero-filled once before
+ * first use; its first 8 bytes are a device error word); 0 for invalid sizes.  Host only. */
+size_t moe_grouped_linear_workspace_size(const moe_grouped* g);
+
+/*
+ * moe_grouped_linear_fwd / _dgrad / _wgrad -- one linear layer per expert on dense ragged rows
+ * (page "Efficient MoE Training for Biological Foundation Models", section "GroupedLinear": one
+ * grouped call takes the tokens collected per expert plus split_sizes; every expert keeps its
+ * own weight, no bias).  The rows of expert e are the split_sizes[e] rows after those of expert
+ * e - 1, without padding (moe_ep_pack with world = 1 writes them so); split_sizes int32 [E] is
+ * read on the device.  Rows past their sum belong to no expert: they are not read, and their
+ * rows of y and dx are not written.  bf16 tensors, f32 accumulation, one rounding at the end.
+ *   w  bf16 [E][N][K]
+ *   fwd    y[r]  = w[e] x[r]              x [rows][K], y [rows][N]
+ *   dgrad  dx[r] = w[e]^T dy[r]           dy [rows][N], dx [rows][K]
+ *   wgrad  dw[e] = sum_r dy[r] x[r]^T     dw [E][N][K], zeros for experts without rows
+ * Row pitches ldx, ldy (of x or dx, and of y or dy) are multiples of 8.  A row holding NaN or
+ * Inf changes its own y and dx and its expert's dw, nothing else.  A negative size or a sum above
+ * rows is recorded in the error word (MOE_ERR_DEVICE_BOUNDS) and nothing is written.
+ */
+moe_status moe_grouped_linear_fwd(const moe_grouped* g, const void* x, int64_t ldx, const int32_t* split_sizes,
+                                  const void* w, void* y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                                  moe_stream_t stream);
+moe_status moe_grouped_linear_dgrad(const moe_grouped* g, const void* dy, int64_t ldy, const int32_t* split_sizes,
+                                    const void* w, void* dx, int64_t ldx, void* workspace, size_t workspace_bytes,
+                                    moe_stream_t stream);
+moe_status moe_grouped_linear_wgrad(const moe_grouped* g, const void* x, int64_t ldx, const void* dy, int64_t ldy,
+                                    const int32_t* split_sizes, void* dw, void* workspace, size_t workspace_bytes,
+                                    moe_stream_t stream);
+
 /* moe_selftest_wait_timeout -- exercises the device-side failure path without
  * faulting anything.  One launch of the grouped GEMM kernel over a single
  * 128x256x128 tile whose producer is told to issue no loads: the MMA, scale

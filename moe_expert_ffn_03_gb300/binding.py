@@ -23,7 +23,9 @@ EXPORTS = (
     "mxfp8_quantize_experts", "fp8_tensor_quantize_experts", "moe_transpose_bf16", "grouped_mlp_bwd_bf16",
     "grouped_mlp_bwd_fp8_tensor", "moe_workspace_tensor", "moe_selftest_epilogue_quant", "moe_selftest_mma_issue",
     "moe_transpose_bf16_experts", "grouped_mlp_fwd_bf16_experts", "moe_route", "moe_permute", "moe_ep_pack",
-    "moe_gather_f32",
+    "moe_gather_f32", "moe_layernorm_workspace_size", "moe_layernorm_fwd", "moe_layernorm_bwd", "moe_act8_pack",
+    "moe_act8_unpack", "moe_swiglu_fwd", "moe_swiglu_bwd", "moe_grouped_linear_workspace_size",
+    "moe_grouped_linear_fwd", "moe_grouped_linear_dgrad", "moe_grouped_linear_wgrad",
 )
 
 # moe_ws_tensor ids (include/moe_ffn.h)
@@ -50,6 +52,25 @@ def dims(T, H, I, E, k, renormalize=1) -> MoeDims:
     return MoeDims(T, H, I, E, k, renormalize)
 
 
+class MoeNorm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("ld_in", ctypes.c_int64), ("ld_out", ctypes.c_int64), ("H", c_int32),
+                ("x_f32", c_int32), ("w_f32", c_int32), ("eps", ctypes.c_float)]
+
+
+def norm(rows, H, x_f32=False, w_f32=False, eps=1e-5, ld_in=None, ld_out=None) -> MoeNorm:
+    """Sizes and types of a layer norm: activations and weights bf16, or f32 where x_f32, w_f32 say so."""
+    return MoeNorm(rows, H if ld_in is None else ld_in, H if ld_out is None else ld_out, H, int(x_f32), int(w_f32), eps)
+
+
+class MoeGrouped(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("K", c_int32), ("N", c_int32), ("E", c_int32)]
+
+
+def grouped(rows, K, N, E) -> MoeGrouped:
+    """Sizes of a grouped linear layer: rows of all experts, K input and N output features, E experts."""
+    return MoeGrouped(rows, K, N, E)
+
+
 _lib = None
 
 
@@ -66,7 +87,7 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"{path} is missing: build it with moe_expert_ffn_03_gb300.build.build()")
         L = ctypes.CDLL(path)
         D = ctypes.POINTER(MoeDims)
-        P = c_void_p
+        P, I64, G = c_void_p, ctypes.c_int64, ctypes.POINTER(MoeGrouped)
         sig = {
             "moe_status_string": ([c_int32], ctypes.c_char_p),
             "moe_last_error_message": ([], ctypes.c_char_p),
@@ -106,6 +127,17 @@ def lib() -> ctypes.CDLL:
             "moe_gather_f32": ([P, ctypes.c_int64, P, ctypes.c_int64, P, P, P], c_int32),
             "grouped_mlp_fwd_bf16_experts": ([D, P, P, P, ctypes.POINTER(P), ctypes.POINTER(P), P, P, P, P, c_size_t,
                                               P], c_int32),
+            "moe_layernorm_workspace_size": ([ctypes.POINTER(MoeNorm)], c_size_t),
+            "moe_layernorm_fwd": ([ctypes.POINTER(MoeNorm)] + [P] * 11, c_int32),
+            "moe_layernorm_bwd": ([ctypes.POINTER(MoeNorm)] + [P] * 12 + [c_size_t, P], c_int32),
+            "moe_act8_pack": ([P, c_int32, I64, c_int32, I64, P, P, P], c_int32),
+            "moe_act8_unpack": ([P, P, I64, c_int32, P, P, c_int32, P, c_int32, I64, P], c_int32),
+            "moe_swiglu_fwd": ([I64, c_int32, P, I64, P, P, I64, P, P, P], c_int32),
+            "moe_swiglu_bwd": ([I64, c_int32, P, I64, P, P, P, P, I64, P, I64, P, P, I64, P], c_int32),
+            "moe_grouped_linear_workspace_size": ([G], c_size_t),
+            "moe_grouped_linear_fwd": ([G, P, I64, P, P, P, I64, P, c_size_t, P], c_int32),
+            "moe_grouped_linear_dgrad": ([G, P, I64, P, P, P, I64, P, c_size_t, P], c_int32),
+            "moe_grouped_linear_wgrad": ([G, P, I64, P, I64, P, P, P, c_size_t, P], c_int32),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -337,3 +369,91 @@ def grouped_mlp_fwd_bf16_experts(d, x_perm, split_sizes, prob_perm, w_gu_list, w
 def fp8_tensor_quantize_experts(w_list, rows, cols, codes, amax, stream=None):
     _check(lib().fp8_tensor_quantize_experts(_ptr_array(w_list), len(w_list), rows, cols, _p(codes), _p(amax),
                                              _st(stream)))
+
+
+# ---- operators around the layer ------------------------------------------------------------------
+# Row pitches and element types are read off the tensors; a tensor's last dimension must be dense.
+def _ld(t, cols):
+    """Row pitch of a 2-D tensor whose rows hold `cols` elements; 0 for None."""
+    if t is None:
+        return 0
+    if t.dim() != 2 or t.shape[1] < cols or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"expected [rows][>={cols}] with dense rows, got {tuple(t.shape)} strides {t.stride()}")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _typed(dtype, *tensors):
+    for t in tensors:
+        if t is not None and t.dtype != dtype:
+            raise TypeError(f"expected {dtype}, got {t.dtype}")
+
+
+def moe_layernorm_workspace_size(n: MoeNorm) -> int:
+    return int(lib().moe_layernorm_workspace_size(ctypes.byref(n)))
+
+
+def moe_layernorm_fwd(n, x, residual, gamma, beta, h, y, mean, rstd, codes=None, scales=None, stream=None):
+    _check(lib().moe_layernorm_fwd(ctypes.byref(n), _p(x), _p(residual), _p(gamma), _p(beta), _p(h), _p(y), _p(mean),
+                                   _p(rstd), _p(codes), _p(scales), _st(stream)))
+
+
+def moe_layernorm_bwd(n, dy, x, mean, rstd, codes, scales, gamma, dres, dx, dgamma, dbeta, workspace, stream=None):
+    """From x and mean, or, where codes is given (x None), from the 8-bit checkpoint."""
+    _check(lib().moe_layernorm_bwd(ctypes.byref(n), _p(dy), _p(x), _p(None if x is None else mean), _p(rstd),
+                                   _p(codes), _p(scales), _p(gamma), _p(dres), _p(dx), _p(dgamma), _p(dbeta),
+                                   _p(workspace), _wsb(workspace), _st(stream)))
+
+
+def moe_act8_pack(src, codes, scales, stream=None):
+    rows, cols = src.shape
+    if src.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"expected bfloat16 or float32, got {src.dtype}")
+    _check(lib().moe_act8_pack(_p(src), int(src.dtype == torch.float32), rows, cols, _ld(src, cols), _p(codes),
+                               _p(scales), _st(stream)))
+
+
+def moe_act8_unpack(codes, scales, gamma, beta, dst, stream=None):
+    rows, cols = codes.shape
+    if dst.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"expected bfloat16 or float32, got {dst.dtype}")
+    if dst.shape[0] != rows:
+        raise ValueError(f"dst has {dst.shape[0]} rows, codes {rows}")
+    w_f32 = gamma is not None and gamma.dtype == torch.float32
+    _check(lib().moe_act8_unpack(_p(codes), _p(scales), rows, cols, _p(gamma), _p(beta), int(w_f32), _p(dst),
+                                 int(dst.dtype == torch.float32), _ld(dst, cols), _st(stream)))
+
+
+def moe_swiglu_fwd(gu, prob, a, codes=None, scales=None, stream=None):
+    rows, I = a.shape
+    _typed(torch.bfloat16, gu, a)
+    _check(lib().moe_swiglu_fwd(rows, I, _p(gu), _ld(gu, 2 * I), _p(prob), _p(a), _ld(a, I), _p(codes), _p(scales),
+                                _st(stream)))
+
+
+def moe_swiglu_bwd(gu, codes, scales, prob, da, dgu, dprob=None, a=None, stream=None):
+    rows, I = da.shape
+    _typed(torch.bfloat16, gu, da, dgu, a)
+    _check(lib().moe_swiglu_bwd(rows, I, _p(gu), _ld(gu, 2 * I), _p(codes), _p(scales), _p(prob), _p(da), _ld(da, I),
+                                _p(dgu), _ld(dgu, 2 * I), _p(dprob), _p(a), _ld(a, I), _st(stream)))
+
+
+def moe_grouped_linear_workspace_size(g: MoeGrouped) -> int:
+    return int(lib().moe_grouped_linear_workspace_size(ctypes.byref(g)))
+
+
+def moe_grouped_linear_fwd(g, x, split_sizes, w, y, workspace, stream=None):
+    _typed(torch.bfloat16, x, w, y)
+    _check(lib().moe_grouped_linear_fwd(ctypes.byref(g), _p(x), _ld(x, g.K), _p(split_sizes), _p(w), _p(y),
+                                        _ld(y, g.N), _p(workspace), _wsb(workspace), _st(stream)))
+
+
+def moe_grouped_linear_dgrad(g, dy, split_sizes, w, dx, workspace, stream=None):
+    _typed(torch.bfloat16, dy, w, dx)
+    _check(lib().moe_grouped_linear_dgrad(ctypes.byref(g), _p(dy), _ld(dy, g.N), _p(split_sizes), _p(w), _p(dx),
+                                          _ld(dx, g.K), _p(workspace), _wsb(workspace), _st(stream)))
+
+
+def moe_grouped_linear_wgrad(g, x, dy, split_sizes, dw, workspace, stream=None):
+    _typed(torch.bfloat16, x, dy, dw)
+    _check(lib().moe_grouped_linear_wgrad(ctypes.byref(g), _p(x), _ld(x, g.K), _p(dy), _ld(dy, g.N), _p(split_sizes),
+                                          _p(dw), _p(workspace), _wsb(workspace), _st(stream)))

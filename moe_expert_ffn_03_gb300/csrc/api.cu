@@ -1263,6 +1263,299 @@ moe_status moe_router_bwd(const moe_dims* d, const void* x, const void* w_r, con
   return MOE_OK;
 }
 
+// ---- operators around the layer: norm, gated activation, act8, grouped linear ------------------
+}  // extern "C"
+
+namespace {
+
+moe_status check_norm(const moe_norm* n) {
+  if (n == nullptr) return fail(MOE_ERR_INVALID_ARG, "norm is NULL");
+  if (n->rows < 0 || n->rows > (int64_t(1) << 31)) return fail(MOE_ERR_INVALID_ARG, "rows=%lld must be in 0..2^31", (long long)n->rows);
+  if (n->H < 1) return fail(MOE_ERR_INVALID_ARG, "H=%d must be >= 1", n->H);
+  if (n->H > 16384) return fail(MOE_ERR_UNSUPPORTED, "H=%d must be <= 16384", n->H);
+  if (n->ld_in < n->H || n->ld_out < n->H)
+    return fail(MOE_ERR_INVALID_ARG, "row pitches %lld, %lld must be >= H=%d", (long long)n->ld_in, (long long)n->ld_out, n->H);
+  if ((n->x_f32 | n->w_f32) & ~1) return fail(MOE_ERR_INVALID_ARG, "x_f32 and w_f32 must be 0 or 1");
+  if (!(n->eps >= 0.f)) return fail(MOE_ERR_INVALID_ARG, "eps must be >= 0");
+  return MOE_OK;
+}
+
+NormArgs norm_args(const moe_norm* n) {
+  NormArgs a{};
+  a.rows = n->rows;
+  a.H = n->H;
+  a.eps = n->eps;
+  a.w_f32 = n->w_f32 != 0;
+  a.ld_in = n->ld_in;
+  a.ld_out = n->ld_out;
+  return a;
+}
+
+// codes and scales: both set (and aligned) or both NULL
+moe_status check_act8(const uint8_t* codes, const uint8_t* scales) {
+  if ((codes == nullptr) != (scales == nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "codes and scales must both be set or both be NULL");
+  if (!al16(codes) || !al16(scales)) return fail(MOE_ERR_ALIGNMENT, "codes or scales is not 16-byte aligned");
+  return MOE_OK;
+}
+
+moe_status check_rows_cols(int64_t rows, int32_t cols) {
+  if (rows < 0 || rows > (int64_t(1) << 31)) return fail(MOE_ERR_INVALID_ARG, "rows=%lld must be in 0..2^31", (long long)rows);
+  if (cols < 1 || cols > (1 << 29)) return fail(MOE_ERR_INVALID_ARG, "row length %d must be in 1..2^29", cols);
+  return MOE_OK;
+}
+
+moe_status check_pitch(int64_t ld, int64_t cols, const char* what) {
+  if (ld < cols) return fail(MOE_ERR_INVALID_ARG, "%s=%lld must be >= %lld", what, (long long)ld, (long long)cols);
+  return MOE_OK;
+}
+
+moe_status check_grouped(const moe_grouped* g) {
+  if (g == nullptr) return fail(MOE_ERR_INVALID_ARG, "grouped is NULL");
+  if (g->rows < 0 || g->rows > (int64_t(1) << 30)) return fail(MOE_ERR_INVALID_ARG, "rows=%lld must be in 0..2^30", (long long)g->rows);
+  if (g->E < 1 || g->E > 256) return fail(MOE_ERR_UNSUPPORTED, "E=%d must be in 1..256", g->E);
+  if (g->K < 8 || g->K % 8 || g->N < 8 || g->N % 8)
+    return fail(MOE_ERR_UNSUPPORTED, "K=%d and N=%d must be positive multiples of 8", g->K, g->N);
+  if (g->K > (1 << 20) || g->N > (1 << 20)) return fail(MOE_ERR_UNSUPPORTED, "K and N must be <= 2^20");
+  return MOE_OK;
+}
+
+moe_status check_grouped_call(const moe_grouped* g, int64_t ldx, int64_t ldy, const void* ws, size_t bytes) {
+  if (moe_status s = check_grouped(g); s != MOE_OK) return s;
+  if (moe_status s = check_pitch(ldx, g->K, "ldx"); s != MOE_OK) return s;
+  if (moe_status s = check_pitch(ldy, g->N, "ldy"); s != MOE_OK) return s;
+  if (ldx % 8 || ldy % 8) return fail(MOE_ERR_UNSUPPORTED, "row pitches %lld, %lld must be multiples of 8", (long long)ldx, (long long)ldy);
+  if (ldx >= (int64_t(1) << 38) || ldy >= (int64_t(1) << 38)) return fail(MOE_ERR_UNSUPPORTED, "row pitch too large");
+  if (ws == nullptr) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return fail(MOE_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+  const size_t need = moe_grouped_linear_workspace_size(g);
+  if (bytes < need) return fail(MOE_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", bytes, need);
+  return MOE_OK;
+}
+
+moe_status run_grouped(int mode, const moe_grouped* g, const void* x, int64_t ldx, const void* dy, int64_t ldy,
+                       const int32_t* split_sizes, const void* w, void* out, int64_t ldo, void* ws, cudaStream_t st) {
+  LinearArgs a{};
+  a.rows = g->rows;
+  a.E = g->E;
+  a.K = g->K;
+  a.N = g->N;
+  a.split_sizes = split_sizes;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.ldo = ldo;
+  a.err = static_cast<int*>(ws);
+  char msg[256] = "";
+  const cudaError_t e = launch_grouped_linear(mode, a, x, ldx, dy, ldy, w, st, msg, sizeof(msg));
+  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "grouped linear: %s %s", cudaGetErrorString(e), msg);
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_layernorm_workspace_size(const moe_norm* n) {
+  return check_norm(n) == MOE_OK ? norm_ws_bytes(n->rows, n->H) : 0;
+}
+
+moe_status moe_layernorm_fwd(const moe_norm* n, const void* x, const void* residual, const void* gamma,
+                             const void* beta, void* h, void* y, float* mean, float* rstd, uint8_t* codes,
+                             uint8_t* scales, moe_stream_t stream) {
+  if (moe_status s = check_norm(n); s != MOE_OK) return s;
+  if (moe_status s = check_act8(codes, scales); s != MOE_OK) return s;
+  if ((residual == nullptr) != (h == nullptr)) return fail(MOE_ERR_INVALID_ARG, "h goes with residual: set both or neither");
+  if (n->rows == 0) return MOE_OK;
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(gamma);
+  REQUIRE_PTR(y);
+  if (!al16(residual) || !al16(h) || !al16(beta) || !al16(mean) || !al16(rstd))
+    return fail(MOE_ERR_ALIGNMENT, "a pointer is not 16-byte aligned");
+  NormArgs a = norm_args(n);
+  a.x = x;
+  a.residual = residual;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.h = h;
+  a.y = y;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.codes = codes;
+  a.scales = scales;
+  CUDA_TRY(launch_norm_fwd(a, n->x_f32 != 0, static_cast<cudaStream_t>(stream)), "layer norm forward");
+  return MOE_OK;
+}
+
+moe_status moe_layernorm_bwd(const moe_norm* n, const void* dy, const void* x, const float* mean, const float* rstd,
+                             const uint8_t* codes, const uint8_t* scales, const void* gamma, const void* dres,
+                             void* dx, void* dgamma, void* dbeta, void* workspace, size_t workspace_bytes,
+                             moe_stream_t stream) {
+  if (moe_status s = check_norm(n); s != MOE_OK) return s;
+  if (moe_status s = check_act8(codes, scales); s != MOE_OK) return s;
+  REQUIRE_PTR(dgamma);
+  if (!al16(dbeta)) return fail(MOE_ERR_ALIGNMENT, "dbeta is not 16-byte aligned");
+  if (n->rows > 0) {
+    if ((x == nullptr) == (codes == nullptr) || (x == nullptr) != (mean == nullptr))
+      return fail(MOE_ERR_INVALID_ARG, "give either x and mean, or codes and scales");
+    REQUIRE_PTR(dy);
+    REQUIRE_PTR(rstd);
+    REQUIRE_PTR(gamma);
+    REQUIRE_PTR(dx);
+    if (!al16(x) || !al16(mean) || !al16(dres)) return fail(MOE_ERR_ALIGNMENT, "x, mean or dres is not 16-byte aligned");
+    if (workspace == nullptr) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return fail(MOE_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+    const size_t need = norm_ws_bytes(n->rows, n->H);
+    if (workspace_bytes < need) return fail(MOE_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+  }
+  NormArgs a = norm_args(n);
+  a.dy = dy;
+  a.x = x;
+  a.mean = const_cast<float*>(mean);
+  a.rstd = const_cast<float*>(rstd);
+  a.codes = const_cast<uint8_t*>(codes);
+  a.scales = const_cast<uint8_t*>(scales);
+  a.gamma = gamma;
+  a.dres = dres;
+  a.dx = dx;
+  a.dgamma = dgamma;
+  a.dbeta = dbeta;
+  CUDA_TRY(launch_norm_bwd(a, n->x_f32 != 0, static_cast<float*>(workspace), static_cast<cudaStream_t>(stream)),
+           "layer norm backward");
+  return MOE_OK;
+}
+
+moe_status moe_act8_pack(const void* src, int32_t src_f32, int64_t rows, int32_t cols, int64_t ld, uint8_t* codes,
+                         uint8_t* scales, moe_stream_t stream) {
+  if (moe_status s = check_rows_cols(rows, cols); s != MOE_OK) return s;
+  if (moe_status s = check_pitch(ld, cols, "ld"); s != MOE_OK) return s;
+  if (rows == 0) return MOE_OK;
+  REQUIRE_PTR(src);
+  REQUIRE_PTR(codes);
+  REQUIRE_PTR(scales);
+  CUDA_TRY(launch_act8_pack(src, src_f32 != 0, rows, cols, ld, codes, scales, static_cast<cudaStream_t>(stream)),
+           "act8 pack");
+  return MOE_OK;
+}
+
+moe_status moe_act8_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols, const void* gamma,
+                           const void* beta, int32_t w_f32, void* dst, int32_t dst_f32, int64_t ld,
+                           moe_stream_t stream) {
+  if (moe_status s = check_rows_cols(rows, cols); s != MOE_OK) return s;
+  if (moe_status s = check_pitch(ld, cols, "ld"); s != MOE_OK) return s;
+  if (gamma == nullptr && beta != nullptr) return fail(MOE_ERR_INVALID_ARG, "beta without gamma");
+  if (rows == 0) return MOE_OK;
+  REQUIRE_PTR(codes);
+  REQUIRE_PTR(scales);
+  REQUIRE_PTR(dst);
+  if (!al16(gamma) || !al16(beta)) return fail(MOE_ERR_ALIGNMENT, "gamma or beta is not 16-byte aligned");
+  CUDA_TRY(launch_act8_unpack(codes, scales, rows, cols, gamma, beta, w_f32 != 0, dst, dst_f32 != 0, ld,
+                              static_cast<cudaStream_t>(stream)),
+           "act8 unpack");
+  return MOE_OK;
+}
+
+moe_status moe_swiglu_fwd(int64_t rows, int32_t I, const void* gu, int64_t ld_gu, const float* prob, void* a,
+                          int64_t ld_a, uint8_t* codes, uint8_t* scales, moe_stream_t stream) {
+  if (moe_status s = check_rows_cols(rows, I); s != MOE_OK) return s;
+  if (moe_status s = check_pitch(ld_gu, 2 * int64_t(I), "ld_gu"); s != MOE_OK) return s;
+  if (moe_status s = check_pitch(ld_a, I, "ld_a"); s != MOE_OK) return s;
+  if (moe_status s = check_act8(codes, scales); s != MOE_OK) return s;
+  if (rows == 0) return MOE_OK;
+  REQUIRE_PTR(gu);
+  REQUIRE_PTR(a);
+  if (!al16(prob)) return fail(MOE_ERR_ALIGNMENT, "prob is not 16-byte aligned");
+  SwigluArgs s{};
+  s.rows = rows;
+  s.I = I;
+  s.gu = static_cast<const __nv_bfloat16*>(gu);
+  s.ld_gu = ld_gu;
+  s.prob = prob;
+  s.a = static_cast<__nv_bfloat16*>(a);
+  s.ld_a = ld_a;
+  s.codes = codes;
+  s.scales = scales;
+  CUDA_TRY(launch_swiglu_fwd(s, static_cast<cudaStream_t>(stream)), "swiglu forward");
+  return MOE_OK;
+}
+
+moe_status moe_swiglu_bwd(int64_t rows, int32_t I, const void* gu, int64_t ld_gu, const uint8_t* codes,
+                          const uint8_t* scales, const float* prob, const void* da, int64_t ld_da, void* dgu,
+                          int64_t ld_dgu, float* dprob, void* a, int64_t ld_a, moe_stream_t stream) {
+  if (moe_status s = check_rows_cols(rows, I); s != MOE_OK) return s;
+  if (moe_status s = check_act8(codes, scales); s != MOE_OK) return s;
+  if (gu != nullptr)
+    if (moe_status s = check_pitch(ld_gu, 2 * int64_t(I), "ld_gu"); s != MOE_OK) return s;
+  if (moe_status s = check_pitch(ld_da, I, "ld_da"); s != MOE_OK) return s;
+  if (moe_status s = check_pitch(ld_dgu, 2 * int64_t(I), "ld_dgu"); s != MOE_OK) return s;
+  if (a != nullptr)
+    if (moe_status s = check_pitch(ld_a, I, "ld_a"); s != MOE_OK) return s;
+  if (prob == nullptr && dprob != nullptr) return fail(MOE_ERR_INVALID_ARG, "dprob without prob");
+  if (rows == 0) return MOE_OK;
+  if ((gu == nullptr) == (codes == nullptr)) return fail(MOE_ERR_INVALID_ARG, "give either gu, or codes and scales");
+  REQUIRE_PTR(da);
+  REQUIRE_PTR(dgu);
+  if (!al16(gu) || !al16(prob) || !al16(dprob) || !al16(a))
+    return fail(MOE_ERR_ALIGNMENT, "gu, prob, dprob or a is not 16-byte aligned");
+  SwigluArgs s{};
+  s.rows = rows;
+  s.I = I;
+  s.gu = static_cast<const __nv_bfloat16*>(gu);
+  s.ld_gu = ld_gu;
+  s.codes = const_cast<uint8_t*>(codes);
+  s.scales = const_cast<uint8_t*>(scales);
+  s.prob = prob;
+  s.da = static_cast<const __nv_bfloat16*>(da);
+  s.ld_da = ld_da;
+  s.dgu = static_cast<__nv_bfloat16*>(dgu);
+  s.ld_dgu = ld_dgu;
+  s.dprob = dprob;
+  s.a = static_cast<__nv_bfloat16*>(a);
+  s.ld_a = ld_a;
+  CUDA_TRY(launch_swiglu_bwd(s, static_cast<cudaStream_t>(stream)), "swiglu backward");
+  return MOE_OK;
+}
+
+size_t moe_grouped_linear_workspace_size(const moe_grouped* g) { return check_grouped(g) == MOE_OK ? 256 : 0; }
+
+moe_status moe_grouped_linear_fwd(const moe_grouped* g, const void* x, int64_t ldx, const int32_t* split_sizes,
+                                  const void* w, void* y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                                  moe_stream_t stream) {
+  if (moe_status s = check_grouped_call(g, ldx, ldy, workspace, workspace_bytes); s != MOE_OK) return s;
+  if (g->rows == 0) return MOE_OK;
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(split_sizes);
+  REQUIRE_PTR(w);
+  REQUIRE_PTR(y);
+  return run_grouped(LIN_FWD, g, x, ldx, nullptr, 0, split_sizes, w, y, ldy, workspace, static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_grouped_linear_dgrad(const moe_grouped* g, const void* dy, int64_t ldy, const int32_t* split_sizes,
+                                    const void* w, void* dx, int64_t ldx, void* workspace, size_t workspace_bytes,
+                                    moe_stream_t stream) {
+  if (moe_status s = check_grouped_call(g, ldx, ldy, workspace, workspace_bytes); s != MOE_OK) return s;
+  if (g->rows == 0) return MOE_OK;
+  REQUIRE_PTR(dy);
+  REQUIRE_PTR(split_sizes);
+  REQUIRE_PTR(w);
+  REQUIRE_PTR(dx);
+  return run_grouped(LIN_DGRAD, g, nullptr, 0, dy, ldy, split_sizes, w, dx, ldx, workspace, static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_grouped_linear_wgrad(const moe_grouped* g, const void* x, int64_t ldx, const void* dy, int64_t ldy,
+                                    const int32_t* split_sizes, void* dw, void* workspace, size_t workspace_bytes,
+                                    moe_stream_t stream) {
+  if (moe_status s = check_grouped_call(g, ldx, ldy, workspace, workspace_bytes); s != MOE_OK) return s;
+  REQUIRE_PTR(dw);
+  if (g->rows == 0) {
+    CUDA_TRY(cudaMemsetAsync(dw, 0, size_t(g->E) * g->N * g->K * 2, static_cast<cudaStream_t>(stream)), "grouped linear wgrad");
+    return MOE_OK;
+  }
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(dy);
+  REQUIRE_PTR(split_sizes);
+  return run_grouped(LIN_WGRAD, g, x, ldx, dy, ldy, split_sizes, nullptr, dw, g->K, workspace,
+                     static_cast<cudaStream_t>(stream));
+}
+
 moe_status moe_selftest_wait_timeout(void* scratch, size_t scratch_bytes, int64_t limit_ns, int32_t* code,
                                      int32_t* site, moe_stream_t stream) {
   g_msg[0] = 0;

@@ -26,6 +26,7 @@ enum ErrSite : int {
   SITE_GEMM_EPILOGUE = 530,
   SITE_GEMM_DRAIN = 540,
   SITE_ROUTER_DW = 600,
+  SITE_LINEAR = 700,
 };
 
 __device__ __forceinline__ void report_error(int* err, int code, int site) {

@@ -167,6 +167,70 @@ cudaError_t launch_dprob_reduce(const float* dp_part, int n_tiles, int64_t cap, 
                                 const int* src_of, const int* row_of, int k, int T, float* dprob, int* err,
                                 cudaStream_t st);
 
+// ---- layer norm (norm.cu) ---------------------------------------------------------------
+struct NormArgs {
+  int64_t rows;
+  int H;
+  float eps;
+  bool w_f32;                // gamma, beta and their gradients: f32 (else bf16)
+  int64_t ld_in, ld_out;     // row pitch of x, residual, dy, dres and of h, y, dx
+  const void* x;             // forward input; backward: the kept h (with mean) when codes is null
+  const void* residual;      // optional, added to x
+  const void* gamma;
+  const void* beta;          // optional
+  void* h;                   // out, optional: x + residual
+  void* y;
+  float* mean;
+  float* rstd;
+  uint8_t* codes;            // the normalised input in 8 bits: out (forward, optional) or in (backward)
+  uint8_t* scales;
+  const void* dy;
+  const void* dres;          // optional, added to dx
+  void* dx;
+  void* dgamma;
+  void* dbeta;               // optional
+};
+size_t norm_ws_bytes(int64_t rows, int H);
+cudaError_t launch_norm_fwd(const NormArgs& a, bool x_f32, cudaStream_t st);
+cudaError_t launch_norm_bwd(const NormArgs& a, bool x_f32, float* partial, cudaStream_t st);
+
+// ---- gated activation and 8-bit checkpoints (act8.cu) -------------------------------------
+struct SwigluArgs {
+  int64_t rows;
+  int I;
+  const __nv_bfloat16* gu;   // [rows][2I] (backward: null when codes is given)
+  int64_t ld_gu;
+  const float* prob;         // optional
+  __nv_bfloat16* a;          // out (backward: optional)
+  int64_t ld_a;
+  uint8_t* codes;            // [rows][2I]; forward: out, optional
+  uint8_t* scales;           // [rows][2 * ceil(I/32)]: g's blocks, then u's
+  const __nv_bfloat16* da;
+  int64_t ld_da;
+  __nv_bfloat16* dgu;
+  int64_t ld_dgu;
+  float* dprob;              // optional
+};
+cudaError_t launch_swiglu_fwd(const SwigluArgs& a, cudaStream_t st);
+cudaError_t launch_swiglu_bwd(const SwigluArgs& a, cudaStream_t st);
+cudaError_t launch_act8_pack(const void* src, bool f32, int64_t rows, int cols, int64_t ld, uint8_t* codes,
+                             uint8_t* scales, cudaStream_t st);
+cudaError_t launch_act8_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols, const void* gamma,
+                               const void* beta, bool w_f32, void* dst, bool f32, int64_t ld, cudaStream_t st);
+
+// ---- linear layers grouped by expert on dense ragged rows (grouped_linear.cu) --------------
+enum LinearMode : int { LIN_FWD = 0, LIN_DGRAD = 1, LIN_WGRAD = 2 };
+struct LinearArgs {
+  int64_t rows;              // rows of x and dy (the sum of split_sizes, or more)
+  int E, K, N;               // w [E][N][K]
+  const int* split_sizes;    // device
+  __nv_bfloat16* out;        // FWD y [rows][N], DGRAD dx [rows][K], WGRAD dw [E][N][K]
+  int64_t ldo;
+  int* err;
+};
+cudaError_t launch_grouped_linear(int mode, const LinearArgs& a, const void* x, int64_t ldx, const void* dy,
+                                  int64_t lddy, const void* w, cudaStream_t st, char* msg, size_t msg_len);
+
 // ---- grouped block-scaled MXFP8 GEMM (tcgen05) ------------------------------------
 // C[M][N] = A[M][K] * B[N][K]^T, both operands K-major MX tensors.
 //   mode 0 (grouped rows): A rows are the permuted token rows, split into

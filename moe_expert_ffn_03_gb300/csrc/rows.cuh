@@ -1,0 +1,199 @@
+// Helpers of the row-wise kernels (layer norm, the gated activation, 8-bit checkpoints):
+// vectors of a row, sums over the threads of a row, and the 8-bit checkpoint's blocks.
+//
+// A row is shared by `tpr` threads (32 .. 1024, a power of two); a block holds blockDim/tpr
+// rows.  Vector i of thread t is columns (i * tpr + t) * VEC .. + VEC - 1: VEC = 8 for rows
+// whose pitch and length are multiples of 8 (16-byte loads of bf16), VEC = 1 for all others.
+// Either way the 32 columns of a checkpoint block sit in one warp: in four neighbouring
+// lanes (VEC = 8) or in all 32 (VEC = 1).
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace moe {
+namespace {
+
+// ---- VEC values of a row as they lie in memory, and as floats -------------------------------
+// Activations are read and written once: loads and stores are marked streaming, so that the
+// weights and partial sums stay in the caches.
+template <typename T, int VEC>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16, 8> {
+  uint4 q;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { q = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void zero() { q = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float* v) const {
+    v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
+    v[4] = bf16_lo(q.z); v[5] = bf16_hi(q.z); v[6] = bf16_lo(q.w); v[7] = bf16_hi(q.w);
+  }
+};
+template <>
+struct Raw<float, 8> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldcs(reinterpret_cast<const float4*>(p));
+    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float* v) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+template <>
+struct Raw<__nv_bfloat16, 1> {
+  __nv_bfloat16 q;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { q = *p; }
+  __device__ __forceinline__ void zero() { q = __float2bfloat16_rn(0.f); }
+  __device__ __forceinline__ void get(float* v) const { v[0] = __bfloat162float(q); }
+};
+template <>
+struct Raw<float, 1> {
+  float q;
+  __device__ __forceinline__ void load(const float* p) { q = *p; }
+  __device__ __forceinline__ void zero() { q = 0.f; }
+  __device__ __forceinline__ void get(float* v) const { v[0] = q; }
+};
+
+template <int VEC>
+__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float* v) {
+  if constexpr (VEC == 8) {
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                   pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+  } else {
+    *p = __float2bfloat16_rn(v[0]);
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void store_vec(float* p, const float* v) {
+  if constexpr (VEC == 8) {
+    __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
+  } else {
+    *p = v[0];
+  }
+}
+
+// VEC values of a weight vector (bf16, or f32 when f32 is set) from column col; these are read
+// once per row by every block and stay in L1.
+template <int VEC>
+__device__ __forceinline__ void load_weight(const void* w, bool f32, int64_t col, float* v) {
+  if constexpr (VEC == 8) {
+    if (f32) {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + col);
+      const float4 a = __ldg(p), b = __ldg(p + 1);
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+      Raw<__nv_bfloat16, 8> r;
+      r.q = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + col));
+      r.get(v);
+    }
+  } else {
+    v[0] = f32 ? __ldg(static_cast<const float*>(w) + col)
+               : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(w) + col));
+  }
+}
+
+// ---- sums over the threads of a row -------------------------------------------------------
+// N sums at once over the tpr threads of each row.  All threads of the block call it (it
+// synchronises the block when a row spans warps); the order is fixed.  buf: 32 * N floats of
+// shared memory; two calls in a row use different ones, so one barrier per call is enough.
+template <int N>
+__device__ __forceinline__ void row_sum(float* v, int tpr, float* buf) {
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v[n] += __shfl_xor_sync(0xFFFFFFFFu, v[n], off);
+  if (tpr > 32) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per = tpr >> 5, first = warp & ~(per - 1);
+    if (lane == 0)
+#pragma unroll
+      for (int n = 0; n < N; ++n) buf[warp * N + n] = v[n];
+    __syncthreads();
+    // every warp adds the row's partial sums in the same tree
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      float s = lane < per ? buf[(first + lane) * N + n] : 0.f;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+      v[n] = s;
+    }
+  }
+}
+
+// ---- 8-bit checkpoints ----------------------------------------------------------------------
+// One power-of-two scale per 32 consecutive values of a row and E4M3 codes, the quantization
+// rule of the MX tensors; the last block of a row may be short.  Codes [rows][cols] row-major,
+// scale codes [rows][ceil(cols/32)] row-major (these tensors feed no MMA, so the scales need
+// no tile layout).
+//
+// Quantizes this thread's VEC values of its block (all lanes of the warp call it; lanes past
+// the row's end bring zeros) and stores codes and scale when `in` is set.
+template <int VEC>
+__device__ __forceinline__ void store_act8(const float* v, bool in, uint8_t* codes, uint8_t* scales, int64_t row,
+                                           int64_t ld_codes, int64_t col0, int col, int64_t ld_scales, int blk0) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) amax = max(amax, abs_bits(v[j]));
+  if constexpr (VEC == 8) {
+    amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+    amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+  } else {
+    amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+  }
+  if (!in) return;
+  const uint32_t c = mx_scale_code(amax);
+  const float m = c == 255u ? 0.f : mx_inv_scale(c);
+  uint8_t* pc = codes + row * ld_codes + col0 + col;
+  if constexpr (VEC == 8) {
+    uint2 q = make_uint2(cvt_e4m3x2(v[0] * m, v[1] * m) | (cvt_e4m3x2(v[2] * m, v[3] * m) << 16),
+                         cvt_e4m3x2(v[4] * m, v[5] * m) | (cvt_e4m3x2(v[6] * m, v[7] * m) << 16));
+    if (c == 255u) q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    __stcs(reinterpret_cast<uint2*>(pc), q);
+  } else {
+    *pc = c == 255u ? 0x7Fu : uint8_t(cvt_e4m3x2(v[0] * m, 0.f));
+  }
+  if ((col & 31) == 0) scales[row * ld_scales + blk0 + (col >> 5)] = uint8_t(c);
+}
+
+// 2^(c - 127); c = 0 is 2^-127 (subnormal), c = 255 only meets NaN codes.
+__device__ __forceinline__ float act8_scale(uint32_t c) { return __uint_as_float(c == 0u ? 0x00400000u : c << 23); }
+
+// Two E4M3 codes (low half of w) as floats.
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t w) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(w)));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// This thread's VEC codes of a row (as stored by store_act8) and their scale code.
+template <int VEC>
+struct Act8 {
+  uint2 q;
+  uint32_t c;
+  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, int64_t row, int64_t ld_codes,
+                                       int64_t col0, int col, int64_t ld_scales, int blk0) {
+    const uint8_t* pc = codes + row * ld_codes + col0 + col;
+    if constexpr (VEC == 8) q = __ldcs(reinterpret_cast<const uint2*>(pc));
+    else q.x = *pc;
+    c = scales[row * ld_scales + blk0 + (col >> 5)];
+  }
+  __device__ __forceinline__ void zero() { q = make_uint2(0, 0); c = 0; }
+  __device__ __forceinline__ void get(float* v) const {
+    const float s = act8_scale(c);
+    if constexpr (VEC == 8) {
+      const float2 a = e4m3x2_to_float2(q.x), b = e4m3x2_to_float2(q.x >> 16);
+      const float2 d = e4m3x2_to_float2(q.y), e = e4m3x2_to_float2(q.y >> 16);
+      v[0] = a.x * s; v[1] = a.y * s; v[2] = b.x * s; v[3] = b.y * s;
+      v[4] = d.x * s; v[5] = d.y * s; v[6] = e.x * s; v[7] = e.y * s;
+    } else {
+      v[0] = e4m3x2_to_float2(q.x).x * s;
+    }
+  }
+};
+
+}  // namespace
+}  // namespace moe
