@@ -155,7 +155,8 @@ def _p(t):
 
 def _st(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the current stream's handle without a Stream object around it (2.9 us of a small call's 7.3)
+        return c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return c_void_p(stream.cuda_stream)
 
 

@@ -165,9 +165,9 @@ cudaError_t pack_t(const void* src, int64_t rows, int cols, int64_t ld, uint8_t*
                    cudaStream_t st) {
   const T* s = static_cast<const T*>(src);
   const bool vec = cols % 8 == 0 && ld % 8 == 0;
-  const int tpr = threads_per_row(rows, cols, vec ? 8 : 1);
+  const int tpr = threads_per_row(rows, cols, vec ? kWide<T> : 1);
   if (vec)
-    return launch_pdl(act8_pack_kernel<T, 8>, row_grid(rows, tpr), dim3(ROW_BLOCK), 0, st, s, rows, cols, ld, codes,
+    return launch_pdl(act8_pack_kernel<T, kWide<T>>, row_grid(rows, tpr), dim3(ROW_BLOCK), 0, st, s, rows, cols, ld, codes,
                       scales, tpr);
   return launch_pdl(act8_pack_kernel<T, 1>, row_grid(rows, tpr), dim3(ROW_BLOCK), 0, st, s, rows, cols, ld, codes,
                     scales, tpr);
@@ -178,9 +178,9 @@ cudaError_t unpack_t(const uint8_t* codes, const uint8_t* scales, int64_t rows, 
                      const void* beta, bool w_f32, void* dst, int64_t ld, cudaStream_t st) {
   T* d = static_cast<T*>(dst);
   const bool vec = cols % 8 == 0 && ld % 8 == 0;
-  const int tpr = threads_per_row(rows, cols, vec ? 8 : 1);
+  const int tpr = threads_per_row(rows, cols, vec ? kWide<T> : 1);
   if (vec)
-    return launch_pdl(act8_unpack_kernel<T, 8>, row_grid(rows, tpr), dim3(ROW_BLOCK), 0, st, codes, scales, rows, cols,
+    return launch_pdl(act8_unpack_kernel<T, kWide<T>>, row_grid(rows, tpr), dim3(ROW_BLOCK), 0, st, codes, scales, rows, cols,
                       gamma, beta, w_f32, d, ld, tpr);
   return launch_pdl(act8_unpack_kernel<T, 1>, row_grid(rows, tpr), dim3(ROW_BLOCK), 0, st, codes, scales, rows, cols,
                     gamma, beta, w_f32, d, ld, tpr);

@@ -2,10 +2,10 @@
 // vectors of a row, sums over the threads of a row, and the 8-bit checkpoint's blocks.
 //
 // A row is shared by `tpr` threads (32 .. 1024, a power of two); a block holds blockDim/tpr
-// rows.  Vector i of thread t is columns (i * tpr + t) * VEC .. + VEC - 1: VEC = 8 for rows
-// whose pitch and length are multiples of 8 (16-byte loads of bf16), VEC = 1 for all others.
-// Either way the 32 columns of a checkpoint block sit in one warp: in four neighbouring
-// lanes (VEC = 8) or in all 32 (VEC = 1).
+// rows.  Vector i of thread t is columns (i * tpr + t) * VEC .. + VEC - 1, where VEC values are
+// 16 bytes (8 of bf16, 4 of f32) for rows whose length and pitch are multiples of 8, and VEC = 1
+// for all others.  Either way the 32 columns of a checkpoint block sit in one warp, in 32 / VEC
+// neighbouring lanes.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -18,6 +18,8 @@ namespace {
 // ---- VEC values of a row as they lie in memory, and as floats -------------------------------
 // Activations are read and written once: loads and stores are marked streaming, so that the
 // weights and partial sums stay in the caches.
+template <typename T>
+constexpr int kWide = 16 / int(sizeof(T));
 template <typename T, int VEC>
 struct Raw;
 template <>
@@ -31,16 +33,11 @@ struct Raw<__nv_bfloat16, 8> {
   }
 };
 template <>
-struct Raw<float, 8> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = __ldcs(reinterpret_cast<const float4*>(p));
-    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-  }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void get(float* v) const {
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  }
+struct Raw<float, 4> {
+  float4 q;
+  __device__ __forceinline__ void load(const float* p) { q = __ldcs(reinterpret_cast<const float4*>(p)); }
+  __device__ __forceinline__ void zero() { q = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float* v) const { v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w; }
 };
 template <>
 struct Raw<__nv_bfloat16, 1> {
@@ -62,17 +59,20 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float* v) {
   if constexpr (VEC == 8) {
     __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
                                                    pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+  } else if constexpr (VEC == 4) {
+    __stcs(reinterpret_cast<uint2*>(p), make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])));
   } else {
     *p = __float2bfloat16_rn(v[0]);
   }
 }
 template <int VEC>
 __device__ __forceinline__ void store_vec(float* p, const float* v) {
-  if constexpr (VEC == 8) {
-    __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
-    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
-  } else {
+  if constexpr (VEC == 1) {
     *p = v[0];
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; j += 4)
+      __stcs(reinterpret_cast<float4*>(p + j), make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
   }
 }
 
@@ -80,20 +80,46 @@ __device__ __forceinline__ void store_vec(float* p, const float* v) {
 // once per row by every block and stay in L1.
 template <int VEC>
 __device__ __forceinline__ void load_weight(const void* w, bool f32, int64_t col, float* v) {
-  if constexpr (VEC == 8) {
-    if (f32) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + col);
-      const float4 a = __ldg(p), b = __ldg(p + 1);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-      Raw<__nv_bfloat16, 8> r;
-      r.q = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + col));
-      r.get(v);
-    }
-  } else {
+  if constexpr (VEC == 1) {
     v[0] = f32 ? __ldg(static_cast<const float*>(w) + col)
                : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(w) + col));
+  } else if (f32) {
+#pragma unroll
+    for (int j = 0; j < VEC; j += 4) {
+      const float4 q = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + col + j));
+      v[j] = q.x; v[j + 1] = q.y; v[j + 2] = q.z; v[j + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; j += 4) {
+      const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(w) + col + j));
+      v[j] = bf16_lo(q.x); v[j + 1] = bf16_hi(q.x); v[j + 2] = bf16_lo(q.y); v[j + 3] = bf16_hi(q.y);
+    }
   }
+}
+
+// ---- rows on their way: a ring of 16-byte pieces in shared memory ----------------------------
+// Every thread copies with cp.async the pieces that it alone will read, so the ring needs no
+// barrier: cp_async_wait<N> returns when all but the thread's last N groups have landed.
+template <int BYTES>                              // 4, 8 or 16
+__device__ __forceinline__ void ring_copy(uint8_t* smem, const void* gmem, bool valid) {
+  if constexpr (BYTES == 16)
+    cp_async16(smem, gmem, valid);
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(smem_u32(smem)), "l"(gmem), "n"(BYTES),
+                 "r"(valid ? BYTES : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void ring_get(const uint8_t* p, float* v) {
+  Raw<T, kWide<T>> r;
+  r.q = *reinterpret_cast<const decltype(r.q)*>(p);
+  r.get(v);
 }
 
 // ---- sums over the threads of a row -------------------------------------------------------
@@ -138,23 +164,27 @@ __device__ __forceinline__ void store_act8(const float* v, bool in, uint8_t* cod
   uint32_t amax = 0;
 #pragma unroll
   for (int j = 0; j < VEC; ++j) amax = max(amax, abs_bits(v[j]));
-  if constexpr (VEC == 8) {
-    amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-    amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-  } else {
+  if constexpr (VEC == 1) {
     amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+  } else {
+#pragma unroll
+    for (int off = 1; off < 32 / VEC; off *= 2) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
   }
   if (!in) return;
   const uint32_t c = mx_scale_code(amax);
   const float m = c == 255u ? 0.f : mx_inv_scale(c);
   uint8_t* pc = codes + row * ld_codes + col0 + col;
-  if constexpr (VEC == 8) {
-    uint2 q = make_uint2(cvt_e4m3x2(v[0] * m, v[1] * m) | (cvt_e4m3x2(v[2] * m, v[3] * m) << 16),
-                         cvt_e4m3x2(v[4] * m, v[5] * m) | (cvt_e4m3x2(v[6] * m, v[7] * m) << 16));
-    if (c == 255u) q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-    __stcs(reinterpret_cast<uint2*>(pc), q);
-  } else {
+  if constexpr (VEC == 1) {
     *pc = c == 255u ? 0x7Fu : uint8_t(cvt_e4m3x2(v[0] * m, 0.f));
+  } else {
+    uint32_t q[VEC / 4];
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i) {
+      q[i] = cvt_e4m3x2(v[4 * i] * m, v[4 * i + 1] * m) | (cvt_e4m3x2(v[4 * i + 2] * m, v[4 * i + 3] * m) << 16);
+      if (c == 255u) q[i] = 0x7F7F7F7Fu;
+    }
+    if constexpr (VEC == 8) __stcs(reinterpret_cast<uint2*>(pc), make_uint2(q[0], q[1]));
+    else __stcs(reinterpret_cast<uint32_t*>(pc), q[0]);
   }
   if ((col & 31) == 0) scales[row * ld_scales + blk0 + (col >> 5)] = uint8_t(c);
 }
@@ -172,25 +202,37 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t w) {
 // This thread's VEC codes of a row (as stored by store_act8) and their scale code.
 template <int VEC>
 struct Act8 {
-  uint2 q;
+  uint32_t q[VEC == 8 ? 2 : 1];
   uint32_t c;
+  __device__ __forceinline__ void take(const uint8_t* p) {        // the codes at p
+    if constexpr (VEC == 8) {
+      const uint2 w = __ldcs(reinterpret_cast<const uint2*>(p));
+      q[0] = w.x;
+      q[1] = w.y;
+    } else if constexpr (VEC == 4) {
+      q[0] = __ldcs(reinterpret_cast<const uint32_t*>(p));
+    } else {
+      q[0] = *p;
+    }
+  }
   __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, int64_t row, int64_t ld_codes,
                                        int64_t col0, int col, int64_t ld_scales, int blk0) {
-    const uint8_t* pc = codes + row * ld_codes + col0 + col;
-    if constexpr (VEC == 8) q = __ldcs(reinterpret_cast<const uint2*>(pc));
-    else q.x = *pc;
+    take(codes + row * ld_codes + col0 + col);
     c = scales[row * ld_scales + blk0 + (col >> 5)];
   }
-  __device__ __forceinline__ void zero() { q = make_uint2(0, 0); c = 0; }
   __device__ __forceinline__ void get(float* v) const {
     const float s = act8_scale(c);
-    if constexpr (VEC == 8) {
-      const float2 a = e4m3x2_to_float2(q.x), b = e4m3x2_to_float2(q.x >> 16);
-      const float2 d = e4m3x2_to_float2(q.y), e = e4m3x2_to_float2(q.y >> 16);
-      v[0] = a.x * s; v[1] = a.y * s; v[2] = b.x * s; v[3] = b.y * s;
-      v[4] = d.x * s; v[5] = d.y * s; v[6] = e.x * s; v[7] = e.y * s;
+    if constexpr (VEC == 1) {
+      v[0] = e4m3x2_to_float2(q[0]).x * s;
     } else {
-      v[0] = e4m3x2_to_float2(q.x).x * s;
+#pragma unroll
+      for (int i = 0; i < VEC / 4; ++i) {
+        const float2 a = e4m3x2_to_float2(q[i]), b = e4m3x2_to_float2(q[i] >> 16);
+        v[4 * i] = a.x * s;
+        v[4 * i + 1] = a.y * s;
+        v[4 * i + 2] = b.x * s;
+        v[4 * i + 3] = b.y * s;
+      }
     }
   }
 };
