@@ -18,134 +18,150 @@
 namespace moe {
 namespace {
 
-// A row has at most 512 threads.  Blocks of that size an SM is to hold: two where a thread has few
-// columns (VEC * NV), else one.
+// A row has at most 512 threads, and an SM holds that many (the kernels take up to 128 registers):
+// what keeps the memory busy is the ring below, not the number of threads.
 constexpr int MAX_TPR = 512;
-constexpr int min_blocks(int vec, int nv) { return vec * nv <= 8 ? 2 : 1; }
-// Rows a block has on their way or in work at once (VEC > 1): up to three, as the 16-byte pieces
-// of all resident blocks fit in shared memory (`pieces` per thread and row).
-constexpr int ring_stages(int vec, int nv, int pieces) {
+// Rows a thread has on their way or in work at once (VEC > 1): up to three, as 512 threads' 16-byte
+// pieces fit in shared memory (`pieces` per thread and row).
+constexpr int ring_stages(int vec, int pieces) {
   if (vec == 1) return 0;
-  const int most = 200 * 1024 / (min_blocks(vec, nv) * MAX_TPR * pieces * 16);
+  const int most = 200 * 1024 / (MAX_TPR * pieces * 16);
   return most > 3 ? 3 : most;
 }
 
+// A thread's place: its row group, its first column (vector i is 32 * VEC columns further, a
+// distance the compiler knows), and its slots of the ring, laid out per warp
+// [stage][operand][vector][lane] of 16 bytes so that they too are constant distances apart.
+template <int VEC, int NV, int OPS, int STG>
+struct Place {
+  int group, groups, t, warp0, col0;
+  uint8_t* slot;
+  __device__ __forceinline__ Place(int tpr, uint8_t* ring) {
+    group = threadIdx.x / tpr;
+    groups = blockDim.x / tpr;
+    t = threadIdx.x - group * tpr;
+    warp0 = group * (tpr >> 5);
+    col0 = (t >> 5) * (32 * NV * VEC) + (t & 31) * VEC;
+    slot = ring + (threadIdx.x >> 5) * (STG * OPS * NV * 512) + (threadIdx.x & 31) * 16;
+  }
+  __device__ __forceinline__ int col(int i) const { return col0 + i * (32 * VEC); }
+  __device__ __forceinline__ uint8_t* piece(int st, int op, int i) const {
+    return slot + st * (OPS * NV * 512) + (op * NV + i) * 512;
+  }
+};
+
 // A persistent grid: block b takes the row groups b, b + grid, ...  The next groups' x (and
 // residual) are on their way to shared memory while the current one is summed, so the two
-// barriers of a row (mean, then the variance of the centred values) cost no memory time.
+// sums of a row (mean, then the variance of the centred values) cost no memory time.
 template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(MAX_TPR, min_blocks(VEC, NV)) norm_fwd_kernel(const NormArgs a, int tpr) {
-  constexpr int STG = ring_stages(VEC, NV, 2 * NV);
+__global__ void __launch_bounds__(MAX_TPR, 1) norm_fwd_kernel(const NormArgs a, int tpr) {
+  constexpr int STG = ring_stages(VEC, 2 * NV);
   __shared__ float sums[2][32];
-  extern __shared__ __align__(16) uint8_t ring[]; // [stage][x, residual][vector][thread] of 16 bytes
-  const int t = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = blockDim.x / tpr;
-  const int pitch = int(blockDim.x) * 16;
+  extern __shared__ __align__(16) uint8_t ring[];
+  const Place<VEC, NV, 2, STG> at(tpr, ring);
   const float inv_H = 1.f / float(a.H);
-  const int64_t step = int64_t(gridDim.x) * groups;
-  const auto piece = [&](int st, int op, int i) {
-    return ring + ((st * 2 + op) * NV + i) * pitch + threadIdx.x * 16;
-  };
+  const int64_t step = int64_t(gridDim.x) * at.groups;
+  const bool has_res = a.residual != nullptr;
   const auto fetch = [&](int64_t row, int st) {
     if constexpr (VEC > 1) {
+      const bool live = row < a.rows;
+      const T* x = static_cast<const T*>(a.x) + (live ? row * a.ld_in + at.col0 : 0);
+      const T* res = static_cast<const T*>(a.residual) + (live ? row * a.ld_in + at.col0 : 0);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int col = (i * tpr + t) * VEC;
-        const bool in = row < a.rows && col < a.H;
-        const int64_t at = in ? row * a.ld_in + col : 0;
-        ring_copy<16>(piece(st, 0, i), static_cast<const T*>(a.x) + at, in);
-        if (a.residual != nullptr) ring_copy<16>(piece(st, 1, i), static_cast<const T*>(a.residual) + at, in);
+        const bool in = live && at.col(i) < a.H;
+        ring_copy<16>(at.piece(st, 0, i), in ? x + i * (32 * VEC) : static_cast<const T*>(a.x), in);
+        if (has_res) ring_copy<16>(at.piece(st, 1, i), in ? res + i * (32 * VEC) : static_cast<const T*>(a.x), in);
       }
       cp_async_commit();
     }
   };
   pdl_wait();
-  int64_t row = int64_t(blockIdx.x) * groups + group;
+  int64_t row = int64_t(blockIdx.x) * at.groups + at.group;
 #pragma unroll
   for (int k = 0; k + 1 < STG; ++k) fetch(row + k * step, k);
   int st = 0;
-  for (int64_t row0 = int64_t(blockIdx.x) * groups; row0 < a.rows; row0 += step, row += step) {
+  for (int64_t row0 = int64_t(blockIdx.x) * at.groups; row0 < a.rows; row0 += step, row += step) {
     const bool live = row < a.rows;
     if constexpr (VEC > 1) {
       fetch(row + (STG - 1) * step, st == 0 ? STG - 1 : st - 1);
       cp_async_wait<STG - 1>();
     }
-    float h[NV][VEC];
-    float s[1] = {0.f};
+    float h[NV][VEC], sum[VEC];
+    v_fill<VEC>(sum, 0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float v[VEC];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) v[j] = 0.f;
       if constexpr (VEC > 1) {
-        ring_get<T>(piece(st, 0, i), h[i]);
-        if (a.residual != nullptr) ring_get<T>(piece(st, 1, i), v);
+        ring_get<T>(at.piece(st, 0, i), h[i]);
+        if (has_res) {
+          ring_get<T>(at.piece(st, 1, i), v);
+          v_add<VEC>(h[i], v);
+        }
       } else {
-        const int col = i * tpr + t;
         Raw<T, 1> x, r;
         x.zero();
         r.zero();
-        if (live && col < a.H) {
-          x.load(static_cast<const T*>(a.x) + row * a.ld_in + col);
-          if (a.residual != nullptr) r.load(static_cast<const T*>(a.residual) + row * a.ld_in + col);
+        if (live && at.col(i) < a.H) {
+          x.load(static_cast<const T*>(a.x) + row * a.ld_in + at.col0 + i * 32);
+          if (has_res) r.load(static_cast<const T*>(a.residual) + row * a.ld_in + at.col0 + i * 32);
         }
         x.get(h[i]);
         r.get(v);
+        h[i][0] += v[0];
       }
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        h[i][j] += v[j];
-        s[0] += h[i][j];
-      }
+      v_add<VEC>(sum, h[i]);
     }
     if constexpr (VEC > 1) st = st + 1 == STG ? 0 : st + 1;
-    row_sum<1>(s, tpr, sums[0]);
+    float s[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) s[0] += sum[j];
+    row_sum<1>(s, tpr, at.warp0, sums[0]);
     const float mu = __fdiv_rn(s[0], float(a.H));   // exact for a constant row whose sum is
     if (a.h != nullptr && live) {
-      T* ho = static_cast<T*>(a.h) + row * a.ld_out;
+      T* ho = static_cast<T*>(a.h) + row * a.ld_out + at.col0;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int col = (i * tpr + t) * VEC;
-        if (col < a.H) store_vec<VEC>(ho + col, h[i]);
-      }
+      for (int i = 0; i < NV; ++i)
+        if (at.col(i) < a.H) store_vec<VEC>(ho + i * (32 * VEC), h[i]);
+    }
+    float minus[VEC], sq[VEC];
+    v_fill<VEC>(minus, -mu);
+    v_fill<VEC>(sq, 0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      v_add<VEC>(h[i], minus);
+      if (at.col(i) >= a.H) v_fill<VEC>(h[i], 0.f);
+      v_fma<VEC>(sq, h[i], h[i]);
     }
     s[0] = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const bool in = (i * tpr + t) * VEC < a.H;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        h[i][j] = in ? h[i][j] - mu : 0.f;
-        s[0] += h[i][j] * h[i][j];
-      }
-    }
-    row_sum<1>(s, tpr, sums[1]);
+    for (int j = 0; j < VEC; ++j) s[0] += sq[j];
+    row_sum<1>(s, tpr, at.warp0, sums[1]);
     const float rstd = 1.f / sqrtf(s[0] * inv_H + a.eps);
-    if (live && t == 0) {
+    if (live && at.t == 0) {
       if (a.mean != nullptr) a.mean[row] = mu;
       if (a.rstd != nullptr) a.rstd[row] = rstd;
     }
-    T* y = static_cast<T*>(a.y) + row * a.ld_out;
+    T* y = static_cast<T*>(a.y) + row * a.ld_out + at.col0;
+    float rs[VEC];
+    v_fill<VEC>(rs, rstd);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = (i * tpr + t) * VEC;
-      const bool in = live && col < a.H;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) h[i][j] *= rstd;
+      const bool in = live && at.col(i) < a.H;
+      v_mul<VEC>(h[i], rs);
       if (a.codes != nullptr)
-        store_act8<VEC>(h[i], in, a.codes, a.scales, row, a.H, 0, col, (a.H + 31) >> 5, 0);
+        store_act8<VEC>(h[i], in, a.codes, a.scales, row, a.H, 0, at.col(i), (a.H + 31) >> 5, 0);
       if (in) {
         float g[VEC], b[VEC];
-        load_weight<VEC>(a.gamma, a.w_f32, col, g);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) b[j] = 0.f;
-        if (a.beta != nullptr) load_weight<VEC>(a.beta, a.w_f32, col, b);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) b[j] = h[i][j] * g[j] + b[j];
-        store_vec<VEC>(y + col, b);
+        load_weight<VEC>(a.gamma, a.w_f32, at.col(i), g);
+        v_fill<VEC>(b, 0.f);
+        if (a.beta != nullptr) load_weight<VEC>(a.beta, a.w_f32, at.col(i), b);
+        v_fma<VEC>(b, h[i], g);
+        store_vec<VEC>(y + i * (32 * VEC), b);
       }
     }
   }
-  if constexpr (VEC > 1) cp_async_wait<0>();     // rows past the end bring zeros, but they are still copies
+  if constexpr (VEC > 1) cp_async_wait<0>();      // rows past the end bring zeros, but they are still copies
 }
 
 // A persistent grid and a ring as in the forward pass.  A thread keeps its columns' sums of
@@ -153,29 +169,30 @@ __global__ void __launch_bounds__(MAX_TPR, min_blocks(VEC, NV)) norm_fwd_kernel(
 // as one partial sum per block, which norm_weight_grad_kernel adds in block order.  The second
 // pass over a row reads the ring again rather than hold the row in registers.
 template <typename T, int VEC, int NV, bool Q8>
-__global__ void __launch_bounds__(MAX_TPR, min_blocks(VEC, NV))
-    norm_bwd_kernel(const NormArgs a, int tpr, float* partial) {
-  constexpr int STG = ring_stages(VEC, NV, 3 * NV);
+__global__ void __launch_bounds__(MAX_TPR, 1) norm_bwd_kernel(const NormArgs a, int tpr, float* partial) {
+  constexpr int STG = ring_stages(VEC, 3 * NV);
   __shared__ float sums[2][64];
-  extern __shared__ __align__(16) uint8_t ring[]; // [stage][dy, dres, kept][vector][thread] of 16 bytes
-  const int t = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = blockDim.x / tpr;
-  const int pitch = int(blockDim.x) * 16;
+  extern __shared__ __align__(16) uint8_t ring[]; // operands dy, dres, kept rows
+  const Place<VEC, NV, 3, STG> at(tpr, ring);
   const int nb = (a.H + 31) >> 5;
-  const int64_t step = int64_t(gridDim.x) * groups;
-  const auto piece = [&](int st, int op, int i) {
-    return ring + ((st * 3 + op) * NV + i) * pitch + threadIdx.x * 16;
-  };
+  const int64_t step = int64_t(gridDim.x) * at.groups;
+  const bool has_res = a.dres != nullptr;
   const auto fetch = [&](int64_t row, int st) {
     if constexpr (VEC > 1) {
+      const bool live = row < a.rows;
+      const int64_t off = live ? row * a.ld_in + at.col0 : 0;
+      const T* dy = static_cast<const T*>(a.dy) + off;
+      const T* res = static_cast<const T*>(a.dres) + off;
+      const T* x = static_cast<const T*>(a.x) + off;
+      const uint8_t* codes = a.codes + (live ? row * a.H + at.col0 : 0);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int col = (i * tpr + t) * VEC;
-        const bool in = row < a.rows && col < a.H;
-        const int64_t at = in ? row * a.ld_in + col : 0;
-        ring_copy<16>(piece(st, 0, i), static_cast<const T*>(a.dy) + at, in);
-        if constexpr (Q8) ring_copy<VEC>(piece(st, 2, i), a.codes + (in ? row * a.H + col : 0), in);
-        else ring_copy<16>(piece(st, 2, i), static_cast<const T*>(a.x) + at, in);
-        if (a.dres != nullptr) ring_copy<16>(piece(st, 1, i), static_cast<const T*>(a.dres) + at, in);
+        const bool in = live && at.col(i) < a.H;
+        const int d = i * (32 * VEC);
+        ring_copy<16>(at.piece(st, 0, i), in ? dy + d : static_cast<const T*>(a.dy), in);
+        if constexpr (Q8) ring_copy<VEC>(at.piece(st, 2, i), in ? codes + d : a.codes, in);
+        else ring_copy<16>(at.piece(st, 2, i), in ? x + d : static_cast<const T*>(a.x), in);
+        if (has_res) ring_copy<16>(at.piece(st, 1, i), in ? res + d : static_cast<const T*>(a.dres), in);
       }
       cp_async_commit();
     }
@@ -191,25 +208,23 @@ __global__ void __launch_bounds__(MAX_TPR, min_blocks(VEC, NV))
     m.mu = !Q8 && live ? a.mean[row] : 0.f;
     m.rstd = live ? a.rstd[row] : 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int col = (i * tpr + t) * VEC;
-      m.c[i] = Q8 && live && col < a.H ? a.scales[row * nb + (col >> 5)] : 0;
-    }
+    for (int i = 0; i < NV; ++i) m.c[i] = Q8 && live && at.col(i) < a.H ? a.scales[row * nb + (at.col(i) >> 5)] : 0;
     return m;
   };
   float dg[NV][VEC], db[NV][VEC];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) dg[i][j] = db[i][j] = 0.f;
+  for (int i = 0; i < NV; ++i) {
+    v_fill<VEC>(dg[i], 0.f);
+    v_fill<VEC>(db[i], 0.f);
+  }
   const float inv_H = 1.f / float(a.H);
   int flip = 0, st = 0;
   pdl_wait();
-  int64_t row = int64_t(blockIdx.x) * groups + group;
+  int64_t row = int64_t(blockIdx.x) * at.groups + at.group;
 #pragma unroll
   for (int k = 0; k + 1 < STG; ++k) fetch(row + k * step, k);
   Small next = fetch_small(row);
-  for (int64_t row0 = int64_t(blockIdx.x) * groups; row0 < a.rows; row0 += step, row += step, flip ^= 1) {
+  for (int64_t row0 = int64_t(blockIdx.x) * at.groups; row0 < a.rows; row0 += step, row += step, flip ^= 1) {
     const bool live = row < a.rows;
     const Small m = next;
     if constexpr (VEC > 1) fetch(row + (STG - 1) * step, st == 0 ? STG - 1 : st - 1);
@@ -217,82 +232,94 @@ __global__ void __launch_bounds__(MAX_TPR, min_blocks(VEC, NV))
     if constexpr (VEC > 1) cp_async_wait<STG - 1>();
     // dy and the normalised values (0 past the row's end) of vector i
     const auto get = [&](int i, float* d, float* n) {
-      const int col = (i * tpr + t) * VEC;
-      const bool in = live && col < a.H;
+      const bool in = live && at.col(i) < a.H;
       if constexpr (VEC > 1) {
-        ring_get<T>(piece(st, 0, i), d);
+        ring_get<T>(at.piece(st, 0, i), d);
         if constexpr (Q8) {
           Act8<VEC> q;
-          q.q[0] = reinterpret_cast<const uint32_t*>(piece(st, 2, i))[0];
-          if constexpr (VEC == 8) q.q[1] = reinterpret_cast<const uint32_t*>(piece(st, 2, i))[1];
+          const uint32_t* p = reinterpret_cast<const uint32_t*>(at.piece(st, 2, i));
+          q.q[0] = p[0];
+          if constexpr (VEC == 8) q.q[1] = p[1];
           q.c = m.c[i];
           q.get(n);
         } else {
-          ring_get<T>(piece(st, 2, i), n);
+          ring_get<T>(at.piece(st, 2, i), n);
         }
       } else {
         Raw<T, 1> r, x;
         r.zero();
         x.zero();
-        if (in) r.load(static_cast<const T*>(a.dy) + row * a.ld_in + col);
+        if (in) r.load(static_cast<const T*>(a.dy) + row * a.ld_in + at.col0 + i * 32);
         r.get(d);
         if constexpr (Q8) {
           Act8<1> q;
-          q.q[0] = in ? a.codes[row * a.H + col] : 0;
+          q.q[0] = in ? a.codes[row * a.H + at.col0 + i * 32] : 0;
           q.c = m.c[i];
           q.get(n);
         } else {
-          if (in) x.load(static_cast<const T*>(a.x) + row * a.ld_in + col);
+          if (in) x.load(static_cast<const T*>(a.x) + row * a.ld_in + at.col0 + i * 32);
           x.get(n);
         }
       }
-      if constexpr (!Q8)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) n[j] = in ? (n[j] - m.mu) * m.rstd : 0.f;
+      if constexpr (!Q8) {
+        float minus[VEC], rs[VEC];
+        v_fill<VEC>(minus, -m.mu);
+        v_fill<VEC>(rs, m.rstd);
+        v_add<VEC>(n, minus);
+        v_mul<VEC>(n, rs);
+        if (!in) v_fill<VEC>(n, 0.f);
+      }
     };
-    float s[2] = {0.f, 0.f};
+    float s1[VEC], s2[VEC];
+    v_fill<VEC>(s1, 0.f);
+    v_fill<VEC>(s2, 0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = (i * tpr + t) * VEC;
       float n[VEC], d[VEC], g[VEC];
       get(i, d, n);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) g[j] = 0.f;
-      if (col < a.H) load_weight<VEC>(a.gamma, a.w_f32, col, g);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        dg[i][j] += d[j] * n[j];
-        db[i][j] += d[j];
-        const float w = d[j] * g[j];
-        s[0] += w;
-        s[1] += w * n[j];
-      }
+      v_fill<VEC>(g, 0.f);
+      if (at.col(i) < a.H) load_weight<VEC>(a.gamma, a.w_f32, at.col(i), g);
+      v_fma<VEC>(dg[i], d, n);
+      v_add<VEC>(db[i], d);
+      v_mul<VEC>(d, g);
+      v_add<VEC>(s1, d);
+      v_fma<VEC>(s2, d, n);
     }
-    row_sum<2>(s, tpr, sums[flip]);
-    const float m1 = s[0] * inv_H, m2 = s[1] * inv_H;
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      s[0] += s1[j];
+      s[1] += s2[j];
+    }
+    row_sum<2>(s, tpr, at.warp0, sums[flip]);
     if (live) {
-      T* dx = static_cast<T*>(a.dx) + row * a.ld_out;
+      // dx = rstd (d - m1 - n m2) + dres
+      float m1[VEC], m2[VEC], rs[VEC];
+      v_fill<VEC>(m1, -(s[0] * inv_H));
+      v_fill<VEC>(m2, -(s[1] * inv_H));
+      v_fill<VEC>(rs, m.rstd);
+      T* dx = static_cast<T*>(a.dx) + row * a.ld_out + at.col0;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int col = (i * tpr + t) * VEC;
-        if (col >= a.H) continue;
+        if (at.col(i) >= a.H) continue;
         float n[VEC], d[VEC], g[VEC], v[VEC];
         get(i, d, n);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) v[j] = 0.f;
-        if (a.dres != nullptr) {
+        v_fill<VEC>(v, 0.f);
+        if (has_res) {
           if constexpr (VEC > 1) {
-            ring_get<T>(piece(st, 1, i), v);
+            ring_get<T>(at.piece(st, 1, i), v);
           } else {
             Raw<T, 1> r;
-            r.load(static_cast<const T*>(a.dres) + row * a.ld_in + col);
+            r.load(static_cast<const T*>(a.dres) + row * a.ld_in + at.col0 + i * 32);
             r.get(v);
           }
         }
-        load_weight<VEC>(a.gamma, a.w_f32, col, g);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) v[j] += m.rstd * (d[j] * g[j] - m1 - n[j] * m2);
-        store_vec<VEC>(dx + col, v);
+        load_weight<VEC>(a.gamma, a.w_f32, at.col(i), g);
+        v_mul<VEC>(d, g);
+        v_add<VEC>(d, m1);
+        v_fma<VEC>(d, n, m2);
+        v_fma<VEC>(v, d, rs);
+        store_vec<VEC>(dx + i * (32 * VEC), v);
       }
     }
     if constexpr (VEC > 1) st = st + 1 == STG ? 0 : st + 1;
@@ -300,40 +327,36 @@ __global__ void __launch_bounds__(MAX_TPR, min_blocks(VEC, NV))
   if constexpr (VEC > 1) cp_async_wait<0>();
   // the block's row groups, added in order (the ring's memory is free by now)
   float* fold = reinterpret_cast<float*>(ring);   // [2][H]
-  for (int g = 1; g < groups; ++g) {
+  for (int g = 1; g < at.groups; ++g) {
     __syncthreads();
-    if (group == g) {
+    if (at.group == g) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const int col = (i * tpr + t) * VEC + j;
-          if (col < a.H) {
-            fold[col] = dg[i][j];
-            fold[a.H + col] = db[i][j];
+        for (int j = 0; j < VEC; ++j)
+          if (at.col(i) < a.H) {
+            fold[at.col(i) + j] = dg[i][j];
+            fold[a.H + at.col(i) + j] = db[i][j];
           }
-        }
     }
     __syncthreads();
-    if (group == 0) {
+    if (at.group == 0) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const int col = (i * tpr + t) * VEC + j;
-          if (col < a.H) {
-            dg[i][j] += fold[col];
-            db[i][j] += fold[a.H + col];
+        for (int j = 0; j < VEC; ++j)
+          if (at.col(i) < a.H) {
+            dg[i][j] += fold[at.col(i) + j];
+            db[i][j] += fold[a.H + at.col(i) + j];
           }
-        }
     }
   }
   pdl_launch_dependents();
-  if (group == 0) {
+  if (at.group == 0) {
     float* p = partial + int64_t(blockIdx.x) * 2 * a.H;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = (i * tpr + t) * VEC;
+      const int col = at.col(i);
       if (col >= a.H) continue;
 #pragma unroll
       for (int j = 0; j < VEC; j += VEC > 1 ? 4 : 1) {
@@ -359,7 +382,7 @@ __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float* __r
   pdl_wait();
   float s = 0.f;
   if (col < 2 * H) {
-#pragma unroll 8
+#pragma unroll 10
     for (int p = warp; p < parts; p += 32) s += partial[int64_t(p) * 2 * H + col];
   }
   acc[warp][lane] = s;
@@ -383,18 +406,19 @@ struct RowShape {
   int block;     // threads per block
 };
 
-// Threads and vectors per row: as few vectors a thread as 512 threads allow (wide) or at least 8
-// (single columns, where nothing else keeps loads in flight).
+// Threads and vectors per row.  Four vectors a thread: the sums over a row's threads and the
+// addresses cost as much as a vector or two of arithmetic, and the kernels are bound by the
+// instructions they issue as soon as a thread has only one (H = 1024: 297 instructions per vector
+// with one, measured).  Shorter rows take fewer vectors so that a warp is not left half empty,
+// longer ones more, up to 512 threads.
 RowShape row_shape(int H, int vec) {
-  RowShape s{vec, vec > 1 ? 1 : 8, 32, 256};
   const int n = (H + vec - 1) / vec;              // vectors of a row
-  while (s.nv * MAX_TPR < n) s.nv *= 2;
-  while (s.tpr * s.nv < n) s.tpr *= 2;
-  s.block = s.tpr > 256 ? s.tpr : 256;
-  return s;
+  int nv = vec > 1 ? 4 : 8;
+  while (vec > 1 && nv > 1 && 32 * (nv / 2) >= n) nv /= 2;
+  while (nv * MAX_TPR < n) nv *= 2;
+  const int tpr = (n + 32 * nv - 1) / (32 * nv) * 32;
+  return RowShape{vec, nv, tpr, tpr >= 256 ? tpr : 256 / tpr * tpr};
 }
-
-bool vec_ok(const NormArgs& a) { return a.H % 8 == 0 && a.ld_in % 8 == 0 && a.ld_out % 8 == 0; }
 
 // Sets a kernel's dynamic shared memory limit once per device, and says how many blocks of a
 // persistent grid the device holds at once (0: look-up failed).
@@ -417,21 +441,21 @@ template <typename T, int VEC, int NV>
 cudaError_t norm_fwd_shape(const NormArgs& a, const RowShape& s, cudaStream_t st) {
   static std::atomic<bool> set[kMaxDevices];
   const int64_t rpb = s.block / s.tpr, need = (a.rows + rpb - 1) / rpb;
-  const size_t smem = size_t(ring_stages(VEC, NV, 2 * NV)) * 2 * NV * 16 * s.block;
+  const size_t smem = size_t(ring_stages(VEC, 2 * NV)) * 2 * NV * 16 * s.block;
   const int64_t most = resident_blocks(norm_fwd_kernel<T, VEC, NV>, s.block, smem, set);
   if (most == 0) return cudaErrorInvalidConfiguration;
   return launch_pdl(norm_fwd_kernel<T, VEC, NV>, dim3(unsigned(need < most ? need : most)), dim3(unsigned(s.block)),
                     smem, st, a, s.tpr);
 }
 
-// Partial sums the backward may write: four blocks of 256 threads per SM.
-constexpr int kNormMaxParts = 608;
+// Partial sums the backward may write: two blocks of 256 threads per SM.
+constexpr int kNormMaxParts = 304;
 
 template <typename T, int VEC, int NV, bool Q8>
 cudaError_t norm_bwd_shape(const NormArgs& a, const RowShape& s, float* partial, int* parts, cudaStream_t st) {
   static std::atomic<bool> set[kMaxDevices];
   const int64_t rpb = s.block / s.tpr, need = (a.rows + rpb - 1) / rpb;
-  size_t smem = size_t(ring_stages(VEC, NV, 3 * NV)) * 3 * NV * 16 * s.block;
+  size_t smem = size_t(ring_stages(VEC, 3 * NV)) * 3 * NV * 16 * s.block;
   if (rpb > 1 && smem < size_t(2) * a.H * sizeof(float)) smem = size_t(2) * a.H * sizeof(float);  // H <= 1024 here
   int64_t grid = resident_blocks(norm_bwd_kernel<T, VEC, NV, Q8>, s.block, smem, set);
   if (grid == 0) return cudaErrorInvalidConfiguration;

@@ -1,11 +1,10 @@
 // Helpers of the row-wise kernels (layer norm, the gated activation, 8-bit checkpoints):
 // vectors of a row, sums over the threads of a row, and the 8-bit checkpoint's blocks.
 //
-// A row is shared by `tpr` threads (32 .. 1024, a power of two); a block holds blockDim/tpr
-// rows.  Vector i of thread t is columns (i * tpr + t) * VEC .. + VEC - 1, where VEC values are
-// 16 bytes (8 of bf16, 4 of f32) for rows whose length and pitch are multiples of 8, and VEC = 1
-// for all others.  Either way the 32 columns of a checkpoint block sit in one warp, in 32 / VEC
-// neighbouring lanes.
+// A row is shared by `tpr` threads (whole warps); a block holds blockDim/tpr rows.  A vector is
+// VEC columns: 16 bytes (8 values of bf16, 4 of f32) for rows whose length and pitch are
+// multiples of 8, one value for all others.  A warp's lanes hold neighbouring vectors, so the
+// 32 columns of a checkpoint block sit in 32 / VEC neighbouring lanes of one warp.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -98,6 +97,57 @@ __device__ __forceinline__ void load_weight(const void* w, bool f32, int64_t col
   }
 }
 
+// ---- arithmetic on vectors: two float32 operations per instruction where they are wide ---------
+// (each rounded to nearest, as the single ones).
+template <int VEC>
+__device__ __forceinline__ void v_add(float* a, const float* b) {            // a += b
+  if constexpr (VEC == 1) a[0] += b[0];
+  else
+#pragma unroll
+    for (int j = 0; j < VEC; j += 2) {
+      const float2 r = __fadd2_rn(make_float2(a[j], a[j + 1]), make_float2(b[j], b[j + 1]));
+      a[j] = r.x;
+      a[j + 1] = r.y;
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void v_mul(float* a, const float* b) {            // a *= b
+  if constexpr (VEC == 1) a[0] *= b[0];
+  else
+#pragma unroll
+    for (int j = 0; j < VEC; j += 2) {
+      const float2 r = __fmul2_rn(make_float2(a[j], a[j + 1]), make_float2(b[j], b[j + 1]));
+      a[j] = r.x;
+      a[j + 1] = r.y;
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void v_fma(float* c, const float* a, const float* b) {   // c = a * b + c
+  if constexpr (VEC == 1) c[0] = fmaf(a[0], b[0], c[0]);
+  else
+#pragma unroll
+    for (int j = 0; j < VEC; j += 2) {
+      const float2 r = __ffma2_rn(make_float2(a[j], a[j + 1]), make_float2(b[j], b[j + 1]), make_float2(c[j], c[j + 1]));
+      c[j] = r.x;
+      c[j + 1] = r.y;
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void v_fill(float* a, float x) {
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) a[j] = x;
+}
+// Largest |v| as float bits; a NaN or Inf among the values gives an exponent field of 255.
+template <int VEC>
+__device__ __forceinline__ uint32_t v_amax(const float* v) {
+  if constexpr (VEC == 1) return abs_bits(v[0]);
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j + 1 < VEC; j += 2)
+    asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(fabsf(v[j])), "f"(fabsf(v[j + 1])));
+  return abs_bits(m);
+}
+
 // ---- rows on their way: a ring of 16-byte pieces in shared memory ----------------------------
 // Every thread copies with cp.async the pieces that it alone will read, so the ring needs no
 // barrier: cp_async_wait<N> returns when all but the thread's last N groups have landed.
@@ -126,15 +176,16 @@ __device__ __forceinline__ void ring_get(const uint8_t* p, float* v) {
 // N sums at once over the tpr threads of each row.  All threads of the block call it (it
 // synchronises the block when a row spans warps); the order is fixed.  buf: 32 * N floats of
 // shared memory; two calls in a row use different ones, so one barrier per call is enough.
+// first: the first warp of this thread's row.
 template <int N>
-__device__ __forceinline__ void row_sum(float* v, int tpr, float* buf) {
+__device__ __forceinline__ void row_sum(float* v, int tpr, int first, float* buf) {
 #pragma unroll
   for (int n = 0; n < N; ++n)
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v[n] += __shfl_xor_sync(0xFFFFFFFFu, v[n], off);
   if (tpr > 32) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int per = tpr >> 5, first = warp & ~(per - 1);
+    const int per = tpr >> 5;
     if (lane == 0)
 #pragma unroll
       for (int n = 0; n < N; ++n) buf[warp * N + n] = v[n];
@@ -161,9 +212,7 @@ __device__ __forceinline__ void row_sum(float* v, int tpr, float* buf) {
 template <int VEC>
 __device__ __forceinline__ void store_act8(const float* v, bool in, uint8_t* codes, uint8_t* scales, int64_t row,
                                            int64_t ld_codes, int64_t col0, int col, int64_t ld_scales, int blk0) {
-  uint32_t amax = 0;
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) amax = max(amax, abs_bits(v[j]));
+  uint32_t amax = v_amax<VEC>(v);
   if constexpr (VEC == 1) {
     amax = __reduce_max_sync(0xFFFFFFFFu, amax);
   } else {
