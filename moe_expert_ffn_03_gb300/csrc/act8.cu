@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(ROW_BLOCK) swiglu_bwd_kernel(const SwigluArgs 
     }
   }
   if (a.dprob == nullptr) return;
-  row_sum<1>(dp, tpr, int(threadIdx.x / tpr) * (tpr >> 5), sums);
+  row_sum<1>(dp, tpr, int(threadIdx.x / tpr), sums);
   if (live && t == 0) a.dprob[row] = dp[0];
 }
 

@@ -34,13 +34,12 @@ constexpr int ring_stages(int vec, int pieces) {
 // [stage][operand][vector][lane] of 16 bytes so that they too are constant distances apart.
 template <int VEC, int NV, int OPS, int STG>
 struct Place {
-  int group, groups, t, warp0, col0;
+  int group, groups, t, col0;
   uint8_t* slot;
   __device__ __forceinline__ Place(int tpr, uint8_t* ring) {
     group = threadIdx.x / tpr;
     groups = blockDim.x / tpr;
     t = threadIdx.x - group * tpr;
-    warp0 = group * (tpr >> 5);
     col0 = (t >> 5) * (32 * NV * VEC) + (t & 31) * VEC;
     slot = ring + (threadIdx.x >> 5) * (STG * OPS * NV * 512) + (threadIdx.x & 31) * 16;
   }
@@ -48,7 +47,25 @@ struct Place {
   __device__ __forceinline__ uint8_t* piece(int st, int op, int i) const {
     return slot + st * (OPS * NV * 512) + (op * NV + i) * 512;
   }
+  // zeros in every slot: vectors past a row's end are never copied and read as zeros
+  __device__ __forceinline__ void clear() const {
+#pragma unroll
+    for (int k = 0; k < STG * OPS * NV; ++k) *reinterpret_cast<uint4*>(slot + k * 512) = make_uint4(0, 0, 0, 0);
+  }
 };
+
+// The mean of a row from its sum: s / H to one rounding (the remainder of s * (1 / H) is added
+// back), so that a constant row whose sum is exact has an exact mean.
+__device__ __forceinline__ float mean_of(float s, float H, float inv_H) {
+  const float q = s * inv_H;
+  return fmaf(fmaf(-q, H, s), inv_H, q);
+}
+// 1 / sqrt(v), with a Newton step after the approximate instruction (v = 0 gives Inf).
+__device__ __forceinline__ float inv_sqrt(float v) {
+  const float r = rsqrtf(v);
+  const float n = r * fmaf(-0.5f * v * r, r, 1.5f);
+  return v > 0.f ? n : r;
+}
 
 // A persistent grid: block b takes the row groups b, b + grid, ...  The next groups' x (and
 // residual) are on their way to shared memory while the current one is summed, so the two
@@ -64,25 +81,27 @@ __global__ void __launch_bounds__(MAX_TPR, 1) norm_fwd_kernel(const NormArgs a, 
   const bool has_res = a.residual != nullptr;
   const auto fetch = [&](int64_t row, int st) {
     if constexpr (VEC > 1) {
-      const bool live = row < a.rows;
-      const T* x = static_cast<const T*>(a.x) + (live ? row * a.ld_in + at.col0 : 0);
-      const T* res = static_cast<const T*>(a.residual) + (live ? row * a.ld_in + at.col0 : 0);
+      if (row < a.rows) {
+        const T* x = static_cast<const T*>(a.x) + row * a.ld_in + at.col0;
+        const T* res = static_cast<const T*>(a.residual) + row * a.ld_in + at.col0;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const bool in = live && at.col(i) < a.H;
-        ring_copy<16>(at.piece(st, 0, i), in ? x + i * (32 * VEC) : static_cast<const T*>(a.x), in);
-        if (has_res) ring_copy<16>(at.piece(st, 1, i), in ? res + i * (32 * VEC) : static_cast<const T*>(a.x), in);
+        for (int i = 0; i < NV; ++i)
+          if (at.col(i) < a.H) {
+            ring_copy<16>(at.piece(st, 0, i), x + i * (32 * VEC));
+            if (has_res) ring_copy<16>(at.piece(st, 1, i), res + i * (32 * VEC));
+          }
       }
       cp_async_commit();
     }
   };
+  if constexpr (VEC > 1) at.clear();
   pdl_wait();
   int64_t row = int64_t(blockIdx.x) * at.groups + at.group;
 #pragma unroll
   for (int k = 0; k + 1 < STG; ++k) fetch(row + k * step, k);
+  const Weight<VEC, NV> gamma(a.gamma, a.w_f32, at.col0, a.H), beta(a.beta, a.w_f32, at.col0, a.H);
   int st = 0;
-  for (int64_t row0 = int64_t(blockIdx.x) * at.groups; row0 < a.rows; row0 += step, row += step) {
-    const bool live = row < a.rows;
+  for (; row < a.rows; row += step) {             // the rows' groups go on independently of one another
     if constexpr (VEC > 1) {
       fetch(row + (STG - 1) * step, st == 0 ? STG - 1 : st - 1);
       cp_async_wait<STG - 1>();
@@ -102,7 +121,7 @@ __global__ void __launch_bounds__(MAX_TPR, 1) norm_fwd_kernel(const NormArgs a, 
         Raw<T, 1> x, r;
         x.zero();
         r.zero();
-        if (live && at.col(i) < a.H) {
+        if (at.col(i) < a.H) {
           x.load(static_cast<const T*>(a.x) + row * a.ld_in + at.col0 + i * 32);
           if (has_res) r.load(static_cast<const T*>(a.residual) + row * a.ld_in + at.col0 + i * 32);
         }
@@ -116,29 +135,28 @@ __global__ void __launch_bounds__(MAX_TPR, 1) norm_fwd_kernel(const NormArgs a, 
     float s[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < VEC; ++j) s[0] += sum[j];
-    row_sum<1>(s, tpr, at.warp0, sums[0]);
-    const float mu = __fdiv_rn(s[0], float(a.H));   // exact for a constant row whose sum is
-    if (a.h != nullptr && live) {
+    row_sum<1>(s, tpr, at.group, sums[0]);
+    const float mu = mean_of(s[0], float(a.H), inv_H);
+    if (a.h != nullptr) {
       T* ho = static_cast<T*>(a.h) + row * a.ld_out + at.col0;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (at.col(i) < a.H) store_vec<VEC>(ho + i * (32 * VEC), h[i]);
     }
     float minus[VEC], sq[VEC];
-    v_fill<VEC>(minus, -mu);
     v_fill<VEC>(sq, 0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+      v_fill<VEC>(minus, at.col(i) < a.H ? -mu : 0.f);
       v_add<VEC>(h[i], minus);
-      if (at.col(i) >= a.H) v_fill<VEC>(h[i], 0.f);
       v_fma<VEC>(sq, h[i], h[i]);
     }
     s[0] = 0.f;
 #pragma unroll
     for (int j = 0; j < VEC; ++j) s[0] += sq[j];
-    row_sum<1>(s, tpr, at.warp0, sums[1]);
-    const float rstd = 1.f / sqrtf(s[0] * inv_H + a.eps);
-    if (live && at.t == 0) {
+    row_sum<1>(s, tpr, at.group, sums[1]);
+    const float rstd = inv_sqrt(s[0] * inv_H + a.eps);
+    if (at.t == 0) {
       if (a.mean != nullptr) a.mean[row] = mu;
       if (a.rstd != nullptr) a.rstd[row] = rstd;
     }
@@ -147,30 +165,30 @@ __global__ void __launch_bounds__(MAX_TPR, 1) norm_fwd_kernel(const NormArgs a, 
     v_fill<VEC>(rs, rstd);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const bool in = live && at.col(i) < a.H;
+      const bool in = at.col(i) < a.H;
       v_mul<VEC>(h[i], rs);
       if (a.codes != nullptr)
         store_act8<VEC>(h[i], in, a.codes, a.scales, row, a.H, 0, at.col(i), (a.H + 31) >> 5, 0);
       if (in) {
         float g[VEC], b[VEC];
-        load_weight<VEC>(a.gamma, a.w_f32, at.col(i), g);
-        v_fill<VEC>(b, 0.f);
-        if (a.beta != nullptr) load_weight<VEC>(a.beta, a.w_f32, at.col(i), b);
+        gamma.get(i, g);
+        beta.get(i, b);
         v_fma<VEC>(b, h[i], g);
         store_vec<VEC>(y + i * (32 * VEC), b);
       }
     }
   }
-  if constexpr (VEC > 1) cp_async_wait<0>();      // rows past the end bring zeros, but they are still copies
 }
 
 // A persistent grid and a ring as in the forward pass.  A thread keeps its columns' sums of
 // dgamma and dbeta in registers; at the end the block's groups are added in order and written
 // as one partial sum per block, which norm_weight_grad_kernel adds in block order.  The second
-// pass over a row reads the ring again rather than hold the row in registers.
+// pass over a row finds it in registers where a thread has up to 16 columns, and reads the ring
+// (single columns: memory) again where it has more.
 template <typename T, int VEC, int NV, bool Q8>
 __global__ void __launch_bounds__(MAX_TPR, 1) norm_bwd_kernel(const NormArgs a, int tpr, float* partial) {
   constexpr int STG = ring_stages(VEC, 3 * NV);
+  constexpr bool HOLD = VEC * NV <= 16;
   __shared__ float sums[2][64];
   extern __shared__ __align__(16) uint8_t ring[]; // operands dy, dres, kept rows
   const Place<VEC, NV, 3, STG> at(tpr, ring);
@@ -179,20 +197,21 @@ __global__ void __launch_bounds__(MAX_TPR, 1) norm_bwd_kernel(const NormArgs a, 
   const bool has_res = a.dres != nullptr;
   const auto fetch = [&](int64_t row, int st) {
     if constexpr (VEC > 1) {
-      const bool live = row < a.rows;
-      const int64_t off = live ? row * a.ld_in + at.col0 : 0;
-      const T* dy = static_cast<const T*>(a.dy) + off;
-      const T* res = static_cast<const T*>(a.dres) + off;
-      const T* x = static_cast<const T*>(a.x) + off;
-      const uint8_t* codes = a.codes + (live ? row * a.H + at.col0 : 0);
+      if (row < a.rows) {
+        const int64_t off = row * a.ld_in + at.col0;
+        const T* dy = static_cast<const T*>(a.dy) + off;
+        const T* res = static_cast<const T*>(a.dres) + off;
+        const T* x = static_cast<const T*>(a.x) + off;
+        const uint8_t* codes = a.codes + row * a.H + at.col0;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const bool in = live && at.col(i) < a.H;
-        const int d = i * (32 * VEC);
-        ring_copy<16>(at.piece(st, 0, i), in ? dy + d : static_cast<const T*>(a.dy), in);
-        if constexpr (Q8) ring_copy<VEC>(at.piece(st, 2, i), in ? codes + d : a.codes, in);
-        else ring_copy<16>(at.piece(st, 2, i), in ? x + d : static_cast<const T*>(a.x), in);
-        if (has_res) ring_copy<16>(at.piece(st, 1, i), in ? res + d : static_cast<const T*>(a.dres), in);
+        for (int i = 0; i < NV; ++i)
+          if (at.col(i) < a.H) {
+            const int d = i * (32 * VEC);
+            ring_copy<16>(at.piece(st, 0, i), dy + d);
+            if constexpr (Q8) ring_copy<VEC>(at.piece(st, 2, i), codes + d);
+            else ring_copy<16>(at.piece(st, 2, i), x + d);
+            if (has_res) ring_copy<16>(at.piece(st, 1, i), res + d);
+          }
       }
       cp_async_commit();
     }
@@ -219,20 +238,21 @@ __global__ void __launch_bounds__(MAX_TPR, 1) norm_bwd_kernel(const NormArgs a, 
   }
   const float inv_H = 1.f / float(a.H);
   int flip = 0, st = 0;
+  if constexpr (VEC > 1) at.clear();
   pdl_wait();
   int64_t row = int64_t(blockIdx.x) * at.groups + at.group;
 #pragma unroll
   for (int k = 0; k + 1 < STG; ++k) fetch(row + k * step, k);
+  const Weight<VEC, NV> gamma(a.gamma, a.w_f32, at.col0, a.H);
   Small next = fetch_small(row);
-  for (int64_t row0 = int64_t(blockIdx.x) * at.groups; row0 < a.rows; row0 += step, row += step, flip ^= 1) {
-    const bool live = row < a.rows;
+  for (; row < a.rows; row += step, flip ^= 1) {
     const Small m = next;
     if constexpr (VEC > 1) fetch(row + (STG - 1) * step, st == 0 ? STG - 1 : st - 1);
     next = fetch_small(row + step);
     if constexpr (VEC > 1) cp_async_wait<STG - 1>();
     // dy and the normalised values (0 past the row's end) of vector i
     const auto get = [&](int i, float* d, float* n) {
-      const bool in = live && at.col(i) < a.H;
+      const bool in = at.col(i) < a.H;
       if constexpr (VEC > 1) {
         ring_get<T>(at.piece(st, 0, i), d);
         if constexpr (Q8) {
@@ -263,22 +283,22 @@ __global__ void __launch_bounds__(MAX_TPR, 1) norm_bwd_kernel(const NormArgs a, 
       }
       if constexpr (!Q8) {
         float minus[VEC], rs[VEC];
-        v_fill<VEC>(minus, -m.mu);
+        v_fill<VEC>(minus, in ? -m.mu : 0.f);
         v_fill<VEC>(rs, m.rstd);
         v_add<VEC>(n, minus);
         v_mul<VEC>(n, rs);
-        if (!in) v_fill<VEC>(n, 0.f);
       }
     };
     float s1[VEC], s2[VEC];
+    float kn[HOLD ? NV : 1][VEC], kd[HOLD ? NV : 1][VEC];         // n and d * gamma, for the second pass
     v_fill<VEC>(s1, 0.f);
     v_fill<VEC>(s2, 0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float n[VEC], d[VEC], g[VEC];
+      float (&n)[VEC] = kn[HOLD ? i : 0], (&d)[VEC] = kd[HOLD ? i : 0], g[VEC];
       get(i, d, n);
       v_fill<VEC>(g, 0.f);
-      if (at.col(i) < a.H) load_weight<VEC>(a.gamma, a.w_f32, at.col(i), g);
+      if (at.col(i) < a.H) gamma.get(i, g);
       v_fma<VEC>(dg[i], d, n);
       v_add<VEC>(db[i], d);
       v_mul<VEC>(d, g);
@@ -291,84 +311,66 @@ __global__ void __launch_bounds__(MAX_TPR, 1) norm_bwd_kernel(const NormArgs a, 
       s[0] += s1[j];
       s[1] += s2[j];
     }
-    row_sum<2>(s, tpr, at.warp0, sums[flip]);
-    if (live) {
-      // dx = rstd (d - m1 - n m2) + dres
-      float m1[VEC], m2[VEC], rs[VEC];
-      v_fill<VEC>(m1, -(s[0] * inv_H));
-      v_fill<VEC>(m2, -(s[1] * inv_H));
-      v_fill<VEC>(rs, m.rstd);
-      T* dx = static_cast<T*>(a.dx) + row * a.ld_out + at.col0;
+    row_sum<2>(s, tpr, at.group, sums[flip]);
+    // dx = rstd (d - m1 - n m2) + dres
+    float m1[VEC], m2[VEC], rs[VEC];
+    v_fill<VEC>(m1, -(s[0] * inv_H));
+    v_fill<VEC>(m2, -(s[1] * inv_H));
+    v_fill<VEC>(rs, m.rstd);
+    T* dx = static_cast<T*>(a.dx) + row * a.ld_out + at.col0;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        if (at.col(i) >= a.H) continue;
-        float n[VEC], d[VEC], g[VEC], v[VEC];
+    for (int i = 0; i < NV; ++i) {
+      if (at.col(i) >= a.H) continue;
+      float (&n)[VEC] = kn[HOLD ? i : 0], (&d)[VEC] = kd[HOLD ? i : 0], v[VEC];
+      if constexpr (!HOLD) {
+        float g[VEC];
         get(i, d, n);
-        v_fill<VEC>(v, 0.f);
-        if (has_res) {
-          if constexpr (VEC > 1) {
-            ring_get<T>(at.piece(st, 1, i), v);
-          } else {
-            Raw<T, 1> r;
-            r.load(static_cast<const T*>(a.dres) + row * a.ld_in + at.col0 + i * 32);
-            r.get(v);
-          }
-        }
-        load_weight<VEC>(a.gamma, a.w_f32, at.col(i), g);
+        gamma.get(i, g);
         v_mul<VEC>(d, g);
-        v_add<VEC>(d, m1);
-        v_fma<VEC>(d, n, m2);
-        v_fma<VEC>(v, d, rs);
-        store_vec<VEC>(dx + i * (32 * VEC), v);
       }
+      v_fill<VEC>(v, 0.f);
+      if (has_res) {
+        if constexpr (VEC > 1) {
+          ring_get<T>(at.piece(st, 1, i), v);
+        } else {
+          Raw<T, 1> r;
+          r.load(static_cast<const T*>(a.dres) + row * a.ld_in + at.col0 + i * 32);
+          r.get(v);
+        }
+      }
+      v_add<VEC>(d, m1);
+      v_fma<VEC>(d, n, m2);
+      v_fma<VEC>(v, d, rs);
+      store_vec<VEC>(dx + i * (32 * VEC), v);
     }
     if constexpr (VEC > 1) st = st + 1 == STG ? 0 : st + 1;
   }
-  if constexpr (VEC > 1) cp_async_wait<0>();
-  // the block's row groups, added in order (the ring's memory is free by now)
-  float* fold = reinterpret_cast<float*>(ring);   // [2][H]
-  for (int g = 1; g < at.groups; ++g) {
-    __syncthreads();
-    if (at.group == g) {
+  // The block's row groups, added in order: every group's sums to shared memory (the ring is
+  // free by now), then all threads add columns.
+  float* fold = reinterpret_cast<float*>(ring);   // [group][2][H]
+  __syncthreads();
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
+    const int col = at.col(i);
+    if (col >= a.H) continue;
+    float* f = fold + size_t(at.group) * 2 * a.H + col;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j)
-          if (at.col(i) < a.H) {
-            fold[at.col(i) + j] = dg[i][j];
-            fold[a.H + at.col(i) + j] = db[i][j];
-          }
-    }
-    __syncthreads();
-    if (at.group == 0) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j)
-          if (at.col(i) < a.H) {
-            dg[i][j] += fold[at.col(i) + j];
-            db[i][j] += fold[a.H + at.col(i) + j];
-          }
-    }
-  }
-  pdl_launch_dependents();
-  if (at.group == 0) {
-    float* p = partial + int64_t(blockIdx.x) * 2 * a.H;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int col = at.col(i);
-      if (col >= a.H) continue;
-#pragma unroll
-      for (int j = 0; j < VEC; j += VEC > 1 ? 4 : 1) {
-        if constexpr (VEC > 1) {
-          *reinterpret_cast<float4*>(p + col + j) = make_float4(dg[i][j], dg[i][j + 1], dg[i][j + 2], dg[i][j + 3]);
-          *reinterpret_cast<float4*>(p + a.H + col + j) = make_float4(db[i][j], db[i][j + 1], db[i][j + 2], db[i][j + 3]);
-        } else {
-          p[col] = dg[i][0];
-          p[a.H + col] = db[i][0];
-        }
+    for (int j = 0; j < VEC; j += VEC > 1 ? 4 : 1) {
+      if constexpr (VEC > 1) {
+        *reinterpret_cast<float4*>(f + j) = make_float4(dg[i][j], dg[i][j + 1], dg[i][j + 2], dg[i][j + 3]);
+        *reinterpret_cast<float4*>(f + a.H + j) = make_float4(db[i][j], db[i][j + 1], db[i][j + 2], db[i][j + 3]);
+      } else {
+        f[0] = dg[i][0];
+        f[a.H] = db[i][0];
       }
     }
+  }
+  __syncthreads();
+  pdl_launch_dependents();
+  for (int c = threadIdx.x; c < 2 * a.H; c += blockDim.x) {
+    float sum = fold[c];
+    for (int g = 1; g < at.groups; ++g) sum += fold[size_t(g) * 2 * a.H + c];
+    partial[int64_t(blockIdx.x) * 2 * a.H + c] = sum;
   }
 }
 
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float* __r
   pdl_wait();
   float s = 0.f;
   if (col < 2 * H) {
-#pragma unroll 10
+#pragma unroll 5
     for (int p = warp; p < parts; p += 32) s += partial[int64_t(p) * 2 * H + col];
   }
   acc[warp][lane] = s;
@@ -411,13 +413,13 @@ struct RowShape {
 // instructions they issue as soon as a thread has only one (H = 1024: 297 instructions per vector
 // with one, measured).  Shorter rows take fewer vectors so that a warp is not left half empty,
 // longer ones more, up to 512 threads.
-RowShape row_shape(int H, int vec) {
+RowShape row_shape(int H, int vec, int wide_nv) {
   const int n = (H + vec - 1) / vec;              // vectors of a row
-  int nv = vec > 1 ? 4 : 8;
+  int nv = vec > 1 ? wide_nv : 8;
   while (vec > 1 && nv > 1 && 32 * (nv / 2) >= n) nv /= 2;
   while (nv * MAX_TPR < n) nv *= 2;
   const int tpr = (n + 32 * nv - 1) / (32 * nv) * 32;
-  return RowShape{vec, nv, tpr, tpr >= 256 ? tpr : 256 / tpr * tpr};
+  return RowShape{vec, nv, tpr, MAX_TPR / tpr * tpr};
 }
 
 // Sets a kernel's dynamic shared memory limit once per device, and says how many blocks of a
@@ -448,15 +450,16 @@ cudaError_t norm_fwd_shape(const NormArgs& a, const RowShape& s, cudaStream_t st
                     smem, st, a, s.tpr);
 }
 
-// Partial sums the backward may write: two blocks of 256 threads per SM.
-constexpr int kNormMaxParts = 304;
+// Partial sums the backward may write: one block per SM.
+constexpr int kNormMaxParts = 152;
 
 template <typename T, int VEC, int NV, bool Q8>
 cudaError_t norm_bwd_shape(const NormArgs& a, const RowShape& s, float* partial, int* parts, cudaStream_t st) {
   static std::atomic<bool> set[kMaxDevices];
   const int64_t rpb = s.block / s.tpr, need = (a.rows + rpb - 1) / rpb;
-  size_t smem = size_t(ring_stages(VEC, 3 * NV)) * 3 * NV * 16 * s.block;
-  if (rpb > 1 && smem < size_t(2) * a.H * sizeof(float)) smem = size_t(2) * a.H * sizeof(float);  // H <= 1024 here
+  const size_t ring = size_t(ring_stages(VEC, 3 * NV)) * 3 * NV * 16 * s.block;
+  const size_t fold = size_t(rpb) * 2 * a.H * sizeof(float);      // H <= tpr * VEC * NV: at most 128 KB
+  const size_t smem = ring > fold ? ring : fold;
   int64_t grid = resident_blocks(norm_bwd_kernel<T, VEC, NV, Q8>, s.block, smem, set);
   if (grid == 0) return cudaErrorInvalidConfiguration;
   grid = grid < kNormMaxParts ? grid : kNormMaxParts;
@@ -483,19 +486,19 @@ cudaError_t with_shape(const RowShape& s, F f) {
 }
 
 template <typename T>
-RowShape shape_of(const NormArgs& a) {
-  return row_shape(a.H, a.H % 8 == 0 && a.ld_in % 8 == 0 && a.ld_out % 8 == 0 ? kWide<T> : 1);
+RowShape shape_of(const NormArgs& a, int wide_nv) {
+  return row_shape(a.H, a.H % 8 == 0 && a.ld_in % 8 == 0 && a.ld_out % 8 == 0 ? kWide<T> : 1, wide_nv);
 }
 
 template <typename T>
 cudaError_t norm_fwd_t(const NormArgs& a, cudaStream_t st) {
-  const RowShape s = shape_of<T>(a);
+  const RowShape s = shape_of<T>(a, 4);
   return with_shape<T>(s, [&](auto vec, auto nv) { return norm_fwd_shape<T, vec.value, nv.value>(a, s, st); });
 }
 
 template <typename T, bool Q8>
 cudaError_t norm_bwd_t(const NormArgs& a, float* partial, int* parts, cudaStream_t st) {
-  const RowShape s = shape_of<T>(a);
+  const RowShape s = shape_of<T>(a, sizeof(T) == 2 ? 2 : 4);
   return with_shape<T>(s, [&](auto vec, auto nv) { return norm_bwd_shape<T, vec.value, nv.value, Q8>(a, s, partial, parts, st); });
 }
 

@@ -25,6 +25,7 @@ template <>
 struct Raw<__nv_bfloat16, 8> {
   uint4 q;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { q = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void load_weight(const __nv_bfloat16* p) { q = __ldg(reinterpret_cast<const uint4*>(p)); }
   __device__ __forceinline__ void zero() { q = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void get(float* v) const {
     v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
@@ -39,9 +40,19 @@ struct Raw<float, 4> {
   __device__ __forceinline__ void get(float* v) const { v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w; }
 };
 template <>
+struct Raw<__nv_bfloat16, 4> {                    // weights beside f32 activations
+  uint2 q;
+  __device__ __forceinline__ void load_weight(const __nv_bfloat16* p) { q = __ldg(reinterpret_cast<const uint2*>(p)); }
+  __device__ __forceinline__ void zero() { q = make_uint2(0, 0); }
+  __device__ __forceinline__ void get(float* v) const {
+    v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
+  }
+};
+template <>
 struct Raw<__nv_bfloat16, 1> {
   __nv_bfloat16 q;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { q = *p; }
+  __device__ __forceinline__ void load_weight(const __nv_bfloat16* p) { q = *p; }
   __device__ __forceinline__ void zero() { q = __float2bfloat16_rn(0.f); }
   __device__ __forceinline__ void get(float* v) const { v[0] = __bfloat162float(q); }
 };
@@ -75,8 +86,7 @@ __device__ __forceinline__ void store_vec(float* p, const float* v) {
   }
 }
 
-// VEC values of a weight vector (bf16, or f32 when f32 is set) from column col; these are read
-// once per row by every block and stay in L1.
+// VEC values of a weight vector (bf16, or f32 when f32 is set) from column col.
 template <int VEC>
 __device__ __forceinline__ void load_weight(const void* w, bool f32, int64_t col, float* v) {
   if constexpr (VEC == 1) {
@@ -96,6 +106,32 @@ __device__ __forceinline__ void load_weight(const void* w, bool f32, int64_t col
     }
   }
 }
+
+// A thread's NV vectors of a weight for a whole kernel: bf16 weights stay in registers as they lie
+// in memory, f32 ones (twice the registers) are read again for every row, from L1.
+template <int VEC, int NV>
+struct Weight {
+  const void* w;
+  bool f32;
+  int col0;
+  Raw<__nv_bfloat16, VEC> r[NV];
+  __device__ __forceinline__ Weight(const void* w_, bool f32_, int col0_, int H) : w(w_), f32(f32_), col0(col0_) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      r[i].zero();
+      if (w != nullptr && !f32 && col0 + i * (32 * VEC) < H)
+        r[i].load_weight(static_cast<const __nv_bfloat16*>(w) + col0 + i * (32 * VEC));
+    }
+  }
+  // vector i, inside the row; zeros without a weight
+  __device__ __forceinline__ void get(int i, float* v) const {
+    if (f32 && w != nullptr) {
+      load_weight<VEC>(w, true, col0 + i * (32 * VEC), v);
+      return;
+    }
+    r[i].get(v);
+  }
+};
 
 // ---- arithmetic on vectors: two float32 operations per instruction where they are wide ---------
 // (each rounded to nearest, as the single ones).
@@ -152,13 +188,11 @@ __device__ __forceinline__ uint32_t v_amax(const float* v) {
 // Every thread copies with cp.async the pieces that it alone will read, so the ring needs no
 // barrier: cp_async_wait<N> returns when all but the thread's last N groups have landed.
 template <int BYTES>                              // 4, 8 or 16
-__device__ __forceinline__ void ring_copy(uint8_t* smem, const void* gmem, bool valid) {
+__device__ __forceinline__ void ring_copy(uint8_t* smem, const void* gmem) {
   if constexpr (BYTES == 16)
-    cp_async16(smem, gmem, valid);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(smem_u32(smem)), "l"(gmem), "n"(BYTES),
-                 "r"(valid ? BYTES : 0)
-                 : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(smem_u32(smem)), "l"(gmem), "n"(BYTES) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int N>
@@ -173,30 +207,30 @@ __device__ __forceinline__ void ring_get(const uint8_t* p, float* v) {
 }
 
 // ---- sums over the threads of a row -------------------------------------------------------
-// N sums at once over the tpr threads of each row.  All threads of the block call it (it
-// synchronises the block when a row spans warps); the order is fixed.  buf: 32 * N floats of
-// shared memory; two calls in a row use different ones, so one barrier per call is enough.
-// first: the first warp of this thread's row.
+// N sums at once over the tpr threads of a row, in a fixed order; the row's threads call it
+// together.  group: the row's place in its block; rows of more than one warp (at most 8 a block of
+// 512 threads) meet at the barrier of that number plus one, 0 being the whole block's.  buf: 32 * N floats of shared memory; two calls in a
+// row use different ones, so one barrier per call is enough.
 template <int N>
-__device__ __forceinline__ void row_sum(float* v, int tpr, int first, float* buf) {
+__device__ __forceinline__ void row_sum(float* v, int tpr, int group, float* buf) {
 #pragma unroll
   for (int n = 0; n < N; ++n)
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v[n] += __shfl_xor_sync(0xFFFFFFFFu, v[n], off);
   if (tpr > 32) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int per = tpr >> 5;
+    const int per = tpr >> 5, first = group * per;
     if (lane == 0)
 #pragma unroll
       for (int n = 0; n < N; ++n) buf[warp * N + n] = v[n];
-    __syncthreads();
-    // every warp adds the row's partial sums in the same tree
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
+    // every warp adds the row's partial sums (16 at most) in the same tree
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       float s = lane < per ? buf[(first + lane) * N + n] : 0.f;
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
-      v[n] = s;
+      for (int off = 8; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+      v[n] = __shfl_sync(0xFFFFFFFFu, s, 0);
     }
   }
 }
