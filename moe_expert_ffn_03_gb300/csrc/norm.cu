@@ -118,16 +118,16 @@ __global__ void __launch_bounds__(MAX_TPR, 1) norm_fwd_kernel(const NormArgs a, 
           v_add<VEC>(h[i], v);
         }
       } else {
+        // unconditional loads (column 0 past the row's end), so that a row's are all in flight at once
+        const bool in = at.col(i) < a.H;
+        const int64_t off = row * a.ld_in + (in ? at.col(i) : 0);
         Raw<T, 1> x, r;
-        x.zero();
+        x.load(static_cast<const T*>(a.x) + off);
         r.zero();
-        if (at.col(i) < a.H) {
-          x.load(static_cast<const T*>(a.x) + row * a.ld_in + at.col0 + i * 32);
-          if (has_res) r.load(static_cast<const T*>(a.residual) + row * a.ld_in + at.col0 + i * 32);
-        }
+        if (has_res) r.load(static_cast<const T*>(a.residual) + off);
         x.get(h[i]);
         r.get(v);
-        h[i][0] += v[0];
+        h[i][0] = in ? h[i][0] + v[0] : 0.f;
       }
       v_add<VEC>(sum, h[i]);
     }
@@ -266,20 +266,22 @@ __global__ void __launch_bounds__(MAX_TPR, 1) norm_bwd_kernel(const NormArgs a, 
           ring_get<T>(at.piece(st, 2, i), n);
         }
       } else {
-        Raw<T, 1> r, x;
-        r.zero();
-        x.zero();
-        if (in) r.load(static_cast<const T*>(a.dy) + row * a.ld_in + at.col0 + i * 32);
+        // unconditional loads, as in the forward pass
+        const int col = in ? at.col(i) : 0;
+        Raw<T, 1> r;
+        r.load(static_cast<const T*>(a.dy) + row * a.ld_in + col);
         r.get(d);
         if constexpr (Q8) {
           Act8<1> q;
-          q.q[0] = in ? a.codes[row * a.H + at.col0 + i * 32] : 0;
+          q.q[0] = a.codes[row * a.H + col];
           q.c = m.c[i];
           q.get(n);
         } else {
-          if (in) x.load(static_cast<const T*>(a.x) + row * a.ld_in + at.col0 + i * 32);
-          x.get(n);
+          r.load(static_cast<const T*>(a.x) + row * a.ld_in + col);
+          r.get(n);
         }
+        d[0] = in ? d[0] : 0.f;
+        n[0] = in ? n[0] : 0.f;
       }
       if constexpr (!Q8) {
         float minus[VEC], rs[VEC];
