@@ -17,6 +17,11 @@
 // along memory, MN-major tiles where it does not, so nothing is transposed or padded first.
 // In every mode m is the contiguous index of the output.
 //
+// A stage of an operand is 128 x 128 values: K-major as two 64-deep steps of 128 rows, MN-major as
+// two 64-wide blocks of 128 deep, each row 128 swizzled bytes.  Where the row lengths are
+// multiples of 64 (ATOMS) one TMA box fetches it whole: what TMA delivers to an SM grows with the
+// bytes of a copy.  Other lengths take two boxes, whose ends TMA fills with zeros.
+//
 // Persistent CTA pairs (clusters of two, one CTA per SM): a pair computes a 256 x 256 tile
 // with tcgen05.mma.cta_group::2; each CTA stages its 128 m and its half of the n columns.
 //   warp 0       TMA producer: stages of two 64-deep steps (64 KB of operands per CTA);
@@ -38,7 +43,8 @@ constexpr int LG_KT = 64;                        // contraction per step: 128 by
 constexpr int LG_PER = 2;                        // steps per barrier stage
 constexpr int LG_NSTG = 3;                       // barrier stages
 constexpr int LG_TILE = 128 * LG_KT * 2;         // bytes of one operand's step in one CTA
-constexpr int LG_STAGE = LG_PER * 2 * LG_TILE;   // 64 KB
+constexpr int LG_OPERAND = LG_PER * LG_TILE;     // of one operand's stage: 32 KB
+constexpr int LG_STAGE = 2 * LG_OPERAND;
 constexpr int LG_EPI_WARPS = 16;
 constexpr int LG_THREADS = 32 * (3 + LG_EPI_WARPS);
 constexpr int LG_MAX_E = 256;
@@ -50,7 +56,12 @@ constexpr int LG_OFF_BAR = LG_NSTG * LG_STAGE;
 constexpr int LG_BARS = 4 * LG_NSTG + 5;
 constexpr int LG_OFF_MISC = LG_OFF_BAR + LG_BARS * 8;
 constexpr int LG_OFF_SEG = (LG_OFF_MISC + 16 + 15) & ~15;   // row0[E+1], tile0[E+1], order[E]
-constexpr int LG_SMEM = LG_OFF_SEG + 3 * (LG_MAX_E + 1) * 4 + 1024;
+// Epilogue: per warp eight column pairs of 32 m, as words {column 2p, column 2p + 1} at a pitch of
+// 36 words, so that both the writes (a word per lane) and the reads (16 bytes) are conflict-free.
+constexpr int LG_TR_PITCH = 36;
+constexpr int LG_OFF_TR = (LG_OFF_SEG + 3 * (LG_MAX_E + 1) * 4 + 15) & ~15;
+constexpr int LG_TR_WARP = 8 * LG_TR_PITCH * 4;
+constexpr int LG_SMEM = LG_OFF_TR + LG_EPI_WARPS * LG_TR_WARP + 1024;
 static_assert(LG_SMEM <= 232448, "shared memory budget");
 
 // kind::f16 instruction descriptor: bf16 x bf16 -> f32, M = 256, N columns; a_mn, b_mn: the
@@ -155,7 +166,7 @@ __device__ __forceinline__ void lin_decode(const LinearArgs& a, const int* row0,
 template <int MODE>
 __device__ __forceinline__ bool lin_tail(const LinTile& tl) { return MODE == LIN_WGRAD && (tl.c_cnt & 15) != 0; }
 
-template <int MODE>
+template <int MODE, bool ATOMS>
 __global__ void __launch_bounds__(LG_THREADS, 1)
     grouped_linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                           const __grid_constant__ CUtensorMap tmBs, const LinearArgs args) {
@@ -292,8 +303,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         const int m = tl.m0 + int(rank) * 128;
         const int nr = tl.n0 + int(rank) * half;
         const bool small = !B_MN && half <= LG_SMALL;
-        const int nb = half > 64 ? 2 : 1;        // 64-column boxes of an MN-major B
-        const uint32_t step_bytes = LG_TILE + (B_MN ? uint32_t(nb) * 8192u : small ? LG_SMALL * 128u : uint32_t(LG_TILE));
+        const uint32_t b_step = small ? LG_SMALL * 128u : uint32_t(LG_TILE);
         for (int kt0 = 0; kt0 < tl.steps; kt0 += LG_PER, ++it) {
           const int st = it % LG_NSTG, round = it / LG_NSTG;
           if (!wait_phase(&empty[st], (round & 1) ^ 1, abort_s, args.err, SITE_LINEAR, kWaitLimitNs)) {
@@ -305,33 +315,41 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
           // CTA's tail barrier, since each clears its own rows (full then only advances its phase)
           const bool tl_stage = lin_tail<MODE>(tl) && kt0 + LG_PER >= tl.steps;
           uint32_t bar_c = full_c0 + uint32_t(st) * 8u;
+          // K-major operands without ATOMS are fetched step by step, everything else whole
+          const uint32_t bytes = (ATOMS || A_MN ? uint32_t(LG_OPERAND) : uint32_t(nk * LG_TILE)) +
+                                 (ATOMS || B_MN ? LG_PER * b_step : uint32_t(nk) * b_step);
           if (tl_stage) {
             if (rank == 0) mbar_arrive_expect_tx(&full[st], 0);
-            mbar_arrive_expect_tx(&tail[st], uint32_t(nk) * step_bytes);
+            mbar_arrive_expect_tx(&tail[st], bytes);
             bar_c = mapa_shared(smem_u32(&tail[st]), rank);
           } else if (rank == 0) {
-            mbar_arrive_expect_tx(&full[st], 2u * uint32_t(nk) * step_bytes);
+            mbar_arrive_expect_tx(&full[st], 2u * bytes);
           }
           last_round[st] = round;
           issued = true;
-          for (int s = 0; s < nk; ++s) {
-            uint8_t* pa = smem + st * LG_STAGE + s * LG_TILE;
-            uint8_t* pb = smem + st * LG_STAGE + (LG_PER + s) * LG_TILE;
-            const int c = tl.c0 + (kt0 + s) * LG_KT;
+          uint8_t* pa = smem + st * LG_STAGE;
+          uint8_t* pb = pa + LG_OPERAND;
+          const int c = tl.c0 + kt0 * LG_KT;
+          if (ATOMS) {
+            // {64 columns, 128 rows, 2 blocks of 64 columns(, expert)}
+            if (MODE == LIN_FWD) tma_load_4d(pa, &tmA, 0, m, c >> 6, tl.e, bar_c);
+            else if (MODE == LIN_DGRAD) tma_load_4d(pa, &tmA, 0, c, m >> 6, tl.e, bar_c);
+            else tma_load_3d(pa, &tmA, 0, c, m >> 6, bar_c);
+            if (B_MN) tma_load_3d(pb, &tmB, 0, c, nr >> 6, bar_c);
+            else tma_load_3d(pb, small ? &tmBs : &tmB, 0, nr, c >> 6, bar_c);
+          } else {
             if (MODE == LIN_FWD) {
-              tma_load_3d(pa, &tmA, c, m, tl.e, bar_c);
+              for (int s = 0; s < nk; ++s) tma_load_3d(pa + s * LG_TILE, &tmA, c + s * LG_KT, m, tl.e, bar_c);
             } else if (MODE == LIN_DGRAD) {
-              tma_load_3d(pa, &tmA, m, c, tl.e, bar_c);
-              tma_load_3d(pa + 8192, &tmA, m + 64, c, tl.e, bar_c);
+              for (int h = 0; h < 2; ++h) tma_load_3d(pa + h * LG_TILE, &tmA, m + h * 64, c, tl.e, bar_c);
             } else {
-              tma_load_2d(pa, &tmA, m, c, bar_c);
-              tma_load_2d(pa + 8192, &tmA, m + 64, c, bar_c);
+              for (int h = 0; h < 2; ++h) tma_load_2d(pa + h * LG_TILE, &tmA, m + h * 64, c, bar_c);
             }
             if (B_MN) {
-              tma_load_2d(pb, &tmB, nr, c, bar_c);
-              if (nb == 2) tma_load_2d(pb + 8192, &tmB, nr + 64, c, bar_c);
+              for (int h = 0; h < 2; ++h) tma_load_2d(pb + h * LG_TILE, &tmB, nr + h * 64, c, bar_c);
             } else {
-              tma_load_2d(pb, small ? &tmBs : &tmB, c, nr, bar_c);
+              for (int s = 0; s < nk; ++s)
+                tma_load_2d(pb + s * b_step, small ? &tmBs : &tmB, c + s * LG_KT, nr, bar_c);
             }
           }
         }
@@ -385,16 +403,19 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
             cleared_par ^= 1u << st;
           }
           tc_fence_after();
+          const uint32_t pa = smem_u32(smem + st * LG_STAGE), pb = pa + LG_OPERAND;
+          const uint64_t ad = A_MN ? desc_sw128_mn(pa, LG_TILE) : desc_sw128(pa);
+          const uint64_t bd = B_MN ? desc_sw128_mn(pb, LG_TILE) : desc_sw128(pb);
+          const uint32_t b_step = !B_MN && tl.n <= 2 * LG_SMALL ? LG_SMALL * 128u : uint32_t(LG_TILE);
           for (int s = 0; s < nk; ++s) {
-            const uint32_t pa = smem_u32(smem + st * LG_STAGE + s * LG_TILE);
-            const uint32_t pb = smem_u32(smem + st * LG_STAGE + (LG_PER + s) * LG_TILE);
-            const uint64_t ad = A_MN ? desc_sw128_mn(pa, 8192) : desc_sw128(pa);
-            const uint64_t bd = B_MN ? desc_sw128_mn(pb, 8192) : desc_sw128(pb);
-            // 16 of the contraction: 32 bytes of a K-major row, two 8-row groups of an MN-major tile
+            // 16 of the contraction, in the descriptors' 16-byte units: 32 bytes of a K-major row,
+            // two 8-row groups (2 KB) of an MN-major block
+            const uint64_t a0 = ad + uint64_t(s * ((A_MN ? 64 * 128 : LG_TILE) >> 4));
+            const uint64_t b0 = bd + uint64_t(s * ((B_MN ? 64 * 128 : int(b_step)) >> 4));
             const int left = tl.c_cnt - (kt0 + s) * LG_KT;
             const int kk_n = left >= LG_KT ? LG_KT / 16 : (left + 15) / 16;
             for (int kk = 0; kk < kk_n; ++kk)
-              tc_mma_bf16(acc, ad + uint64_t((A_MN ? 128 : 2) * kk), bd + uint64_t((B_MN ? 128 : 2) * kk), idesc,
+              tc_mma_bf16(acc, a0 + uint64_t((A_MN ? 128 : 2) * kk), b0 + uint64_t((B_MN ? 128 : 2) * kk), idesc,
                           (kt0 | s | kk) != 0);
           }
           issued = true;
@@ -417,7 +438,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
     const uint32_t tmem_row = tmem + (uint32_t(q * 32) << 16) + uint32_t(cg * 64);
     const uint32_t tmem_empty_c0 = mapa_shared(smem_u32(tmem_empty), 0);
     const int M = lin_m<MODE>(args);
-    const bool odd = lane & 1;
+    uint32_t* tr = reinterpret_cast<uint32_t*>(smem + LG_OFF_TR + (warp - 2) * LG_TR_WARP);
     int tcount = 0;
     for (int t = pair; t < total; t += num_pairs, ++tcount) {
       LinTile tl;
@@ -434,22 +455,33 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster_relaxed(tmem_empty_c0 + uint32_t(ab) * 8u);
-      // Lane l holds m = l of 64 columns.  Neighbouring lanes trade values so that each stores
-      // the pair of m (l & ~1, l | 1) of every other column: 4-byte stores, 64 bytes per column.
-      const int m = tl.m0 + int(rank) * 128 + q * 32 + (lane & ~1);
+      // Lane l holds m = l of 64 columns.  Through shared memory, 16 columns at a time, a lane
+      // gets eight m of two columns, p and p + 1: 16-byte stores, 64 bytes per column and warp.
+      const int p = lane >> 2, m = tl.m0 + int(rank) * 128 + q * 32 + (lane & 3) * 8;
       const int64_t first = (MODE == LIN_WGRAD ? int64_t(tl.e) * args.N : 0) + tl.n0 + cg * 64;
-      __nv_bfloat16* o = args.out + first * args.ldo + m;
+      __nv_bfloat16* o = args.out + (first + 2 * p) * args.ldo + m;
       const bool zero = tl.steps == 0;           // wgrad of an expert without rows
 #pragma unroll
-      for (int c = 0; c < 64; c += 2) {
-        if (cg * 64 + c >= tl.cnt) break;
-        const float mine = __uint_as_float(odd ? r[c + 1] : r[c]);
-        const float give = __uint_as_float(odd ? r[c] : r[c + 1]);
-        const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
-        const int cc = c + int(odd);
-        uint32_t w = odd ? pack_bf16x2(got, mine) : pack_bf16x2(mine, got);
-        if (zero) w = 0;
-        if (m < M && cg * 64 + cc < tl.cnt) *reinterpret_cast<uint32_t*>(o + int64_t(cc) * args.ldo) = w;
+      for (int c0 = 0; c0 < 64; c0 += 16) {
+        if (cg * 64 + c0 >= tl.cnt) break;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t w = pack_bf16x2(__uint_as_float(r[c0 + 2 * i]), __uint_as_float(r[c0 + 2 * i + 1]));
+          tr[i * LG_TR_PITCH + lane] = zero ? 0u : w;
+        }
+        __syncwarp();
+        const uint4* src = reinterpret_cast<const uint4*>(tr + p * LG_TR_PITCH + (lane & 3) * 8);
+        const uint4 u = src[0], v = src[1];
+        __syncwarp();
+        const int left = tl.cnt - (cg * 64 + c0 + 2 * p);        // columns of the tile from this pair on
+        __nv_bfloat16* oc = o + int64_t(c0) * args.ldo;
+        if (m < M && left > 0)
+          *reinterpret_cast<uint4*>(oc) = make_uint4(__byte_perm(u.x, u.y, 0x5410), __byte_perm(u.z, u.w, 0x5410),
+                                                     __byte_perm(v.x, v.y, 0x5410), __byte_perm(v.z, v.w, 0x5410));
+        if (m < M && left > 1)
+          *reinterpret_cast<uint4*>(oc + args.ldo) =
+              make_uint4(__byte_perm(u.x, u.y, 0x7632), __byte_perm(u.z, u.w, 0x7632), __byte_perm(v.x, v.y, 0x7632),
+                         __byte_perm(v.z, v.w, 0x7632));
       }
     }
   } else if (MODE == LIN_WGRAD) {
@@ -471,16 +503,15 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         par ^= 1u << st;
-        const int s = (tl.steps - 1) % LG_PER;                    // the step that holds the end
-        const int valid = tl.c_cnt - (tl.steps - 1) * LG_KT;      // its rows
+        const int valid = tl.c_cnt - (stages - 1) * LG_PER * LG_KT;   // the stage's rows
         const int upto = (valid + 15) & ~15;
-        // 4 boxes (A, A + 64 columns, B, B + 64 columns) x rows x eight 16-byte chunks
+        // 4 blocks (A's two of 64 columns, B's two) x rows x eight 16-byte chunks
         const int n = (upto - valid) * 8;
         for (int i = lane; i < 4 * n; i += 32) {
-          const int box = i / n, j = i - box * n;
+          const int block = i / n, j = i - block * n;
           const int row = valid + (j >> 3);
-          uint8_t* base = smem + st * LG_STAGE + ((box >> 1) * LG_PER + s) * LG_TILE + (box & 1) * 8192;
-          *reinterpret_cast<uint4*>(base + (row >> 3) * 1024 + (row & 7) * 128 + (j & 7) * 16) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(smem + st * LG_STAGE + block * LG_TILE + row * 128 + (j & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
         }
         asm volatile("fence.proxy.async;" ::: "memory");          // visible to the MMAs' reads
         __syncwarp();
@@ -496,20 +527,30 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// bf16 map of rank 2 or 3 with a {64, box_rows(, 1)} box and 128-byte swizzle.
-bool lin_map(CUtensorMap* m, const void* base, int64_t inner, int64_t rows, int64_t ld, int64_t batch, int box_rows) {
+// bf16 map over row-major [batch][rows][inner] (batch 0: no such dimension) with 128-byte swizzle.
+// atoms: the columns as {64, inner / 64} and a box of {64, box_rows, 2(, 1)}; else {64, box_rows(, 1)}.
+bool lin_map(CUtensorMap* m, bool atoms, const void* base, int64_t inner, int64_t rows, int64_t ld, int64_t batch,
+             int box_rows) {
   EncodeTiledFn fn = get_encode_fn();
   if (fn == nullptr) return false;
-  cuuint64_t dims[3] = {cuuint64_t(inner), cuuint64_t(rows), cuuint64_t(batch)};
-  cuuint64_t strides[2] = {cuuint64_t(ld) * 2, cuuint64_t(ld) * cuuint64_t(rows) * 2};
-  cuuint32_t box[3] = {64, cuuint32_t(box_rows), 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, batch > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
+  cuuint64_t dims[4] = {cuuint64_t(atoms ? 64 : inner), cuuint64_t(rows)}, strides[3] = {cuuint64_t(ld) * 2};
+  cuuint32_t box[4] = {64, cuuint32_t(box_rows), 1, 1}, estr[4] = {1, 1, 1, 1};
+  int rank = 2;
+  if (atoms) {
+    strides[rank - 1] = 128;
+    box[rank] = 2;
+    dims[rank++] = cuuint64_t(inner / 64);
+  }
+  if (batch > 0) {
+    strides[rank - 1] = cuuint64_t(ld) * cuuint64_t(rows) * 2;
+    dims[rank++] = cuuint64_t(batch);
+  }
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank), const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE>
+template <int MODE, bool ATOMS>
 cudaError_t lin_launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mbs, const LinearArgs& a,
                        int grid, cudaStream_t st) {
   // the shared-memory attribute is per device: set it once on each device this process uses
@@ -519,7 +560,7 @@ cudaError_t lin_launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUten
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices || !attr_set[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(grouped_linear_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, LG_SMEM);
+    e = cudaFuncSetAttribute(grouped_linear_kernel<MODE, ATOMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, LG_SMEM);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices) attr_set[dev].store(true, std::memory_order_release);
   }
@@ -537,7 +578,7 @@ cudaError_t lin_launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUten
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, grouped_linear_kernel<MODE>, ma, mb, mbs, a);
+  return cudaLaunchKernelEx(&cfg, grouped_linear_kernel<MODE, ATOMS>, ma, mb, mbs, a);
 }
 
 }  // namespace
@@ -546,14 +587,15 @@ cudaError_t launch_grouped_linear(int mode, const LinearArgs& a, const void* x, 
                                   int64_t lddy, const void* w, cudaStream_t st, char* msg, size_t msg_len) {
   CUtensorMap ma, mb, mbs;
   bool ok;
+  const bool at = a.K % 64 == 0 && a.N % 64 == 0;
   if (mode == LIN_FWD) {
-    ok = lin_map(&ma, w, a.K, a.N, a.K, a.E, 128) && lin_map(&mb, x, a.K, a.rows, ldx, 0, 128) &&
-         lin_map(&mbs, x, a.K, a.rows, ldx, 0, LG_SMALL);
+    ok = lin_map(&ma, at, w, a.K, a.N, a.K, a.E, 128) && lin_map(&mb, at, x, a.K, a.rows, ldx, 0, 128) &&
+         lin_map(&mbs, at, x, a.K, a.rows, ldx, 0, LG_SMALL);
   } else if (mode == LIN_DGRAD) {
-    ok = lin_map(&ma, w, a.K, a.N, a.K, a.E, 64) && lin_map(&mb, dy, a.N, a.rows, lddy, 0, 128) &&
-         lin_map(&mbs, dy, a.N, a.rows, lddy, 0, LG_SMALL);
+    ok = lin_map(&ma, at, w, a.K, a.N, a.K, a.E, 128) && lin_map(&mb, at, dy, a.N, a.rows, lddy, 0, 128) &&
+         lin_map(&mbs, at, dy, a.N, a.rows, lddy, 0, LG_SMALL);
   } else {
-    ok = lin_map(&ma, x, a.K, a.rows, ldx, 0, 64) && lin_map(&mb, dy, a.N, a.rows, lddy, 0, 64);
+    ok = lin_map(&ma, at, x, a.K, a.rows, ldx, 0, 128) && lin_map(&mb, at, dy, a.N, a.rows, lddy, 0, 128);
     mbs = mb;                                    // not used
   }
   if (!ok) {
@@ -571,10 +613,13 @@ cudaError_t launch_grouped_linear(int mode, const LinearArgs& a, const void* x, 
                                        : (a.rows < a.E ? a.rows : a.E) + a.rows / LG_N;
   const int64_t pairs = sms / 2 < 1 ? 1 : sms / 2;
   const int grid = 2 * int(mt * nt < pairs ? mt * nt : pairs);
-  switch (mode) {
-    case LIN_FWD: return lin_launch<LIN_FWD>(ma, mb, mbs, a, grid, st);
-    case LIN_DGRAD: return lin_launch<LIN_DGRAD>(ma, mb, mbs, a, grid, st);
-    default: return lin_launch<LIN_WGRAD>(ma, mb, mbs, a, grid, st);
+  switch (mode * 2 + int(at)) {
+    case LIN_FWD * 2: return lin_launch<LIN_FWD, false>(ma, mb, mbs, a, grid, st);
+    case LIN_FWD * 2 + 1: return lin_launch<LIN_FWD, true>(ma, mb, mbs, a, grid, st);
+    case LIN_DGRAD * 2: return lin_launch<LIN_DGRAD, false>(ma, mb, mbs, a, grid, st);
+    case LIN_DGRAD * 2 + 1: return lin_launch<LIN_DGRAD, true>(ma, mb, mbs, a, grid, st);
+    case LIN_WGRAD * 2: return lin_launch<LIN_WGRAD, false>(ma, mb, mbs, a, grid, st);
+    default: return lin_launch<LIN_WGRAD, true>(ma, mb, mbs, a, grid, st);
   }
 }
 
