@@ -17,17 +17,21 @@
 // along memory, MN-major tiles where it does not, so nothing is transposed or padded first.
 // In every mode m is the contiguous index of the output.
 //
-// A stage of an operand is 128 x 128 values: K-major as two 64-deep steps of 128 rows, MN-major as
-// two 64-wide blocks of 128 deep, each row 128 swizzled bytes.  Where the row lengths are
-// multiples of 64 (ATOMS) one TMA box fetches it whole: what TMA delivers to an SM grows with the
-// bytes of a copy.  Other lengths take two boxes, whose ends TMA fills with zeros.
-//
-// Persistent CTA pairs (clusters of two, one CTA per SM): a pair computes a 256 x 256 tile
-// with tcgen05.mma.cta_group::2; each CTA stages its 128 m and its half of the n columns.
-//   warp 0       TMA producer: stages of two 64-deep steps (64 KB of operands per CTA);
-//   warp 1       TMEM allocation; in the leader, the MMAs; two 256-column accumulators;
-//   warps 2..17  epilogue, four per TMEM lane quarter, 64 accumulator columns each;
+// Persistent CTA pairs (clusters of two, one CTA per SM): a pair computes a tile of 256 m and up
+// to tn = 64, 256 or 512 n with tcgen05.mma.cta_group::2; each CTA stages its 128 m and its half of
+// the n.  What bounds the main loop of large tiles is the bytes a step needs against the ring's
+// bytes in flight: 512 columns need 48 B per clock and SM at the full MMA rate, 256 columns 64 B,
+// and TMA delivers about 50.  The 512 columns of TMEM are two accumulators of 256, handed out in
+// turn: a wide tile takes both, a narrow one leaves the other to the next tile.  A wide tile
+// starts on its first accumulator while the epilogue still reads the second.
+//   warp 0       TMA producer of the M side, warp 19 of the N side: one 64-deep step per stage, as
+//                many stages as 192 KB hold (9 of 64 columns, 6 of 256, 4 of 512);
+//   warp 1       TMEM allocation; in the leader, the MMAs;
+//   warps 2..17  epilogue, four per TMEM lane quarter, 64 columns of an accumulator each;
 //   warp 18      wgrad: clears the rows of a tile's last step that belong to the next expert.
+// A stage's operands are blocks of 128 bytes per row, swizzled: K-major 128 (m or n) rows of 64
+// deep, MN-major 64 deep rows of 64 (m or n).  MN-major operands whose rows are multiples of 64
+// (ATOMS) come two blocks to a TMA box, others one by one so that TMA fills the end with zeros.
 // Every wait is bounded.
 #include <atomic>
 #include <cstdio>
@@ -38,22 +42,27 @@
 namespace moe {
 namespace {
 
-constexpr int LG_M = 256, LG_N = 256;            // the pair's tile
-constexpr int LG_KT = 64;                        // contraction per step: 128 bytes of a K-major row
-constexpr int LG_PER = 2;                        // steps per barrier stage
-constexpr int LG_NSTG = 3;                       // barrier stages
-constexpr int LG_TILE = 128 * LG_KT * 2;         // bytes of one operand's step in one CTA
-constexpr int LG_OPERAND = LG_PER * LG_TILE;     // of one operand's stage: 32 KB
-constexpr int LG_STAGE = 2 * LG_OPERAND;
+constexpr int LG_M = 256;                        // the pair's tile: m
+constexpr int LG_ACC = 256;                      // columns of an accumulator
+constexpr int LG_KT = 64;                        // contraction per stage
+constexpr int LG_MAX_STG = 9;
+constexpr int LG_TILE = 128 * LG_KT * 2;         // 128 m or n of a stage: 16 KB
+constexpr int LG_BLOCK = LG_TILE / 2;            // one MN-major block
+constexpr int LG_RING = 192 * 1024;
+constexpr int LG_LEAD = 3;                       // stages a wide tile's first accumulator may run ahead
 constexpr int LG_EPI_WARPS = 16;
-constexpr int LG_THREADS = 32 * (3 + LG_EPI_WARPS);
+constexpr int LG_THREADS = 32 * (4 + LG_EPI_WARPS);
 constexpr int LG_MAX_E = 256;
 constexpr int LG_GROUP = 8;                      // row tiles that share the sweep over the weights
 constexpr int LG_SMALL = 32;                     // rows of the small row box
 
-constexpr int LG_OFF_BAR = LG_NSTG * LG_STAGE;
-// full[3], empty[3], tail[3], cleared[3], tmem_full[2], tmem_empty[2], drain
-constexpr int LG_BARS = 4 * LG_NSTG + 5;
+constexpr int LG_OFF_BAR = LG_RING;
+// full, empty, tail, cleared [LG_MAX_STG] each, tmem_full[2], tmem_empty[2], drain
+constexpr int LG_BARS = 4 * LG_MAX_STG + 5;
+
+// Bytes of a stage's N side in one CTA, and the stages of a ring, for tiles of tn columns.
+__host__ __device__ __forceinline__ int lin_b_bytes(int tn) { return tn / 2 * 128; }
+__host__ __device__ __forceinline__ int lin_stages(int tn) { return LG_RING / (LG_TILE + lin_b_bytes(tn)); }
 constexpr int LG_OFF_MISC = LG_OFF_BAR + LG_BARS * 8;
 constexpr int LG_OFF_SEG = (LG_OFF_MISC + 16 + 15) & ~15;   // row0[E+1], tile0[E+1], order[E]
 // Epilogue: per warp eight column pairs of 32 m, as words {column 2p, column 2p + 1} at a pitch of
@@ -89,11 +98,13 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
 }
 __device__ __noinline__ bool wait_phase_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
                                                 int site) {
-  const uint64_t t0 = globaltimer_ns();
+  uint64_t t0 = 0;                               // as wait_phase
   for (uint32_t n = 1; !mbar_try_wait_cluster(bar, parity); ++n) {
-    if ((n & 31u) != 0) continue;
+    if ((n & 255u) != 0) continue;
     if (*abort_flag) return false;
-    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitLimitNs) {
       report_error(err, MOE_ERR_DEVICE_TIMEOUT, site);
       *abort_flag = 1;
       return false;
@@ -102,13 +113,55 @@ __device__ __noinline__ bool wait_phase_cluster(uint64_t* bar, uint32_t parity, 
   return true;
 }
 
+// Whether a phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// A place in the ring: stage and the parity of its current phase.
+struct Cursor {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++st == stages) {
+      st = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
+// One tcgen05.mma (bf16, f32 accumulation) from descriptors given as their two halves: all
+// descriptors of a kernel differ in the low half only.
+__device__ __forceinline__ void lg_mma(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 da, {%1, %2};\n\t"
+      "mov.b64 db, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t}"
+      ::"r"(d), "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 struct LinTile {
   int e;
   int m0;          // first m of the pair's tile
   int n0, cnt;     // first n (row, or output feature in wgrad) and how many the tile has
-  int n;           // MMA columns: cnt rounded up to 32 (wgrad: 128)
+  int n;           // MMA columns: cnt rounded up to 32 (wgrad: 128); CTA r holds n0 + r * n/2 ..
   int c0, c_cnt;   // contraction: first index and length
   int steps;       // ceil(c_cnt / 64)
+  // accumulators of the tile, and columns of accumulator h: each CTA's first 128 n, then the rest
+  __device__ __forceinline__ int accs() const { return n > LG_ACC ? 2 : 1; }
+  __device__ __forceinline__ int cols(int h) const { return h == 0 ? (n > LG_ACC ? LG_ACC : n) : n - LG_ACC; }
 };
 
 template <int MODE>
@@ -117,7 +170,7 @@ __device__ __forceinline__ int lin_m(const LinearArgs& a) { return MODE == LIN_F
 template <int MODE>
 __device__ __forceinline__ int lin_tiles(const LinearArgs& a, const int* tile0) {
   const int mt = (lin_m<MODE>(a) + LG_M - 1) / LG_M;
-  if (MODE == LIN_WGRAD) return a.E * mt * ((a.N + LG_N - 1) / LG_N);
+  if (MODE == LIN_WGRAD) return a.E * mt * ((a.N + a.tn - 1) / a.tn);
   return tile0[a.E] * mt;
 }
 
@@ -127,15 +180,15 @@ __device__ __forceinline__ void lin_decode(const LinearArgs& a, const int* row0,
   const int mt = (lin_m<MODE>(a) + LG_M - 1) / LG_M;
   if (MODE == LIN_WGRAD) {
     // experts with the most rows first; inside an expert the m tiles of a few n tiles in turn
-    const int nt = (a.N + LG_N - 1) / LG_N;
+    const int nt = (a.N + a.tn - 1) / a.tn;
     const int slot = t / (mt * nt), rem = t - slot * (mt * nt);
     const int per = LG_GROUP * mt;
     const int g = rem / per, first = g * LG_GROUP, gs = min(LG_GROUP, nt - first);
     const int local = rem - g * per;
     tl.e = order[slot];
     tl.m0 = (local / gs) * LG_M;
-    tl.n0 = (first + local % gs) * LG_N;
-    tl.cnt = min(LG_N, a.N - tl.n0);
+    tl.n0 = (first + local % gs) * a.tn;
+    tl.cnt = min(a.tn, a.N - tl.n0);
     tl.c0 = row0[tl.e];
     tl.c_cnt = row0[tl.e + 1] - tl.c0;
   } else {
@@ -151,8 +204,8 @@ __device__ __forceinline__ void lin_decode(const LinearArgs& a, const int* row0,
     }
     tl.e = lo;
     tl.m0 = (local / gs) * LG_M;
-    tl.n0 = row0[lo] + (tt - tile0[lo]) * LG_N;
-    tl.cnt = min(LG_N, row0[lo + 1] - tl.n0);
+    tl.n0 = row0[lo] + (tt - tile0[lo]) * a.tn;
+    tl.cnt = min(a.tn, row0[lo + 1] - tl.n0);
     tl.c0 = 0;
     tl.c_cnt = MODE == LIN_FWD ? a.K : a.N;
   }
@@ -174,10 +227,10 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + LG_OFF_BAR);
-  uint64_t* empty = full + LG_NSTG;
-  uint64_t* tail = empty + LG_NSTG;              // this CTA's copies of a tail stage have landed
-  uint64_t* cleared = tail + LG_NSTG;            // leader: both CTAs have cleared a tail stage
-  uint64_t* tmem_full = cleared + LG_NSTG;
+  uint64_t* empty = full + LG_MAX_STG;
+  uint64_t* tail = empty + LG_MAX_STG;              // this CTA's copies of a tail stage have landed
+  uint64_t* cleared = tail + LG_MAX_STG;            // leader: both CTAs have cleared a tail stage
+  uint64_t* tmem_full = cleared + LG_MAX_STG;
   uint64_t* tmem_empty = tmem_full + 2;
   uint64_t* drain = tmem_empty + 2;
   uint32_t* tmem_base_s = reinterpret_cast<uint32_t*>(smem + LG_OFF_MISC);
@@ -190,9 +243,10 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();       // 0: leader (issues the MMAs), 1: peer
   const int pair = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
+  const int stages = lin_stages(args.tn), stage_bytes = LG_TILE + lin_b_bytes(args.tn);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < LG_NSTG; ++s) {
+    for (int s = 0; s < LG_MAX_STG; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
       mbar_init(&tail[s], 1);
@@ -231,7 +285,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
     for (int i = 0; i < 8; ++i) {
       sum += rows[i];
       all += rows[i];
-      tiles += (rows[i] + LG_N - 1) / LG_N;
+      tiles += (rows[i] + args.tn - 1) / args.tn;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, off);
@@ -259,7 +313,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         tile0[e] = ts;
       }
       rs += rows[i];
-      ts += (rows[i] + LG_N - 1) / LG_N;
+      ts += (rows[i] + args.tn - 1) / args.tn;
     }
     if (lane == 31 && args.E == LG_MAX_E) {
       row0[LG_MAX_E] = rs;
@@ -286,16 +340,13 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
   // inconsistent split_sizes: nothing is computed (the error word says so)
   const int total = *bad_s ? 0 : lin_tiles<MODE>(args, tile0);
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 19) {
     if (lane == 0) {
-      // ---------------- TMA producer (both CTAs) ----------------
+      // ---------------- TMA producers (both CTAs): warp 0 the M side, warp 19 the N side ----------------
+      const bool m_side = warp == 0;
       const uint32_t full_c0 = mapa_shared(smem_u32(full), 0);
-      int it = 0;
+      Cursor cur;
       bool ok = true;
-      int last_round[LG_NSTG];
-#pragma unroll
-      for (int s = 0; s < LG_NSTG; ++s) last_round[s] = -1;
-      bool issued = false;
       for (int t = pair; t < total && ok; t += num_pairs) {
         LinTile tl;
         lin_decode<MODE>(args, row0, tile0, order, t, tl);
@@ -303,69 +354,56 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         const int m = tl.m0 + int(rank) * 128;
         const int nr = tl.n0 + int(rank) * half;
         const bool small = !B_MN && half <= LG_SMALL;
-        const uint32_t b_step = small ? LG_SMALL * 128u : uint32_t(LG_TILE);
-        for (int kt0 = 0; kt0 < tl.steps; kt0 += LG_PER, ++it) {
-          const int st = it % LG_NSTG, round = it / LG_NSTG;
-          if (!wait_phase(&empty[st], (round & 1) ^ 1, abort_s, args.err, SITE_LINEAR, kWaitLimitNs)) {
+        const int nb = half > 128 ? 2 : 1;       // 128-wide parts of the N side
+        const uint32_t bytes = LG_TILE + (small ? LG_SMALL * 128u : uint32_t(nb * LG_TILE));
+        for (int kt = 0; kt < tl.steps; ++kt, cur.next(stages)) {
+          if (!wait_phase(&empty[cur.st], cur.ph ^ 1u, abort_s, args.err, SITE_LINEAR, kWaitLimitNs)) {
             ok = false;
             break;
           }
-          const int nk = min(LG_PER, tl.steps - kt0);
           // both CTAs' copies complete on the leader's full barrier; those of a tail stage on each
           // CTA's tail barrier, since each clears its own rows (full then only advances its phase)
-          const bool tl_stage = lin_tail<MODE>(tl) && kt0 + LG_PER >= tl.steps;
-          uint32_t bar_c = full_c0 + uint32_t(st) * 8u;
-          // K-major operands without ATOMS are fetched step by step, everything else whole
-          const uint32_t bytes = (ATOMS || A_MN ? uint32_t(LG_OPERAND) : uint32_t(nk * LG_TILE)) +
-                                 (ATOMS || B_MN ? LG_PER * b_step : uint32_t(nk) * b_step);
-          if (tl_stage) {
-            if (rank == 0) mbar_arrive_expect_tx(&full[st], 0);
-            mbar_arrive_expect_tx(&tail[st], bytes);
-            bar_c = mapa_shared(smem_u32(&tail[st]), rank);
-          } else if (rank == 0) {
-            mbar_arrive_expect_tx(&full[st], 2u * bytes);
-          }
-          last_round[st] = round;
-          issued = true;
-          uint8_t* pa = smem + st * LG_STAGE;
-          uint8_t* pb = pa + LG_OPERAND;
-          const int c = tl.c0 + kt0 * LG_KT;
-          if (ATOMS) {
-            // {64 columns, 128 rows, 2 blocks of 64 columns(, expert)}
-            if (MODE == LIN_FWD) tma_load_4d(pa, &tmA, 0, m, c >> 6, tl.e, bar_c);
-            else if (MODE == LIN_DGRAD) tma_load_4d(pa, &tmA, 0, c, m >> 6, tl.e, bar_c);
-            else tma_load_3d(pa, &tmA, 0, c, m >> 6, bar_c);
-            if (B_MN) tma_load_3d(pb, &tmB, 0, c, nr >> 6, bar_c);
-            else tma_load_3d(pb, small ? &tmBs : &tmB, 0, nr, c >> 6, bar_c);
-          } else {
-            if (MODE == LIN_FWD) {
-              for (int s = 0; s < nk; ++s) tma_load_3d(pa + s * LG_TILE, &tmA, c + s * LG_KT, m, tl.e, bar_c);
-            } else if (MODE == LIN_DGRAD) {
-              for (int h = 0; h < 2; ++h) tma_load_3d(pa + h * LG_TILE, &tmA, m + h * 64, c, tl.e, bar_c);
-            } else {
-              for (int h = 0; h < 2; ++h) tma_load_2d(pa + h * LG_TILE, &tmA, m + h * 64, c, bar_c);
+          uint32_t bar_c = full_c0 + uint32_t(cur.st) * 8u;
+          if (lin_tail<MODE>(tl) && kt + 1 == tl.steps) {
+            bar_c = mapa_shared(smem_u32(&tail[cur.st]), rank);
+            if (m_side) {
+              if (rank == 0) mbar_arrive_expect_tx(&full[cur.st], 0);
+              mbar_arrive_expect_tx(&tail[cur.st], bytes);
             }
-            if (B_MN) {
-              for (int h = 0; h < 2; ++h) tma_load_2d(pb + h * LG_TILE, &tmB, nr + h * 64, c, bar_c);
+          } else if (m_side && rank == 0) {
+            mbar_arrive_expect_tx(&full[cur.st], 2u * bytes);
+          }
+          uint8_t* pa = smem + cur.st * stage_bytes;
+          uint8_t* pb = pa + LG_TILE;
+          const int c = tl.c0 + kt * LG_KT;
+          if (m_side) {
+            if (MODE == LIN_FWD) {
+              tma_load_3d(pa, &tmA, c, m, tl.e, bar_c);
+            } else if (ATOMS) {
+              if (MODE == LIN_DGRAD) tma_load_4d(pa, &tmA, 0, c, m >> 6, tl.e, bar_c);
+              else tma_load_3d(pa, &tmA, 0, c, m >> 6, bar_c);
             } else {
-              for (int s = 0; s < nk; ++s)
-                tma_load_2d(pb + s * b_step, small ? &tmBs : &tmB, c + s * LG_KT, nr, bar_c);
+              for (int k = 0; k < 2; ++k) {
+                if (MODE == LIN_DGRAD) tma_load_3d(pa + k * LG_BLOCK, &tmA, m + k * 64, c, tl.e, bar_c);
+                else tma_load_2d(pa + k * LG_BLOCK, &tmA, m + k * 64, c, bar_c);
+              }
+            }
+          } else if (small) {
+            tma_load_2d(pb, &tmBs, c, nr, bar_c);
+          } else {
+            for (int h = 0; h < nb; ++h) {
+              if (!B_MN) tma_load_2d(pb + h * LG_TILE, &tmB, c, nr + h * 128, bar_c);
+              else if (ATOMS) tma_load_3d(pb + h * LG_TILE, &tmB, 0, c, (nr + h * 128) >> 6, bar_c);
+              else
+                for (int k = 0; k < 2; ++k)
+                  tma_load_2d(pb + h * LG_TILE + k * LG_BLOCK, &tmB, nr + h * 128 + k * 64, c, bar_c);
             }
           }
         }
       }
       pdl_launch_dependents();
-      if (!ok && issued) {
-        // let copies already issued land before the CTA exits: the leader watches the full
-        // barriers, then a fixed grace period for copies that signal elsewhere
-        if (rank == 0) {
-          for (int s = 0; s < LG_NSTG; ++s) {
-            if (last_round[s] < 0) continue;
-            const uint64_t t0 = globaltimer_ns();
-            while (!mbar_try_wait(&full[s], last_round[s] & 1) && globaltimer_ns() - t0 < 20000000ull) {
-            }
-          }
-        }
+      if (!ok) {
+        // copies already issued land before the CTA exits (they take microseconds; bounded)
         const uint64_t t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < 2000000ull) {
         }
@@ -374,55 +412,95 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       // ---------------- MMA issuer (leader) ----------------
-      int it = 0, tcount = 0;
+      // The thread's own time per stage counts: the tensor pipe takes a few MMAs ahead, and what
+      // the thread does between the last of a stage and the first of the next is idle time once
+      // they have run out.  So the descriptors are kept as offsets, whole steps are unrolled, and
+      // the next stage's barrier is looked at before this stage's MMAs.
+      const uint64_t a_desc = A_MN ? desc_sw128_mn(smem_u32(smem), LG_BLOCK) : desc_sw128(smem_u32(smem));
+      const uint64_t b_desc = B_MN ? desc_sw128_mn(smem_u32(smem + LG_TILE), LG_BLOCK) : desc_sw128(smem_u32(smem + LG_TILE));
+      const uint32_t alo0 = uint32_t(a_desc), ahi = uint32_t(a_desc >> 32), blo0 = uint32_t(b_desc), bhi = uint32_t(b_desc >> 32);
+      // 16 of the contraction, in the descriptors' 16-byte units: 32 bytes of a K-major row, two
+      // 8-row groups (2 KB) of an MN-major block
+      constexpr uint32_t A_K = A_MN ? 128 : 2, B_K = B_MN ? 128 : 2;
+      // the MMAs of one stage into accumulator half h
+      const auto mma = [&](int st, bool first, int groups, int h, uint32_t acc, uint32_t idesc) {
+        const uint32_t off = uint32_t(st * (stage_bytes >> 4));
+        const uint32_t a0 = alo0 + off, b0 = blo0 + off + uint32_t(h * (LG_TILE >> 4));
+        if (groups == LG_KT / 16) {
+#pragma unroll
+          for (uint32_t kk = 0; kk < LG_KT / 16; ++kk)
+            lg_mma(acc, a0 + A_K * kk, ahi, b0 + B_K * kk, bhi, idesc, kk == 0 ? uint32_t(!first) : 1u);
+        } else {
+          for (uint32_t kk = 0; kk < uint32_t(groups); ++kk)
+            lg_mma(acc, a0 + A_K * kk, ahi, b0 + B_K * kk, bhi, idesc, uint32_t(!first) | kk);
+        }
+      };
+      Cursor cur;
+      int ac = 0;                                // accumulators used so far
       uint32_t cleared_par = 0;                  // bit s: parity of the next tail phase of stage s
-      bool ok = true, issued = false;
-      for (int t = pair; t < total && ok; t += num_pairs, ++tcount) {
+      bool ok = true, issued = false, ready = false;
+      for (int t = pair; t < total && ok; t += num_pairs) {
         LinTile tl;
         lin_decode<MODE>(args, row0, tile0, order, t, tl);
-        const uint32_t idesc = lg_idesc(A_MN, B_MN, tl.n);
-        const int ab = tcount & 1, use = tcount >> 1;
-        const uint32_t acc = tmem + uint32_t(ab) * 256u;
-        if (!wait_phase(&tmem_empty[ab], (use & 1) ^ 1, abort_s, args.err, SITE_LINEAR + 1, kWaitLimitNs)) {
+        const int accs = tl.accs();
+        const int b0 = ac & 1, b1 = (ac + 1) & 1;
+        const uint32_t acc0 = tmem + uint32_t(b0 * LG_ACC), acc1 = tmem + uint32_t(b1 * LG_ACC);
+        const uint32_t id0 = lg_idesc(A_MN, B_MN, tl.cols(0)), id1 = lg_idesc(A_MN, B_MN, tl.cols(1));
+        const uint32_t par1 = (((ac + 1) >> 1) & 1) ^ 1;
+        const int last_groups = (tl.c_cnt - (tl.steps - 1) * LG_KT + 15) / 16;
+        if (!wait_phase(&tmem_empty[b0], ((ac >> 1) & 1) ^ 1, abort_s, args.err, SITE_LINEAR + 1, kWaitLimitNs)) {
           ok = false;
           break;
         }
+        // steps to run ahead on the first accumulator while the epilogue reads the second
+        const int lead = accs == 1 || mbar_test(&tmem_empty[b1], par1) ? 0 : min(LG_LEAD, tl.steps);
+        Cursor behind = cur;
         tc_fence_after();
-        for (int kt0 = 0; kt0 < tl.steps; kt0 += LG_PER, ++it) {
-          const int st = it % LG_NSTG, round = it / LG_NSTG;
-          const int nk = min(LG_PER, tl.steps - kt0);
-          if (!wait_phase(&full[st], round & 1, abort_s, args.err, SITE_LINEAR + 2, kWaitLimitNs)) {
+        for (int kt = 0; kt < tl.steps; ++kt) {
+          if (!ready && !wait_phase(&full[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR + 2, kWaitLimitNs)) {
             ok = false;
             break;
           }
-          if (lin_tail<MODE>(tl) && kt0 + LG_PER >= tl.steps) {
+          const int st = cur.st;
+          if (lin_tail<MODE>(tl) && kt + 1 == tl.steps) {
             if (!wait_phase_cluster(&cleared[st], (cleared_par >> st) & 1u, abort_s, args.err, SITE_LINEAR + 3)) {
               ok = false;
               break;
             }
             cleared_par ^= 1u << st;
           }
+          cur.next(stages);
+          ready = mbar_test(&full[cur.st], cur.ph);
           tc_fence_after();
-          const uint32_t pa = smem_u32(smem + st * LG_STAGE), pb = pa + LG_OPERAND;
-          const uint64_t ad = A_MN ? desc_sw128_mn(pa, LG_TILE) : desc_sw128(pa);
-          const uint64_t bd = B_MN ? desc_sw128_mn(pb, LG_TILE) : desc_sw128(pb);
-          const uint32_t b_step = !B_MN && tl.n <= 2 * LG_SMALL ? LG_SMALL * 128u : uint32_t(LG_TILE);
-          for (int s = 0; s < nk; ++s) {
-            // 16 of the contraction, in the descriptors' 16-byte units: 32 bytes of a K-major row,
-            // two 8-row groups (2 KB) of an MN-major block
-            const uint64_t a0 = ad + uint64_t(s * ((A_MN ? 64 * 128 : LG_TILE) >> 4));
-            const uint64_t b0 = bd + uint64_t(s * ((B_MN ? 64 * 128 : int(b_step)) >> 4));
-            const int left = tl.c_cnt - (kt0 + s) * LG_KT;
-            const int kk_n = left >= LG_KT ? LG_KT / 16 : (left + 15) / 16;
-            for (int kk = 0; kk < kk_n; ++kk)
-              tc_mma_bf16(acc, a0 + uint64_t((A_MN ? 128 : 2) * kk), b0 + uint64_t((B_MN ? 128 : 2) * kk), idesc,
-                          (kt0 | s | kk) != 0);
-          }
+          const int groups = kt + 1 == tl.steps ? last_groups : LG_KT / 16;
+          mma(st, kt == 0, groups, 0, acc0, id0);
           issued = true;
+          if (kt < lead) {
+            if (kt + 1 < lead) continue;
+            if (!wait_phase(&tmem_empty[b1], par1, abort_s, args.err, SITE_LINEAR + 1, kWaitLimitNs)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            for (int j = 0; j <= kt; ++j, behind.next(stages)) {
+              mma(behind.st, j == 0, j == kt ? groups : LG_KT / 16, 1, acc1, id1);
+              tc_commit(&empty[behind.st]);
+            }
+            continue;
+          }
+          if (accs == 2) mma(st, kt == 0, groups, 1, acc1, id1);
           tc_commit(&empty[st]);                 // frees the stage in both CTAs
         }
         if (!ok) break;
-        tc_commit(&tmem_full[ab]);
+        // a tile without steps (an empty expert's weight gradient) takes its accumulators all the same
+        if (accs == 2 && tl.steps == 0 &&
+            !wait_phase(&tmem_empty[b1], par1, abort_s, args.err, SITE_LINEAR + 1, kWaitLimitNs)) {
+          ok = false;
+          break;
+        }
+        tc_commit(&tmem_full[b0]);
+        if (accs == 2) tc_commit(&tmem_full[b1]);
+        ac += accs;
       }
       if (!ok && issued) {
         tc_commit(drain);
@@ -439,85 +517,91 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
     const uint32_t tmem_empty_c0 = mapa_shared(smem_u32(tmem_empty), 0);
     const int M = lin_m<MODE>(args);
     uint32_t* tr = reinterpret_cast<uint32_t*>(smem + LG_OFF_TR + (warp - 2) * LG_TR_WARP);
-    int tcount = 0;
-    for (int t = pair; t < total; t += num_pairs, ++tcount) {
-      LinTile tl;
-      lin_decode<MODE>(args, row0, tile0, order, t, tl);
-      const int ab = tcount & 1, use = tcount >> 1;
-      if (!wait_phase(&tmem_full[ab], use & 1, abort_s, args.err, SITE_LINEAR + 4, kWaitLimitNs)) break;
-      tc_fence_after();
-      uint32_t r[64];
-      if (cg * 64 < tl.cnt) {
-        tmem_ld32_async(tmem_row + uint32_t(ab) * 256u, r);
-        if (cg * 64 + 32 < tl.cnt) tmem_ld32_async(tmem_row + uint32_t(ab) * 256u + 32u, r + 32);
-        tmem_wait_ld<64>(r);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_relaxed(tmem_empty_c0 + uint32_t(ab) * 8u);
-      // Lane l holds m = l of 64 columns.  Through shared memory, 16 columns at a time, a lane
-      // gets eight m of two columns, p and p + 1: 16-byte stores, 64 bytes per column and warp.
-      const int p = lane >> 2, m = tl.m0 + int(rank) * 128 + q * 32 + (lane & 3) * 8;
-      const int64_t first = (MODE == LIN_WGRAD ? int64_t(tl.e) * args.N : 0) + tl.n0 + cg * 64;
-      __nv_bfloat16* o = args.out + (first + 2 * p) * args.ldo + m;
-      const bool zero = tl.steps == 0;           // wgrad of an expert without rows
-#pragma unroll
-      for (int c0 = 0; c0 < 64; c0 += 16) {
-        if (cg * 64 + c0 >= tl.cnt) break;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t w = pack_bf16x2(__uint_as_float(r[c0 + 2 * i]), __uint_as_float(r[c0 + 2 * i + 1]));
-          tr[i * LG_TR_PITCH + lane] = zero ? 0u : w;
-        }
-        __syncwarp();
-        const uint4* src = reinterpret_cast<const uint4*>(tr + p * LG_TR_PITCH + (lane & 3) * 8);
-        const uint4 u = src[0], v = src[1];
-        __syncwarp();
-        const int left = tl.cnt - (cg * 64 + c0 + 2 * p);        // columns of the tile from this pair on
-        __nv_bfloat16* oc = o + int64_t(c0) * args.ldo;
-        if (m < M && left > 0)
-          *reinterpret_cast<uint4*>(oc) = make_uint4(__byte_perm(u.x, u.y, 0x5410), __byte_perm(u.z, u.w, 0x5410),
-                                                     __byte_perm(v.x, v.y, 0x5410), __byte_perm(v.z, v.w, 0x5410));
-        if (m < M && left > 1)
-          *reinterpret_cast<uint4*>(oc + args.ldo) =
-              make_uint4(__byte_perm(u.x, u.y, 0x7632), __byte_perm(u.z, u.w, 0x7632), __byte_perm(v.x, v.y, 0x7632),
-                         __byte_perm(v.z, v.w, 0x7632));
-      }
-    }
-  } else if (MODE == LIN_WGRAD) {
-    // ---------------- warp 18: rows of a tail stage past the expert's end (both CTAs) ----------------
-    const uint32_t cleared_c0 = mapa_shared(smem_u32(cleared), 0);
-    uint32_t par = 0;
-    int it = 0;
+    int ac = 0;
     bool ok = true;
     for (int t = pair; t < total && ok; t += num_pairs) {
       LinTile tl;
       lin_decode<MODE>(args, row0, tile0, order, t, tl);
-      const int stages = (tl.steps + LG_PER - 1) / LG_PER;
-      if (lin_tail<MODE>(tl)) {
-        // (a barrier is waited on in every one of its phases or not at all: skipping phases, this
-        // warp would take an older phase of the same parity for the one it wants; so tail stages
-        // have barriers of their own)
-        const int st = (it + stages - 1) % LG_NSTG;
-        ok = wait_phase(&tail[st], (par >> st) & 1u, abort_s, args.err, SITE_LINEAR + 5, kWaitLimitNs);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        par ^= 1u << st;
-        const int valid = tl.c_cnt - (stages - 1) * LG_PER * LG_KT;   // the stage's rows
-        const int upto = (valid + 15) & ~15;
-        // 4 blocks (A's two of 64 columns, B's two) x rows x eight 16-byte chunks
-        const int n = (upto - valid) * 8;
-        for (int i = lane; i < 4 * n; i += 32) {
-          const int block = i / n, j = i - block * n;
-          const int row = valid + (j >> 3);
-          *reinterpret_cast<uint4*>(smem + st * LG_STAGE + block * LG_TILE + row * 128 + (j & 7) * 16) =
-              make_uint4(0, 0, 0, 0);
+      const int accs = tl.accs();
+      for (int h = 0; h < accs; ++h, ++ac) {
+        const int ab = ac & 1;
+        if (!wait_phase(&tmem_full[ab], (ac >> 1) & 1, abort_s, args.err, SITE_LINEAR + 4, kWaitLimitNs)) {
+          ok = false;
+          break;
         }
-        asm volatile("fence.proxy.async;" ::: "memory");          // visible to the MMAs' reads
+        tc_fence_after();
+        const int cols = tl.cols(h), part = cols >> 1;           // the first `part` columns are the leader's n
+        uint32_t r[64];
+        if (cg * 64 < cols) {
+          tmem_ld32_async(tmem_row + uint32_t(ab * LG_ACC), r);
+          if (cg * 64 + 32 < cols) tmem_ld32_async(tmem_row + uint32_t(ab * LG_ACC) + 32u, r + 32);
+          tmem_wait_ld<64>(r);
+        }
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_release(cleared_c0 + uint32_t(st) * 8u);
+        if (lane == 0) mbar_arrive_cluster_relaxed(tmem_empty_c0 + uint32_t(ab) * 8u);
+        // Lane l holds m = l of 64 columns.  Through shared memory, 16 columns at a time, a lane
+        // gets eight m of two columns, p and p + 1: 16-byte stores, 64 bytes per column and warp.
+        const int p = lane >> 2, m = tl.m0 + int(rank) * 128 + q * 32 + (lane & 3) * 8;
+        __nv_bfloat16* o = args.out + ((MODE == LIN_WGRAD ? int64_t(tl.e) * args.N : 0) + tl.n0 + 2 * p) * args.ldo + m;
+        const bool zero = tl.steps == 0;         // wgrad of an expert without rows
+#pragma unroll
+        for (int c0 = 0; c0 < 64; c0 += 16) {
+          const int j = cg * 64 + c0;
+          if (j >= cols) break;
+          const int off = (j >= part ? (tl.n >> 1) + j - part : j) + h * 128;    // n - n0 of column j
+          if (off >= tl.cnt) continue;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t w = pack_bf16x2(__uint_as_float(r[c0 + 2 * i]), __uint_as_float(r[c0 + 2 * i + 1]));
+            tr[i * LG_TR_PITCH + lane] = zero ? 0u : w;
+          }
+          __syncwarp();
+          const uint4* src = reinterpret_cast<const uint4*>(tr + p * LG_TR_PITCH + (lane & 3) * 8);
+          const uint4 u = src[0], v = src[1];
+          __syncwarp();
+          const int left = tl.cnt - (off + 2 * p);               // columns of the tile from this pair on
+          __nv_bfloat16* oc = o + int64_t(off) * args.ldo;
+          if (m < M && left > 0)
+            *reinterpret_cast<uint4*>(oc) = make_uint4(__byte_perm(u.x, u.y, 0x5410), __byte_perm(u.z, u.w, 0x5410),
+                                                       __byte_perm(v.x, v.y, 0x5410), __byte_perm(v.z, v.w, 0x5410));
+          if (m < M && left > 1)
+            *reinterpret_cast<uint4*>(oc + args.ldo) =
+                make_uint4(__byte_perm(u.x, u.y, 0x7632), __byte_perm(u.z, u.w, 0x7632),
+                           __byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x7632));
+        }
       }
-      it += stages;
+    }
+  } else if (warp == 18 && MODE == LIN_WGRAD) {
+    // ---------------- rows of a tail stage past the expert's end (both CTAs) ----------------
+    const uint32_t cleared_c0 = mapa_shared(smem_u32(cleared), 0);
+    uint32_t par = 0;                            // bit s: parity of the next tail phase of stage s
+    int at = 0;                                  // stages used so far
+    bool ok = true;
+    for (int t = pair; t < total && ok; t += num_pairs) {
+      LinTile tl;
+      lin_decode<MODE>(args, row0, tile0, order, t, tl);
+      at += tl.steps;
+      if (!lin_tail<MODE>(tl)) continue;
+      // (a barrier is waited on in every one of its phases or not at all: skipping phases, this
+      // warp would take an older phase of the same parity for the one it wants; so tail stages
+      // have barriers of their own)
+      const int st = (at - 1) % stages;
+      ok = wait_phase(&tail[st], (par >> st) & 1u, abort_s, args.err, SITE_LINEAR + 5, kWaitLimitNs);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      par ^= 1u << st;
+      const int valid = tl.c_cnt - (tl.steps - 1) * LG_KT;       // the stage's rows
+      const int n = (((valid + 15) & ~15) - valid) * 8;          // 16-byte chunks to clear in each block
+      const int blocks = tl.n > LG_ACC ? 6 : 4;                  // of 64 columns: M's two, N's two or four
+      for (int i = lane; i < blocks * n; i += 32) {
+        const int block = i / n, j = i - block * n;
+        *reinterpret_cast<uint4*>(smem + st * stage_bytes + block * LG_BLOCK + (valid + (j >> 3)) * 128 + (j & 7) * 16) =
+            make_uint4(0, 0, 0, 0);
+      }
+      asm volatile("fence.proxy.async;" ::: "memory");            // visible to the MMAs' reads
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_release(cleared_c0 + uint32_t(st) * 8u);
     }
   }
   tc_fence_before();
@@ -583,19 +667,20 @@ cudaError_t lin_launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUten
 
 }  // namespace
 
-cudaError_t launch_grouped_linear(int mode, const LinearArgs& a, const void* x, int64_t ldx, const void* dy,
+cudaError_t launch_grouped_linear(int mode, const LinearArgs& args, const void* x, int64_t ldx, const void* dy,
                                   int64_t lddy, const void* w, cudaStream_t st, char* msg, size_t msg_len) {
+  LinearArgs a = args;
   CUtensorMap ma, mb, mbs;
   bool ok;
-  const bool at = a.K % 64 == 0 && a.N % 64 == 0;
+  const bool at = a.K % 64 == 0 && (mode == LIN_DGRAD || a.N % 64 == 0);   // rows of the MN-major operands
   if (mode == LIN_FWD) {
-    ok = lin_map(&ma, at, w, a.K, a.N, a.K, a.E, 128) && lin_map(&mb, at, x, a.K, a.rows, ldx, 0, 128) &&
-         lin_map(&mbs, at, x, a.K, a.rows, ldx, 0, LG_SMALL);
+    ok = lin_map(&ma, false, w, a.K, a.N, a.K, a.E, 128) && lin_map(&mb, false, x, a.K, a.rows, ldx, 0, 128) &&
+         lin_map(&mbs, false, x, a.K, a.rows, ldx, 0, LG_SMALL);
   } else if (mode == LIN_DGRAD) {
-    ok = lin_map(&ma, at, w, a.K, a.N, a.K, a.E, 128) && lin_map(&mb, at, dy, a.N, a.rows, lddy, 0, 128) &&
-         lin_map(&mbs, at, dy, a.N, a.rows, lddy, 0, LG_SMALL);
+    ok = lin_map(&ma, at, w, a.K, a.N, a.K, a.E, 64) && lin_map(&mb, false, dy, a.N, a.rows, lddy, 0, 128) &&
+         lin_map(&mbs, false, dy, a.N, a.rows, lddy, 0, LG_SMALL);
   } else {
-    ok = lin_map(&ma, at, x, a.K, a.rows, ldx, 0, 128) && lin_map(&mb, at, dy, a.N, a.rows, lddy, 0, 128);
+    ok = lin_map(&ma, at, x, a.K, a.rows, ldx, 0, 64) && lin_map(&mb, at, dy, a.N, a.rows, lddy, 0, 64);
     mbs = mb;                                    // not used
   }
   if (!ok) {
@@ -607,15 +692,20 @@ cudaError_t launch_grouped_linear(int mode, const LinearArgs& a, const void* x, 
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  // no more pairs than tiles there can be
-  const int64_t mt = ((mode == LIN_FWD ? a.N : a.K) + LG_M - 1) / LG_M;
-  const int64_t nt = mode == LIN_WGRAD ? int64_t(a.E) * ((a.N + LG_N - 1) / LG_N)
-                                       : (a.rows < a.E ? a.rows : a.E) + a.rows / LG_N;
+  // Columns of a tile.  64 where an expert has few rows, so that the call reads the weights and
+  // little else: their stages are small and nine are in flight.  512 where they still make four
+  // tiles a pair, else 256 (fewer, larger tiles leave pairs idle at the end).
   const int64_t pairs = sms / 2 < 1 ? 1 : sms / 2;
+  const int64_t mt = ((mode == LIN_FWD ? a.N : a.K) + LG_M - 1) / LG_M;
+  const int64_t wide = mode == LIN_WGRAD ? int64_t(a.E) * ((a.N + 511) / 512) : a.rows / 512;
+  a.tn = mode != LIN_WGRAD && (a.rows <= 64 || a.rows <= int64_t(32) * a.E) ? 64 : mt * wide >= 4 * pairs ? 512 : 256;
+  // no more pairs than tiles there can be
+  const int64_t nt = mode == LIN_WGRAD ? int64_t(a.E) * ((a.N + a.tn - 1) / a.tn)
+                                       : (a.rows < a.E ? a.rows : a.E) + a.rows / a.tn;
   const int grid = 2 * int(mt * nt < pairs ? mt * nt : pairs);
   switch (mode * 2 + int(at)) {
-    case LIN_FWD * 2: return lin_launch<LIN_FWD, false>(ma, mb, mbs, a, grid, st);
-    case LIN_FWD * 2 + 1: return lin_launch<LIN_FWD, true>(ma, mb, mbs, a, grid, st);
+    case LIN_FWD * 2:
+    case LIN_FWD * 2 + 1: return lin_launch<LIN_FWD, false>(ma, mb, mbs, a, grid, st);   // both K-major
     case LIN_DGRAD * 2: return lin_launch<LIN_DGRAD, false>(ma, mb, mbs, a, grid, st);
     case LIN_DGRAD * 2 + 1: return lin_launch<LIN_DGRAD, true>(ma, mb, mbs, a, grid, st);
     case LIN_WGRAD * 2: return lin_launch<LIN_WGRAD, false>(ma, mb, mbs, a, grid, st);

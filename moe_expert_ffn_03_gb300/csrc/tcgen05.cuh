@@ -198,20 +198,21 @@ __device__ __forceinline__ void tc_mma_bf16(uint32_t d, uint64_t adesc, uint64_t
 // the limit ran out (then records the timeout and raises the abort flag).
 __device__ __noinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
                                         int site, uint64_t limit_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  uint32_t n = 0;
-  while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((++n & 31u) == 0) {
-      if (*abort_flag) return false;
-      if (globaltimer_ns() - t0 > limit_ns) {
-        report_error(err, MOE_ERR_DEVICE_TIMEOUT, site);
-        *abort_flag = 1;
-        return false;
-      }
+  // The clock is read only after many failed tries: a read costs hundreds of cycles, and a wait
+  // that ends in the meantime would notice that much later.
+  uint64_t t0 = 0;
+  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+    if ((n & 255u) != 0) continue;
+    if (*abort_flag) return false;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > limit_ns) {
+      report_error(err, MOE_ERR_DEVICE_TIMEOUT, site);
+      *abort_flag = 1;
+      return false;
     }
   }
+  return true;
 }
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
