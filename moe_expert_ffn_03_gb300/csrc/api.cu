@@ -1514,7 +1514,7 @@ moe_status moe_swiglu_bwd(int64_t rows, int32_t I, const void* gu, int64_t ld_gu
   return MOE_OK;
 }
 
-size_t moe_grouped_linear_workspace_size(const moe_grouped* g) { return check_grouped(g) == MOE_OK ? 256 : 0; }
+size_t moe_grouped_linear_workspace_size(const moe_grouped* g) { return check_grouped(g) == MOE_OK ? linear_ws_bytes() : 0; }
 
 moe_status moe_grouped_linear_fwd(const moe_grouped* g, const void* x, int64_t ldx, const int32_t* split_sizes,
                                   const void* w, void* y, int64_t ldy, void* workspace, size_t workspace_bytes,

@@ -32,6 +32,14 @@
 // A stage's operands are blocks of 128 bytes per row, swizzled: K-major 128 (m or n) rows of 64
 // deep, MN-major 64 deep rows of 64 (m or n).  MN-major operands whose rows are multiples of 64
 // (ATOMS) come two blocks to a TMA box, others one by one so that TMA fills the end with zeros.
+// Few rows and few tiles (CUT): the call is bound by reading the weights, and the last round of
+// whole tiles would leave pairs idle.  Where twice its tiles or more fit the pairs, its tiles are
+// cut along the contraction into as many equal pieces as fit.  The pieces of one place in the
+// contraction run side by side, so that the weights are still read in long stretches (shares cut
+// without regard to that read them 12% slower, measured).  The warp that finishes a tile's last
+// piece adds the f32 partial sums from the workspace in the order of the contraction, so
+// results do not depend on timing; nobody waits for anybody.  A kernel of its own: the code that
+// puts pieces together costs the others' main loops 2 to 5% by being there.
 // Every wait is bounded.
 #include <atomic>
 #include <cstdio>
@@ -55,6 +63,8 @@ constexpr int LG_THREADS = 32 * (4 + LG_EPI_WARPS);
 constexpr int LG_MAX_E = 256;
 constexpr int LG_GROUP = 8;                      // row tiles that share the sweep over the weights
 constexpr int LG_SMALL = 32;                     // rows of the small row box
+constexpr int LG_MIN_PIECE = 8;                  // steps a piece of a tile has at least
+constexpr int LG_PIECE = 64 * 32;                // f32 of a warp's partial sums: 64 columns of 32 m
 
 constexpr int LG_OFF_BAR = LG_RING;
 // full, empty, tail, cleared [LG_MAX_STG] each, tmem_full[2], tmem_empty[2], drain
@@ -158,7 +168,10 @@ struct LinTile {
   int n0, cnt;     // first n (row, or output feature in wgrad) and how many the tile has
   int n;           // MMA columns: cnt rounded up to 32 (wgrad: 128); CTA r holds n0 + r * n/2 ..
   int c0, c_cnt;   // contraction: first index and length
-  int steps;       // ceil(c_cnt / 64)
+  int all;         // its 64-deep steps: ceil(c_cnt / 64)
+  int k0, steps;   // those of this piece of the tile: first, number
+  int part, parts; // the piece's place among the tile's pieces
+  int cut;         // the tile's place among those cut
   // accumulators of the tile, and columns of accumulator h: each CTA's first 128 n, then the rest
   __device__ __forceinline__ int accs() const { return n > LG_ACC ? 2 : 1; }
   __device__ __forceinline__ int cols(int h) const { return h == 0 ? (n > LG_ACC ? LG_ACC : n) : n - LG_ACC; }
@@ -211,7 +224,48 @@ __device__ __forceinline__ void lin_decode(const LinearArgs& a, const int* row0,
   }
   // wgrad's columns come in 64-wide swizzle atoms per CTA, the rows of the others in 16s
   tl.n = MODE == LIN_WGRAD ? (tl.cnt + 127) & ~127 : (tl.cnt + 31) & ~31;
-  tl.steps = (tl.c_cnt + LG_KT - 1) / LG_KT;
+  tl.all = (tl.c_cnt + LG_KT - 1) / LG_KT;
+  tl.k0 = 0;
+  tl.steps = tl.all;
+  tl.part = 0;
+  tl.parts = 1;
+  tl.cut = 0;
+}
+
+// The pieces of work of a pair: every num_pairs-th of the tiles taken whole, then at most one
+// piece of the `rest` tiles that are cut into `parts` each.
+struct Plan {
+  int whole, rest, parts;
+};
+template <int MODE, bool CUT>
+__device__ __forceinline__ Plan lin_plan(const LinearArgs& a, int total, int num_pairs) {
+  Plan p{total, 0, 1};
+  if (!CUT) return p;
+  const int all = ((MODE == LIN_FWD ? a.K : a.N) + LG_KT - 1) / LG_KT;
+  const int rest = total % num_pairs;
+  const int parts = rest == 0 ? 1 : min(num_pairs / rest, all / LG_MIN_PIECE);
+  if (parts < 2) return p;
+  return Plan{total - rest, rest, parts};
+}
+// The next of the pair's pieces; t: its next tile, from pair on.
+template <int MODE, bool CUT>
+__device__ __forceinline__ bool lin_next(const LinearArgs& a, const int* row0, const int* tile0, const int* order,
+                                         const Plan& p, int pair, int num_pairs, int& t, LinTile& tl) {
+  if (t < p.whole) {
+    lin_decode<MODE>(a, row0, tile0, order, t, tl);
+    t += num_pairs;
+    return true;
+  }
+  if (!CUT || t >= p.whole + num_pairs || pair >= p.rest * p.parts) return false;
+  t += num_pairs;
+  const int cut = pair % p.rest, part = pair / p.rest;
+  lin_decode<MODE>(a, row0, tile0, order, p.whole + cut, tl);
+  tl.cut = cut;
+  tl.part = part;
+  tl.parts = p.parts;
+  tl.k0 = part * tl.all / p.parts;
+  tl.steps = (part + 1) * tl.all / p.parts - tl.k0;
+  return true;
 }
 
 // A wgrad tile whose contraction does not end on a multiple of 16 rows: its last stage is
@@ -219,7 +273,43 @@ __device__ __forceinline__ void lin_decode(const LinearArgs& a, const int* row0,
 template <int MODE>
 __device__ __forceinline__ bool lin_tail(const LinTile& tl) { return MODE == LIN_WGRAD && (tl.c_cnt & 15) != 0; }
 
-template <int MODE, bool ATOMS>
+// A warp's 32 m x 64 columns of a piece of a tile: written to the workspace, unless this is the
+// last of the tile's pieces to arrive here; then r becomes the sum of all of them, in the order of
+// the contraction, and the caller stores it (true).  tn = 64: only the warps of column group 0
+// have columns.
+__device__ __forceinline__ bool join_pieces(const LinearArgs& a, const LinTile& tl, int rest, int quarter, int cg, int cols,
+                                            int lane, uint32_t* r) {
+  if (cg != 0) return false;
+  const auto slot = [&](int part) {              // piece `part` of cut tile c is pair part * rest + c's
+    return a.pieces + (int64_t(part * rest + tl.cut) * 8 + quarter) * LG_PIECE + lane;
+  };
+  float* mine = slot(tl.part);
+#pragma unroll
+  for (int c = 0; c < 64; ++c)
+    if (c < cols) __stcg(mine + c * 32, __uint_as_float(r[c]));
+  __threadfence();
+  __syncwarp();
+  unsigned* arrived = a.arrived + tl.cut * 8 + quarter;
+  unsigned before = 0;
+  if (lane == 0) before = atomicAdd(arrived, 1u);
+  before = __shfl_sync(0xFFFFFFFFu, before, 0);
+  if (before + 1 != unsigned(tl.parts)) return false;
+  __threadfence();
+  if (lane == 0) *arrived = 0;                   // for the next call
+  const float* first = slot(0);
+#pragma unroll
+  for (int c = 0; c < 64; ++c)
+    if (c < cols) r[c] = __float_as_uint(__ldcg(first + c * 32));
+  for (int p = 1; p < tl.parts; ++p) {
+    const float* s = slot(p);
+#pragma unroll
+    for (int c = 0; c < 64; ++c)
+      if (c < cols) r[c] = __float_as_uint(__uint_as_float(r[c]) + __ldcg(s + c * 32));
+  }
+  return true;
+}
+
+template <int MODE, bool ATOMS, bool CUT>
 __global__ void __launch_bounds__(LG_THREADS, 1)
     grouped_linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                           const __grid_constant__ CUtensorMap tmBs, const LinearArgs args) {
@@ -339,6 +429,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
   const uint32_t tmem = *tmem_base_s;
   // inconsistent split_sizes: nothing is computed (the error word says so)
   const int total = *bad_s ? 0 : lin_tiles<MODE>(args, tile0);
+  const Plan plan = lin_plan<MODE, CUT>(args, total, num_pairs);
 
   if (warp == 0 || warp == 19) {
     if (lane == 0) {
@@ -347,9 +438,8 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
       const uint32_t full_c0 = mapa_shared(smem_u32(full), 0);
       Cursor cur;
       bool ok = true;
-      for (int t = pair; t < total && ok; t += num_pairs) {
-        LinTile tl;
-        lin_decode<MODE>(args, row0, tile0, order, t, tl);
+      int next = pair;
+      for (LinTile tl; ok && lin_next<MODE, CUT>(args, row0, tile0, order, plan, pair, num_pairs, next, tl);) {
         const int half = tl.n >> 1;
         const int m = tl.m0 + int(rank) * 128;
         const int nr = tl.n0 + int(rank) * half;
@@ -375,7 +465,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
           }
           uint8_t* pa = smem + cur.st * stage_bytes;
           uint8_t* pb = pa + LG_TILE;
-          const int c = tl.c0 + kt * LG_KT;
+          const int c = tl.c0 + (tl.k0 + kt) * LG_KT;
           if (m_side) {
             if (MODE == LIN_FWD) {
               tma_load_3d(pa, &tmA, c, m, tl.e, bar_c);
@@ -439,15 +529,14 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
       int ac = 0;                                // accumulators used so far
       uint32_t cleared_par = 0;                  // bit s: parity of the next tail phase of stage s
       bool ok = true, issued = false, ready = false;
-      for (int t = pair; t < total && ok; t += num_pairs) {
-        LinTile tl;
-        lin_decode<MODE>(args, row0, tile0, order, t, tl);
+      int next = pair;
+      for (LinTile tl; ok && lin_next<MODE, CUT>(args, row0, tile0, order, plan, pair, num_pairs, next, tl);) {
         const int accs = tl.accs();
         const int b0 = ac & 1, b1 = (ac + 1) & 1;
         const uint32_t acc0 = tmem + uint32_t(b0 * LG_ACC), acc1 = tmem + uint32_t(b1 * LG_ACC);
         const uint32_t id0 = lg_idesc(A_MN, B_MN, tl.cols(0)), id1 = lg_idesc(A_MN, B_MN, tl.cols(1));
         const uint32_t par1 = (((ac + 1) >> 1) & 1) ^ 1;
-        const int last_groups = (tl.c_cnt - (tl.steps - 1) * LG_KT + 15) / 16;
+        const int last_groups = min(LG_KT, tl.c_cnt - (tl.k0 + tl.steps - 1) * LG_KT) + 15 >> 4;
         if (!wait_phase(&tmem_empty[b0], ((ac >> 1) & 1) ^ 1, abort_s, args.err, SITE_LINEAR + 1, kWaitLimitNs)) {
           ok = false;
           break;
@@ -519,9 +608,8 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
     uint32_t* tr = reinterpret_cast<uint32_t*>(smem + LG_OFF_TR + (warp - 2) * LG_TR_WARP);
     int ac = 0;
     bool ok = true;
-    for (int t = pair; t < total && ok; t += num_pairs) {
-      LinTile tl;
-      lin_decode<MODE>(args, row0, tile0, order, t, tl);
+    int next = pair;
+    for (LinTile tl; ok && lin_next<MODE, CUT>(args, row0, tile0, order, plan, pair, num_pairs, next, tl);) {
       const int accs = tl.accs();
       for (int h = 0; h < accs; ++h, ++ac) {
         const int ab = ac & 1;
@@ -543,6 +631,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         // Lane l holds m = l of 64 columns.  Through shared memory, 16 columns at a time, a lane
         // gets eight m of two columns, p and p + 1: 16-byte stores, 64 bytes per column and warp.
         const int p = lane >> 2, m = tl.m0 + int(rank) * 128 + q * 32 + (lane & 3) * 8;
+        if (CUT && tl.parts > 1 && !join_pieces(args, tl, plan.rest, int(rank) * 4 + q, cg, cols, lane, r)) continue;
         __nv_bfloat16* o = args.out + ((MODE == LIN_WGRAD ? int64_t(tl.e) * args.N : 0) + tl.n0 + 2 * p) * args.ldo + m;
         const bool zero = tl.steps == 0;         // wgrad of an expert without rows
 #pragma unroll
@@ -578,9 +667,8 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
     uint32_t par = 0;                            // bit s: parity of the next tail phase of stage s
     int at = 0;                                  // stages used so far
     bool ok = true;
-    for (int t = pair; t < total && ok; t += num_pairs) {
-      LinTile tl;
-      lin_decode<MODE>(args, row0, tile0, order, t, tl);
+    int next = pair;
+    for (LinTile tl; ok && lin_next<MODE, CUT>(args, row0, tile0, order, plan, pair, num_pairs, next, tl);) {
       at += tl.steps;
       if (!lin_tail<MODE>(tl)) continue;
       // (a barrier is waited on in every one of its phases or not at all: skipping phases, this
@@ -634,7 +722,7 @@ bool lin_map(CUtensorMap* m, bool atoms, const void* base, int64_t inner, int64_
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, bool ATOMS>
+template <int MODE, bool ATOMS, bool CUT>
 cudaError_t lin_launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mbs, const LinearArgs& a,
                        int grid, cudaStream_t st) {
   // the shared-memory attribute is per device: set it once on each device this process uses
@@ -644,7 +732,7 @@ cudaError_t lin_launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUten
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices || !attr_set[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(grouped_linear_kernel<MODE, ATOMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, LG_SMEM);
+    e = cudaFuncSetAttribute(grouped_linear_kernel<MODE, ATOMS, CUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, LG_SMEM);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices) attr_set[dev].store(true, std::memory_order_release);
   }
@@ -662,14 +750,19 @@ cudaError_t lin_launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUten
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, grouped_linear_kernel<MODE, ATOMS>, ma, mb, mbs, a);
+  return cudaLaunchKernelEx(&cfg, grouped_linear_kernel<MODE, ATOMS, CUT>, ma, mb, mbs, a);
 }
 
 }  // namespace
 
+size_t linear_ws_bytes() { return 256 + size_t(kLinearMaxPairs) * 8 * (sizeof(unsigned) + LG_PIECE * sizeof(float)); }
+
 cudaError_t launch_grouped_linear(int mode, const LinearArgs& args, const void* x, int64_t ldx, const void* dy,
                                   int64_t lddy, const void* w, cudaStream_t st, char* msg, size_t msg_len) {
   LinearArgs a = args;
+  // the workspace: error word, arrival counts, pieces
+  a.arrived = reinterpret_cast<unsigned*>(reinterpret_cast<uint8_t*>(a.err) + 256);
+  a.pieces = reinterpret_cast<float*>(a.arrived + kLinearMaxPairs * 8);
   CUtensorMap ma, mb, mbs;
   bool ok;
   const bool at = a.K % 64 == 0 && (mode == LIN_DGRAD || a.N % 64 == 0);   // rows of the MN-major operands
@@ -699,17 +792,26 @@ cudaError_t launch_grouped_linear(int mode, const LinearArgs& args, const void* 
   const int64_t mt = ((mode == LIN_FWD ? a.N : a.K) + LG_M - 1) / LG_M;
   const int64_t wide = mode == LIN_WGRAD ? int64_t(a.E) * ((a.N + 511) / 512) : a.rows / 512;
   a.tn = mode != LIN_WGRAD && (a.rows <= 64 || a.rows <= int64_t(32) * a.E) ? 64 : mt * wide >= 4 * pairs ? 512 : 256;
-  // no more pairs than tiles there can be
   const int64_t nt = mode == LIN_WGRAD ? int64_t(a.E) * ((a.N + a.tn - 1) / a.tn)
                                        : (a.rows < a.E ? a.rows : a.E) + a.rows / a.tn;
-  const int grid = 2 * int(mt * nt < pairs ? mt * nt : pairs);
-  switch (mode * 2 + int(at)) {
-    case LIN_FWD * 2:
-    case LIN_FWD * 2 + 1: return lin_launch<LIN_FWD, false>(ma, mb, mbs, a, grid, st);   // both K-major
-    case LIN_DGRAD * 2: return lin_launch<LIN_DGRAD, false>(ma, mb, mbs, a, grid, st);
-    case LIN_DGRAD * 2 + 1: return lin_launch<LIN_DGRAD, true>(ma, mb, mbs, a, grid, st);
-    case LIN_WGRAD * 2: return lin_launch<LIN_WGRAD, false>(ma, mb, mbs, a, grid, st);
-    default: return lin_launch<LIN_WGRAD, true>(ma, mb, mbs, a, grid, st);
+  // Tiles are cut where at most half the pairs have one, or where there is a second round at most
+  // (16 rows, K = 14336, N = 4096: 165 -> 143 us; 2 rows, N = 14336, K = 4096 back: 79 -> 57 us).  One
+  // round of more than half the pairs cannot be cut, and the plain kernel is 2 us faster there.
+  const int64_t tiles = mt * nt;
+  const bool cut = a.tn == 64 && pairs <= kLinearMaxPairs && (2 * tiles <= pairs || (tiles > pairs && tiles <= 2 * pairs));
+  // else no more pairs than tiles there can be
+  const int grid = 2 * int(tiles < pairs && !cut ? tiles : pairs);
+  switch (mode * 4 + int(at) * 2 + int(cut)) {
+    case LIN_FWD * 4:
+    case LIN_FWD * 4 + 2: return lin_launch<LIN_FWD, false, false>(ma, mb, mbs, a, grid, st);   // both K-major
+    case LIN_FWD * 4 + 1:
+    case LIN_FWD * 4 + 3: return lin_launch<LIN_FWD, false, true>(ma, mb, mbs, a, grid, st);
+    case LIN_DGRAD * 4: return lin_launch<LIN_DGRAD, false, false>(ma, mb, mbs, a, grid, st);
+    case LIN_DGRAD * 4 + 1: return lin_launch<LIN_DGRAD, false, true>(ma, mb, mbs, a, grid, st);
+    case LIN_DGRAD * 4 + 2: return lin_launch<LIN_DGRAD, true, false>(ma, mb, mbs, a, grid, st);
+    case LIN_DGRAD * 4 + 3: return lin_launch<LIN_DGRAD, true, true>(ma, mb, mbs, a, grid, st);
+    case LIN_WGRAD * 4: return lin_launch<LIN_WGRAD, false, false>(ma, mb, mbs, a, grid, st);
+    default: return lin_launch<LIN_WGRAD, true, false>(ma, mb, mbs, a, grid, st);
   }
 }
 

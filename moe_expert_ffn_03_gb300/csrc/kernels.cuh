@@ -227,8 +227,12 @@ struct LinearArgs {
   __nv_bfloat16* out;        // FWD y [rows][N], DGRAD dx [rows][K], WGRAD dw [E][N][K]
   int64_t ldo;
   int* err;
-  int tn;                    // columns of a tile: 64, 256 or 512 (set by launch_grouped_linear)
+  int tn;                    // set by launch_grouped_linear: columns of a tile (64, 256 or 512) and,
+  unsigned* arrived;         // of the workspace, the arrivals and partial sums of cut tiles
+  float* pieces;
 };
+constexpr int kLinearMaxPairs = 76;               // CTA pairs (two SMs each) that cut tiles
+size_t linear_ws_bytes();
 cudaError_t launch_grouped_linear(int mode, const LinearArgs& a, const void* x, int64_t ldx, const void* dy,
                                   int64_t lddy, const void* w, cudaStream_t st, char* msg, size_t msg_len);
 

@@ -105,6 +105,23 @@ def test_many_tiles_per_pair():
     check([33, 1, 70, 5, 129, 18, 0, 3, 250, 45, 7, 66], 1032, 1544, seed=3)
 
 
+@pytest.mark.parametrize("split,K,N", [([5, 0, 3], 2056, 264), ([1], 8192, 8), ([2, 1], 264, 4104), ([64], 1000, 1000),
+                                       ([1, 0, 0, 1], 520, 520), ([30, 2] * 16, 328, 1040)])
+def test_tiles_cut_along_the_contraction(split, K, N):
+    """Few rows: the steps of all tiles are shared out evenly, tiles cut where the shares end.  The
+    second call on the same workspace finds the arrival counts as the first did."""
+    x, dy, w, ss = tensors(split, K, N, sum(split), K, True)
+    d = B.grouped(sum(split), K, N, len(split))
+    ws = torch.zeros(B.moe_grouped_linear_workspace_size(d), dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        y = torch.full((sum(split), N), 77.0, dtype=torch.bfloat16, device="cuda")
+        dx = torch.full((sum(split), K), 77.0, dtype=torch.bfloat16, device="cuda")
+        B.moe_grouped_linear_fwd(d, x, ss, w, y, ws)
+        B.moe_grouped_linear_dgrad(d, dy, ss, w, dx, ws)
+        assert np.array_equal(f64(y), bl.grouped_linear(f64(x), f64(w), split))
+        assert np.array_equal(f64(dx), bl.grouped_linear_dgrad(f64(dy), f64(w), split))
+
+
 def test_rows_past_the_sum_and_pitches():
     check([40, 0, 9], 88, 104, rows=300, seed=4, pad=24)
 
