@@ -16,109 +16,159 @@ namespace {
 
 constexpr int ROW_BLOCK = 256;
 
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
-
+// 1 / (1 + e^-g): the exponential and the reciprocal are the approximate instructions (about
+// 1 + 1.2 |g| and 1 units in the last place); e^-g = Inf gives 0.
 template <int VEC>
+__device__ __forceinline__ void v_sigmoid(float* s, const float* g) {
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s[j]) : "f"(1.f + __expf(-g[j])));
+}
+template <int VEC>
+__device__ __forceinline__ void v_copy(float* a, const float* b) {
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) a[j] = b[j];
+}
+
+// A thread's place in a row that tpr threads walk: its row, whether there is one, its first column.
+struct RowPlace {
+  int64_t row;
+  int t;
+  __device__ __forceinline__ explicit RowPlace(int tpr)
+      : row(int64_t(blockIdx.x) * (ROW_BLOCK / tpr) + threadIdx.x / tpr), t(threadIdx.x & (tpr - 1)) {}
+};
+
+template <int VEC, bool KEEP>
 __global__ void __launch_bounds__(ROW_BLOCK) swiglu_fwd_kernel(const SwigluArgs a, int tpr) {
-  const int t = threadIdx.x & (tpr - 1);
-  const int64_t row = int64_t(blockIdx.x) * (ROW_BLOCK / tpr) + threadIdx.x / tpr;
-  const bool live = row < a.rows;
+  const RowPlace at(tpr);
   const int nb = (a.I + 31) >> 5;                 // checkpoint blocks of g (and of u)
   pdl_wait();
-  const __nv_bfloat16* gp = a.gu + row * a.ld_gu;
-  const float p = a.prob != nullptr && live ? a.prob[row] : 1.f;
-  for (int c0 = 0; c0 < a.I; c0 += tpr * VEC) {
-    const int col = c0 + t * VEC;
-    const bool in = live && col < a.I;
+  if (at.row >= a.rows) return;                   // whole warps
+  const int col0 = at.t * VEC, step = tpr * VEC;
+  const __nv_bfloat16* gp = a.gu + at.row * a.ld_gu + col0;
+  __nv_bfloat16* ap = a.a + at.row * a.ld_a + col0;
+  uint8_t* codes = a.codes + at.row * 2 * a.I + col0;
+  uint8_t* scales = a.scales + at.row * 2 * nb + (col0 >> 5);
+  float p[VEC];
+  v_fill<VEC>(p, a.prob != nullptr ? a.prob[at.row] : 1.f);
+  for (int left = a.I - col0, base = a.I; base > 0; base -= step, left -= step) {
+    const bool in = left > 0;                     // this thread's columns are inside the row
     Raw<__nv_bfloat16, VEC> rg, ru;
     rg.zero();
     ru.zero();
     if (in) {
-      rg.load(gp + col);
-      ru.load(gp + a.I + col);
+      rg.load(gp);
+      ru.load(gp + a.I);
     }
-    float g[VEC], u[VEC];
+    float g[VEC], u[VEC], s[VEC];
     rg.get(g);
     ru.get(u);
-    if (a.codes != nullptr) {
-      store_act8<VEC>(g, in, a.codes, a.scales, row, 2 * int64_t(a.I), 0, col, 2 * nb, 0);
-      store_act8<VEC>(u, in, a.codes, a.scales, row, 2 * int64_t(a.I), a.I, col, 2 * nb, nb);
+    if constexpr (KEEP) {
+      store_act8<VEC>(g, in, codes, scales, (col0 & 31) == 0);
+      store_act8<VEC>(u, in, codes + a.I, scales + nb, (col0 & 31) == 0);
     }
     if (in) {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) g[j] = g[j] * sigmoid(g[j]) * u[j] * p;
-      store_vec<VEC>(a.a + row * a.ld_a + col, g);
+      v_sigmoid<VEC>(s, g);
+      v_mul<VEC>(s, g);
+      v_mul<VEC>(s, u);
+      v_mul<VEC>(s, p);
+      store_vec<VEC>(ap, s);
     }
+    gp += step;
+    ap += step;
+    codes += step;
+    scales += step >> 5;
   }
 }
 
 template <int VEC, bool Q8>
 __global__ void __launch_bounds__(ROW_BLOCK) swiglu_bwd_kernel(const SwigluArgs a, int tpr) {
   __shared__ float sums[32];
-  const int t = threadIdx.x & (tpr - 1);
-  const int64_t row = int64_t(blockIdx.x) * (ROW_BLOCK / tpr) + threadIdx.x / tpr;
-  const bool live = row < a.rows;
+  const RowPlace at(tpr);
   const int nb = (a.I + 31) >> 5;
   pdl_wait();
-  const float p = a.prob != nullptr && live ? a.prob[row] : 1.f;
-  float dp[1] = {0.f};
-  if (live) {
-    for (int col = t * VEC; col < a.I; col += tpr * VEC) {
-      float g[VEC], u[VEC], da[VEC];
-      if constexpr (Q8) {
-        Act8<VEC> qg, qu;
-        qg.load(a.codes, a.scales, row, 2 * int64_t(a.I), 0, col, 2 * nb, 0);
-        qu.load(a.codes, a.scales, row, 2 * int64_t(a.I), a.I, col, 2 * nb, nb);
-        qg.get(g);
-        qu.get(u);
-      } else {
-        Raw<__nv_bfloat16, VEC> rg, ru;
-        rg.load(a.gu + row * a.ld_gu + col);
-        ru.load(a.gu + row * a.ld_gu + a.I + col);
-        rg.get(g);
-        ru.get(u);
-      }
-      Raw<__nv_bfloat16, VEC> r;
-      r.load(a.da + row * a.ld_da + col);
-      r.get(da);
-      float du[VEC];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float s = sigmoid(g[j]);
-        const float silu = g[j] * s;
-        const float dap = da[j] * p;
-        dp[0] += da[j] * (silu * u[j]);
-        du[j] = dap * silu;
-        da[j] = silu * u[j] * p;                       // a
-        g[j] = dap * u[j] * (s * (1.f + g[j] * (1.f - s)));
-      }
-      __nv_bfloat16* o = a.dgu + row * a.ld_dgu + col;
-      store_vec<VEC>(o, g);
-      store_vec<VEC>(o + a.I, du);
-      if (a.a != nullptr) store_vec<VEC>(a.a + row * a.ld_a + col, da);
+  if (at.row >= a.rows) return;                   // whole rows: row_sum's barriers are a row's own
+  const int col0 = at.t * VEC, step = tpr * VEC;
+  const __nv_bfloat16* gp = a.gu + at.row * a.ld_gu + col0;
+  const __nv_bfloat16* dp_ = a.da + at.row * a.ld_da + col0;
+  const uint8_t* codes = a.codes + at.row * 2 * a.I + col0;
+  const uint8_t* scales = a.scales + at.row * 2 * nb + (col0 >> 5);
+  __nv_bfloat16* o = a.dgu + at.row * a.ld_dgu + col0;
+  __nv_bfloat16* ap = a.a + at.row * a.ld_a + col0;
+  float p[VEC], dp[VEC];
+  v_fill<VEC>(p, a.prob != nullptr ? a.prob[at.row] : 1.f);
+  v_fill<VEC>(dp, 0.f);
+  for (int left = a.I - col0; left > 0; left -= step) {
+    float g[VEC], u[VEC], d[VEC], s[VEC], w[VEC];
+    Raw<__nv_bfloat16, VEC> r;
+    r.load(dp_);
+    if constexpr (Q8) {
+      Act8<VEC> qg, qu;
+      qg.take(codes);
+      qu.take(codes + a.I);
+      qg.c = scales[0];
+      qu.c = scales[nb];
+      qg.get(g);
+      qu.get(u);
+    } else {
+      Raw<__nv_bfloat16, VEC> rg, ru;
+      rg.load(gp);
+      ru.load(gp + a.I);
+      rg.get(g);
+      ru.get(u);
     }
+    r.get(d);
+    v_sigmoid<VEC>(s, g);
+    v_mul<VEC>(g, s);                              // silu(g) = g s
+    v_fill<VEC>(w, 1.f);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) w[j] -= s[j];
+    v_fma<VEC>(s, g, w);                           // silu'(g) = s + g s (1 - s)
+    v_copy<VEC>(w, g);
+    v_mul<VEC>(w, u);                              // silu(g) u
+    v_fma<VEC>(dp, d, w);
+    v_mul<VEC>(w, p);                              // a
+    v_mul<VEC>(d, p);
+    v_mul<VEC>(s, u);
+    v_mul<VEC>(s, d);                              // dg
+    v_mul<VEC>(g, d);                              // du
+    store_vec<VEC>(o, s);
+    store_vec<VEC>(o + a.I, g);
+    if (a.a != nullptr) store_vec<VEC>(ap, w);
+    gp += step;
+    dp_ += step;
+    codes += step;
+    scales += step >> 5;
+    o += step;
+    ap += step;
   }
   if (a.dprob == nullptr) return;
-  row_sum<1>(dp, tpr, int(threadIdx.x / tpr), sums);
-  if (live && t == 0) a.dprob[row] = dp[0];
+  float sum[1] = {0.f};
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) sum[0] += dp[j];
+  row_sum<1>(sum, tpr, int(threadIdx.x / tpr), sums);
+  if (at.t == 0) a.dprob[at.row] = sum[0];
 }
 
 template <typename T, int VEC>
 __global__ void __launch_bounds__(ROW_BLOCK) act8_pack_kernel(const T* __restrict__ src, int64_t rows, int cols,
                                                               int64_t ld, uint8_t* codes, uint8_t* scales, int tpr) {
-  const int t = threadIdx.x & (tpr - 1);
-  const int64_t row = int64_t(blockIdx.x) * (ROW_BLOCK / tpr) + threadIdx.x / tpr;
-  const bool live = row < rows;
+  const RowPlace at(tpr);
   pdl_wait();
-  for (int c0 = 0; c0 < cols; c0 += tpr * VEC) {
-    const int col = c0 + t * VEC;
-    const bool in = live && col < cols;
+  if (at.row >= rows) return;                     // whole warps
+  const int col0 = at.t * VEC, step = tpr * VEC;
+  src += at.row * ld + col0;
+  codes += at.row * cols + col0;
+  scales += at.row * ((cols + 31) >> 5) + (col0 >> 5);
+  for (int left = cols - col0, base = cols; base > 0; base -= step, left -= step) {
     Raw<T, VEC> r;
     r.zero();
-    if (in) r.load(src + row * ld + col);
+    if (left > 0) r.load(src);
     float v[VEC];
     r.get(v);
-    store_act8<VEC>(v, in, codes, scales, row, cols, 0, col, (cols + 31) >> 5, 0);
+    store_act8<VEC>(v, left > 0, codes, scales, (col0 & 31) == 0);
+    src += step;
+    codes += step;
+    scales += step >> 5;
   }
 }
 
@@ -129,25 +179,32 @@ __global__ void __launch_bounds__(ROW_BLOCK) act8_unpack_kernel(const uint8_t* _
                                                                 const uint8_t* __restrict__ scales, int64_t rows,
                                                                 int cols, const void* gamma, const void* beta,
                                                                 bool w_f32, T* dst, int64_t ld, int tpr) {
-  const int t = threadIdx.x & (tpr - 1);
-  const int64_t row = int64_t(blockIdx.x) * (ROW_BLOCK / tpr) + threadIdx.x / tpr;
+  const RowPlace at(tpr);
   pdl_wait();
-  if (row >= rows) return;
-  for (int col = t * VEC; col < cols; col += tpr * VEC) {
+  if (at.row >= rows) return;
+  const int col0 = at.t * VEC, step = tpr * VEC;
+  codes += at.row * cols + col0;
+  scales += at.row * ((cols + 31) >> 5) + (col0 >> 5);
+  dst += at.row * ld + col0;
+  for (int col = col0; col < cols; col += step) {
     Act8<VEC> q;
-    q.load(codes, scales, row, cols, 0, col, (cols + 31) >> 5, 0);
+    q.take(codes);
+    q.c = *scales;
     float v[VEC];
     q.get(v);
     if (gamma != nullptr) {
       float g[VEC], b[VEC];
       load_weight<VEC>(gamma, w_f32, col, g);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) b[j] = 0.f;
+      v_fill<VEC>(b, 0.f);
       if (beta != nullptr) load_weight<VEC>(beta, w_f32, col, b);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) v[j] = v[j] * g[j] + b[j];
+      v_fma<VEC>(b, v, g);
+      store_vec<VEC>(dst, b);
+    } else {
+      store_vec<VEC>(dst, v);
     }
-    store_vec<VEC>(dst + row * ld + col, v);
+    codes += step;
+    scales += step >> 5;
+    dst += step;
   }
 }
 
@@ -192,8 +249,12 @@ cudaError_t launch_swiglu_fwd(const SwigluArgs& a, cudaStream_t st) {
   const bool vec = a.I % 8 == 0 && a.ld_gu % 8 == 0 && a.ld_a % 8 == 0;
   const int tpr = threads_per_row(a.rows, a.I, vec ? 8 : 1);
   const dim3 grid = row_grid(a.rows, tpr);
-  if (vec) return launch_pdl(swiglu_fwd_kernel<8>, grid, dim3(ROW_BLOCK), 0, st, a, tpr);
-  return launch_pdl(swiglu_fwd_kernel<1>, grid, dim3(ROW_BLOCK), 0, st, a, tpr);
+  if (a.codes != nullptr) {
+    if (vec) return launch_pdl(swiglu_fwd_kernel<8, true>, grid, dim3(ROW_BLOCK), 0, st, a, tpr);
+    return launch_pdl(swiglu_fwd_kernel<1, true>, grid, dim3(ROW_BLOCK), 0, st, a, tpr);
+  }
+  if (vec) return launch_pdl(swiglu_fwd_kernel<8, false>, grid, dim3(ROW_BLOCK), 0, st, a, tpr);
+  return launch_pdl(swiglu_fwd_kernel<1, false>, grid, dim3(ROW_BLOCK), 0, st, a, tpr);
 }
 
 cudaError_t launch_swiglu_bwd(const SwigluArgs& a, cudaStream_t st) {

@@ -161,6 +161,8 @@ __global__ void __launch_bounds__(MAX_TPR, 1) norm_fwd_kernel(const NormArgs a, 
       if (a.rstd != nullptr) a.rstd[row] = rstd;
     }
     T* y = static_cast<T*>(a.y) + row * a.ld_out + at.col0;
+    uint8_t* codes = a.codes + row * a.H + at.col0;
+    uint8_t* scales = a.scales + row * ((a.H + 31) >> 5) + (at.col0 >> 5);
     float rs[VEC];
     v_fill<VEC>(rs, rstd);
 #pragma unroll
@@ -168,7 +170,7 @@ __global__ void __launch_bounds__(MAX_TPR, 1) norm_fwd_kernel(const NormArgs a, 
       const bool in = at.col(i) < a.H;
       v_mul<VEC>(h[i], rs);
       if (a.codes != nullptr)
-        store_act8<VEC>(h[i], in, a.codes, a.scales, row, a.H, 0, at.col(i), (a.H + 31) >> 5, 0);
+        store_act8<VEC>(h[i], in, codes + i * (32 * VEC), scales + i * VEC, (at.col0 & 31) == 0);
       if (in) {
         float g[VEC], b[VEC];
         gamma.get(i, g);

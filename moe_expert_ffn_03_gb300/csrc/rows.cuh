@@ -241,11 +241,11 @@ __device__ __forceinline__ void row_sum(float* v, int tpr, int group, float* buf
 // scale codes [rows][ceil(cols/32)] row-major (these tensors feed no MMA, so the scales need
 // no tile layout).
 //
-// Quantizes this thread's VEC values of its block (all lanes of the warp call it; lanes past
-// the row's end bring zeros) and stores codes and scale when `in` is set.
+// Quantizes this thread's VEC values of its block (all lanes of the warp call it; lanes past the
+// row's end bring zeros) and, when `in` is set, stores the codes at `codes` and, from the block's
+// first lane (`first`), the scale code at `scale`.
 template <int VEC>
-__device__ __forceinline__ void store_act8(const float* v, bool in, uint8_t* codes, uint8_t* scales, int64_t row,
-                                           int64_t ld_codes, int64_t col0, int col, int64_t ld_scales, int blk0) {
+__device__ __forceinline__ void store_act8(const float* v, bool in, uint8_t* codes, uint8_t* scale, bool first) {
   uint32_t amax = v_amax<VEC>(v);
   if constexpr (VEC == 1) {
     amax = __reduce_max_sync(0xFFFFFFFFu, amax);
@@ -256,9 +256,8 @@ __device__ __forceinline__ void store_act8(const float* v, bool in, uint8_t* cod
   if (!in) return;
   const uint32_t c = mx_scale_code(amax);
   const float m = c == 255u ? 0.f : mx_inv_scale(c);
-  uint8_t* pc = codes + row * ld_codes + col0 + col;
   if constexpr (VEC == 1) {
-    *pc = c == 255u ? 0x7Fu : uint8_t(cvt_e4m3x2(v[0] * m, 0.f));
+    *codes = c == 255u ? 0x7Fu : uint8_t(cvt_e4m3x2(v[0] * m, 0.f));
   } else {
     uint32_t q[VEC / 4];
 #pragma unroll
@@ -266,10 +265,10 @@ __device__ __forceinline__ void store_act8(const float* v, bool in, uint8_t* cod
       q[i] = cvt_e4m3x2(v[4 * i] * m, v[4 * i + 1] * m) | (cvt_e4m3x2(v[4 * i + 2] * m, v[4 * i + 3] * m) << 16);
       if (c == 255u) q[i] = 0x7F7F7F7Fu;
     }
-    if constexpr (VEC == 8) __stcs(reinterpret_cast<uint2*>(pc), make_uint2(q[0], q[1]));
-    else __stcs(reinterpret_cast<uint32_t*>(pc), q[0]);
+    if constexpr (VEC == 8) __stcs(reinterpret_cast<uint2*>(codes), make_uint2(q[0], q[1]));
+    else __stcs(reinterpret_cast<uint32_t*>(codes), q[0]);
   }
-  if ((col & 31) == 0) scales[row * ld_scales + blk0 + (col >> 5)] = uint8_t(c);
+  if (first) *scale = uint8_t(c);
 }
 
 // 2^(c - 127); c = 0 is 2^-127 (subnormal), c = 255 only meets NaN codes.
@@ -282,7 +281,7 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// This thread's VEC codes of a row (as stored by store_act8) and their scale code.
+// A thread's VEC codes (as stored by store_act8) and their block's scale code.
 template <int VEC>
 struct Act8 {
   uint32_t q[VEC == 8 ? 2 : 1];
@@ -298,23 +297,19 @@ struct Act8 {
       q[0] = *p;
     }
   }
-  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, int64_t row, int64_t ld_codes,
-                                       int64_t col0, int col, int64_t ld_scales, int blk0) {
-    take(codes + row * ld_codes + col0 + col);
-    c = scales[row * ld_scales + blk0 + (col >> 5)];
-  }
   __device__ __forceinline__ void get(float* v) const {
     const float s = act8_scale(c);
     if constexpr (VEC == 1) {
       v[0] = e4m3x2_to_float2(q[0]).x * s;
     } else {
+      const float2 s2 = make_float2(s, s);
 #pragma unroll
       for (int i = 0; i < VEC / 4; ++i) {
-        const float2 a = e4m3x2_to_float2(q[i]), b = e4m3x2_to_float2(q[i] >> 16);
-        v[4 * i] = a.x * s;
-        v[4 * i + 1] = a.y * s;
-        v[4 * i + 2] = b.x * s;
-        v[4 * i + 3] = b.y * s;
+        const float2 a = __fmul2_rn(e4m3x2_to_float2(q[i]), s2), b = __fmul2_rn(e4m3x2_to_float2(q[i] >> 16), s2);
+        v[4 * i] = a.x;
+        v[4 * i + 1] = a.y;
+        v[4 * i + 2] = b.x;
+        v[4 * i + 3] = b.y;
       }
     }
   }
