@@ -15,6 +15,13 @@ namespace moe {
 namespace {
 
 constexpr int ROW_BLOCK = 256;
+// Vectors of a thread that are loaded before the first is worked on: with one, the loads of a row's
+// next vector wait for the stores of the last (forward 371 -> 340 us at 196608 x 1408, unpack
+// 31 -> 23 us at 8192 x 5632).  The backward pass on wide vectors, with three streams to write and
+// 16 more registers a vector, is faster with one (480 us; 518 with two).
+constexpr int unroll_fwd(int vec) { return vec == 1 ? 4 : 2; }
+constexpr int unroll_bwd(int vec) { return vec == 1 ? 4 : 1; }
+constexpr int unroll_act8(int) { return 4; }
 
 // 1 / (1 + e^-g): the exponential and the reciprocal are the approximate instructions (about
 // 1 + 1.2 |g| and 1 units in the last place); e^-g = Inf gives 0.
@@ -39,6 +46,7 @@ struct RowPlace {
 
 template <int VEC, bool KEEP>
 __global__ void __launch_bounds__(ROW_BLOCK) swiglu_fwd_kernel(const SwigluArgs a, int tpr) {
+  constexpr int U = unroll_fwd(VEC);
   const RowPlace at(tpr);
   const int nb = (a.I + 31) >> 5;                 // checkpoint blocks of g (and of u)
   pdl_wait();
@@ -50,38 +58,46 @@ __global__ void __launch_bounds__(ROW_BLOCK) swiglu_fwd_kernel(const SwigluArgs 
   uint8_t* scales = a.scales + at.row * 2 * nb + (col0 >> 5);
   float p[VEC];
   v_fill<VEC>(p, a.prob != nullptr ? a.prob[at.row] : 1.f);
-  for (int left = a.I - col0, base = a.I; base > 0; base -= step, left -= step) {
-    const bool in = left > 0;                     // this thread's columns are inside the row
-    Raw<__nv_bfloat16, VEC> rg, ru;
-    rg.zero();
-    ru.zero();
-    if (in) {
-      rg.load(gp);
-      ru.load(gp + a.I);
+  for (int left = a.I - col0, base = a.I; base > 0; base -= U * step, left -= U * step) {
+    Raw<__nv_bfloat16, VEC> rg[U], ru[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      rg[k].zero();
+      ru[k].zero();
+      if (left > k * step) {                      // this thread's columns are inside the row
+        rg[k].load(gp + k * step);
+        ru[k].load(gp + k * step + a.I);
+      }
     }
-    float g[VEC], u[VEC], s[VEC];
-    rg.get(g);
-    ru.get(u);
-    if constexpr (KEEP) {
-      store_act8<VEC>(g, in, codes, scales, (col0 & 31) == 0);
-      store_act8<VEC>(u, in, codes + a.I, scales + nb, (col0 & 31) == 0);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (base <= k * step) break;                // whole rows' threads
+      const bool in = left > k * step;
+      float g[VEC], u[VEC], s[VEC];
+      rg[k].get(g);
+      ru[k].get(u);
+      if constexpr (KEEP) {
+        store_act8<VEC>(g, in, codes + k * step, scales + k * (step >> 5), (col0 & 31) == 0);
+        store_act8<VEC>(u, in, codes + k * step + a.I, scales + k * (step >> 5) + nb, (col0 & 31) == 0);
+      }
+      if (in) {
+        v_sigmoid<VEC>(s, g);
+        v_mul<VEC>(s, g);
+        v_mul<VEC>(s, u);
+        v_mul<VEC>(s, p);
+        store_vec<VEC>(ap + k * step, s);
+      }
     }
-    if (in) {
-      v_sigmoid<VEC>(s, g);
-      v_mul<VEC>(s, g);
-      v_mul<VEC>(s, u);
-      v_mul<VEC>(s, p);
-      store_vec<VEC>(ap, s);
-    }
-    gp += step;
-    ap += step;
-    codes += step;
-    scales += step >> 5;
+    gp += U * step;
+    ap += U * step;
+    codes += U * step;
+    scales += U * (step >> 5);
   }
 }
 
 template <int VEC, bool Q8>
 __global__ void __launch_bounds__(ROW_BLOCK) swiglu_bwd_kernel(const SwigluArgs a, int tpr) {
+  constexpr int U = unroll_bwd(VEC);
   __shared__ float sums[32];
   const RowPlace at(tpr);
   const int nb = (a.I + 31) >> 5;
@@ -97,49 +113,59 @@ __global__ void __launch_bounds__(ROW_BLOCK) swiglu_bwd_kernel(const SwigluArgs 
   float p[VEC], dp[VEC];
   v_fill<VEC>(p, a.prob != nullptr ? a.prob[at.row] : 1.f);
   v_fill<VEC>(dp, 0.f);
-  for (int left = a.I - col0; left > 0; left -= step) {
-    float g[VEC], u[VEC], d[VEC], s[VEC], w[VEC];
-    Raw<__nv_bfloat16, VEC> r;
-    r.load(dp_);
-    if constexpr (Q8) {
-      Act8<VEC> qg, qu;
-      qg.take(codes);
-      qu.take(codes + a.I);
-      qg.c = scales[0];
-      qu.c = scales[nb];
-      qg.get(g);
-      qu.get(u);
-    } else {
-      Raw<__nv_bfloat16, VEC> rg, ru;
-      rg.load(gp);
-      ru.load(gp + a.I);
-      rg.get(g);
-      ru.get(u);
-    }
-    r.get(d);
-    v_sigmoid<VEC>(s, g);
-    v_mul<VEC>(g, s);                              // silu(g) = g s
-    v_fill<VEC>(w, 1.f);
+  for (int left = a.I - col0; left > 0; left -= U * step) {
+    Raw<__nv_bfloat16, VEC> r[U], rg[U], ru[U];    // rg, ru or qg, qu
+    Act8<VEC> qg[U], qu[U];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) w[j] -= s[j];
-    v_fma<VEC>(s, g, w);                           // silu'(g) = s + g s (1 - s)
-    v_copy<VEC>(w, g);
-    v_mul<VEC>(w, u);                              // silu(g) u
-    v_fma<VEC>(dp, d, w);
-    v_mul<VEC>(w, p);                              // a
-    v_mul<VEC>(d, p);
-    v_mul<VEC>(s, u);
-    v_mul<VEC>(s, d);                              // dg
-    v_mul<VEC>(g, d);                              // du
-    store_vec<VEC>(o, s);
-    store_vec<VEC>(o + a.I, g);
-    if (a.a != nullptr) store_vec<VEC>(ap, w);
-    gp += step;
-    dp_ += step;
-    codes += step;
-    scales += step >> 5;
-    o += step;
-    ap += step;
+    for (int k = 0; k < U; ++k) {
+      if (left <= k * step) break;
+      r[k].load(dp_ + k * step);
+      if constexpr (Q8) {
+        qg[k].take(codes + k * step);
+        qu[k].take(codes + k * step + a.I);
+        qg[k].c = scales[k * (step >> 5)];
+        qu[k].c = scales[k * (step >> 5) + nb];
+      } else {
+        rg[k].load(gp + k * step);
+        ru[k].load(gp + k * step + a.I);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (left <= k * step) break;
+      float g[VEC], u[VEC], d[VEC], s[VEC], w[VEC];
+      if constexpr (Q8) {
+        qg[k].get(g);
+        qu[k].get(u);
+      } else {
+        rg[k].get(g);
+        ru[k].get(u);
+      }
+      r[k].get(d);
+      v_sigmoid<VEC>(s, g);
+      v_mul<VEC>(g, s);                            // silu(g) = g s
+      v_fill<VEC>(w, 1.f);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) w[j] -= s[j];
+      v_fma<VEC>(s, g, w);                         // silu'(g) = s + g s (1 - s)
+      v_copy<VEC>(w, g);
+      v_mul<VEC>(w, u);                            // silu(g) u
+      v_fma<VEC>(dp, d, w);
+      v_mul<VEC>(w, p);                            // a
+      v_mul<VEC>(d, p);
+      v_mul<VEC>(s, u);
+      v_mul<VEC>(s, d);                            // dg
+      v_mul<VEC>(g, d);                            // du
+      store_vec<VEC>(o + k * step, s);
+      store_vec<VEC>(o + k * step + a.I, g);
+      if (a.a != nullptr) store_vec<VEC>(ap + k * step, w);
+    }
+    gp += U * step;
+    dp_ += U * step;
+    codes += U * step;
+    scales += U * (step >> 5);
+    o += U * step;
+    ap += U * step;
   }
   if (a.dprob == nullptr) return;
   float sum[1] = {0.f};
@@ -152,6 +178,7 @@ __global__ void __launch_bounds__(ROW_BLOCK) swiglu_bwd_kernel(const SwigluArgs 
 template <typename T, int VEC>
 __global__ void __launch_bounds__(ROW_BLOCK) act8_pack_kernel(const T* __restrict__ src, int64_t rows, int cols,
                                                               int64_t ld, uint8_t* codes, uint8_t* scales, int tpr) {
+  constexpr int U = unroll_act8(VEC);
   const RowPlace at(tpr);
   pdl_wait();
   if (at.row >= rows) return;                     // whole warps
@@ -159,16 +186,23 @@ __global__ void __launch_bounds__(ROW_BLOCK) act8_pack_kernel(const T* __restric
   src += at.row * ld + col0;
   codes += at.row * cols + col0;
   scales += at.row * ((cols + 31) >> 5) + (col0 >> 5);
-  for (int left = cols - col0, base = cols; base > 0; base -= step, left -= step) {
-    Raw<T, VEC> r;
-    r.zero();
-    if (left > 0) r.load(src);
-    float v[VEC];
-    r.get(v);
-    store_act8<VEC>(v, left > 0, codes, scales, (col0 & 31) == 0);
-    src += step;
-    codes += step;
-    scales += step >> 5;
+  for (int left = cols - col0, base = cols; base > 0; base -= U * step, left -= U * step) {
+    Raw<T, VEC> r[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      r[k].zero();
+      if (left > k * step) r[k].load(src + k * step);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (base <= k * step) break;                // whole rows' threads
+      float v[VEC];
+      r[k].get(v);
+      store_act8<VEC>(v, left > k * step, codes + k * step, scales + k * (step >> 5), (col0 & 31) == 0);
+    }
+    src += U * step;
+    codes += U * step;
+    scales += U * (step >> 5);
   }
 }
 
@@ -179,6 +213,7 @@ __global__ void __launch_bounds__(ROW_BLOCK) act8_unpack_kernel(const uint8_t* _
                                                                 const uint8_t* __restrict__ scales, int64_t rows,
                                                                 int cols, const void* gamma, const void* beta,
                                                                 bool w_f32, T* dst, int64_t ld, int tpr) {
+  constexpr int U = unroll_act8(VEC);
   const RowPlace at(tpr);
   pdl_wait();
   if (at.row >= rows) return;
@@ -186,33 +221,44 @@ __global__ void __launch_bounds__(ROW_BLOCK) act8_unpack_kernel(const uint8_t* _
   codes += at.row * cols + col0;
   scales += at.row * ((cols + 31) >> 5) + (col0 >> 5);
   dst += at.row * ld + col0;
-  for (int col = col0; col < cols; col += step) {
-    Act8<VEC> q;
-    q.take(codes);
-    q.c = *scales;
-    float v[VEC];
-    q.get(v);
-    if (gamma != nullptr) {
-      float g[VEC], b[VEC];
-      load_weight<VEC>(gamma, w_f32, col, g);
-      v_fill<VEC>(b, 0.f);
-      if (beta != nullptr) load_weight<VEC>(beta, w_f32, col, b);
-      v_fma<VEC>(b, v, g);
-      store_vec<VEC>(dst, b);
-    } else {
-      store_vec<VEC>(dst, v);
+  for (int col = col0; col < cols; col += U * step) {
+    Act8<VEC> q[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (col + k * step >= cols) break;
+      q[k].take(codes + k * step);
+      q[k].c = scales[k * (step >> 5)];
     }
-    codes += step;
-    scales += step >> 5;
-    dst += step;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (col + k * step >= cols) break;
+      float v[VEC];
+      q[k].get(v);
+      if (gamma != nullptr) {
+        float g[VEC], b[VEC];
+        load_weight<VEC>(gamma, w_f32, col + k * step, g);
+        v_fill<VEC>(b, 0.f);
+        if (beta != nullptr) load_weight<VEC>(beta, w_f32, col + k * step, b);
+        v_fma<VEC>(b, v, g);
+        v_copy<VEC>(v, b);
+      }
+      store_vec<VEC>(dst + k * step, v);
+    }
+    codes += U * step;
+    scales += U * (step >> 5);
+    dst += U * step;
   }
 }
 
 // Threads per row: a warp walks a row by itself when there are rows enough to fill the GPU
-// with warps; fewer rows are shared by up to a whole block.
-int threads_per_row(int64_t rows, int cols, int vec) {
+// with warps; fewer rows are shared by up to a whole block, and so are rows of at least `steps` = 4
+// steps a thread: long rows shared by a block touch fewer places of memory at once (gated activation of
+// 14336 columns, forward 593 -> 554 us; two steps a thread already cost 1408 columns 11%).
+int threads_per_row(int64_t rows, int cols, int vec, int steps = 1 << 20) {
   int tpr = 32;
-  while (tpr < ROW_BLOCK && tpr * vec < cols && rows * tpr < int64_t(152) * 2048) tpr *= 2;
+  while (tpr < ROW_BLOCK && tpr * vec < cols &&
+         (rows * tpr < int64_t(152) * 2048 || int64_t(tpr) * 2 * vec * steps <= cols))
+    tpr *= 2;
   return tpr;
 }
 dim3 row_grid(int64_t rows, int tpr) { return dim3(unsigned((rows + ROW_BLOCK / tpr - 1) / (ROW_BLOCK / tpr))); }
@@ -247,7 +293,7 @@ cudaError_t unpack_t(const uint8_t* codes, const uint8_t* scales, int64_t rows, 
 
 cudaError_t launch_swiglu_fwd(const SwigluArgs& a, cudaStream_t st) {
   const bool vec = a.I % 8 == 0 && a.ld_gu % 8 == 0 && a.ld_a % 8 == 0;
-  const int tpr = threads_per_row(a.rows, a.I, vec ? 8 : 1);
+  const int tpr = vec ? threads_per_row(a.rows, a.I, 8, 4) : threads_per_row(a.rows, a.I, 1);
   const dim3 grid = row_grid(a.rows, tpr);
   if (a.codes != nullptr) {
     if (vec) return launch_pdl(swiglu_fwd_kernel<8, true>, grid, dim3(ROW_BLOCK), 0, st, a, tpr);
@@ -261,7 +307,7 @@ cudaError_t launch_swiglu_bwd(const SwigluArgs& a, cudaStream_t st) {
   const bool q8 = a.codes != nullptr;
   const bool vec = a.I % 8 == 0 && (q8 || a.ld_gu % 8 == 0) && a.ld_da % 8 == 0 && a.ld_dgu % 8 == 0 &&
                    (a.a == nullptr || a.ld_a % 8 == 0);
-  const int tpr = threads_per_row(a.rows, a.I, vec ? 8 : 1);
+  const int tpr = vec ? threads_per_row(a.rows, a.I, 8, 4) : threads_per_row(a.rows, a.I, 1);
   const dim3 grid = row_grid(a.rows, tpr);
   if (vec) {
     if (q8) return launch_pdl(swiglu_bwd_kernel<8, true>, grid, dim3(ROW_BLOCK), 0, st, a, tpr);

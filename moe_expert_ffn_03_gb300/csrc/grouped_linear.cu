@@ -531,6 +531,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
       bool ok = true, issued = false, ready = false;
       int next = pair;
       for (LinTile tl; ok && lin_next<MODE, CUT>(args, row0, tile0, order, plan, pair, num_pairs, next, tl);) {
+        if (MODE == LIN_WGRAD && tl.steps == 0) continue;        // the epilogue writes zeros
         const int accs = tl.accs();
         const int b0 = ac & 1, b1 = (ac + 1) & 1;
         const uint32_t acc0 = tmem + uint32_t(b0 * LG_ACC), acc1 = tmem + uint32_t(b1 * LG_ACC);
@@ -581,12 +582,6 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
           tc_commit(&empty[st]);                 // frees the stage in both CTAs
         }
         if (!ok) break;
-        // a tile without steps (an empty expert's weight gradient) takes its accumulators all the same
-        if (accs == 2 && tl.steps == 0 &&
-            !wait_phase(&tmem_empty[b1], par1, abort_s, args.err, SITE_LINEAR + 1, kWaitLimitNs)) {
-          ok = false;
-          break;
-        }
         tc_commit(&tmem_full[b0]);
         if (accs == 2) tc_commit(&tmem_full[b1]);
         ac += accs;
@@ -610,6 +605,14 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
     bool ok = true;
     int next = pair;
     for (LinTile tl; ok && lin_next<MODE, CUT>(args, row0, tile0, order, plan, pair, num_pairs, next, tl);) {
+      if (MODE == LIN_WGRAD && tl.steps == 0) {
+        // the weight gradient of an expert without rows: zeros, 256 bytes of an output row per 16 lanes
+        const int m = tl.m0 + int(rank) * 128 + (lane & 15) * 8;
+        if (m < M)
+          for (int c = (warp - 2) * 2 + (lane >> 4); c < tl.cnt; c += 2 * LG_EPI_WARPS)
+            *reinterpret_cast<uint4*>(args.out + (int64_t(tl.e) * args.N + tl.n0 + c) * args.ldo + m) = make_uint4(0, 0, 0, 0);
+        continue;
+      }
       const int accs = tl.accs();
       for (int h = 0; h < accs; ++h, ++ac) {
         const int ab = ac & 1;
@@ -633,7 +636,6 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         const int p = lane >> 2, m = tl.m0 + int(rank) * 128 + q * 32 + (lane & 3) * 8;
         if (CUT && tl.parts > 1 && !join_pieces(args, tl, plan.rest, int(rank) * 4 + q, cg, cols, lane, r)) continue;
         __nv_bfloat16* o = args.out + ((MODE == LIN_WGRAD ? int64_t(tl.e) * args.N : 0) + tl.n0 + 2 * p) * args.ldo + m;
-        const bool zero = tl.steps == 0;         // wgrad of an expert without rows
 #pragma unroll
         for (int c0 = 0; c0 < 64; c0 += 16) {
           const int j = cg * 64 + c0;
@@ -643,7 +645,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint32_t w = pack_bf16x2(__uint_as_float(r[c0 + 2 * i]), __uint_as_float(r[c0 + 2 * i + 1]));
-            tr[i * LG_TR_PITCH + lane] = zero ? 0u : w;
+            tr[i * LG_TR_PITCH + lane] = w;
           }
           __syncwarp();
           const uint4* src = reinterpret_cast<const uint4*>(tr + p * LG_TR_PITCH + (lane & 3) * 8);

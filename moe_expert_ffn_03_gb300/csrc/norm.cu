@@ -18,9 +18,11 @@
 namespace moe {
 namespace {
 
-// A row has at most 512 threads, and an SM holds that many (the kernels take up to 128 registers):
-// what keeps the memory busy is the ring below, not the number of threads.
+// Wide rows have at most 512 threads, and an SM holds that many (the kernels take up to 128
+// registers): what keeps the memory busy is the ring below, not the number of threads.  Rows of
+// single columns have no ring but 1024 threads an SM.
 constexpr int MAX_TPR = 512;
+constexpr int max_block(int vec) { return vec == 1 ? 1024 : MAX_TPR; }
 // Rows a thread has on their way or in work at once (VEC > 1): up to three, as 512 threads' 16-byte
 // pieces fit in shared memory (`pieces` per thread and row).
 constexpr int ring_stages(int vec, int pieces) {
@@ -71,7 +73,7 @@ __device__ __forceinline__ float inv_sqrt(float v) {
 // residual) are on their way to shared memory while the current one is summed, so the two
 // sums of a row (mean, then the variance of the centred values) cost no memory time.
 template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(MAX_TPR, 1) norm_fwd_kernel(const NormArgs a, int tpr) {
+__global__ void __launch_bounds__(max_block(VEC), 1) norm_fwd_kernel(const NormArgs a, int tpr) {
   constexpr int STG = ring_stages(VEC, 2 * NV);
   __shared__ float sums[2][32];
   extern __shared__ __align__(16) uint8_t ring[];
@@ -188,7 +190,7 @@ __global__ void __launch_bounds__(MAX_TPR, 1) norm_fwd_kernel(const NormArgs a, 
 // pass over a row finds it in registers where a thread has up to 16 columns, and reads the ring
 // (single columns: memory) again where it has more.
 template <typename T, int VEC, int NV, bool Q8>
-__global__ void __launch_bounds__(MAX_TPR, 1) norm_bwd_kernel(const NormArgs a, int tpr, float* partial) {
+__global__ void __launch_bounds__(max_block(VEC), 1) norm_bwd_kernel(const NormArgs a, int tpr, float* partial) {
   constexpr int STG = ring_stages(VEC, 3 * NV);
   constexpr bool HOLD = VEC * NV <= 16;
   __shared__ float sums[2][64];
@@ -412,18 +414,22 @@ struct RowShape {
   int block;     // threads per block
 };
 
-// Threads and vectors per row.  Four vectors a thread: the sums over a row's threads and the
-// addresses cost as much as a vector or two of arithmetic, and the kernels are bound by the
-// instructions they issue as soon as a thread has only one (H = 1024: 297 instructions per vector
-// with one, measured).  Shorter rows take fewer vectors so that a warp is not left half empty,
-// longer ones more, up to 512 threads.
+// Threads and vectors per row.  Wide rows, four vectors a thread in the forward pass, two in the
+// backward (wide_nv): the sums over a row's threads and the addresses cost as much as a vector or
+// two of arithmetic, and the kernels are bound by the instructions they issue as soon as a thread
+// has only one (H = 1024: 297 instructions per vector with one, measured); with four, the
+// backward's sums of the weights' gradients do not fit the registers (144 us, 106 with two, at
+// T = 32768, H = 2048).  Shorter rows take fewer vectors so that a warp is not left half empty,
+// longer ones more, up to 512 threads.  Single columns: four a thread up to 1024 threads, so that
+// many threads' loads are in flight (H = 5001, backward: 800 us with 16 columns on 320 threads).
 RowShape row_shape(int H, int vec, int wide_nv) {
   const int n = (H + vec - 1) / vec;              // vectors of a row
-  int nv = vec > 1 ? wide_nv : 8;
+  const int most = max_block(vec);
+  int nv = vec > 1 ? wide_nv : 4;
   while (vec > 1 && nv > 1 && 32 * (nv / 2) >= n) nv /= 2;
-  while (nv * MAX_TPR < n) nv *= 2;
+  while (nv * most < n) nv *= 2;
   const int tpr = (n + 32 * nv - 1) / (32 * nv) * 32;
-  return RowShape{vec, nv, tpr, MAX_TPR / tpr * tpr};
+  return RowShape{vec, nv, tpr, tpr > MAX_TPR ? tpr : MAX_TPR / tpr * tpr};
 }
 
 // Sets a kernel's dynamic shared memory limit once per device, and says how many blocks of a
@@ -454,8 +460,8 @@ cudaError_t norm_fwd_shape(const NormArgs& a, const RowShape& s, cudaStream_t st
                     smem, st, a, s.tpr);
 }
 
-// Partial sums the backward may write: one block per SM.
-constexpr int kNormMaxParts = 152;
+// Partial sums the backward may write: two blocks per SM (single columns; wide rows: one).
+constexpr int kNormMaxParts = 304;
 
 template <typename T, int VEC, int NV, bool Q8>
 cudaError_t norm_bwd_shape(const NormArgs& a, const RowShape& s, float* partial, int* parts, cudaStream_t st) {
@@ -478,9 +484,9 @@ template <typename T, typename F>
 cudaError_t with_shape(const RowShape& s, F f) {
   constexpr int W = kWide<T>;
   if (s.vec == 1) {
+    if (s.nv == 4) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
     if (s.nv == 8) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{});
-    if (s.nv == 16) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 16>{});
-    return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 32>{});
+    return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 16>{});
   }
   if (s.nv == 1) return f(std::integral_constant<int, W>{}, std::integral_constant<int, 1>{});
   if (s.nv == 2) return f(std::integral_constant<int, W>{}, std::integral_constant<int, 2>{});

@@ -224,13 +224,13 @@ __device__ __forceinline__ void row_sum(float* v, int tpr, int group, float* buf
 #pragma unroll
       for (int n = 0; n < N; ++n) buf[warp * N + n] = v[n];
     asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
-    // every warp adds the row's partial sums (16 at most) in the same tree
+    // every warp adds the row's partial sums in the same tree
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       float s = lane < per ? buf[(first + lane) * N + n] : 0.f;
 #pragma unroll
-      for (int off = 8; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
-      v[n] = __shfl_sync(0xFFFFFFFFu, s, 0);
+      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+      v[n] = s;
     }
   }
 }
