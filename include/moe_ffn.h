@@ -563,7 +563,7 @@ moe_status moe_router_bwd(const moe_dims* d, const void* x, const void* w_r, con
  * and its scales are not tiled.
  */
 typedef struct moe_norm {
-  int64_t rows;         /* >= 0 */
+  int64_t rows;         /* 0..2^31-1 */
   int64_t ld_in;        /* row pitch of x, residual (forward) and of dy, x, dres (backward) */
   int64_t ld_out;       /* row pitch of h, y (forward) and of dx (backward) */
   int32_t H;            /* 1..16384 */
@@ -652,7 +652,10 @@ typedef struct moe_grouped {
 } moe_grouped;
 
 /* Bytes of workspace of the grouped linear calls (256-byte aligned, zero-filled once before
- * first use; its first 8 bytes are a device error word); 0 for invalid sizes.  Host only. */
+ * first use: a device error word, then arrival counts that every call leaves at zero and partial
+ * sums of tiles that calls with few rows cut along the contraction).  Later calls on the same
+ * stream may reuse it, for any sizes; calls running at the same time on other streams need their
+ * own.  0 for invalid sizes.  Host only. */
 size_t moe_grouped_linear_workspace_size(const moe_grouped* g);
 
 /*

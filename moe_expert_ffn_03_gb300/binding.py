@@ -148,16 +148,14 @@ def lib() -> ctypes.CDLL:
 
 
 def _p(t):
-    if t is None:
-        return None
-    return c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _st(stream):
     if stream is None:
         # the current stream's handle without a Stream object around it (2.9 us of a small call's 7.3)
-        return c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
-    return c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _check(status: int):
@@ -373,20 +371,41 @@ def fp8_tensor_quantize_experts(w_list, rows, cols, codes, amax, stream=None):
 
 
 # ---- operators around the layer ------------------------------------------------------------------
-# Row pitches and element types are read off the tensors; a tensor's last dimension must be dense.
-def _ld(t, cols):
-    """Row pitch of a 2-D tensor whose rows hold `cols` elements; 0 for None."""
+# Row pitches and element types are read off the tensors.  What the library cannot see -- types,
+# shapes, dense rows -- is checked here, since a mismatch would read past a tensor's end.
+_ROW_TYPES = (torch.bfloat16, torch.float32)
+
+
+def _ld(t, rows, cols, dtype=torch.bfloat16):
+    """Row pitch of a 2-D tensor of `dtype` with at least `rows` rows of `cols` values; 0 for None."""
     if t is None:
         return 0
-    if t.dim() != 2 or t.shape[1] < cols or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"expected [rows][>={cols}] with dense rows, got {tuple(t.shape)} strides {t.stride()}")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    shape, stride = t.shape, t.stride()
+    if t.dtype != dtype or len(shape) != 2 or shape[0] < rows or shape[1] < cols or (stride[1] != 1 and shape[1] > 1):
+        raise ValueError(f"expected {dtype} [>={rows}][>={cols}] with dense rows, got {t.dtype} {tuple(shape)} strides {stride}")
+    return stride[0] if shape[0] > 1 else max(stride[0], shape[1])
 
 
-def _typed(dtype, *tensors):
-    for t in tensors:
-        if t is not None and t.dtype != dtype:
-            raise TypeError(f"expected {dtype}, got {t.dtype}")
+def _dense(t, dtype, n):
+    """Pointer of a contiguous tensor of `dtype` with at least n values; None for None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"expected a contiguous {dtype} tensor of at least {n} values, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _pitched(t, rows, cols, ld, dtype):
+    """Pointer of a [rows][cols] tensor whose row pitch has to be ld; None for None."""
+    if t is None:
+        return None
+    if _ld(t, rows, cols, dtype) != ld and rows > 1:
+        raise ValueError(f"row pitch {t.stride(0)} of a {tuple(t.shape)} tensor, {ld} expected")
+    return t.data_ptr()
+
+
+def _act8_scales(cols):
+    return (cols + 31) // 32
 
 
 def moe_layernorm_workspace_size(n: MoeNorm) -> int:
@@ -394,48 +413,58 @@ def moe_layernorm_workspace_size(n: MoeNorm) -> int:
 
 
 def moe_layernorm_fwd(n, x, residual, gamma, beta, h, y, mean, rstd, codes=None, scales=None, stream=None):
-    _check(lib().moe_layernorm_fwd(ctypes.byref(n), _p(x), _p(residual), _p(gamma), _p(beta), _p(h), _p(y), _p(mean),
-                                   _p(rstd), _p(codes), _p(scales), _st(stream)))
+    R, H, f32 = n.rows, n.H, torch.float32
+    t, w = _ROW_TYPES[n.x_f32], _ROW_TYPES[n.w_f32]
+    _check(lib().moe_layernorm_fwd(ctypes.byref(n), _pitched(x, R, H, n.ld_in, t), _pitched(residual, R, H, n.ld_in, t),
+                                   _dense(gamma, w, H), _dense(beta, w, H), _pitched(h, R, H, n.ld_out, t),
+                                   _pitched(y, R, H, n.ld_out, t), _dense(mean, f32, R), _dense(rstd, f32, R),
+                                   _dense(codes, torch.uint8, R * H), _dense(scales, torch.uint8, R * _act8_scales(H)),
+                                   _st(stream)))
 
 
 def moe_layernorm_bwd(n, dy, x, mean, rstd, codes, scales, gamma, dres, dx, dgamma, dbeta, workspace, stream=None):
     """From x and mean, or, where codes is given (x None), from the 8-bit checkpoint."""
-    _check(lib().moe_layernorm_bwd(ctypes.byref(n), _p(dy), _p(x), _p(None if x is None else mean), _p(rstd),
-                                   _p(codes), _p(scales), _p(gamma), _p(dres), _p(dx), _p(dgamma), _p(dbeta),
+    R, H, f32 = n.rows, n.H, torch.float32
+    t, w = _ROW_TYPES[n.x_f32], _ROW_TYPES[n.w_f32]
+    _check(lib().moe_layernorm_bwd(ctypes.byref(n), _pitched(dy, R, H, n.ld_in, t), _pitched(x, R, H, n.ld_in, t),
+                                   None if x is None else _dense(mean, f32, R), _dense(rstd, f32, R),
+                                   _dense(codes, torch.uint8, R * H), _dense(scales, torch.uint8, R * _act8_scales(H)),
+                                   _dense(gamma, w, H), _pitched(dres, R, H, n.ld_in, t),
+                                   _pitched(dx, R, H, n.ld_out, t), _dense(dgamma, w, H), _dense(dbeta, w, H),
                                    _p(workspace), _wsb(workspace), _st(stream)))
 
 
 def moe_act8_pack(src, codes, scales, stream=None):
     rows, cols = src.shape
-    if src.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"expected bfloat16 or float32, got {src.dtype}")
-    _check(lib().moe_act8_pack(_p(src), int(src.dtype == torch.float32), rows, cols, _ld(src, cols), _p(codes),
-                               _p(scales), _st(stream)))
+    f32 = src.dtype == torch.float32
+    _check(lib().moe_act8_pack(_p(src), int(f32), rows, cols, _ld(src, rows, cols, _ROW_TYPES[f32]),
+                               _dense(codes, torch.uint8, rows * cols),
+                               _dense(scales, torch.uint8, rows * _act8_scales(cols)), _st(stream)))
 
 
 def moe_act8_unpack(codes, scales, gamma, beta, dst, stream=None):
     rows, cols = codes.shape
-    if dst.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"expected bfloat16 or float32, got {dst.dtype}")
-    if dst.shape[0] != rows:
-        raise ValueError(f"dst has {dst.shape[0]} rows, codes {rows}")
-    w_f32 = gamma is not None and gamma.dtype == torch.float32
-    _check(lib().moe_act8_unpack(_p(codes), _p(scales), rows, cols, _p(gamma), _p(beta), int(w_f32), _p(dst),
-                                 int(dst.dtype == torch.float32), _ld(dst, cols), _st(stream)))
+    f32, w_f32 = dst.dtype == torch.float32, gamma is not None and gamma.dtype == torch.float32
+    _check(lib().moe_act8_unpack(_dense(codes, torch.uint8, rows * cols),
+                                 _dense(scales, torch.uint8, rows * _act8_scales(cols)), rows, cols,
+                                 _dense(gamma, _ROW_TYPES[w_f32], cols), _dense(beta, _ROW_TYPES[w_f32], cols),
+                                 int(w_f32), _p(dst), int(f32), _ld(dst, rows, cols, _ROW_TYPES[f32]), _st(stream)))
 
 
 def moe_swiglu_fwd(gu, prob, a, codes=None, scales=None, stream=None):
     rows, I = a.shape
-    _typed(torch.bfloat16, gu, a)
-    _check(lib().moe_swiglu_fwd(rows, I, _p(gu), _ld(gu, 2 * I), _p(prob), _p(a), _ld(a, I), _p(codes), _p(scales),
-                                _st(stream)))
+    _check(lib().moe_swiglu_fwd(rows, I, _p(gu), _ld(gu, rows, 2 * I), _dense(prob, torch.float32, rows), _p(a),
+                                _ld(a, rows, I), _dense(codes, torch.uint8, rows * 2 * I),
+                                _dense(scales, torch.uint8, rows * 2 * _act8_scales(I)), _st(stream)))
 
 
 def moe_swiglu_bwd(gu, codes, scales, prob, da, dgu, dprob=None, a=None, stream=None):
     rows, I = da.shape
-    _typed(torch.bfloat16, gu, da, dgu, a)
-    _check(lib().moe_swiglu_bwd(rows, I, _p(gu), _ld(gu, 2 * I), _p(codes), _p(scales), _p(prob), _p(da), _ld(da, I),
-                                _p(dgu), _ld(dgu, 2 * I), _p(dprob), _p(a), _ld(a, I), _st(stream)))
+    _check(lib().moe_swiglu_bwd(rows, I, _p(gu), _ld(gu, rows, 2 * I), _dense(codes, torch.uint8, rows * 2 * I),
+                                _dense(scales, torch.uint8, rows * 2 * _act8_scales(I)),
+                                _dense(prob, torch.float32, rows), _p(da), _ld(da, rows, I), _p(dgu),
+                                _ld(dgu, rows, 2 * I), _dense(dprob, torch.float32, rows), _p(a), _ld(a, rows, I),
+                                _st(stream)))
 
 
 def moe_grouped_linear_workspace_size(g: MoeGrouped) -> int:
@@ -443,18 +472,22 @@ def moe_grouped_linear_workspace_size(g: MoeGrouped) -> int:
 
 
 def moe_grouped_linear_fwd(g, x, split_sizes, w, y, workspace, stream=None):
-    _typed(torch.bfloat16, x, w, y)
-    _check(lib().moe_grouped_linear_fwd(ctypes.byref(g), _p(x), _ld(x, g.K), _p(split_sizes), _p(w), _p(y),
-                                        _ld(y, g.N), _p(workspace), _wsb(workspace), _st(stream)))
+    R, K, N = g.rows, g.K, g.N
+    _check(lib().moe_grouped_linear_fwd(ctypes.byref(g), _p(x), _ld(x, R, K), _dense(split_sizes, torch.int32, g.E),
+                                        _dense(w, torch.bfloat16, g.E * N * K), _p(y), _ld(y, R, N), _p(workspace),
+                                        _wsb(workspace), _st(stream)))
 
 
 def moe_grouped_linear_dgrad(g, dy, split_sizes, w, dx, workspace, stream=None):
-    _typed(torch.bfloat16, dy, w, dx)
-    _check(lib().moe_grouped_linear_dgrad(ctypes.byref(g), _p(dy), _ld(dy, g.N), _p(split_sizes), _p(w), _p(dx),
-                                          _ld(dx, g.K), _p(workspace), _wsb(workspace), _st(stream)))
+    R, K, N = g.rows, g.K, g.N
+    _check(lib().moe_grouped_linear_dgrad(ctypes.byref(g), _p(dy), _ld(dy, R, N), _dense(split_sizes, torch.int32, g.E),
+                                          _dense(w, torch.bfloat16, g.E * N * K), _p(dx), _ld(dx, R, K), _p(workspace),
+                                          _wsb(workspace), _st(stream)))
 
 
 def moe_grouped_linear_wgrad(g, x, dy, split_sizes, dw, workspace, stream=None):
-    _typed(torch.bfloat16, x, dy, dw)
-    _check(lib().moe_grouped_linear_wgrad(ctypes.byref(g), _p(x), _ld(x, g.K), _p(dy), _ld(dy, g.N), _p(split_sizes),
-                                          _p(dw), _p(workspace), _wsb(workspace), _st(stream)))
+    R, K, N = g.rows, g.K, g.N
+    _check(lib().moe_grouped_linear_wgrad(ctypes.byref(g), _p(x), _ld(x, R, K), _p(dy), _ld(dy, R, N),
+                                          _dense(split_sizes, torch.int32, g.E),
+                                          _dense(dw, torch.bfloat16, g.E * N * K), _p(workspace), _wsb(workspace),
+                                          _st(stream)))

@@ -1270,7 +1270,7 @@ namespace {
 
 moe_status check_norm(const moe_norm* n) {
   if (n == nullptr) return fail(MOE_ERR_INVALID_ARG, "norm is NULL");
-  if (n->rows < 0 || n->rows > (int64_t(1) << 31)) return fail(MOE_ERR_INVALID_ARG, "rows=%lld must be in 0..2^31", (long long)n->rows);
+  if (n->rows < 0 || n->rows >= (int64_t(1) << 31)) return fail(MOE_ERR_INVALID_ARG, "rows=%lld must be in 0..2^31-1", (long long)n->rows);
   if (n->H < 1) return fail(MOE_ERR_INVALID_ARG, "H=%d must be >= 1", n->H);
   if (n->H > 16384) return fail(MOE_ERR_UNSUPPORTED, "H=%d must be <= 16384", n->H);
   if (n->ld_in < n->H || n->ld_out < n->H)
@@ -1300,7 +1300,7 @@ moe_status check_act8(const uint8_t* codes, const uint8_t* scales) {
 }
 
 moe_status check_rows_cols(int64_t rows, int32_t cols) {
-  if (rows < 0 || rows > (int64_t(1) << 31)) return fail(MOE_ERR_INVALID_ARG, "rows=%lld must be in 0..2^31", (long long)rows);
+  if (rows < 0 || rows >= (int64_t(1) << 31)) return fail(MOE_ERR_INVALID_ARG, "rows=%lld must be in 0..2^31-1", (long long)rows);
   if (cols < 1 || cols > (1 << 29)) return fail(MOE_ERR_INVALID_ARG, "row length %d must be in 1..2^29", cols);
   return MOE_OK;
 }

@@ -432,30 +432,36 @@ RowShape row_shape(int H, int vec, int wide_nv) {
   return RowShape{vec, nv, tpr, tpr > MAX_TPR ? tpr : MAX_TPR / tpr * tpr};
 }
 
-// Sets a kernel's dynamic shared memory limit once per device, and says how many blocks of a
-// persistent grid the device holds at once (0: look-up failed).
+// How many blocks of a persistent grid each device holds at once, looked up once per row shape
+// (block and shared memory follow from tpr), with the kernel's dynamic shared memory limit set.
+struct Resident {
+  std::atomic<int> blocks[kMaxDevices][max_block(1) / 32 + 1];
+};
 template <typename K>
-int64_t resident_blocks(K* kernel, int block, size_t smem, std::atomic<bool>* set) {
+cudaError_t resident_blocks(K* kernel, const RowShape& s, size_t smem, Resident& known, int64_t* out) {
   int dev = 0, sms = 0, per = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (smem > 40 * 1024 && (dev >= kMaxDevices || !set[dev].load(std::memory_order_acquire))) {
-    // above the 48 KB (static memory included) that need no asking; one call serves all sizes
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) != cudaSuccess) return 0;
-    if (dev < kMaxDevices) set[dev].store(true, std::memory_order_release);
-  }
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, block, smem) != cudaSuccess || per < 1)
-    return 0;
-  return int64_t(sms) * per;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::atomic<int>* slot = dev < kMaxDevices ? &known.blocks[dev][s.tpr / 32] : nullptr;
+  if (slot != nullptr && (*out = slot->load(std::memory_order_acquire)) != 0) return cudaSuccess;
+  // above the 48 KB (static memory included) that need no asking
+  if (smem > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, s.block, smem);
+  if (e != cudaSuccess) return e;
+  if (per < 1) return cudaErrorInvalidConfiguration;
+  *out = int64_t(sms) * per;
+  if (slot != nullptr) slot->store(sms * per, std::memory_order_release);
+  return cudaSuccess;
 }
 
 template <typename T, int VEC, int NV>
 cudaError_t norm_fwd_shape(const NormArgs& a, const RowShape& s, cudaStream_t st) {
-  static std::atomic<bool> set[kMaxDevices];
+  static Resident known;
   const int64_t rpb = s.block / s.tpr, need = (a.rows + rpb - 1) / rpb;
   const size_t smem = size_t(ring_stages(VEC, 2 * NV)) * 2 * NV * 16 * s.block;
-  const int64_t most = resident_blocks(norm_fwd_kernel<T, VEC, NV>, s.block, smem, set);
-  if (most == 0) return cudaErrorInvalidConfiguration;
+  int64_t most = 0;
+  if (const cudaError_t e = resident_blocks(norm_fwd_kernel<T, VEC, NV>, s, smem, known, &most); e != cudaSuccess) return e;
   return launch_pdl(norm_fwd_kernel<T, VEC, NV>, dim3(unsigned(need < most ? need : most)), dim3(unsigned(s.block)),
                     smem, st, a, s.tpr);
 }
@@ -465,13 +471,13 @@ constexpr int kNormMaxParts = 304;
 
 template <typename T, int VEC, int NV, bool Q8>
 cudaError_t norm_bwd_shape(const NormArgs& a, const RowShape& s, float* partial, int* parts, cudaStream_t st) {
-  static std::atomic<bool> set[kMaxDevices];
+  static Resident known;
   const int64_t rpb = s.block / s.tpr, need = (a.rows + rpb - 1) / rpb;
   const size_t ring = size_t(ring_stages(VEC, 3 * NV)) * 3 * NV * 16 * s.block;
   const size_t fold = size_t(rpb) * 2 * a.H * sizeof(float);      // H <= tpr * VEC * NV: at most 128 KB
   const size_t smem = ring > fold ? ring : fold;
-  int64_t grid = resident_blocks(norm_bwd_kernel<T, VEC, NV, Q8>, s.block, smem, set);
-  if (grid == 0) return cudaErrorInvalidConfiguration;
+  int64_t grid = 0;
+  if (const cudaError_t e = resident_blocks(norm_bwd_kernel<T, VEC, NV, Q8>, s, smem, known, &grid); e != cudaSuccess) return e;
   grid = grid < kNormMaxParts ? grid : kNormMaxParts;
   grid = grid < need ? grid : need;
   *parts = int(grid);

@@ -175,7 +175,7 @@ def test_no_rows_and_constant_rows():
     e = torch.empty(0, H, dtype=torch.bfloat16, device="cuda")
     ws = torch.zeros(B.moe_layernorm_workspace_size(n), dtype=torch.uint8, device="cuda")
     B.moe_layernorm_fwd(n, e, None, gamma, None, None, e, None, None)
-    B.moe_layernorm_bwd(n, e, None, None, e, None, None, gamma, None, e, dgamma, dbeta, ws)
+    B.moe_layernorm_bwd(n, e, None, None, torch.empty(0, device="cuda"), None, None, gamma, None, e, dgamma, dbeta, ws)
     assert not bool(dgamma.any()) and not bool(dbeta.any())
     # a constant row: n = 0, y = beta; a row with a NaN stays alone with it
     n = B.norm(3, H)
