@@ -390,7 +390,7 @@ def _dense(t, dtype, n):
     """Pointer of a contiguous tensor of `dtype` with at least n values; None for None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.numel() < n or not t.is_contiguous():
+    if t.dtype is not dtype or not t.is_contiguous() or t.numel() < n:
         raise ValueError(f"expected a contiguous {dtype} tensor of at least {n} values, got {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
 
@@ -399,8 +399,10 @@ def _pitched(t, rows, cols, ld, dtype):
     """Pointer of a [rows][cols] tensor whose row pitch has to be ld; None for None."""
     if t is None:
         return None
-    if _ld(t, rows, cols, dtype) != ld and rows > 1:
-        raise ValueError(f"row pitch {t.stride(0)} of a {tuple(t.shape)} tensor, {ld} expected")
+    if t.dtype is not dtype or t.stride() != (ld, 1) or t.shape != (rows, cols):
+        # one row has no pitch, one column no stride
+        if _ld(t, rows, cols, dtype) != ld and rows > 1:
+            raise ValueError(f"row pitch {t.stride(0)} of a {tuple(t.shape)} tensor, {ld} expected")
     return t.data_ptr()
 
 
