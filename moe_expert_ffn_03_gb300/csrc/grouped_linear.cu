@@ -27,7 +27,7 @@
 //   warp 0       TMA producer of the M side, warp 19 of the N side: one 64-deep step per stage, as
 //                many stages as 192 KB hold (9 of 64 columns, 6 of 256, 4 of 512);
 //   warp 1       TMEM allocation; in the leader, the MMAs;
-//   warps 2..17  epilogue, four per TMEM lane quarter, 64 columns of an accumulator each;
+//   warps 2..17  epilogue, four per TMEM lane quarter, a quarter of the columns each;
 //   warp 18      wgrad: clears the rows of a tile's last step that belong to the next expert.
 // A stage's operands are blocks of 128 bytes per row, swizzled: K-major 128 (m or n) rows of 64
 // deep, MN-major 64 deep rows of 64 (m or n).  MN-major operands whose rows are multiples of 64
@@ -64,7 +64,8 @@ constexpr int LG_MAX_E = 256;
 constexpr int LG_GROUP = 8;                      // row tiles that share the sweep over the weights
 constexpr int LG_SMALL = 32;                     // rows of the small row box
 constexpr int LG_MIN_PIECE = 8;                  // steps a piece of a tile has at least
-constexpr int LG_PIECE = 64 * 32;                // f32 of a warp's partial sums: 64 columns of 32 m
+constexpr int LG_PIECE = 16 * 32;                // f32 of a warp's partial sums: 16 columns of 32 m
+constexpr int LG_PLACES = 32;                    // warps that share a tile of 64 columns: 2 CTAs x 16
 
 constexpr int LG_OFF_BAR = LG_RING;
 // full, empty, tail, cleared [LG_MAX_STG] each, tmem_full[2], tmem_empty[2], drain
@@ -273,23 +274,21 @@ __device__ __forceinline__ bool lin_next(const LinearArgs& a, const int* row0, c
 template <int MODE>
 __device__ __forceinline__ bool lin_tail(const LinTile& tl) { return MODE == LIN_WGRAD && (tl.c_cnt & 15) != 0; }
 
-// A warp's 32 m x 64 columns of a piece of a tile: written to the workspace, unless this is the
-// last of the tile's pieces to arrive here; then r becomes the sum of all of them, in the order of
-// the contraction, and the caller stores it (true).  tn = 64: only the warps of column group 0
-// have columns.
-__device__ __forceinline__ bool join_pieces(const LinearArgs& a, const LinTile& tl, int rest, int quarter, int cg, int cols,
-                                            int lane, uint32_t* r) {
-  if (cg != 0) return false;
+// A warp's 32 m x 16 columns of a piece of a tile (tn = 64): written to the workspace, unless this
+// is the last of the tile's pieces to arrive here; then r becomes the sum of all of them, in the
+// order of the contraction, and the caller stores it (true).  place: the warp's among the tile's
+// 32 (CTA, lane quarter, column group).
+__device__ __forceinline__ bool join_pieces(const LinearArgs& a, const LinTile& tl, int rest, int place, int lane,
+                                            uint32_t* r) {
   const auto slot = [&](int part) {              // piece `part` of cut tile c is pair part * rest + c's
-    return a.pieces + (int64_t(part * rest + tl.cut) * 8 + quarter) * LG_PIECE + lane;
+    return a.pieces + (int64_t(part * rest + tl.cut) * LG_PLACES + place) * LG_PIECE + lane;
   };
   float* mine = slot(tl.part);
 #pragma unroll
-  for (int c = 0; c < 64; ++c)
-    if (c < cols) __stcg(mine + c * 32, __uint_as_float(r[c]));
+  for (int c = 0; c < 16; ++c) __stcg(mine + c * 32, __uint_as_float(r[c]));
   __threadfence();
   __syncwarp();
-  unsigned* arrived = a.arrived + tl.cut * 8 + quarter;
+  unsigned* arrived = a.arrived + tl.cut * LG_PLACES + place;
   unsigned before = 0;
   if (lane == 0) before = atomicAdd(arrived, 1u);
   before = __shfl_sync(0xFFFFFFFFu, before, 0);
@@ -298,13 +297,11 @@ __device__ __forceinline__ bool join_pieces(const LinearArgs& a, const LinTile& 
   if (lane == 0) *arrived = 0;                   // for the next call
   const float* first = slot(0);
 #pragma unroll
-  for (int c = 0; c < 64; ++c)
-    if (c < cols) r[c] = __float_as_uint(__ldcg(first + c * 32));
+  for (int c = 0; c < 16; ++c) r[c] = __float_as_uint(__ldcg(first + c * 32));
   for (int p = 1; p < tl.parts; ++p) {
     const float* s = slot(p);
 #pragma unroll
-    for (int c = 0; c < 64; ++c)
-      if (c < cols) r[c] = __float_as_uint(__uint_as_float(r[c]) + __ldcg(s + c * 32));
+    for (int c = 0; c < 16; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) + __ldcg(s + c * 32));
   }
   return true;
 }
@@ -597,7 +594,8 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
     // ---------------- epilogue warps (both CTAs) ----------------
     const int q = warp & 3;                      // TMEM lane quarter this warp may access
     const int cg = (warp - 2) >> 2;              // column group 0..3
-    const uint32_t tmem_row = tmem + (uint32_t(q * 32) << 16) + uint32_t(cg * 64);
+    const int col0 = cg * (args.tn == 64 ? 16 : 64);             // first of this warp's columns
+    const uint32_t tmem_row = tmem + (uint32_t(q * 32) << 16) + uint32_t(col0);
     const uint32_t tmem_empty_c0 = mapa_shared(smem_u32(tmem_empty), 0);
     const int M = lin_m<MODE>(args);
     uint32_t* tr = reinterpret_cast<uint32_t*>(smem + LG_OFF_TR + (warp - 2) * LG_TR_WARP);
@@ -623,23 +621,26 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         tc_fence_after();
         const int cols = tl.cols(h), part = cols >> 1;           // the first `part` columns are the leader's n
         uint32_t r[64];
-        if (cg * 64 < cols) {
+        if (args.tn == 64) {
+          tmem_ld16_async(tmem_row + uint32_t(ab * LG_ACC), r);  // (past cols: columns that nobody stores)
+          tmem_wait_ld<16>(r);
+        } else if (col0 < cols) {
           tmem_ld32_async(tmem_row + uint32_t(ab * LG_ACC), r);
-          if (cg * 64 + 32 < cols) tmem_ld32_async(tmem_row + uint32_t(ab * LG_ACC) + 32u, r + 32);
+          if (col0 + 32 < cols) tmem_ld32_async(tmem_row + uint32_t(ab * LG_ACC) + 32u, r + 32);
           tmem_wait_ld<64>(r);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster_relaxed(tmem_empty_c0 + uint32_t(ab) * 8u);
-        // Lane l holds m = l of 64 columns.  Through shared memory, 16 columns at a time, a lane
+        // Lane l holds m = l of its warp's columns.  Through shared memory, 16 columns at a time, a lane
         // gets eight m of two columns, p and p + 1: 16-byte stores, 64 bytes per column and warp.
         const int p = lane >> 2, m = tl.m0 + int(rank) * 128 + q * 32 + (lane & 3) * 8;
-        if (CUT && tl.parts > 1 && !join_pieces(args, tl, plan.rest, int(rank) * 4 + q, cg, cols, lane, r)) continue;
+        if (CUT && tl.parts > 1 && !join_pieces(args, tl, plan.rest, (int(rank) * 4 + q) * 4 + cg, lane, r)) continue;
         __nv_bfloat16* o = args.out + ((MODE == LIN_WGRAD ? int64_t(tl.e) * args.N : 0) + tl.n0 + 2 * p) * args.ldo + m;
 #pragma unroll
         for (int c0 = 0; c0 < 64; c0 += 16) {
-          const int j = cg * 64 + c0;
-          if (j >= cols) break;
+          const int j = col0 + c0;
+          if (j >= cols || (c0 > 0 && args.tn == 64)) break;
           const int off = (j >= part ? (tl.n >> 1) + j - part : j) + h * 128;    // n - n0 of column j
           if (off >= tl.cnt) continue;
 #pragma unroll
@@ -757,14 +758,16 @@ cudaError_t lin_launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUten
 
 }  // namespace
 
-size_t linear_ws_bytes() { return 256 + size_t(kLinearMaxPairs) * 8 * (sizeof(unsigned) + LG_PIECE * sizeof(float)); }
+size_t linear_ws_bytes() {
+  return 256 + size_t(kLinearMaxPairs) * LG_PLACES * (sizeof(unsigned) + LG_PIECE * sizeof(float));
+}
 
 cudaError_t launch_grouped_linear(int mode, const LinearArgs& args, const void* x, int64_t ldx, const void* dy,
                                   int64_t lddy, const void* w, cudaStream_t st, char* msg, size_t msg_len) {
   LinearArgs a = args;
   // the workspace: error word, arrival counts, pieces
   a.arrived = reinterpret_cast<unsigned*>(reinterpret_cast<uint8_t*>(a.err) + 256);
-  a.pieces = reinterpret_cast<float*>(a.arrived + kLinearMaxPairs * 8);
+  a.pieces = reinterpret_cast<float*>(a.arrived + kLinearMaxPairs * LG_PLACES);
   CUtensorMap ma, mb, mbs;
   bool ok;
   const bool at = a.K % 64 == 0 && (mode == LIN_DGRAD || a.N % 64 == 0);   // rows of the MN-major operands
