@@ -254,7 +254,14 @@ __device__ __forceinline__ bool lin_next(const LinearArgs& a, const int* row0, c
                                          const Plan& p, int pair, int num_pairs, int& t, LinTile& tl) {
   if (t < p.whole) {
     lin_decode<MODE>(a, row0, tile0, order, t, tl);
-    t += num_pairs;
+    if (MODE == LIN_WGRAD) {
+      // there and back: tiles come longest first, so the pair that got the longest of one round gets
+      // the shortest of the next
+      const int at = t % num_pairs;
+      t += 2 * (num_pairs - 1 - at) + 1;
+    } else {
+      t += num_pairs;
+    }
     return true;
   }
   if (!CUT || t >= p.whole + num_pairs || pair >= p.rest * p.parts) return false;
