@@ -18,14 +18,14 @@
 // In every mode m is the contiguous index of the output.
 //
 // Persistent CTA pairs (clusters of two, one CTA per SM): a pair computes a tile of 256 m and up
-// to tn = 64, 256 or 512 n with tcgen05.mma.cta_group::2; each CTA stages its 128 m and its half of
+// to tn = 64, 128, 256 or 512 n with tcgen05.mma.cta_group::2; each CTA stages its 128 m and its half of
 // the n.  What bounds the main loop of large tiles is the bytes a step needs against the ring's
 // bytes in flight: 512 columns need 48 B per clock and SM at the full MMA rate, 256 columns 64 B,
 // and TMA delivers about 50.  The 512 columns of TMEM are two accumulators of 256, handed out in
 // turn: a wide tile takes both, a narrow one leaves the other to the next tile.  A wide tile
 // starts on its first accumulator while the epilogue still reads the second.
 //   warp 0       TMA producer of the M side, warp 19 of the N side: one 64-deep step per stage, as
-//                many stages as 192 KB hold (9 of 64 columns, 6 of 256, 4 of 512);
+//                many stages as 192 KB hold (9 of 64 columns, 8 of 128, 6 of 256, 4 of 512);
 //   warp 1       TMEM allocation; in the leader, the MMAs;
 //   warps 2..17  epilogue, four per TMEM lane quarter, a quarter of the columns each;
 //   warp 18      wgrad: clears the rows of a tile's last step that belong to the next expert.
@@ -62,7 +62,7 @@ constexpr int LG_EPI_WARPS = 16;
 constexpr int LG_THREADS = 32 * (4 + LG_EPI_WARPS);
 constexpr int LG_MAX_E = 256;
 constexpr int LG_GROUP = 8;                      // row tiles that share the sweep over the weights
-constexpr int LG_SMALL = 32;                     // rows of the small row box
+constexpr int LG_SMALL = 32;                     // rows of the small box of rows
 constexpr int LG_MIN_PIECE = 8;                  // steps a piece of a tile has at least
 constexpr int LG_PIECE = 16 * 32;                // f32 of a warp's partial sums: 16 columns of 32 m
 constexpr int LG_PLACES = 32;                    // warps that share a tile of 64 columns: 2 CTAs x 16
@@ -361,6 +361,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
     tmem_alloc(tmem_base_s, 512);                // collectively with the peer CTA
     tmem_relinquish();
   }
+  cluster_arrive();                              // this CTA's barriers are initialised
   // Up to here the kernel touches only its own shared memory, TMEM and parameters.
   pdl_wait();
   if (warp == 2) {
@@ -428,7 +429,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();                                // the pair's barriers are initialised before any remote arrival
+  cluster_wait();                                // and the other's, before anything arrives there
   tc_fence_after();
   const uint32_t tmem = *tmem_base_s;
   // inconsistent split_sizes: nothing is computed (the error word says so)
@@ -447,9 +448,9 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         const int half = tl.n >> 1;
         const int m = tl.m0 + int(rank) * 128;
         const int nr = tl.n0 + int(rank) * half;
-        const bool small = !B_MN && half <= LG_SMALL;
+        const bool small = half <= (B_MN ? 64 : LG_SMALL);       // one MN-major block, or few rows
         const int nb = half > 128 ? 2 : 1;       // 128-wide parts of the N side
-        const uint32_t bytes = LG_TILE + (small ? LG_SMALL * 128u : uint32_t(nb * LG_TILE));
+        const uint32_t bytes = LG_TILE + (small ? uint32_t(B_MN ? LG_BLOCK : LG_SMALL * 128) : uint32_t(nb * LG_TILE));
         for (int kt = 0; kt < tl.steps; ++kt, cur.next(stages)) {
           if (!wait_phase(&empty[cur.st], cur.ph ^ 1u, abort_s, args.err, SITE_LINEAR, kWaitLimitNs)) {
             ok = false;
@@ -483,7 +484,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
               }
             }
           } else if (small) {
-            tma_load_2d(pb, &tmBs, c, nr, bar_c);
+            tma_load_2d(pb, &tmBs, B_MN ? nr : c, B_MN ? c : nr, bar_c);
           } else {
             for (int h = 0; h < nb; ++h) {
               if (!B_MN) tma_load_2d(pb + h * LG_TILE, &tmB, c, nr + h * 128, bar_c);
@@ -601,7 +602,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
     // ---------------- epilogue warps (both CTAs) ----------------
     const int q = warp & 3;                      // TMEM lane quarter this warp may access
     const int cg = (warp - 2) >> 2;              // column group 0..3
-    const int col0 = cg * (args.tn == 64 ? 16 : 64);             // first of this warp's columns
+    const int width = min(64, args.tn >> 2), col0 = cg * width;  // this warp's columns of an accumulator
     const uint32_t tmem_row = tmem + (uint32_t(q * 32) << 16) + uint32_t(col0);
     const uint32_t tmem_empty_c0 = mapa_shared(smem_u32(tmem_empty), 0);
     const int M = lin_m<MODE>(args);
@@ -628,12 +629,12 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         tc_fence_after();
         const int cols = tl.cols(h), part = cols >> 1;           // the first `part` columns are the leader's n
         uint32_t r[64];
-        if (args.tn == 64) {
+        if (width == 16) {
           tmem_ld16_async(tmem_row + uint32_t(ab * LG_ACC), r);  // (past cols: columns that nobody stores)
           tmem_wait_ld<16>(r);
         } else if (col0 < cols) {
           tmem_ld32_async(tmem_row + uint32_t(ab * LG_ACC), r);
-          if (col0 + 32 < cols) tmem_ld32_async(tmem_row + uint32_t(ab * LG_ACC) + 32u, r + 32);
+          if (width == 64 && col0 + 32 < cols) tmem_ld32_async(tmem_row + uint32_t(ab * LG_ACC) + 32u, r + 32);
           tmem_wait_ld<64>(r);
         }
         tc_fence_before();
@@ -647,7 +648,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
 #pragma unroll
         for (int c0 = 0; c0 < 64; c0 += 16) {
           const int j = col0 + c0;
-          if (j >= cols || (c0 > 0 && args.tn == 64)) break;
+          if (j >= cols || c0 >= width) break;
           const int off = (j >= part ? (tl.n >> 1) + j - part : j) + h * 128;    // n - n0 of column j
           if (off >= tl.cnt) continue;
 #pragma unroll
@@ -691,7 +692,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
       par ^= 1u << st;
       const int valid = tl.c_cnt - (tl.steps - 1) * LG_KT;       // the stage's rows
       const int n = (((valid + 15) & ~15) - valid) * 8;          // 16-byte chunks to clear in each block
-      const int blocks = tl.n > LG_ACC ? 6 : 4;                  // of 64 columns: M's two, N's two or four
+      const int blocks = 2 + (tl.n >> 7);                        // of 64 columns: M's two, N's one to four
       for (int i = lane; i < blocks * n; i += 32) {
         const int block = i / n, j = i - block * n;
         *reinterpret_cast<uint4*>(smem + st * stage_bytes + block * LG_BLOCK + (valid + (j >> 3)) * 128 + (j & 7) * 16) =
@@ -785,8 +786,8 @@ cudaError_t launch_grouped_linear(int mode, const LinearArgs& args, const void* 
     ok = lin_map(&ma, at, w, a.K, a.N, a.K, a.E, 64) && lin_map(&mb, false, dy, a.N, a.rows, lddy, 0, 128) &&
          lin_map(&mbs, false, dy, a.N, a.rows, lddy, 0, LG_SMALL);
   } else {
-    ok = lin_map(&ma, at, x, a.K, a.rows, ldx, 0, 64) && lin_map(&mb, at, dy, a.N, a.rows, lddy, 0, 64);
-    mbs = mb;                                    // not used
+    ok = lin_map(&ma, at, x, a.K, a.rows, ldx, 0, 64) && lin_map(&mb, at, dy, a.N, a.rows, lddy, 0, 64) &&
+         lin_map(&mbs, false, dy, a.N, a.rows, lddy, 0, 64);
   }
   if (!ok) {
     snprintf(msg, msg_len, "cuTensorMapEncodeTiled failed (rows %lld, K %d, N %d, E %d)", (long long)a.rows, a.K, a.N,
@@ -797,20 +798,28 @@ cudaError_t launch_grouped_linear(int mode, const LinearArgs& args, const void* 
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  // Columns of a tile.  64 where an expert has few rows, so that the call reads the weights and
-  // little else: their stages are small and nine are in flight.  512 where they still make four
-  // tiles a pair, else 256 (fewer, larger tiles leave pairs idle at the end).
+  // Columns of a tile.  64 (wgrad 128) where an expert has few rows, so that the call reads the
+  // weights and little else: their stages are small and nine are in flight; and where 256 would
+  // leave half the pairs without a tile (777 rows, K = 200, N = 136, E = 5: 8.6 -> 6.6 us a call).  512
+  // where they still
+  // make four tiles a pair, else 256 (fewer, larger tiles leave pairs idle at the end).
   const int64_t pairs = sms / 2 < 1 ? 1 : sms / 2;
   const int64_t mt = ((mode == LIN_FWD ? a.N : a.K) + LG_M - 1) / LG_M;
-  const int64_t wide = mode == LIN_WGRAD ? int64_t(a.E) * ((a.N + 511) / 512) : a.rows / 512;
-  a.tn = mode != LIN_WGRAD && (a.rows <= 64 || a.rows <= int64_t(32) * a.E) ? 64 : mt * wide >= 4 * pairs ? 512 : 256;
-  const int64_t nt = mode == LIN_WGRAD ? int64_t(a.E) * ((a.N + a.tn - 1) / a.tn)
-                                       : (a.rows < a.E ? a.rows : a.E) + a.rows / a.tn;
+  const auto n_tiles = [&](int tn) {
+    return mode == LIN_WGRAD ? int64_t(a.E) * ((a.N + tn - 1) / tn) : (a.rows < a.E ? a.rows : a.E) + a.rows / tn;
+  };
+  const int64_t wide = mode == LIN_WGRAD ? n_tiles(512) : a.rows / 512;
+  const bool few_rows = mode != LIN_WGRAD && (a.rows <= 64 || a.rows <= int64_t(32) * a.E);
+  if (few_rows || 2 * mt * n_tiles(256) <= pairs) a.tn = mode == LIN_WGRAD ? 128 : 64;
+  else a.tn = mt * wide >= 4 * pairs ? 512 : 256;
+  const int64_t nt = n_tiles(a.tn);
   // Tiles are cut where at most half the pairs have one, or where there is a second round at most
-  // (16 rows, K = 14336, N = 4096: 165 -> 143 us; 2 rows, N = 14336, K = 4096 back: 79 -> 57 us).  One
+  // (16 rows, K = 14336, N = 4096: 165 -> 143 us; 2 rows, N = 14336, K = 4096, dgrad: 79 -> 57 us).  One
   // round of more than half the pairs cannot be cut, and the plain kernel is 2 us faster there.
   const int64_t tiles = mt * nt;
-  const bool cut = a.tn == 64 && pairs <= kLinearMaxPairs && (2 * tiles <= pairs || (tiles > pairs && tiles <= 2 * pairs));
+  const int steps = ((mode == LIN_FWD ? a.K : a.N) + LG_KT - 1) / LG_KT;
+  const bool cut = a.tn == 64 && steps >= 2 * LG_MIN_PIECE && pairs <= kLinearMaxPairs &&
+                   (2 * tiles <= pairs || (tiles > pairs && tiles <= 2 * pairs));
   // else no more pairs than tiles there can be
   const int grid = 2 * int(tiles < pairs && !cut ? tiles : pairs);
   switch (mode * 4 + int(at) * 2 + int(cut)) {
