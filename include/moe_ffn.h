@@ -655,7 +655,8 @@ typedef struct moe_grouped {
  * first use: a device error word, then arrival counts that every call leaves at zero and partial
  * sums of tiles that calls with few rows cut along the contraction).  Later calls on the same
  * stream may reuse it, for any sizes; calls running at the same time on other streams need their
- * own.  0 for invalid sizes.  Host only. */
+ * own.  After a recorded device timeout it is zero-filled again as a whole: the counts of the call
+ * that gave up may be left over.  0 for invalid sizes.  Host only. */
 size_t moe_grouped_linear_workspace_size(const moe_grouped* g);
 
 /*

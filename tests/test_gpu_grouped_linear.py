@@ -108,8 +108,8 @@ def test_many_tiles_per_pair():
 @pytest.mark.parametrize("split,K,N", [([5, 0, 3], 2056, 264), ([1], 8192, 8), ([2, 1], 264, 4104), ([64], 1000, 1000),
                                        ([1, 0, 0, 1], 520, 520), ([30, 2] * 16, 328, 1040)])
 def test_tiles_cut_along_the_contraction(split, K, N):
-    """Few rows: the steps of all tiles are shared out evenly, tiles cut where the shares end.  The
-    second call on the same workspace finds the arrival counts as the first did."""
+    """Few rows: the tiles of the last round are cut into equal pieces along the contraction.  The second
+    call on the same workspace finds the arrival counts as the first did."""
     x, dy, w, ss = tensors(split, K, N, sum(split), K, True)
     d = B.grouped(sum(split), K, N, len(split))
     ws = torch.zeros(B.moe_grouped_linear_workspace_size(d), dtype=torch.uint8, device="cuda")
@@ -180,6 +180,21 @@ def test_no_rows():
     B.moe_grouped_linear_dgrad(d, e, ss, w, e, ws)
     B.moe_grouped_linear_wgrad(d, e, e, ss, w, ws)
     assert not bool(w.any())
+
+
+@pytest.mark.parametrize("rows,K,N", [(1, 64, 64), (40, 1032, 520), (3000, 256, 136)])
+def test_rows_but_no_expert_has_any(rows, K, N):
+    x, dy, w, _ = tensors([rows], K, N, rows, 2, True)
+    w = w.expand(3, N, K).contiguous()
+    ss = torch.zeros(3, dtype=torch.int32, device="cuda")
+    d = B.grouped(rows, K, N, 3)
+    ws = torch.zeros(B.moe_grouped_linear_workspace_size(d), dtype=torch.uint8, device="cuda")
+    y, dx, dw = (torch.full(s, 77.0, dtype=torch.bfloat16, device="cuda") for s in ((rows, N), (rows, K), (3, N, K)))
+    B.moe_grouped_linear_fwd(d, x, ss, w, y, ws)
+    B.moe_grouped_linear_dgrad(d, dy, ss, w, dx, ws)
+    B.moe_grouped_linear_wgrad(d, x, dy, ss, dw, ws)
+    assert B.moe_get_device_error(ws) == (0, 0)
+    assert bool((y == 77.0).all()) and bool((dx == 77.0).all()) and not bool(dw.any())
 
 
 def test_reproducible():
