@@ -1067,7 +1067,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       const int ab = Ops<EPI>::ACC_BUFS == 2 ? (tcount & 1) : 0;
       const int use = Ops<EPI>::ACC_BUFS == 2 ? (tcount >> 1) : tcount;
-      if (!wait_phase(&tmem_full[ab], use & 1, abort_s, args.err, SITE_GEMM_EPILOGUE, lim)) break;
+      if (!wait_phase_warp(&tmem_full[ab], use & 1, abort_s, args.err, SITE_GEMM_EPILOGUE, lim)) break;
       tc_fence_after();
       epilogue_tile<EPI>(args, tl, tmem_row + uint32_t(ab) * 256u, q, cg, lane, tmem_empty_c0 + uint32_t(ab) * 8u,
                          tr, gu_s);
@@ -1328,8 +1328,7 @@ __global__ void __launch_bounds__(192, 1) router_dw_tc_kernel(const __grid_const
     // ---------------- epilogue warps 2..5: warp w reads TMEM lanes 32*(w%4).. ----------------
     const int q = warp & 3;
     const int h = h0 + 32 * q + lane;
-    bool ok = wait_phase(&done, 0, abort_s, a.err, SITE_ROUTER_DW + 2, kWaitLimitNs);
-    ok = __all_sync(0xFFFFFFFFu, ok);
+    const bool ok = wait_phase_warp(&done, 0, abort_s, a.err, SITE_ROUTER_DW + 2, kWaitLimitNs);
     if (ok) {
       tc_fence_after();
       for (int j0 = 0; j0 < a.N; j0 += 16) {
@@ -1474,8 +1473,7 @@ __global__ void __launch_bounds__(192, 1) router_fwd_tc_kernel(const __grid_cons
     // ---------------- epilogue warps 2..5: warp w reads TMEM lanes 32*(w%4).. (tokens) ----------------
     const int q = warp & 3;
     const int t = t0 + 32 * q + lane;
-    bool ok = wait_phase(&done, 0, abort_s, a.err, SITE_ROUTER_DW + 12, kWaitLimitNs);
-    ok = __all_sync(0xFFFFFFFFu, ok);
+    const bool ok = wait_phase_warp(&done, 0, abort_s, a.err, SITE_ROUTER_DW + 12, kWaitLimitNs);
     if (ok) {
       tc_fence_after();
       float* orow = a.logits + int64_t(t) * a.E;

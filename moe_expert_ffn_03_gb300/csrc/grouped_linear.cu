@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
       const int accs = tl.accs();
       for (int h = 0; h < accs; ++h, ++ac) {
         const int ab = ac & 1;
-        if (!wait_phase(&tmem_full[ab], (ac >> 1) & 1, abort_s, args.err, SITE_LINEAR + 4, kWaitLimitNs)) {
+        if (!wait_phase_warp(&tmem_full[ab], (ac >> 1) & 1, abort_s, args.err, SITE_LINEAR + 4, kWaitLimitNs)) {
           ok = false;
           break;
         }
@@ -691,8 +691,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
       // warp would take an older phase of the same parity for the one it wants; so tail stages
       // have barriers of their own)
       const int st = (at - 1) % stages;
-      ok = wait_phase(&tail[st], (par >> st) & 1u, abort_s, args.err, SITE_LINEAR + 5, kWaitLimitNs);
-      ok = __all_sync(0xFFFFFFFFu, ok);
+      ok = wait_phase_warp(&tail[st], (par >> st) & 1u, abort_s, args.err, SITE_LINEAR + 5, kWaitLimitNs);
       if (!ok) break;
       par ^= 1u << st;
       const int valid = tl.c_cnt - (tl.steps - 1) * LG_KT;       // the stage's rows

@@ -217,6 +217,13 @@ __device__ __noinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile
   }
   return true;
 }
+// wait_phase for the lanes of a warp that go on together (tcgen05.ld, shuffles, __syncwarp): the lanes
+// poll one by one, and at the limit, or when another warp raises the flag, some may see the phase and
+// others not.  The warp goes on only if all of them have.
+__device__ __forceinline__ bool wait_phase_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
+                                                int site, uint64_t limit_ns) {
+  return __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, abort_flag, err, site, limit_ns));
+}
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);

@@ -1,0 +1,43 @@
+"""What a kernel's bounded waits have to keep to where they give up.
+
+These are read off the CUDA sources: the ways in which they matter (lanes of a warp that part, memory
+that goes while something is on its way) show only where a wait runs out in an unlucky moment.
+"""
+import re
+
+from test_pdl_waits import sources
+
+# one thread only: a branch on a lane or a thread, at the call or around it
+ONE_THREAD = re.compile(r"if \((?:lane|threadIdx\.x) == 0")
+
+
+def wait_calls(src):
+    """(line number, its text, text of the enclosing blocks' heads) of every call of a bounded wait."""
+    heads, out, start = [], [], 0
+    text = re.sub(r"//[^\n]*", lambda m: " " * len(m.group()), src)
+    for m in re.finditer(r"[{};]|\bwait_phase(?:_cluster|_warp)?\(", text):
+        if m.group() == "{":
+            heads.append(text[start:m.start()])
+            start = m.end()
+        elif m.group() == "}":
+            heads.pop()
+            start = m.end()
+        elif m.group() == ";":
+            start = m.end()
+        else:
+            out.append((text.count("\n", 0, m.start()) + 1, m.group(), text[start:m.start()], list(heads)))
+    return out
+
+
+def test_a_warp_gives_up_together():
+    """tcgen05.ld, shuffles and __syncwarp need all lanes of a warp, so a wait whose warp goes on to them
+    has to end alike in all lanes; the others are a single thread's."""
+    seen = 0
+    for name, src in sources().items():
+        for line, call, statement, heads in wait_calls(src):
+            if "__device__" in statement:
+                continue                                     # the definition
+            seen += 1
+            single = any(ONE_THREAD.search(h) for h in heads + [statement])
+            assert single or call == "wait_phase_warp(", f"{name}:{line}: lanes of a warp may part here"
+    assert seen >= 15
