@@ -1076,6 +1076,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (*abort_s) {
+    // a wait gave up in this CTA, of whichever warp: copies of a producer that has finished since
+    // land before the shared memory goes (they take microseconds; bounded)
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000ull) {
+    }
+  }
   cluster_sync();                                // no CTA leaves while the pair's MMAs or arrivals may touch it
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);

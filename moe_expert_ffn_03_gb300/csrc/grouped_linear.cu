@@ -502,12 +502,6 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         }
       }
       pdl_launch_dependents();
-      if (!ok) {
-        // copies already issued land before the CTA exits (they take microseconds; bounded)
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 2000000ull) {
-        }
-      }
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
@@ -709,6 +703,13 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (*abort_s) {
+    // A wait gave up in this CTA, of whichever warp: copies issued before, by producers that may have
+    // finished since, land before the shared memory goes (they take microseconds; bounded).
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000ull) {
+    }
+  }
   cluster_sync();                                // no CTA leaves while the pair's MMAs or arrivals may touch it
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);

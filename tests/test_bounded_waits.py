@@ -5,7 +5,7 @@ that goes while something is on its way) show only where a wait runs out in an u
 """
 import re
 
-from test_pdl_waits import sources
+from test_pdl_waits import kernel_body, sources
 
 # one thread only: a branch on a lane or a thread, at the call or around it
 ONE_THREAD = re.compile(r"if \((?:lane|threadIdx\.x) == 0")
@@ -41,3 +41,13 @@ def test_a_warp_gives_up_together():
             single = any(ONE_THREAD.search(h) for h in heads + [statement])
             assert single or call == "wait_phase_warp(", f"{name}:{line}: lanes of a warp may part here"
     assert seen >= 15
+
+
+def test_copies_land_after_any_wait_gave_up():
+    """A producer may have issued its last copies and left when another warp's wait gives up; so it is the
+    whole block, behind its last barrier, that lets copies land before its shared memory goes."""
+    for file, kernel in (("grouped_linear.cu", "grouped_linear_kernel"), ("gemm.cu", "grouped_gemm_kernel")):
+        body = kernel_body(sources()[file], kernel)
+        end = body[body.rindex("__syncthreads();"):]
+        assert re.search(r"if \(\*abort_s\) \{[^}]*globaltimer_ns\(\)", end), kernel
+        assert end.index("*abort_s") < end.index("cluster_sync();") < end.index("tmem_dealloc"), kernel
