@@ -32,6 +32,7 @@ class Scratch:
         R = T * k
         dev = torch.device(device)
         e = lambda *s, dt=BF16: torch.empty(*s, dtype=dt, device=dev)  # noqa: E731
+        self.sizes = (T, H, I, E, k)
         self.d = B.dims(T, H, I, E, k)
         self.cap = B.moe_rows_capacity(self.d)
         if self.cap == 0:
@@ -56,6 +57,9 @@ class MoEBlock:
     def __init__(self, T, H, I, E, k, device="cuda", scratch=None, eps=1e-5):
         self.T, self.H, self.I, self.E, self.k = T, H, I, E, k
         self.s = scratch if scratch is not None else Scratch(T, H, I, E, k, device)
+        if self.s.sizes != (T, H, I, E, k):
+            # the calls take their sizes from the scratch and would run past this block's tensors
+            raise ValueError(f"scratch made for T, H, I, E, k = {self.s.sizes}, block for {(T, H, I, E, k)}")
         self.norm = B.norm(T, H, eps=eps)
         R, dev = T * k, self.s.ws.device
         e = lambda *s, dt=BF16: torch.empty(*s, dtype=dt, device=dev)  # noqa: E731
