@@ -91,6 +91,7 @@ class MoEBlock:
         """(h, out) of x bf16 [T][H] (and residual); weights: gamma, beta bf16 [H], w_r bf16 [E][H],
         w_gu bf16 [E][2I][H], w_d bf16 [E][H][I].  Without a residual h is x itself."""
         s, w = self.s, weights
+        B._dense(w["w_r"], BF16, self.E * self.H)            # the router's call does not look at its tensors
         h = self.h if residual is not None else None
         B.moe_layernorm_fwd(self.norm, x, residual, w["gamma"], w["beta"], h, s.n, None, self.rstd, self.n_codes,
                             self.n_scales, stream)
@@ -106,6 +107,9 @@ class MoEBlock:
     def backward(self, dout, weights, stream=None):
         """From the gradient of h + out: dx (of x and of residual), and dgamma, dbeta, dw_r, dw_gu, dw_d."""
         s, w = self.s, weights
+        # the packing's and the router's calls do not look at their tensors; a gradient may well be expanded
+        B._pitched(dout, self.T, self.H, self.H, BF16)
+        B._dense(w["w_r"], BF16, self.E * self.H)
         self._pack(dout, s.drows, stream)
         B.moe_grouped_linear_dgrad(s.down, s.drows, self.split_sizes, w["w_d"], s.a, s.ws_linear, stream)
         B.moe_swiglu_bwd(None, self.gu_codes, self.gu_scales, self.prob_rows, s.a, s.dgu, s.dprob_rows, s.a, stream)
