@@ -74,6 +74,7 @@ class MoEBlock:
         self.h, self.out, self.dx = e(T, H), e(T, H), e(T, H)
         self.dgamma, self.dbeta, self.dw_r = e(H), e(H), e(E, H, dt=F32)
         self.dw_gu, self.dw_d = e(E, 2 * I, H), e(E, H, I)
+        self._kept = False                                   # nothing kept yet
 
     def kept_bytes(self) -> int:
         """Bytes that this block keeps between the passes."""
@@ -102,6 +103,7 @@ class MoEBlock:
         B.moe_swiglu_fwd(s.gu, self.prob_rows, s.a, self.gu_codes, self.gu_scales, stream)
         B.moe_grouped_linear_fwd(s.down, s.a, self.split_sizes, w["w_d"], s.rows, s.ws_linear, stream)
         B.moe_unpermute_combine(s.d, s.rows, self.pos_of, None, self.out, stream)
+        self._kept = True
         return (x if h is None else h), self.out
 
     def backward(self, dout, weights, stream=None):
@@ -110,6 +112,8 @@ class MoEBlock:
         # the packing's and the router's calls do not look at their tensors; a gradient may well be expanded
         B._pitched(dout, self.T, self.H, self.H, BF16)
         B._dense(w["w_r"], BF16, self.E * self.H)
+        if not self._kept:
+            raise RuntimeError("backward before forward: the rows' places are not set yet")
         self._pack(dout, s.drows, stream)
         B.moe_grouped_linear_dgrad(s.down, s.drows, self.split_sizes, w["w_d"], s.a, s.ws_linear, stream)
         B.moe_swiglu_bwd(None, self.gu_codes, self.gu_scales, self.prob_rows, s.a, s.dgu, s.dprob_rows, s.a, stream)

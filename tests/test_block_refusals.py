@@ -63,3 +63,10 @@ def test_router_weights(w_r):
         blk.forward(made(T, H), weights(*SIZES, w_r=w_r))
     with pytest.raises(ValueError):
         blk.backward(made(T, H), weights(*SIZES, w_r=w_r))
+
+
+def test_backward_before_forward():
+    """The places of the rows would be whatever the memory held, and rows would be written there."""
+    blk = MoEBlock(*SIZES, device="cpu")
+    with pytest.raises(RuntimeError, match="before forward"):
+        blk.backward(made(T, H), weights(*SIZES))
