@@ -673,7 +673,8 @@ size_t moe_grouped_linear_workspace_size(const moe_grouped* g);
  *   wgrad  dw[e] = sum_r dy[r] x[r]^T     dw [E][N][K], zeros for experts without rows
  * Row pitches ldx, ldy (of x or dx, and of y or dy) are multiples of 8.  A row holding NaN or
  * Inf changes its own y and dx and its expert's dw, nothing else.  A negative size or a sum above
- * rows is recorded in the error word (MOE_ERR_DEVICE_BOUNDS) and nothing is written.
+ * rows is recorded in the error word (MOE_ERR_DEVICE_BOUNDS) and nothing is written.  Waits on the device
+ * give up (MOE_ERR_DEVICE_TIMEOUT) after 2 s in which nothing moves, however long the call itself takes.
  */
 moe_status moe_grouped_linear_fwd(const moe_grouped* g, const void* x, int64_t ldx, const int32_t* split_sizes,
                                   const void* w, void* y, int64_t ldy, void* workspace, size_t workspace_bytes,
@@ -696,6 +697,17 @@ moe_status moe_grouped_linear_wgrad(const moe_grouped* g, const void* x, int64_t
  * overwritten.  The context stays usable afterwards. */
 moe_status moe_selftest_wait_timeout(void* scratch, size_t scratch_bytes, int64_t limit_ns, int32_t* code,
                                      int32_t* site, moe_stream_t stream);
+
+/* moe_selftest_grouped_linear_wait -- a grouped linear call whose waits on the device give up after
+ * limit_ns (1 ms .. 2 s) in place of 2 s; with loads = 0 its producers issue no loads, so that every wait
+ * runs out, MOE_ERR_DEVICE_TIMEOUT and a site in 700..709 are recorded and the call ends without its
+ * results.  op 0 forward: rows_in = x, other = w, out = y; 1 input gradient: rows_in = dy, other = w,
+ * out = dx; 2 weight gradient: rows_in = x, other = dy, out = dw.  ldx, ldy, sizes and workspace as for
+ * the calls themselves; rows >= 1.  The context stays usable afterwards. */
+moe_status moe_selftest_grouped_linear_wait(const moe_grouped* g, int32_t op, const void* rows_in, int64_t ldx,
+                                            const void* other, int64_t ldy, const int32_t* split_sizes, void* out,
+                                            int32_t loads, int64_t limit_ns, void* workspace, size_t workspace_bytes,
+                                            moe_stream_t stream);
 
 /*
  * moe_workspace_tensor -- where an intermediate tensor of the layer sits in a

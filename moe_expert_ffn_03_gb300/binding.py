@@ -26,6 +26,7 @@ EXPORTS = (
     "moe_gather_f32", "moe_layernorm_workspace_size", "moe_layernorm_fwd", "moe_layernorm_bwd", "moe_act8_pack",
     "moe_act8_unpack", "moe_swiglu_fwd", "moe_swiglu_bwd", "moe_grouped_linear_workspace_size",
     "moe_grouped_linear_fwd", "moe_grouped_linear_dgrad", "moe_grouped_linear_wgrad",
+    "moe_selftest_grouped_linear_wait",
 )
 
 # moe_ws_tensor ids (include/moe_ffn.h)
@@ -138,6 +139,7 @@ def lib() -> ctypes.CDLL:
             "moe_grouped_linear_fwd": ([G, P, I64, P, P, P, I64, P, c_size_t, P], c_int32),
             "moe_grouped_linear_dgrad": ([G, P, I64, P, P, P, I64, P, c_size_t, P], c_int32),
             "moe_grouped_linear_wgrad": ([G, P, I64, P, I64, P, P, P, c_size_t, P], c_int32),
+            "moe_selftest_grouped_linear_wait": ([G, c_int32, P, I64, P, I64, P, P, c_int32, I64, P, c_size_t, P], c_int32),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -493,3 +495,15 @@ def moe_grouped_linear_wgrad(g, x, dy, split_sizes, dw, workspace, stream=None):
                                           _dense(split_sizes, torch.int32, g.E),
                                           _dense(dw, torch.bfloat16, g.E * N * K), _p(workspace), _wsb(workspace),
                                           _st(stream)))
+
+
+def moe_selftest_grouped_linear_wait(g, op, rows_in, other, split_sizes, out, workspace, loads, limit_ns, stream=None):
+    """A grouped linear call (op 0 forward, 1 input gradient, 2 weight gradient) under another limit of its
+    waits, with or without its loads."""
+    R, K, N, b16 = g.rows, g.K, g.N, torch.bfloat16
+    x, dy = (out, rows_in) if op == 1 else (rows_in, other if op == 2 else out)
+    ldx, ldy = _ld(x, R, K), _ld(dy, R, N)
+    _dense(other if op < 2 else out, b16, g.E * N * K)
+    _check(lib().moe_selftest_grouped_linear_wait(ctypes.byref(g), op, _p(rows_in), ldx, _p(other), ldy,
+                                                  _dense(split_sizes, torch.int32, g.E), _p(out), int(loads),
+                                                  int(limit_ns), _p(workspace), _wsb(workspace), _st(stream)))

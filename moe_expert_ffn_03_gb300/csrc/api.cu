@@ -1334,8 +1334,11 @@ moe_status check_grouped_call(const moe_grouped* g, int64_t ldx, int64_t ldy, co
 }
 
 moe_status run_grouped(int mode, const moe_grouped* g, const void* x, int64_t ldx, const void* dy, int64_t ldy,
-                       const int32_t* split_sizes, const void* w, void* out, int64_t ldo, void* ws, cudaStream_t st) {
+                       const int32_t* split_sizes, const void* w, void* out, int64_t ldo, void* ws, cudaStream_t st,
+                       uint64_t wait_limit_ns = kWaitLimitNs, bool no_loads = false) {
   LinearArgs a{};
+  a.wait_limit_ns = wait_limit_ns;
+  a.selftest_no_loads = no_loads;
   a.rows = g->rows;
   a.E = g->E;
   a.K = g->K;
@@ -1600,6 +1603,24 @@ moe_status moe_selftest_wait_timeout(void* scratch, size_t scratch_bytes, int64_
   *code = h[0];
   *site = h[1];
   return MOE_OK;
+}
+
+moe_status moe_selftest_grouped_linear_wait(const moe_grouped* g, int32_t op, const void* rows_in, int64_t ldx,
+                                            const void* other, int64_t ldy, const int32_t* split_sizes, void* out,
+                                            int32_t loads, int64_t limit_ns, void* workspace, size_t workspace_bytes,
+                                            moe_stream_t stream) {
+  if (moe_status s = check_grouped_call(g, ldx, ldy, workspace, workspace_bytes); s != MOE_OK) return s;
+  if (op < LIN_FWD || op > LIN_WGRAD) return fail(MOE_ERR_INVALID_ARG, "op=%d must be in 0..2", op);
+  if (limit_ns < 1000000 || limit_ns > 2000000000) return fail(MOE_ERR_INVALID_ARG, "limit_ns must be in [1 ms, 2 s]");
+  if (g->rows == 0) return fail(MOE_ERR_INVALID_ARG, "rows must be >= 1");
+  REQUIRE_PTR(rows_in);
+  REQUIRE_PTR(other);
+  REQUIRE_PTR(split_sizes);
+  REQUIRE_PTR(out);
+  const bool dgrad = op == LIN_DGRAD, wgrad = op == LIN_WGRAD;
+  return run_grouped(op, g, dgrad ? nullptr : rows_in, ldx, dgrad ? rows_in : other, ldy, split_sizes, other, out,
+                     wgrad ? g->K : dgrad ? ldx : ldy, workspace, static_cast<cudaStream_t>(stream), uint64_t(limit_ns),
+                     loads == 0);
 }
 
 moe_status moe_workspace_tensor(const moe_dims* d, int32_t training, int32_t which, size_t* offset, size_t* bytes) {

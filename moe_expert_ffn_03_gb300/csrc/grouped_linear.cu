@@ -40,7 +40,10 @@
 // piece adds the f32 partial sums from the workspace in the order of the contraction, so
 // results do not depend on timing; nobody waits for anybody.  A kernel of its own: the code that
 // puts pieces together costs the others' main loops 2 to 5% by being there.
-// Every wait is bounded.
+// Every wait is bounded.  The epilogue's wait for an accumulator lasts as long as a tile's contraction,
+// warp 18's for a tail stage as long as all tiles without one before it, and in wgrad both have no upper
+// limit but the number of rows (2^30 rows on one pair take seconds).  So their limit starts anew with
+// every stage that the producer finds free again: they give up when nothing moves.
 //
 // Many rows are bound by the tensor pipe under the power limit: 32768 rows, K = 4096, N = 28672, E = 8,
 // forward 4738 us, dgrad 4720, wgrad 4637 (1.62, 1.63, 1.66 PFLOP/s); 196608 rows, 2048 -> 2816, E = 64:
@@ -113,20 +116,46 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
   return ok != 0;
 }
 __device__ __noinline__ bool wait_phase_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
-                                                int site) {
+                                                int site, uint64_t limit_ns) {
   uint64_t t0 = 0;                               // as wait_phase
   for (uint32_t n = 1; !mbar_try_wait_cluster(bar, parity); ++n) {
     if ((n & 255u) != 0) continue;
     if (*abort_flag) return false;
     const uint64_t now = globaltimer_ns();
     if (t0 == 0) t0 = now;
-    if (now - t0 > kWaitLimitNs) {
+    if (now - t0 > limit_ns) {
       report_error(err, MOE_ERR_DEVICE_TIMEOUT, site);
       *abort_flag = 1;
       return false;
     }
   }
   return true;
+}
+// wait_phase_warp for waits across many stages: limit_ns without a change of *stages_used.
+__device__ __noinline__ bool wait_phase_warp_moving(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
+                                                    int site, uint64_t limit_ns, const volatile uint32_t* stages_used) {
+  uint64_t t0 = 0;
+  uint32_t seen = 0;
+  bool ok = true;
+  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+    if ((n & 255u) != 0) continue;
+    if (*abort_flag) {
+      ok = false;
+      break;
+    }
+    const uint64_t now = globaltimer_ns();
+    const uint32_t used = *stages_used;
+    if (t0 == 0 || used != seen) {
+      t0 = now;
+      seen = used;
+    } else if (now - t0 > limit_ns) {
+      report_error(err, MOE_ERR_DEVICE_TIMEOUT, site);
+      *abort_flag = 1;
+      ok = false;
+      break;
+    }
+  }
+  return __all_sync(0xFFFFFFFFu, ok);
 }
 
 // Whether a phase has completed, without waiting.
@@ -335,6 +364,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
   uint32_t* tmem_base_s = reinterpret_cast<uint32_t*>(smem + LG_OFF_MISC);
   volatile int* abort_s = reinterpret_cast<volatile int*>(smem + LG_OFF_MISC + 4);
   volatile int* bad_s = reinterpret_cast<volatile int*>(smem + LG_OFF_MISC + 8);
+  volatile uint32_t* stages_used = reinterpret_cast<volatile uint32_t*>(smem + LG_OFF_MISC + 12);
   int* row0 = reinterpret_cast<int*>(smem + LG_OFF_SEG);
   int* tile0 = row0 + LG_MAX_E + 1;
   int* order = tile0 + LG_MAX_E + 1;
@@ -357,6 +387,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
     }
     mbar_init(drain, 1);
     *abort_s = 0;
+    *stages_used = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmB);
@@ -440,13 +471,15 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
   // inconsistent split_sizes: nothing is computed (the error word says so)
   const int total = *bad_s ? 0 : lin_tiles<MODE>(args, tile0);
   const Plan plan = lin_plan<MODE, CUT>(args, total, num_pairs);
+  const uint64_t lim = args.wait_limit_ns;
 
   if (warp == 0 || warp == 19) {
-    if (lane == 0) {
+    if (lane == 0 && !args.selftest_no_loads) {
       // ---------------- TMA producers (both CTAs): warp 0 the M side, warp 19 the N side ----------------
       const bool m_side = warp == 0;
       const uint32_t full_c0 = mapa_shared(smem_u32(full), 0);
       Cursor cur;
+      uint32_t used = 0;
       bool ok = true;
       int next = pair;
       for (LinTile tl; ok && lin_next<MODE, CUT>(args, row0, tile0, order, plan, pair, num_pairs, next, tl);) {
@@ -457,10 +490,11 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         const int nb = half > 128 ? 2 : 1;       // 128-wide parts of the N side
         const uint32_t bytes = LG_TILE + (small ? uint32_t(B_MN ? LG_BLOCK : LG_SMALL * 128) : uint32_t(nb * LG_TILE));
         for (int kt = 0; kt < tl.steps; ++kt, cur.next(stages)) {
-          if (!wait_phase(&empty[cur.st], cur.ph ^ 1u, abort_s, args.err, SITE_LINEAR, kWaitLimitNs)) {
+          if (!wait_phase(&empty[cur.st], cur.ph ^ 1u, abort_s, args.err, SITE_LINEAR, lim)) {
             ok = false;
             break;
           }
+          if (MODE == LIN_WGRAD && m_side) *stages_used = ++used;
           // both CTAs' copies complete on the leader's full barrier; those of a tail stage on each
           // CTA's tail barrier, since each clears its own rows (full then only advances its phase)
           uint32_t bar_c = full_c0 + uint32_t(cur.st) * 8u;
@@ -542,7 +576,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         const uint32_t id0 = lg_idesc(A_MN, B_MN, tl.cols(0)), id1 = lg_idesc(A_MN, B_MN, tl.cols(1));
         const uint32_t par1 = (((ac + 1) >> 1) & 1) ^ 1;
         const int last_groups = min(LG_KT, tl.c_cnt - (tl.k0 + tl.steps - 1) * LG_KT) + 15 >> 4;
-        if (!wait_phase(&tmem_empty[b0], ((ac >> 1) & 1) ^ 1, abort_s, args.err, SITE_LINEAR + 1, kWaitLimitNs)) {
+        if (!wait_phase(&tmem_empty[b0], ((ac >> 1) & 1) ^ 1, abort_s, args.err, SITE_LINEAR + 1, lim)) {
           ok = false;
           break;
         }
@@ -551,13 +585,13 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
         Cursor behind = cur;
         tc_fence_after();
         for (int kt = 0; kt < tl.steps; ++kt) {
-          if (!ready && !wait_phase(&full[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR + 2, kWaitLimitNs)) {
+          if (!ready && !wait_phase(&full[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR + 2, lim)) {
             ok = false;
             break;
           }
           const int st = cur.st;
           if (lin_tail<MODE>(tl) && kt + 1 == tl.steps) {
-            if (!wait_phase_cluster(&cleared[st], (cleared_par >> st) & 1u, abort_s, args.err, SITE_LINEAR + 3)) {
+            if (!wait_phase_cluster(&cleared[st], (cleared_par >> st) & 1u, abort_s, args.err, SITE_LINEAR + 3, lim)) {
               ok = false;
               break;
             }
@@ -571,7 +605,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
           issued = true;
           if (kt < lead) {
             if (kt + 1 < lead) continue;
-            if (!wait_phase(&tmem_empty[b1], par1, abort_s, args.err, SITE_LINEAR + 1, kWaitLimitNs)) {
+            if (!wait_phase(&tmem_empty[b1], par1, abort_s, args.err, SITE_LINEAR + 1, lim)) {
               ok = false;
               break;
             }
@@ -621,7 +655,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
       const int accs = tl.accs();
       for (int h = 0; h < accs; ++h, ++ac) {
         const int ab = ac & 1;
-        if (!wait_phase_warp(&tmem_full[ab], (ac >> 1) & 1, abort_s, args.err, SITE_LINEAR + 4, kWaitLimitNs)) {
+        if (!wait_phase_warp_moving(&tmem_full[ab], (ac >> 1) & 1, abort_s, args.err, SITE_LINEAR + 4, lim, stages_used)) {
           ok = false;
           break;
         }
@@ -685,7 +719,7 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
       // warp would take an older phase of the same parity for the one it wants; so tail stages
       // have barriers of their own)
       const int st = (at - 1) % stages;
-      ok = wait_phase_warp(&tail[st], (par >> st) & 1u, abort_s, args.err, SITE_LINEAR + 5, kWaitLimitNs);
+      ok = wait_phase_warp_moving(&tail[st], (par >> st) & 1u, abort_s, args.err, SITE_LINEAR + 5, lim, stages_used);
       if (!ok) break;
       par ^= 1u << st;
       const int valid = tl.c_cnt - (tl.steps - 1) * LG_KT;       // the stage's rows

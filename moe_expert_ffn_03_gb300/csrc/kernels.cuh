@@ -227,6 +227,8 @@ struct LinearArgs {
   __nv_bfloat16* out;        // FWD y [rows][N], DGRAD dx [rows][K], WGRAD dw [E][N][K]
   int64_t ldo;
   int* err;
+  uint64_t wait_limit_ns;    // of every bounded wait
+  int selftest_no_loads;     // the producers issue nothing
   int tn;                    // set by launch_grouped_linear: columns of a tile (64, 128, 256 or 512) and,
   unsigned* arrived;         // of the workspace, the arrivals and partial sums of cut tiles
   float* pieces;
