@@ -586,8 +586,12 @@ size_t moe_layernorm_workspace_size(const moe_norm* n);
  *   y             out [rows][H] at pitch ld_out
  *   mean, rstd    out f32 [rows], each may be NULL
  *   codes,scales  both set or both NULL: out act8 of (h - mean) * rstd
+ * Finite rows have the norm of its definition also where float32 cannot hold their sum or variance; what
+ * passes the output's range there is Inf, as a rstd above 3.4e38 with eps = 0.  A row with a NaN or an Inf
+ * gives NaN throughout (mean: NaN or that Inf).
  * h and y must not overlap x and residual, except that h may be x or residual itself when
- * ld_in = ld_out (each row is read before it is written).
+ * ld_in = ld_out (each row is read before it is written; a bf16 row whose variance float32 cannot hold, or
+ * only just, is then normalised as stored in h).
  */
 moe_status moe_layernorm_fwd(const moe_norm* n, const void* x, const void* residual, const void* gamma,
                              const void* beta, void* h, void* y, float* mean, float* rstd, uint8_t* codes,

@@ -30,11 +30,6 @@ __device__ __forceinline__ void v_sigmoid(float* s, const float* g) {
 #pragma unroll
   for (int j = 0; j < VEC; ++j) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s[j]) : "f"(1.f + __expf(-g[j])));
 }
-template <int VEC>
-__device__ __forceinline__ void v_copy(float* a, const float* b) {
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) a[j] = b[j];
-}
 
 // A thread's place in a row that tpr threads walk: its row, whether there is one, its first column.
 struct RowPlace {

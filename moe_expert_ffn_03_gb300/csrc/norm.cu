@@ -8,9 +8,12 @@
 //
 // Everything between the loads and the stores is float32: the variance is that of the centred
 // values (a second pass over registers), and the sum h is normalised before it is rounded.
+// Where a row's sum or squares would leave float32's range, the row is worked on times a power of two,
+// which changes no quotient: every finite row has the norm of its definition.
 // Each activation is read once and written once; wide rows are held by the instructions per vector
 // and their latency at 16 warps an SM before they are held by memory.
 #include <atomic>
+#include <cfloat>
 #include <type_traits>
 
 #include "kernels.cuh"
@@ -63,11 +66,115 @@ __device__ __forceinline__ float mean_of(float s, float H, float inv_H) {
   const float q = s * inv_H;
   return fmaf(fmaf(-q, H, s), inv_H, q);
 }
-// 1 / sqrt(v), with a Newton step after the approximate instruction (v = 0 gives Inf).
+// 1 / sqrt(v), with a Newton step after the approximate instruction (0 gives Inf, Inf gives 0).
 __device__ __forceinline__ float inv_sqrt(float v) {
   const float r = rsqrtf(v);
   const float n = r * fmaf(-0.5f * v * r, r, 1.5f);
-  return v > 0.f ? n : r;
+  return v > 0.f && r > 0.f ? n : r;
+}
+// Factors for rows whose variance (with eps) is above float32's range or below 2^-120.  LARGE on the row
+// as it came: values below 2^48, squares whose sum stays below 2^112, and as long as the row is not
+// constant a variance above 2^-60.  SMALL on the centred values, which are below 2^-53 then: their
+// squares are normal numbers down to the smallest subnormal value's.
+constexpr float LARGE = 0x1p-80f, SMALL = 0x1p100f;
+__device__ __forceinline__ bool in_range(float var) { return var >= 0x1p-120f && var <= FLT_MAX; }
+
+// The rows of this thread's row group whose variance (with eps) is above float32's range or below 2^-120,
+// once more, on times a power of two.  A loop of its own behind the kernel's: with these rows' work in
+// that loop, in line or called, all others took 3 to 13% longer.  Everything is read again from memory.
+// Where h has taken the place of x or the residual by then, the row is h as stored; in bf16 its variance
+// is not quite the sum's, so that rows near the bounds are taken along.
+template <typename T, int VEC, int NV>
+__device__ __noinline__ void norm_fwd_rescaled(const NormArgs& a, int tpr, float* buf0, float* buf1, float* buf2) {
+  const Place<VEC, NV, 2, 0> at(tpr, nullptr);
+  const float inv_H = 1.f / float(a.H);
+  const bool summed = a.h != nullptr && (a.h == a.x || a.h == a.residual);
+  const T* x = static_cast<const T*>(summed ? a.h : a.x);
+  const T* res = static_cast<const T*>(summed ? nullptr : a.residual);
+  float h[NV][VEC], w[VEC], sum[VEC];
+  const auto total = [&](float* buf) {
+    float s[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) s[0] += sum[j];
+    row_sum<1>(s, tpr, at.group, buf);
+    return s[0];
+  };
+  // h = the row times f, and its sum per thread
+  const auto load = [&](int64_t row, float f) {
+    v_fill<VEC>(w, f);
+    v_fill<VEC>(sum, 0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      v_fill<VEC>(h[i], 0.f);
+      if (at.col(i) >= a.H) continue;
+      Raw<T, VEC> r;
+      r.load(x + row * a.ld_in + at.col(i));
+      r.get(h[i]);
+      if (res != nullptr) {
+        float v[VEC];
+        r.load(res + row * a.ld_in + at.col(i));
+        r.get(v);
+        v_add<VEC>(h[i], v);
+      }
+      v_mul<VEC>(h[i], w);
+      v_add<VEC>(sum, h[i]);
+    }
+  };
+  // h = (h - mu) * f, and its squares' sum per thread
+  const auto centre = [&](float mu, float f) {
+    v_fill<VEC>(w, f);
+    v_fill<VEC>(sum, 0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float minus[VEC];
+      v_fill<VEC>(minus, at.col(i) < a.H ? -mu : 0.f);
+      v_add<VEC>(h[i], minus);
+      v_mul<VEC>(h[i], w);
+      v_fma<VEC>(sum, h[i], h[i]);
+    }
+  };
+  for (int64_t row = int64_t(blockIdx.x) * at.groups + at.group; row < a.rows; row += int64_t(gridDim.x) * at.groups) {
+    load(row, 1.f);
+    float mean = mean_of(total(buf0), float(a.H), inv_H);
+    centre(mean, 1.f);
+    const float var = total(buf1) * inv_H + a.eps;
+    if (summed ? var >= 0x1p-119f && var <= 0x1p127f : in_range(var)) continue;
+    float f = SMALL;
+    if (!(var < 1.f)) {
+      f = LARGE;
+      load(row, LARGE);
+      const float s = total(buf2), mu = fabsf(s) <= FLT_MAX ? mean_of(s, float(a.H), inv_H) : s;
+      mean = mu * (1.f / LARGE);
+      centre(mu, 1.f);
+    } else {
+      centre(0.f, SMALL);
+    }
+    const float squares = total(f == LARGE ? buf1 : buf2);
+    float rstd = inv_sqrt(squares * inv_H + a.eps * f * f);        // of the row as it is held
+    if (at.t == 0) {
+      if (a.mean != nullptr) a.mean[row] = mean;
+      if (a.rstd != nullptr) a.rstd[row] = squares == 0.f ? inv_sqrt(a.eps) : rstd * f;
+    }
+    if (squares == 0.f && a.eps > 0.f) rstd = 0.f;                 // eps * f * f may have gone under
+    T* y = static_cast<T*>(a.y) + row * a.ld_out + at.col0;
+    uint8_t* codes = a.codes + row * a.H + at.col0;
+    uint8_t* scales = a.scales + row * ((a.H + 31) >> 5) + (at.col0 >> 5);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const bool in = at.col(i) < a.H;
+      v_fill<VEC>(w, rstd);
+      v_mul<VEC>(h[i], w);
+      if (a.codes != nullptr)
+        store_act8<VEC>(h[i], in, codes + i * (32 * VEC), scales + i * VEC, (at.col0 & 31) == 0);
+      if (!in) continue;
+      float b[VEC];
+      v_fill<VEC>(b, 0.f);
+      load_weight<VEC>(a.gamma, a.w_f32, at.col(i), w);
+      if (a.beta != nullptr) load_weight<VEC>(a.beta, a.w_f32, at.col(i), b);
+      v_fma<VEC>(b, h[i], w);
+      store_vec<VEC>(y + i * (32 * VEC), b);
+    }
+  }
 }
 
 // A persistent grid: block b takes the row groups b, b + grid, ...  The next groups' x (and
@@ -76,9 +183,9 @@ __device__ __forceinline__ float inv_sqrt(float v) {
 // 32768 x 2048 bf16 with residual and checkpoint: 100 us, 6.1 TB/s.  Single columns are bound by their
 // narrow loads (8192 x 5001: 2.0 TB/s).
 template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(max_block(VEC), 1) norm_fwd_kernel(const NormArgs a, int tpr) {
+__global__ void __launch_bounds__(max_block(VEC), 1) norm_fwd_kernel(const __grid_constant__ NormArgs a, int tpr) {
   constexpr int STG = ring_stages(VEC, 2 * NV);
-  __shared__ float sums[2][32];
+  __shared__ float sums[3][32];
   extern __shared__ __align__(16) uint8_t ring[];
   const Place<VEC, NV, 2, STG> at(tpr, ring);
   const float inv_H = 1.f / float(a.H);
@@ -106,6 +213,7 @@ __global__ void __launch_bounds__(max_block(VEC), 1) norm_fwd_kernel(const NormA
   for (int k = 0; k + 1 < STG; ++k) fetch(row + k * step, k);
   const Weight<VEC, NV> gamma(a.gamma, a.w_f32, at.col0, a.H), beta(a.beta, a.w_f32, at.col0, a.H);
   int st = 0;
+  bool odd = false;                               // the same in all of a row group's threads
   for (; row < a.rows; row += step) {             // the rows' groups go on independently of one another
     if constexpr (VEC > 1) {
       fetch(row + (STG - 1) * step, st == 0 ? STG - 1 : st - 1);
@@ -160,7 +268,8 @@ __global__ void __launch_bounds__(max_block(VEC), 1) norm_fwd_kernel(const NormA
 #pragma unroll
     for (int j = 0; j < VEC; ++j) s[0] += sq[j];
     row_sum<1>(s, tpr, at.group, sums[1]);
-    const float rstd = inv_sqrt(s[0] * inv_H + a.eps);
+    const float var = s[0] * inv_H + a.eps, rstd = inv_sqrt(var);
+    odd |= !in_range(var);
     if (at.t == 0) {
       if (a.mean != nullptr) a.mean[row] = mu;
       if (a.rstd != nullptr) a.rstd[row] = rstd;
@@ -185,6 +294,7 @@ __global__ void __launch_bounds__(max_block(VEC), 1) norm_fwd_kernel(const NormA
       }
     }
   }
+  if (odd) norm_fwd_rescaled<T, VEC, NV>(a, tpr, sums[0], sums[1], sums[2]);
 }
 
 // A persistent grid and a ring as in the forward pass.  A thread keeps its columns' sums of
@@ -258,6 +368,9 @@ __global__ void __launch_bounds__(max_block(VEC), 1) norm_bwd_kernel(const NormA
     const Small m = next;
     if constexpr (VEC > 1) fetch(row + (STG - 1) * step, st == 0 ? STG - 1 : st - 1);
     next = fetch_small(row + step);
+    // n from halves where x - mean could overflow (x is below 2^128, and a mean up to 2^100 does not move it)
+    const bool halve = !Q8 && fabsf(m.mu) > 0x1p100f;
+    const float minus_mu = halve ? -0.5f * m.mu : -m.mu, scale = halve ? 2.f * m.rstd : m.rstd;
     if constexpr (VEC > 1) cp_async_wait<STG - 1>();
     // dy and the normalised values (0 past the row's end) of vector i
     const auto get = [&](int i, float* d, float* n) {
@@ -294,8 +407,12 @@ __global__ void __launch_bounds__(max_block(VEC), 1) norm_bwd_kernel(const NormA
       }
       if constexpr (!Q8) {
         float minus[VEC], rs[VEC];
-        v_fill<VEC>(minus, in ? -m.mu : 0.f);
-        v_fill<VEC>(rs, m.rstd);
+        if (halve) {
+          v_fill<VEC>(rs, 0.5f);
+          v_mul<VEC>(n, rs);
+        }
+        v_fill<VEC>(minus, in ? minus_mu : 0.f);
+        v_fill<VEC>(rs, scale);
         v_add<VEC>(n, minus);
         v_mul<VEC>(n, rs);
       }

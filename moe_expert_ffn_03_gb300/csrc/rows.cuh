@@ -174,6 +174,11 @@ __device__ __forceinline__ void v_fill(float* a, float x) {
 #pragma unroll
   for (int j = 0; j < VEC; ++j) a[j] = x;
 }
+template <int VEC>
+__device__ __forceinline__ void v_copy(float* a, const float* b) {
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) a[j] = b[j];
+}
 // Largest |v| as float bits; a NaN or Inf among the values gives an exponent field of 255.
 template <int VEC>
 __device__ __forceinline__ uint32_t v_amax(const float* v) {
