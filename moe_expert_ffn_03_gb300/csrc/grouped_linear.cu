@@ -131,8 +131,9 @@ __device__ __noinline__ bool wait_phase_cluster(uint64_t* bar, uint32_t parity, 
   }
   return true;
 }
-// wait_phase_warp for waits across many stages: limit_ns without a change of *stages_used.
-__device__ __noinline__ bool wait_phase_warp_moving(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
+// wait_phase_warp for waits across many stages: limit_ns without a change of *stages_used.  In line, since
+// the epilogue's wait is on a short call's path (wgrad of 64 rows over 64 experts 102.8 -> 99.6 us).
+__device__ __forceinline__ bool wait_phase_warp_moving(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
                                                     int site, uint64_t limit_ns, const volatile uint32_t* stages_used) {
   uint64_t t0 = 0;
   uint32_t seen = 0;
@@ -737,9 +738,10 @@ __global__ void __launch_bounds__(LG_THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (*abort_s) {
+  if (warp == 0 && *abort_s) {
     // A wait gave up in this CTA, of whichever warp: copies issued before, by producers that may have
-    // finished since, land before the shared memory goes (they take microseconds; bounded).
+    // finished since, land before the shared memory goes (they take microseconds; bounded).  The others
+    // wait for this warp at the cluster's barrier.
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 2000000ull) {
     }

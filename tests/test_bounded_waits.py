@@ -51,7 +51,7 @@ def test_copies_land_after_any_wait_gave_up():
     for file, kernel in (("grouped_linear.cu", "grouped_linear_kernel"), ("gemm.cu", "grouped_gemm_kernel")):
         body = kernel_body(sources()[file], kernel)
         end = body[body.rindex("__syncthreads();"):]
-        assert re.search(r"if \(\*abort_s\) \{[^}]*globaltimer_ns\(\)", end), kernel
+        assert re.search(r"if \((?:warp == 0 && )?\*abort_s\) \{[^}]*globaltimer_ns\(\)", end), kernel
         assert end.index("*abort_s") < end.index("cluster_sync();") < end.index("tmem_dealloc"), kernel
 
 
