@@ -374,7 +374,8 @@ def fp8_tensor_quantize_experts(w_list, rows, cols, codes, amax, stream=None):
 
 # ---- operators around the layer ------------------------------------------------------------------
 # Row pitches and element types are read off the tensors.  What the library cannot see -- types,
-# shapes, dense rows -- is checked here, since a mismatch would read past a tensor's end.
+# shapes, dense rows, devices -- is checked here, since a mismatch would read past a tensor's end or
+# where no tensor of this GPU is.
 _ROW_TYPES = (torch.bfloat16, torch.float32)
 
 
@@ -408,6 +409,17 @@ def _pitched(t, rows, cols, ld, dtype):
     return t.data_ptr()
 
 
+def _on(stream, *tensors):
+    """Handle of the stream of a call whose tensors all have to be on the current GPU."""
+    dev = None
+    for t in tensors:
+        if t is not None and (d := t.get_device()) != dev:
+            if dev is not None or d < 0 or d != torch._C._cuda_getDevice():
+                raise ValueError(f"tensor on {t.device}: all of a call's tensors have to be on the current GPU")
+            dev = d
+    return _st(None) if dev is None else torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
 def _act8_scales(cols):
     return (cols + 31) // 32
 
@@ -423,7 +435,7 @@ def moe_layernorm_fwd(n, x, residual, gamma, beta, h, y, mean, rstd, codes=None,
                                    _dense(gamma, w, H), _dense(beta, w, H), _pitched(h, R, H, n.ld_out, t),
                                    _pitched(y, R, H, n.ld_out, t), _dense(mean, f32, R), _dense(rstd, f32, R),
                                    _dense(codes, torch.uint8, R * H), _dense(scales, torch.uint8, R * _act8_scales(H)),
-                                   _st(stream)))
+                                   _on(stream, x, residual, gamma, beta, h, y, mean, rstd, codes, scales)))
 
 
 def moe_layernorm_bwd(n, dy, x, mean, rstd, codes, scales, gamma, dres, dx, dgamma, dbeta, workspace, stream=None):
@@ -435,7 +447,9 @@ def moe_layernorm_bwd(n, dy, x, mean, rstd, codes, scales, gamma, dres, dx, dgam
                                    _dense(codes, torch.uint8, R * H), _dense(scales, torch.uint8, R * _act8_scales(H)),
                                    _dense(gamma, w, H), _pitched(dres, R, H, n.ld_in, t),
                                    _pitched(dx, R, H, n.ld_out, t), _dense(dgamma, w, H), _dense(dbeta, w, H),
-                                   _p(workspace), _wsb(workspace), _st(stream)))
+                                   _p(workspace), _wsb(workspace),
+                                   _on(stream, dy, x, None if x is None else mean, rstd, codes, scales, gamma, dres, dx,
+                                       dgamma, dbeta, workspace)))
 
 
 def moe_act8_pack(src, codes, scales, stream=None):
@@ -443,7 +457,7 @@ def moe_act8_pack(src, codes, scales, stream=None):
     f32 = src.dtype == torch.float32
     _check(lib().moe_act8_pack(_p(src), int(f32), rows, cols, _ld(src, rows, cols, _ROW_TYPES[f32]),
                                _dense(codes, torch.uint8, rows * cols),
-                               _dense(scales, torch.uint8, rows * _act8_scales(cols)), _st(stream)))
+                               _dense(scales, torch.uint8, rows * _act8_scales(cols)), _on(stream, src, codes, scales)))
 
 
 def moe_act8_unpack(codes, scales, gamma, beta, dst, stream=None):
@@ -452,14 +466,16 @@ def moe_act8_unpack(codes, scales, gamma, beta, dst, stream=None):
     _check(lib().moe_act8_unpack(_dense(codes, torch.uint8, rows * cols),
                                  _dense(scales, torch.uint8, rows * _act8_scales(cols)), rows, cols,
                                  _dense(gamma, _ROW_TYPES[w_f32], cols), _dense(beta, _ROW_TYPES[w_f32], cols),
-                                 int(w_f32), _p(dst), int(f32), _ld(dst, rows, cols, _ROW_TYPES[f32]), _st(stream)))
+                                 int(w_f32), _p(dst), int(f32), _ld(dst, rows, cols, _ROW_TYPES[f32]),
+                                 _on(stream, codes, scales, gamma, beta, dst)))
 
 
 def moe_swiglu_fwd(gu, prob, a, codes=None, scales=None, stream=None):
     rows, I = a.shape
     _check(lib().moe_swiglu_fwd(rows, I, _p(gu), _ld(gu, rows, 2 * I), _dense(prob, torch.float32, rows), _p(a),
                                 _ld(a, rows, I), _dense(codes, torch.uint8, rows * 2 * I),
-                                _dense(scales, torch.uint8, rows * 2 * _act8_scales(I)), _st(stream)))
+                                _dense(scales, torch.uint8, rows * 2 * _act8_scales(I)),
+                                _on(stream, gu, prob, a, codes, scales)))
 
 
 def moe_swiglu_bwd(gu, codes, scales, prob, da, dgu, dprob=None, a=None, stream=None):
@@ -468,7 +484,7 @@ def moe_swiglu_bwd(gu, codes, scales, prob, da, dgu, dprob=None, a=None, stream=
                                 _dense(scales, torch.uint8, rows * 2 * _act8_scales(I)),
                                 _dense(prob, torch.float32, rows), _p(da), _ld(da, rows, I), _p(dgu),
                                 _ld(dgu, rows, 2 * I), _dense(dprob, torch.float32, rows), _p(a), _ld(a, rows, I),
-                                _st(stream)))
+                                _on(stream, gu, codes, scales, prob, da, dgu, dprob, a)))
 
 
 def moe_grouped_linear_workspace_size(g: MoeGrouped) -> int:
@@ -479,14 +495,14 @@ def moe_grouped_linear_fwd(g, x, split_sizes, w, y, workspace, stream=None):
     R, K, N = g.rows, g.K, g.N
     _check(lib().moe_grouped_linear_fwd(ctypes.byref(g), _p(x), _ld(x, R, K), _dense(split_sizes, torch.int32, g.E),
                                         _dense(w, torch.bfloat16, g.E * N * K), _p(y), _ld(y, R, N), _p(workspace),
-                                        _wsb(workspace), _st(stream)))
+                                        _wsb(workspace), _on(stream, x, split_sizes, w, y, workspace)))
 
 
 def moe_grouped_linear_dgrad(g, dy, split_sizes, w, dx, workspace, stream=None):
     R, K, N = g.rows, g.K, g.N
     _check(lib().moe_grouped_linear_dgrad(ctypes.byref(g), _p(dy), _ld(dy, R, N), _dense(split_sizes, torch.int32, g.E),
                                           _dense(w, torch.bfloat16, g.E * N * K), _p(dx), _ld(dx, R, K), _p(workspace),
-                                          _wsb(workspace), _st(stream)))
+                                          _wsb(workspace), _on(stream, dy, split_sizes, w, dx, workspace)))
 
 
 def moe_grouped_linear_wgrad(g, x, dy, split_sizes, dw, workspace, stream=None):
@@ -494,7 +510,7 @@ def moe_grouped_linear_wgrad(g, x, dy, split_sizes, dw, workspace, stream=None):
     _check(lib().moe_grouped_linear_wgrad(ctypes.byref(g), _p(x), _ld(x, R, K), _p(dy), _ld(dy, R, N),
                                           _dense(split_sizes, torch.int32, g.E),
                                           _dense(dw, torch.bfloat16, g.E * N * K), _p(workspace), _wsb(workspace),
-                                          _st(stream)))
+                                          _on(stream, x, dy, split_sizes, dw, workspace)))
 
 
 def moe_selftest_grouped_linear_wait(g, op, rows_in, other, split_sizes, out, workspace, loads, limit_ns, stream=None):
@@ -506,4 +522,5 @@ def moe_selftest_grouped_linear_wait(g, op, rows_in, other, split_sizes, out, wo
     _dense(other if op < 2 else out, b16, g.E * N * K)
     _check(lib().moe_selftest_grouped_linear_wait(ctypes.byref(g), op, _p(rows_in), ldx, _p(other), ldy,
                                                   _dense(split_sizes, torch.int32, g.E), _p(out), int(loads),
-                                                  int(limit_ns), _p(workspace), _wsb(workspace), _st(stream)))
+                                                  int(limit_ns), _p(workspace), _wsb(workspace),
+                                                  _on(stream, rows_in, other, split_sizes, out, workspace)))

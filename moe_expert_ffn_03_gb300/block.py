@@ -96,6 +96,7 @@ class MoEBlock:
         h = self.h if residual is not None else None
         B.moe_layernorm_fwd(self.norm, x, residual, w["gamma"], w["beta"], h, s.n, None, self.rstd, self.n_codes,
                             self.n_scales, stream)
+        B._on(stream, w["w_r"])
         B.moe_router_fwd(s.d, s.n, w["w_r"], self.logits, s.ws, stream)
         B.moe_route(s.d, self.logits, self.idx, self.prob, self.split_sizes, self.row_of, s.src_of, s.prob_perm, s.ws, stream)
         self._pack(s.n, s.rows, stream)
@@ -114,6 +115,7 @@ class MoEBlock:
         B._dense(w["w_r"], BF16, self.E * self.H)
         if not self._kept:
             raise RuntimeError("backward before forward: the rows' places are not set yet")
+        B._on(stream, dout, w["w_r"])
         self._pack(dout, s.drows, stream)
         B.moe_grouped_linear_dgrad(s.down, s.drows, self.split_sizes, w["w_d"], s.a, s.ws_linear, stream)
         B.moe_swiglu_bwd(None, self.gu_codes, self.gu_scales, self.prob_rows, s.a, s.dgu, s.dprob_rows, s.a, stream)
