@@ -11,9 +11,9 @@ Forward:  moe_layernorm_fwd -> moe_router_fwd -> moe_route -> moe_ep_pack (world
           moe_unpermute_combine
 Backward: the same in reverse, from 8-bit checkpoints of the normalised input (T * H bytes) and
           of g and u (T * k * 2I bytes); n, the packed rows and the activation are computed
-          again.  ``layer.ExpertFFN`` is the fused layer in MXFP8; this block is for sizes, experts
-          and precision that it does not have, and for training whose memory is bound by
-          what each layer keeps: everything in Scratch is shared by all blocks of a model.
+          again.  ``layer.ExpertFFN`` is the fused layer, in MXFP8, FP8 or bf16, for the same sizes;
+          this block adds the norm and the 8-bit checkpoints, for bf16 training whose memory is bound
+          by what each layer keeps: everything in Scratch is shared by all blocks of a model.
 """
 from __future__ import annotations
 

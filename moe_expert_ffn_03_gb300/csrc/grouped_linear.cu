@@ -46,9 +46,9 @@
 // every stage that the producer finds free again: they give up when nothing moves.
 //
 // Many rows are bound by the tensor pipe under the power limit: 32768 rows, K = 4096, N = 28672, E = 8,
-// forward 4738 us, dgrad 4720, wgrad 4637 (1.62, 1.63, 1.66 PFLOP/s); 196608 rows, 2048 -> 2816, E = 64:
-// 1449, 1460, 1649 us (1.57, 1.55, 1.38; boxes differ by 3%, wgrad there by 7%).  Few rows are bound by
-// the weights: 16 rows, 4096 -> 28672, six of eight experts used, 248 us, 5.7 TB/s.
+// forward 4573 us, dgrad 4595, wgrad 4495 (1.68, 1.67, 1.71 PFLOP/s); 196608 rows, 2048 -> 2816, E = 64:
+// 1383, 1392, 1578 us (1.64, 1.63, 1.44); other cards take up to 9% longer.  Few rows are bound by the
+// weights: 16 rows, 4096 -> 28672, six of eight experts used, 247 us, 5.7 TB/s.
 #include <atomic>
 #include <cstdio>
 

@@ -300,8 +300,8 @@ __global__ void __launch_bounds__(max_block(VEC), 1) norm_fwd_kernel(const __gri
 // A persistent grid and a ring as in the forward pass.  A thread keeps its columns' sums of
 // dgamma and dbeta in registers; at the end the block's groups are added in order and written
 // as one partial sum per block, which norm_weight_grad_kernel adds in block order.  The second
-// pass over a row finds it in registers where a thread has up to 16 columns, and reads the ring
-// (single columns: memory) again where it has more.  32768 x 2048 bf16 from the checkpoint, with dres,
+// pass over a row finds it in registers where a thread has up to 16 columns (single columns always),
+// and reads the ring again where it has more.  32768 x 2048 bf16 from the checkpoint, with dres,
 // weights' gradients included: 99 us, 4.8 TB/s, bound by 219 instructions a vector at half the issue
 // rate (single columns, 8192 x 5001: 0.7 TB/s).
 template <typename T, int VEC, int NV, bool Q8>
