@@ -133,8 +133,9 @@ __device__ __noinline__ bool wait_phase_cluster(uint64_t* bar, uint32_t parity, 
 }
 // wait_phase_warp for waits across many stages: limit_ns without a change of *stages_used.  In line, since
 // the epilogue's wait is on a short call's path (wgrad of 64 rows over 64 experts 102.8 -> 99.6 us).
-__device__ __forceinline__ bool wait_phase_warp_moving(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
-                                                    int site, uint64_t limit_ns, const volatile uint32_t* stages_used) {
+__device__ __forceinline__ bool wait_phase_warp_moving(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                       int* err, int site, uint64_t limit_ns,
+                                                       const volatile uint32_t* stages_used) {
   uint64_t t0 = 0;
   uint32_t seen = 0;
   bool ok = true;
