@@ -544,6 +544,13 @@ moe_status moe_router_bwd(const moe_dims* d, const void* x, const void* w_r, con
                           const int32_t* idx, const float* prob, const float* dprob, float* dlogits,
                           void* dx, float* dw_r, void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
+/* moe_router_bwd_aux -- moe_router_bwd with a gradient f32 [T][E] that reaches the logits past the
+ * probabilities (the balance loss's): aux is added to dlogits, and dx and dw_r take it along, over all
+ * experts.  aux NULL is moe_router_bwd itself; it must not overlap dlogits. */
+moe_status moe_router_bwd_aux(const moe_dims* d, const void* x, const void* w_r, const float* logits,
+                          const int32_t* idx, const float* prob, const float* dprob, const float* aux, float* dlogits,
+                          void* dx, float* dw_r, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
 /*
  * Operators around the expert FFN: layer norm, the gated activation, activations kept in 8
  * bits between forward and backward, and linear layers grouped by expert on dense ragged
@@ -689,6 +696,158 @@ moe_status moe_grouped_linear_dgrad(const moe_grouped* g, const void* dy, int64_
 moe_status moe_grouped_linear_wgrad(const moe_grouped* g, const void* x, int64_t ldx, const void* dy, int64_t ldy,
                                     const int32_t* split_sizes, void* dw, void* workspace, size_t workspace_bytes,
                                     moe_stream_t stream);
+
+/*
+ * Root-mean-square norm, the router's balance loss, and 8-bit operands with one f32 scale per block of 128:
+ * interface additions for blocks whose products read such operands (page "Efficient MoE Training for
+ * Biological Foundation Models", section "GroupedLinear", names the grouped products, "MoE训练的瓶颈与TE的
+ * 对应能力" 8-bit operands with scales of blocks; page "英伟达开源MoE加速神器", section "三板斧", the router).
+ *
+ * moe_rmsnorm_fwd -- h = x (+ residual), y = h * rstd * gamma per row, rstd = 1 / sqrt(mean h^2 + eps).
+ *   x, residual   [rows][H] at pitch ld_in; residual may be NULL
+ *   gamma         [H]
+ *   h             out [rows][H] at pitch ld_out: the sum, rounded (rstd, y and the codes are those of the
+ *                 unrounded sum); required with residual, else NULL
+ *   y             out [rows][H] at pitch ld_out; may be NULL where codes is set
+ *   rstd          out f32 [rows] or NULL
+ *   codes,scales  both set or both NULL: out y in 8 bits, made before y is rounded ("rows" below): codes
+ *                 [rows][H], scales f32 [ceil(H/128)][rows]
+ * Types and sizes are those of moe_norm.  Finite rows have the norm of its definition also where float32
+ * cannot hold their squares' sum; what passes the output's range there is Inf.  A row with a NaN or an Inf
+ * gives NaN.  h and y must not overlap x and residual, except that h may be x or residual itself when
+ * ld_in = ld_out (a bf16 row whose mean square float32 cannot hold, or only just, is then normalised as
+ * stored in h).
+ */
+size_t moe_rmsnorm_workspace_size(const moe_norm* n);
+moe_status moe_rmsnorm_fwd(const moe_norm* n, const void* x, const void* residual, const void* gamma, void* h, void* y,
+                           float* rstd, uint8_t* codes, float* scales, moe_stream_t stream);
+
+/*
+ * moe_rmsnorm_bwd -- gradients of moe_rmsnorm_fwd, with n = x * rstd and d = dy * gamma:
+ *   dx = rstd * (d - n * mean(d * n)) (+ dres),  dgamma = sum over rows of dy * n (zeros for rows = 0).
+ *   dy, x         [rows][H] at pitch ld_in; x: what was normalised (x, or h where there was a residual)
+ *   dres          [rows][H] at pitch ld_in or NULL: the gradient that reaches h past the norm
+ *   dx            out [rows][H] at pitch ld_out; with a residual it is the gradient of both summands; may
+ *                 be dy or dres itself when ld_in = ld_out
+ *   dgamma        out [H] in gamma's type, summed in f32 in a fixed order
+ *   workspace     of moe_rmsnorm_workspace_size(n) bytes (256-byte aligned, need not be zeroed)
+ */
+moe_status moe_rmsnorm_bwd(const moe_norm* n, const void* dy, const void* x, const float* rstd, const void* gamma,
+                           const void* dres, void* dx, void* dgamma, void* workspace, size_t workspace_bytes,
+                           moe_stream_t stream);
+
+typedef struct moe_balance {
+  int32_t T;            /* tokens, >= 1, T * k <= 2^30 */
+  int32_t E;            /* experts, 1..256 */
+  int32_t k;            /* choices per token, 1..min(E, 8) */
+  float alpha;          /* weight of the balance loss */
+  float beta;           /* weight of the z loss */
+} moe_balance;
+
+/* Bytes of workspace of moe_balance_loss_fwd (256-byte aligned, zero-filled once before first use: a
+ * device error word, then a counter that every call leaves at zero).  Calls that run at the same time
+ * need one each.  0 for invalid sizes.  Host only. */
+size_t moe_balance_loss_workspace_size(const moe_balance* b);
+
+/*
+ * moe_balance_loss_fwd / _bwd -- over the n tokens that mask leaves, with s = softmax(logits) over the
+ * experts, c_e the choices of expert e and P_e the mean of s_e:
+ *   balance = E / (k n) * sum_e c_e P_e,  z = mean (log sum exp logits)^2,  loss = alpha balance + beta z
+ *   dlogits = grad * d loss / d logits, the counts held constant
+ *   logits        f32 [T][E]
+ *   idx           int32 [T][k], the choices (moe_route's); one outside 0..E-1 is recorded in the error
+ *                 word (MOE_ERR_DEVICE_BOUNDS) and not counted
+ *   mask          uint8 [T] or NULL: tokens with 0 are padding.  They are not read, count nothing and have
+ *                 dlogits of zero
+ *   counts        int32 [E + 1]: the choices of every expert, then n.  Out (forward), in (backward)
+ *   prob          out f32 [E]: P
+ *   loss          out f32 [3]: loss, balance, z.  Zeros where no token is left
+ *   grad          f32 [1] on the device or NULL (1): what the loss is multiplied by behind it
+ *   dlogits       out f32 [T][E]
+ * Logits of -Inf are experts that cannot be chosen; a token with no other is counted but adds nothing
+ * and has dlogits of zero.  A NaN or +Inf makes prob, loss and that token's dlogits NaN.  Results do not
+ * depend on timing.
+ */
+moe_status moe_balance_loss_fwd(const moe_balance* b, const float* logits, const int32_t* idx, const uint8_t* mask,
+                                int32_t* counts, float* prob, float* loss, void* workspace, size_t workspace_bytes,
+                                moe_stream_t stream);
+moe_status moe_balance_loss_bwd(const moe_balance* b, const float* logits, const uint8_t* mask, const int32_t* counts,
+                                const float* grad, float* dlogits, moe_stream_t stream);
+
+/*
+ * 8 bits with one f32 scale per block of 128: E4M3 codes of value * (448 / amax) and the scale amax / 448,
+ * both quotients rounded once, amax the block's largest magnitude (taken as 2^-100 where it is smaller).
+ * A block with a NaN or an Inf has NaN codes and scale 1.  Formats:
+ *   MOE_FP8_ROWS    blocks of 128 consecutive values of a row (the last may be short):
+ *                   codes [rows][cols], scales [ceil(cols/128)][rows]
+ *   MOE_FP8_TOKENS  blocks of 128 rows of one column.  Every expert's rows begin on a multiple of 128 rows:
+ *                   codes [B*128][cols], scales [B][cols], B = rows/128 (rounded down) + E blocks, which
+ *                   hold any split of the rows.  Rows past an expert's last are zeros up to its last block's
+ *                   end; blocks past the last expert's are not written
+ *   MOE_FP8_TILES   blocks of 128 rows x 128 columns: the same layout, scales [B][ceil(cols/128)].  Weights
+ *                   [E][N][K] keep their rows, each matrix cut on its own: scales
+ *                   [E][ceil(N/128)][ceil(K/128)]
+ */
+enum moe_fp8_format { MOE_FP8_ROWS = 0, MOE_FP8_TOKENS = 1, MOE_FP8_TILES = 2 };
+
+/*
+ * moe_fp8_block_quantize -- src (bf16, or f32 with src_f32) [rows][cols] at pitch ld, read once, into rows
+ * (codes, scales) and/or into tokens or tiles (tcodes, tscales, format); NULL leaves one out.
+ * split_sizes int32 [E] (device; required for tcodes, else it may be NULL): the experts' rows one after the
+ * other, as the grouped linear calls have them; rows past their sum belong to no expert, and their codes
+ * and scales are not written.  A negative size or a sum above rows: nothing is written (the product that
+ * takes the same sizes records the error).
+ */
+moe_status moe_fp8_block_quantize(const void* src, int32_t src_f32, int64_t rows, int32_t cols, int64_t ld, uint8_t* codes,
+                                  float* scales, const int32_t* split_sizes, int32_t E, uint8_t* tcodes, float* tscales,
+                                  int32_t format, moe_stream_t stream);
+/* Weights [E][N][K], dense, in tiles; both of the products that read them take these codes. */
+moe_status moe_fp8_block_quantize_weights(const void* w, int32_t w_f32, int32_t E, int32_t N, int32_t K, uint8_t* codes,
+                                          float* scales, moe_stream_t stream);
+/* The values of codes [rows][cols] (rows = B*128 for tokens and tiles) in bf16, or f32 with dst_f32, at pitch
+ * ld; mat_rows: the rows of each matrix of weights (tiles), else 0. */
+moe_status moe_fp8_block_dequantize(const uint8_t* codes, const float* scales, int32_t format, int64_t rows, int32_t mat_rows,
+                                    int32_t cols, void* dst, int32_t dst_f32, int64_t ld, moe_stream_t stream);
+/* Rows (MOE_FP8_ROWS) of T tokens copied to their places by expert: row pos_of[t][j] of the output is token
+ * t (moe_ep_pack's pos_of); cols a multiple of 16.  A place outside 0..rows-1 is recorded in the workspace's
+ * error word (256 bytes, zero-filled once) and skipped. */
+moe_status moe_fp8_block_pack(const uint8_t* codes, const float* scales, const int32_t* pos_of, int32_t T, int32_t k,
+                              int32_t cols, int64_t rows, uint8_t* codes_out, float* scales_out, void* workspace,
+                              moe_stream_t stream);
+
+/* Bytes of workspace of the calls below (256-byte aligned, zero-filled once before first use); later calls
+ * on the same stream may reuse it, for any sizes; calls running at the same time on other streams need
+ * their own.  After a recorded device timeout it is zero-filled again as a whole.  0 for invalid sizes. */
+size_t moe_grouped_linear_fp8_workspace_size(const moe_grouped* g);
+
+/*
+ * moe_grouped_linear_fp8_fwd / _dgrad / _wgrad -- moe_grouped_linear_* on 8-bit operands with scales of blocks
+ * of 128; K and N multiples of 16.  Products of codes are summed in f32 over each block of the contraction,
+ * scaled, and the blocks' sums added in f32; one rounding to bf16 at the end.
+ *   fwd    y[r]  = w[e] x[r]             x rows [rows][K]; w tiles [E][N][K]; y bf16 [rows][N] at pitch ldy
+ *   dgrad  dx[r] = w[e]^T dy[r]          dy rows [rows][N]; dx bf16 [rows][K] at pitch ldx
+ *   wgrad  dw[e] = sum_r dy[r] x[r]^T    x tiles and dy tokens of moe_fp8_block_quantize, [B*128][K] and
+ *                                        [B*128][N]; dw bf16 [E][N][K], zeros for experts without rows
+ * Pitches are multiples of 8.  Rows past the sum of split_sizes are not read and not written; the rest is as
+ * there: NaN stays in its row and its expert, inconsistent sizes are recorded and nothing is written,
+ * waits on the device give up after 2 s.
+ */
+moe_status moe_grouped_linear_fp8_fwd(const moe_grouped* g, const uint8_t* x, const float* x_scales,
+                                      const int32_t* split_sizes, const uint8_t* w, const float* w_scales, void* y,
+                                      int64_t ldy, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+moe_status moe_grouped_linear_fp8_dgrad(const moe_grouped* g, const uint8_t* dy, const float* dy_scales,
+                                        const int32_t* split_sizes, const uint8_t* w, const float* w_scales, void* dx,
+                                        int64_t ldx, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+moe_status moe_grouped_linear_fp8_wgrad(const moe_grouped* g, const uint8_t* x, const float* x_scales, const uint8_t* dy,
+                                        const float* dy_scales, const int32_t* split_sizes, void* dw, void* workspace,
+                                        size_t workspace_bytes, moe_stream_t stream);
+
+/* moe_selftest_grouped_linear_fp8_wait -- as moe_selftest_grouped_linear_wait, for the call on 8-bit operands:
+ * a, b and their scales are x and w (op 0), dy and w (1), dy and x (2); out dense; sites 720..729. */
+moe_status moe_selftest_grouped_linear_fp8_wait(const moe_grouped* g, int32_t op, const uint8_t* a, const float* a_scales,
+                                                const uint8_t* b, const float* b_scales, const int32_t* split_sizes,
+                                                void* out, int32_t loads, int64_t limit_ns, void* workspace,
+                                                size_t workspace_bytes, moe_stream_t stream);
 
 /* moe_selftest_wait_timeout -- exercises the device-side failure path without
  * faulting anything.  One launch of the grouped GEMM kernel over a single

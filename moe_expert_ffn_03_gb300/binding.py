@@ -26,7 +26,11 @@ EXPORTS = (
     "moe_gather_f32", "moe_layernorm_workspace_size", "moe_layernorm_fwd", "moe_layernorm_bwd", "moe_act8_pack",
     "moe_act8_unpack", "moe_swiglu_fwd", "moe_swiglu_bwd", "moe_grouped_linear_workspace_size",
     "moe_grouped_linear_fwd", "moe_grouped_linear_dgrad", "moe_grouped_linear_wgrad",
-    "moe_selftest_grouped_linear_wait",
+    "moe_selftest_grouped_linear_wait", "moe_router_bwd_aux", "moe_rmsnorm_workspace_size", "moe_rmsnorm_fwd",
+    "moe_rmsnorm_bwd", "moe_balance_loss_workspace_size", "moe_balance_loss_fwd", "moe_balance_loss_bwd",
+    "moe_fp8_block_quantize", "moe_fp8_block_quantize_weights", "moe_fp8_block_dequantize", "moe_fp8_block_pack",
+    "moe_grouped_linear_fp8_workspace_size", "moe_grouped_linear_fp8_fwd", "moe_grouped_linear_fp8_dgrad",
+    "moe_grouped_linear_fp8_wgrad", "moe_selftest_grouped_linear_fp8_wait",
 )
 
 # moe_ws_tensor ids (include/moe_ffn.h)
@@ -70,6 +74,15 @@ class MoeGrouped(ctypes.Structure):
 def grouped(rows, K, N, E) -> MoeGrouped:
     """Sizes of a grouped linear layer: rows of all experts, K input and N output features, E experts."""
     return MoeGrouped(rows, K, N, E)
+
+
+class MoeBalance(ctypes.Structure):
+    _fields_ = [("T", c_int32), ("E", c_int32), ("k", c_int32), ("alpha", ctypes.c_float), ("beta", ctypes.c_float)]
+
+
+def balance(T, E, k, alpha=0.01, beta=0.0) -> MoeBalance:
+    """Sizes of a balance loss over T tokens' k choices of E experts, and the weights of the balance and z losses."""
+    return MoeBalance(T, E, k, alpha, beta)
 
 
 _lib = None
@@ -139,6 +152,22 @@ def lib() -> ctypes.CDLL:
             "moe_grouped_linear_fwd": ([G, P, I64, P, P, P, I64, P, c_size_t, P], c_int32),
             "moe_grouped_linear_dgrad": ([G, P, I64, P, P, P, I64, P, c_size_t, P], c_int32),
             "moe_grouped_linear_wgrad": ([G, P, I64, P, I64, P, P, P, c_size_t, P], c_int32),
+            "moe_router_bwd_aux": ([D] + [P] * 11 + [c_size_t, P], c_int32),
+            "moe_rmsnorm_workspace_size": ([ctypes.POINTER(MoeNorm)], c_size_t),
+            "moe_rmsnorm_fwd": ([ctypes.POINTER(MoeNorm)] + [P] * 9, c_int32),
+            "moe_rmsnorm_bwd": ([ctypes.POINTER(MoeNorm)] + [P] * 8 + [c_size_t, P], c_int32),
+            "moe_balance_loss_workspace_size": ([ctypes.POINTER(MoeBalance)], c_size_t),
+            "moe_balance_loss_fwd": ([ctypes.POINTER(MoeBalance)] + [P] * 7 + [c_size_t, P], c_int32),
+            "moe_balance_loss_bwd": ([ctypes.POINTER(MoeBalance)] + [P] * 6, c_int32),
+            "moe_fp8_block_quantize": ([P, c_int32, I64, c_int32, I64, P, P, P, c_int32, P, P, c_int32, P], c_int32),
+            "moe_fp8_block_quantize_weights": ([P, c_int32, c_int32, c_int32, c_int32, P, P, P], c_int32),
+            "moe_fp8_block_dequantize": ([P, P, c_int32, I64, c_int32, c_int32, P, c_int32, I64, P], c_int32),
+            "moe_fp8_block_pack": ([P, P, P, c_int32, c_int32, c_int32, I64, P, P, P, P], c_int32),
+            "moe_grouped_linear_fp8_workspace_size": ([G], c_size_t),
+            "moe_grouped_linear_fp8_fwd": ([G] + [P] * 6 + [I64, P, c_size_t, P], c_int32),
+            "moe_grouped_linear_fp8_dgrad": ([G] + [P] * 6 + [I64, P, c_size_t, P], c_int32),
+            "moe_grouped_linear_fp8_wgrad": ([G] + [P] * 7 + [c_size_t, P], c_int32),
+            "moe_selftest_grouped_linear_fp8_wait": ([G, c_int32] + [P] * 6 + [c_int32, I64, P, c_size_t, P], c_int32),
             "moe_selftest_grouped_linear_wait": ([G, c_int32, P, I64, P, I64, P, P, c_int32, I64, P, c_size_t, P], c_int32),
         }
         for name, (args, res) in sig.items():
@@ -524,3 +553,177 @@ def moe_selftest_grouped_linear_wait(g, op, rows_in, other, split_sizes, out, wo
                                                   _dense(split_sizes, torch.int32, g.E), _p(out), int(loads),
                                                   int(limit_ns), _p(workspace), _wsb(workspace),
                                                   _on(stream, rows_in, other, split_sizes, out, workspace)))
+
+
+# ---- root-mean-square norm, balance loss, 8 bits with one f32 scale per block of 128 --------------
+FP8_FORMATS = {"rows": 0, "tokens": 1, "tiles": 2}
+_F32, _U8, _I32 = torch.float32, torch.uint8, torch.int32
+
+
+def _cuts(n):
+    """Blocks of 128 that n values are cut into."""
+    return (n + 127) // 128
+
+
+def fp8_blocks(rows, E) -> int:
+    """Blocks of 128 rows of the layout that holds any split of `rows` rows over E experts, each on blocks of its own."""
+    return rows // 128 + E
+
+
+def moe_rmsnorm_workspace_size(n: MoeNorm) -> int:
+    return int(lib().moe_rmsnorm_workspace_size(ctypes.byref(n)))
+
+
+def moe_rmsnorm_fwd(n, x, residual, gamma, h, y, rstd, codes=None, scales=None, stream=None):
+    R, H = n.rows, n.H
+    t, w = _ROW_TYPES[n.x_f32], _ROW_TYPES[n.w_f32]
+    _check(lib().moe_rmsnorm_fwd(ctypes.byref(n), _pitched(x, R, H, n.ld_in, t), _pitched(residual, R, H, n.ld_in, t),
+                                 _dense(gamma, w, H), _pitched(h, R, H, n.ld_out, t), _pitched(y, R, H, n.ld_out, t),
+                                 _dense(rstd, _F32, R), _dense(codes, _U8, R * H), _dense(scales, _F32, R * _cuts(H)),
+                                 _on(stream, x, residual, gamma, h, y, rstd, codes, scales)))
+
+
+def moe_rmsnorm_bwd(n, dy, x, rstd, gamma, dres, dx, dgamma, workspace, stream=None):
+    R, H = n.rows, n.H
+    t, w = _ROW_TYPES[n.x_f32], _ROW_TYPES[n.w_f32]
+    _check(lib().moe_rmsnorm_bwd(ctypes.byref(n), _pitched(dy, R, H, n.ld_in, t), _pitched(x, R, H, n.ld_in, t),
+                                 _dense(rstd, _F32, R), _dense(gamma, w, H), _pitched(dres, R, H, n.ld_in, t),
+                                 _pitched(dx, R, H, n.ld_out, t), _dense(dgamma, w, H), _p(workspace), _wsb(workspace),
+                                 _on(stream, dy, x, rstd, gamma, dres, dx, dgamma, workspace)))
+
+
+def moe_balance_loss_workspace_size(b: MoeBalance) -> int:
+    return int(lib().moe_balance_loss_workspace_size(ctypes.byref(b)))
+
+
+def moe_balance_loss_fwd(b, logits, idx, mask, counts, prob, loss, workspace, stream=None):
+    _check(lib().moe_balance_loss_fwd(ctypes.byref(b), _dense(logits, _F32, b.T * b.E), _dense(idx, _I32, b.T * b.k),
+                                      _dense(mask, _U8, b.T), _dense(counts, _I32, b.E + 1), _dense(prob, _F32, b.E),
+                                      _dense(loss, _F32, 3), _p(workspace), _wsb(workspace),
+                                      _on(stream, logits, idx, mask, counts, prob, loss, workspace)))
+
+
+def moe_balance_loss_bwd(b, logits, mask, counts, grad, dlogits, stream=None):
+    _check(lib().moe_balance_loss_bwd(ctypes.byref(b), _dense(logits, _F32, b.T * b.E), _dense(mask, _U8, b.T),
+                                      _dense(counts, _I32, b.E + 1), _dense(grad, _F32, 1), _dense(dlogits, _F32, b.T * b.E),
+                                      _on(stream, logits, mask, counts, grad, dlogits)))
+
+
+def moe_router_bwd_aux(d, x, w_r, logits, idx, prob, dprob, aux, dlogits, dx, dw_r, workspace, stream=None):
+    T, H, E, k, b16 = d.T, d.H, d.E, d.k, torch.bfloat16
+    _check(lib().moe_router_bwd_aux(ctypes.byref(d), _dense(x, b16, T * H), _dense(w_r, b16, E * H),
+                                    _dense(logits, _F32, T * E), _dense(idx, _I32, T * k), _dense(prob, _F32, T * k),
+                                    _dense(dprob, _F32, T * k), _dense(aux, _F32, T * E), _dense(dlogits, _F32, T * E),
+                                    _dense(dx, b16, T * H), _dense(dw_r, _F32, E * H), _p(workspace), _wsb(workspace),
+                                    _on(stream, x, w_r, logits, idx, prob, dprob, aux, dlogits, dx, dw_r, workspace)))
+
+
+def _tscales(kind, blocks, cols):
+    return blocks * (_cuts(cols) if kind == "tiles" else cols)
+
+
+def moe_fp8_block_quantize(src, codes, scales, split_sizes=None, tcodes=None, tscales=None, kind="tokens", stream=None):
+    """Rows (codes, scales) and, with split_sizes, the experts' rows along tokens (tcodes, tscales: kind "tokens" or
+    "tiles"); None leaves one out."""
+    rows, cols = src.shape
+    f32 = src.dtype == torch.float32
+    E = 0 if split_sizes is None else split_sizes.numel()
+    blocks = fp8_blocks(rows, E)
+    _check(lib().moe_fp8_block_quantize(_p(src), int(f32), rows, cols, _ld(src, rows, cols, _ROW_TYPES[f32]),
+                                        _dense(codes, _U8, rows * cols), _dense(scales, _F32, rows * _cuts(cols)),
+                                        _dense(split_sizes, _I32, E), E, _dense(tcodes, _U8, blocks * 128 * cols),
+                                        _dense(tscales, _F32, _tscales(kind, blocks, cols)), FP8_FORMATS[kind],
+                                        _on(stream, src, codes, scales, split_sizes, tcodes, tscales)))
+
+
+def moe_fp8_block_quantize_weights(w, codes, scales, stream=None):
+    E, N, K = w.shape
+    f32 = w.dtype == torch.float32
+    _check(lib().moe_fp8_block_quantize_weights(_dense(w, _ROW_TYPES[f32], E * N * K), int(f32), E, N, K,
+                                                _dense(codes, _U8, E * N * K), _dense(scales, _F32, E * _cuts(N) * _cuts(K)),
+                                                _on(stream, w, codes, scales)))
+
+
+def moe_fp8_block_dequantize(codes, scales, kind, dst, stream=None):
+    """Values of codes [rows][cols], or of weights [E][N][K] (kind "tiles"), in dst's type (bf16 or f32) and shape."""
+    if codes.dim() == 3 and kind == "tiles":
+        (E, N, cols), rows = codes.shape, codes.shape[0] * codes.shape[1]
+        mat_rows, n_scales = N, E * _cuts(N) * _cuts(cols)
+        if dst.shape != codes.shape or not dst.is_contiguous():
+            raise ValueError(f"expected a contiguous tensor of shape {tuple(codes.shape)}, got {tuple(dst.shape)}")
+        flat = dst.view(rows, cols)
+    else:
+        (rows, cols), mat_rows, flat = codes.shape, 0, dst
+        if kind != "rows" and rows % 128:
+            raise ValueError(f"{rows} rows of {kind}: not whole blocks of 128")
+        n_scales = rows * _cuts(cols) if kind == "rows" else _tscales(kind, rows // 128, cols)
+    f32 = dst.dtype == torch.float32
+    _check(lib().moe_fp8_block_dequantize(_dense(codes, _U8, rows * cols), _dense(scales, _F32, n_scales), FP8_FORMATS[kind],
+                                          rows, mat_rows, cols, _p(flat), int(f32), _ld(flat, rows, cols, _ROW_TYPES[f32]),
+                                          _on(stream, codes, scales, dst)))
+
+
+def moe_fp8_block_pack(codes, scales, pos_of, codes_out, scales_out, workspace, stream=None):
+    """Rows of tokens (codes [T][cols], scales [ceil(cols/128)][T]) copied to their places pos_of [T][k] in codes_out."""
+    (T, cols), k, rows = codes.shape, pos_of.shape[1], codes_out.shape[0]
+    _dense(workspace, _U8, 256)
+    _check(lib().moe_fp8_block_pack(_dense(codes, _U8, T * cols), _dense(scales, _F32, T * _cuts(cols)),
+                                    _dense(pos_of, _I32, T * k), T, k, cols, rows, _dense(codes_out, _U8, rows * cols),
+                                    _dense(scales_out, _F32, rows * _cuts(cols)), _p(workspace),
+                                    _on(stream, codes, scales, pos_of, codes_out, scales_out, workspace)))
+
+
+def moe_grouped_linear_fp8_workspace_size(g: MoeGrouped) -> int:
+    return int(lib().moe_grouped_linear_fp8_workspace_size(ctypes.byref(g)))
+
+
+def _weights8(g, w, w_scales):
+    return _dense(w, _U8, g.E * g.N * g.K), _dense(w_scales, _F32, g.E * _cuts(g.N) * _cuts(g.K))
+
+
+def moe_grouped_linear_fp8_fwd(g, x, x_scales, split_sizes, w, w_scales, y, workspace, stream=None):
+    R, K, N = g.rows, g.K, g.N
+    _check(lib().moe_grouped_linear_fp8_fwd(ctypes.byref(g), _dense(x, _U8, R * K), _dense(x_scales, _F32, R * _cuts(K)),
+                                            _dense(split_sizes, _I32, g.E), *_weights8(g, w, w_scales), _p(y),
+                                            _ld(y, R, N), _p(workspace), _wsb(workspace),
+                                            _on(stream, x, x_scales, split_sizes, w, w_scales, y, workspace)))
+
+
+def moe_grouped_linear_fp8_dgrad(g, dy, dy_scales, split_sizes, w, w_scales, dx, workspace, stream=None):
+    R, K, N = g.rows, g.K, g.N
+    _check(lib().moe_grouped_linear_fp8_dgrad(ctypes.byref(g), _dense(dy, _U8, R * N), _dense(dy_scales, _F32, R * _cuts(N)),
+                                              _dense(split_sizes, _I32, g.E), *_weights8(g, w, w_scales), _p(dx),
+                                              _ld(dx, R, K), _p(workspace), _wsb(workspace),
+                                              _on(stream, dy, dy_scales, split_sizes, w, w_scales, dx, workspace)))
+
+
+def _tokens8(g, x, x_scales, dy, dy_scales):
+    """Checked pointers of the weight gradient's operands: x in tiles, dy along tokens."""
+    B = fp8_blocks(g.rows, g.E)
+    return (_dense(x, _U8, B * 128 * g.K), _dense(x_scales, _F32, B * _cuts(g.K)), _dense(dy, _U8, B * 128 * g.N),
+            _dense(dy_scales, _F32, B * g.N))
+
+
+def moe_grouped_linear_fp8_wgrad(g, x, x_scales, dy, dy_scales, split_sizes, dw, workspace, stream=None):
+    _check(lib().moe_grouped_linear_fp8_wgrad(ctypes.byref(g), *_tokens8(g, x, x_scales, dy, dy_scales),
+                                              _dense(split_sizes, _I32, g.E), _dense(dw, torch.bfloat16, g.E * g.N * g.K),
+                                              _p(workspace), _wsb(workspace),
+                                              _on(stream, x, x_scales, dy, dy_scales, split_sizes, dw, workspace)))
+
+
+def moe_selftest_grouped_linear_fp8_wait(g, op, a, a_scales, b, b_scales, split_sizes, out, workspace, loads, limit_ns,
+                                         stream=None):
+    """A grouped linear call on 8-bit operands (op 0 forward, 1 input gradient: a rows, b weights; 2 weight gradient:
+    a dy, b x) under another limit of its waits, with or without its loads."""
+    R, K, N = g.rows, g.K, g.N
+    if op == 2:
+        pb, psb, pa, psa = _tokens8(g, b, b_scales, a, a_scales)
+    else:
+        c = K if op == 0 else N
+        pa, psa = _dense(a, _U8, R * c), _dense(a_scales, _F32, R * _cuts(c))
+        pb, psb = _weights8(g, b, b_scales)
+    n_out = g.E * N * K if op == 2 else R * (N if op == 0 else K)
+    _check(lib().moe_selftest_grouped_linear_fp8_wait(ctypes.byref(g), op, pa, psa, pb, psb, _dense(split_sizes, _I32, g.E),
+                                                      _dense(out, torch.bfloat16, n_out), int(loads), int(limit_ns),
+                                                      _p(workspace), _wsb(workspace),
+                                                      _on(stream, a, a_scales, b, b_scales, split_sizes, out, workspace)))

@@ -1238,8 +1238,8 @@ moe_status moe_router_fwd(const moe_dims* d, const void* x, const void* w_r, flo
   return MOE_OK;
 }
 
-moe_status moe_router_bwd(const moe_dims* d, const void* x, const void* w_r, const float* logits, const int32_t* idx,
-                          const float* prob, const float* dprob, float* dlogits, void* dx, float* dw_r,
+moe_status moe_router_bwd_aux(const moe_dims* d, const void* x, const void* w_r, const float* logits, const int32_t* idx,
+                          const float* prob, const float* dprob, const float* aux, float* dlogits, void* dx, float* dw_r,
                           void* workspace, size_t workspace_bytes, moe_stream_t stream) {
   g_msg[0] = 0;
   moe_status s = check_dims(d);
@@ -1253,14 +1253,22 @@ moe_status moe_router_bwd(const moe_dims* d, const void* x, const void* w_r, con
   REQUIRE_PTR(dlogits);
   REQUIRE_PTR(dx);
   REQUIRE_PTR(dw_r);
+  if (!al16(aux)) return fail(MOE_ERR_ALIGNMENT, "aux is not 16-byte aligned");
   s = check_ws(d, workspace, workspace_bytes, true);
   if (s != MOE_OK) return s;
   const WsLayout w = ws_layout(d, true);
-  CUDA_TRY(launch_router_bwd(x, w_r, logits, idx, prob, dprob, d->T, d->H, d->E, d->k, d->renormalize, dlogits, dx,
-                             dw_r, at<uint8_t>(workspace, w.rpart), at<int>(workspace, w.err),
+  CUDA_TRY(launch_router_bwd(x, w_r, logits, idx, prob, dprob, aux, d->T, d->H, d->E, d->k, d->renormalize, dlogits,
+                             dx, dw_r, at<uint8_t>(workspace, w.rpart), at<int>(workspace, w.err),
                              static_cast<cudaStream_t>(stream)),
            "router bwd");
   return MOE_OK;
+}
+
+moe_status moe_router_bwd(const moe_dims* d, const void* x, const void* w_r, const float* logits, const int32_t* idx,
+                          const float* prob, const float* dprob, float* dlogits, void* dx, float* dw_r,
+                          void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  return moe_router_bwd_aux(d, x, w_r, logits, idx, prob, dprob, nullptr, dlogits, dx, dw_r, workspace, workspace_bytes,
+                            stream);
 }
 
 // ---- operators around the layer: norm, gated activation, act8, grouped linear ------------------
@@ -1350,6 +1358,88 @@ moe_status run_grouped(int mode, const moe_grouped* g, const void* x, int64_t ld
   char msg[256] = "";
   const cudaError_t e = launch_grouped_linear(mode, a, x, ldx, dy, ldy, w, st, msg, sizeof(msg));
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "grouped linear: %s %s", cudaGetErrorString(e), msg);
+  return MOE_OK;
+}
+
+RmsArgs rms_args(const moe_norm* n) {
+  RmsArgs a{};
+  a.rows = n->rows;
+  a.H = n->H;
+  a.eps = n->eps;
+  a.w_f32 = n->w_f32 != 0;
+  a.ld_in = n->ld_in;
+  a.ld_out = n->ld_out;
+  return a;
+}
+
+moe_status check_balance(const moe_balance* b) {
+  g_msg[0] = 0;
+  if (b == nullptr) return fail(MOE_ERR_INVALID_ARG, "balance is NULL");
+  if (b->T < 1) return fail(MOE_ERR_INVALID_ARG, "T=%d must be >= 1", b->T);
+  if (b->E < 1 || b->E > 256) return fail(MOE_ERR_UNSUPPORTED, "E=%d must be in 1..256", b->E);
+  if (b->k < 1 || b->k > 8 || b->k > b->E) return fail(MOE_ERR_UNSUPPORTED, "k=%d must be in 1..min(E,8)", b->k);
+  if (int64_t(b->T) * b->k > (int64_t(1) << 30)) return fail(MOE_ERR_UNSUPPORTED, "T*k must be <= 2^30");
+  return MOE_OK;
+}
+
+BalanceArgs balance_args(const moe_balance* b, const float* logits, const uint8_t* mask, int32_t* counts) {
+  BalanceArgs a{};
+  a.T = b->T;
+  a.E = b->E;
+  a.k = b->k;
+  a.alpha = b->alpha;
+  a.beta = b->beta;
+  a.logits = logits;
+  a.mask = mask;
+  a.counts = counts;
+  return a;
+}
+
+moe_status check_block8(int64_t rows, int32_t cols) {
+  g_msg[0] = 0;
+  if (rows < 0 || rows >= (int64_t(1) << 31)) return fail(MOE_ERR_INVALID_ARG, "rows=%lld must be in 0..2^31-1", (long long)rows);
+  if (cols < 1 || cols > (1 << 29)) return fail(MOE_ERR_INVALID_ARG, "row length %d must be in 1..2^29", cols);
+  return MOE_OK;
+}
+
+// Rows of codes are TMA rows: multiples of 16 bytes, in both directions.
+moe_status check_grouped8(const moe_grouped* g) {
+  if (moe_status s = check_grouped(g); s != MOE_OK) return s;
+  if (g->K % 16 || g->N % 16) return fail(MOE_ERR_UNSUPPORTED, "K=%d and N=%d must be multiples of 16", g->K, g->N);
+  return MOE_OK;
+}
+
+moe_status check_grouped8_call(const moe_grouped* g, int64_t ldo, int64_t cols, const void* ws, size_t bytes) {
+  g_msg[0] = 0;
+  if (moe_status s = check_grouped8(g); s != MOE_OK) return s;
+  if (moe_status s = check_pitch(ldo, cols, "row pitch"); s != MOE_OK) return s;
+  if (ldo % 8) return fail(MOE_ERR_UNSUPPORTED, "row pitch %lld must be a multiple of 8", (long long)ldo);
+  if (ldo >= (int64_t(1) << 38)) return fail(MOE_ERR_UNSUPPORTED, "row pitch too large");
+  if (ws == nullptr) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return fail(MOE_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+  if (bytes < linear8_ws_bytes()) return fail(MOE_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", bytes, linear8_ws_bytes());
+  return MOE_OK;
+}
+
+moe_status run_grouped8(int mode, const moe_grouped* g, const uint8_t* a_codes, const float* sa, const uint8_t* b_codes,
+                        const float* sb, const int32_t* split_sizes, void* out, int64_t ldo, void* ws, cudaStream_t st,
+                        uint64_t wait_limit_ns = kWaitLimitNs, bool no_loads = false) {
+  Linear8Args a{};
+  a.rows = g->rows;
+  a.E = g->E;
+  a.K = g->K;
+  a.N = g->N;
+  a.split_sizes = split_sizes;
+  a.sa = sa;
+  a.sb = sb;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.ldo = ldo;
+  a.err = static_cast<int*>(ws);
+  a.wait_limit_ns = wait_limit_ns;
+  a.selftest_no_loads = no_loads;
+  char msg[256] = "";
+  const cudaError_t e = launch_grouped_linear_fp8(mode, a, a_codes, b_codes, st, msg, sizeof(msg));
+  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "grouped linear fp8: %s %s", cudaGetErrorString(e), msg);
   return MOE_OK;
 }
 
@@ -1557,6 +1647,276 @@ moe_status moe_grouped_linear_wgrad(const moe_grouped* g, const void* x, int64_t
   REQUIRE_PTR(split_sizes);
   return run_grouped(LIN_WGRAD, g, x, ldx, dy, ldy, split_sizes, nullptr, dw, g->K, workspace,
                      static_cast<cudaStream_t>(stream));
+}
+
+// ---- root-mean-square norm, balance loss, 8 bits with a scale per block of 128 ------------------
+size_t moe_rmsnorm_workspace_size(const moe_norm* n) { return check_norm(n) == MOE_OK ? rms_ws_bytes(n->rows, n->H) : 0; }
+
+moe_status moe_rmsnorm_fwd(const moe_norm* n, const void* x, const void* residual, const void* gamma, void* h, void* y,
+                           float* rstd, uint8_t* codes, float* scales, moe_stream_t stream) {
+  if (moe_status s = check_norm(n); s != MOE_OK) return s;
+  if (moe_status s = check_act8(codes, reinterpret_cast<const uint8_t*>(scales)); s != MOE_OK) return s;
+  if ((residual == nullptr) != (h == nullptr)) return fail(MOE_ERR_INVALID_ARG, "h goes with residual: set both or neither");
+  if (n->rows == 0) return MOE_OK;
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(gamma);
+  if (y == nullptr && codes == nullptr) return fail(MOE_ERR_INVALID_ARG, "neither y nor codes is set");
+  if (!al16(residual) || !al16(h) || !al16(y) || !al16(rstd)) return fail(MOE_ERR_ALIGNMENT, "a pointer is not 16-byte aligned");
+  RmsArgs a = rms_args(n);
+  a.x = x;
+  a.residual = residual;
+  a.gamma = gamma;
+  a.h = h;
+  a.y = y;
+  a.rstd = rstd;
+  a.codes = codes;
+  a.scales = scales;
+  CUDA_TRY(launch_rms_fwd(a, n->x_f32 != 0, static_cast<cudaStream_t>(stream)), "root-mean-square norm forward");
+  return MOE_OK;
+}
+
+moe_status moe_rmsnorm_bwd(const moe_norm* n, const void* dy, const void* x, const float* rstd, const void* gamma,
+                           const void* dres, void* dx, void* dgamma, void* workspace, size_t workspace_bytes,
+                           moe_stream_t stream) {
+  if (moe_status s = check_norm(n); s != MOE_OK) return s;
+  REQUIRE_PTR(dgamma);
+  if (n->rows > 0) {
+    REQUIRE_PTR(dy);
+    REQUIRE_PTR(x);
+    REQUIRE_PTR(rstd);
+    REQUIRE_PTR(gamma);
+    REQUIRE_PTR(dx);
+    if (!al16(dres)) return fail(MOE_ERR_ALIGNMENT, "dres is not 16-byte aligned");
+    if (workspace == nullptr) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return fail(MOE_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+    const size_t need = rms_ws_bytes(n->rows, n->H);
+    if (workspace_bytes < need) return fail(MOE_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+  }
+  RmsArgs a = rms_args(n);
+  a.dy = dy;
+  a.x = x;
+  a.rstd = const_cast<float*>(rstd);
+  a.gamma = gamma;
+  a.dres = dres;
+  a.dx = dx;
+  a.dgamma = dgamma;
+  CUDA_TRY(launch_rms_bwd(a, n->x_f32 != 0, static_cast<float*>(workspace), static_cast<cudaStream_t>(stream)),
+           "root-mean-square norm backward");
+  return MOE_OK;
+}
+
+size_t moe_balance_loss_workspace_size(const moe_balance* b) { return check_balance(b) == MOE_OK ? balance_ws_bytes(b->E) : 0; }
+
+moe_status moe_balance_loss_fwd(const moe_balance* b, const float* logits, const int32_t* idx, const uint8_t* mask,
+                                int32_t* counts, float* prob, float* loss, void* workspace, size_t workspace_bytes,
+                                moe_stream_t stream) {
+  if (moe_status s = check_balance(b); s != MOE_OK) return s;
+  REQUIRE_PTR(logits);
+  REQUIRE_PTR(idx);
+  REQUIRE_PTR(counts);
+  REQUIRE_PTR(prob);
+  REQUIRE_PTR(loss);
+  if (!al16(mask)) return fail(MOE_ERR_ALIGNMENT, "mask is not 16-byte aligned");
+  if (workspace == nullptr) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return fail(MOE_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+  const size_t need = balance_ws_bytes(b->E);
+  if (workspace_bytes < need) return fail(MOE_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+  BalanceArgs a = balance_args(b, logits, mask, counts);
+  a.idx = idx;
+  a.prob = prob;
+  a.loss = loss;
+  a.err = static_cast<int*>(workspace);
+  a.ticket = reinterpret_cast<unsigned*>(a.err + 8);
+  a.partial = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + 256);
+  CUDA_TRY(launch_balance(a, false, static_cast<cudaStream_t>(stream)), "balance loss forward");
+  return MOE_OK;
+}
+
+moe_status moe_balance_loss_bwd(const moe_balance* b, const float* logits, const uint8_t* mask, const int32_t* counts,
+                                const float* grad, float* dlogits, moe_stream_t stream) {
+  if (moe_status s = check_balance(b); s != MOE_OK) return s;
+  REQUIRE_PTR(logits);
+  REQUIRE_PTR(counts);
+  REQUIRE_PTR(dlogits);
+  if (!al16(mask)) return fail(MOE_ERR_ALIGNMENT, "mask is not 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(grad) & 3u) != 0) return fail(MOE_ERR_ALIGNMENT, "grad is not 4-byte aligned");
+  BalanceArgs a = balance_args(b, logits, mask, const_cast<int32_t*>(counts));
+  a.grad = grad;
+  a.dlogits = dlogits;
+  CUDA_TRY(launch_balance(a, true, static_cast<cudaStream_t>(stream)), "balance loss backward");
+  return MOE_OK;
+}
+
+moe_status moe_fp8_block_quantize(const void* src, int32_t src_f32, int64_t rows, int32_t cols, int64_t ld, uint8_t* codes,
+                                  float* scales, const int32_t* split_sizes, int32_t E, uint8_t* tcodes, float* tscales,
+                                  int32_t format, moe_stream_t stream) {
+  if (moe_status s = check_block8(rows, cols); s != MOE_OK) return s;
+  if (moe_status s = check_pitch(ld, cols, "ld"); s != MOE_OK) return s;
+  if ((src_f32 & ~1) != 0) return fail(MOE_ERR_INVALID_ARG, "src_f32 must be 0 or 1");
+  if ((codes == nullptr) != (scales == nullptr) || (tcodes == nullptr) != (tscales == nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "codes and scales go together, as do tcodes and tscales");
+  if (codes == nullptr && tcodes == nullptr) return fail(MOE_ERR_INVALID_ARG, "neither codes nor tcodes is set");
+  if (split_sizes != nullptr && (E < 1 || E > 256)) return fail(MOE_ERR_UNSUPPORTED, "E=%d must be in 1..256", E);
+  if (tcodes != nullptr && split_sizes == nullptr) return fail(MOE_ERR_INVALID_ARG, "tcodes needs split_sizes");
+  if (tcodes != nullptr && format != MOE_FP8_TOKENS && format != MOE_FP8_TILES)
+    return fail(MOE_ERR_INVALID_ARG, "format=%d must be MOE_FP8_TOKENS or MOE_FP8_TILES", format);
+  if (rows == 0) return MOE_OK;
+  REQUIRE_PTR(src);
+  if (!al16(codes) || !al16(scales) || !al16(tcodes) || !al16(tscales) || !al16(split_sizes))
+    return fail(MOE_ERR_ALIGNMENT, "a pointer is not 16-byte aligned");
+  Block8Args a{};
+  a.src = src;
+  a.rows = rows;
+  a.cols = cols;
+  a.ld = ld;
+  a.codes = codes;
+  a.scales = scales;
+  a.split_sizes = split_sizes;
+  a.E = split_sizes != nullptr ? E : 0;
+  a.tcodes = tcodes;
+  a.tscales = tscales;
+  a.tiles = format == MOE_FP8_TILES;
+  CUDA_TRY(launch_block8_quantize(a, src_f32 != 0, static_cast<cudaStream_t>(stream)), "block quantizer");
+  return MOE_OK;
+}
+
+moe_status moe_fp8_block_quantize_weights(const void* w, int32_t w_f32, int32_t E, int32_t N, int32_t K, uint8_t* codes,
+                                          float* scales, moe_stream_t stream) {
+  g_msg[0] = 0;
+  if ((w_f32 & ~1) != 0) return fail(MOE_ERR_INVALID_ARG, "w_f32 must be 0 or 1");
+  if (E < 1 || N < 1 || K < 1) return fail(MOE_ERR_INVALID_ARG, "E=%d, N=%d and K=%d must be >= 1", E, N, K);
+  if (E > 65536 || N > (1 << 20) || K > (1 << 20)) return fail(MOE_ERR_UNSUPPORTED, "E must be <= 65536, N and K <= 2^20");
+  REQUIRE_PTR(w);
+  REQUIRE_PTR(codes);
+  REQUIRE_PTR(scales);
+  Block8Args a{};
+  a.src = w;
+  a.rows = int64_t(E) * N;
+  a.cols = K;
+  a.ld = K;
+  a.E = E;
+  a.mat_rows = N;
+  a.tcodes = codes;
+  a.tscales = scales;
+  a.tiles = true;
+  CUDA_TRY(launch_block8_quantize(a, w_f32 != 0, static_cast<cudaStream_t>(stream)), "block quantizer of weights");
+  return MOE_OK;
+}
+
+moe_status moe_fp8_block_dequantize(const uint8_t* codes, const float* scales, int32_t format, int64_t rows, int32_t mat_rows,
+                                    int32_t cols, void* dst, int32_t dst_f32, int64_t ld, moe_stream_t stream) {
+  if (moe_status s = check_block8(rows, cols); s != MOE_OK) return s;
+  if (moe_status s = check_pitch(ld, cols, "ld"); s != MOE_OK) return s;
+  if ((dst_f32 & ~1) != 0) return fail(MOE_ERR_INVALID_ARG, "dst_f32 must be 0 or 1");
+  if (format < MOE_FP8_ROWS || format > MOE_FP8_TILES) return fail(MOE_ERR_INVALID_ARG, "unknown format %d", format);
+  if (mat_rows < 0 || (mat_rows > 0 && (rows % mat_rows != 0 || format != MOE_FP8_TILES)))
+    return fail(MOE_ERR_INVALID_ARG, "mat_rows=%d: whole matrices of tiles, or 0", mat_rows);
+  if (rows == 0) return MOE_OK;
+  REQUIRE_PTR(codes);
+  REQUIRE_PTR(scales);
+  REQUIRE_PTR(dst);
+  Block8Back a{};
+  a.codes = codes;
+  a.scales = scales;
+  a.rows = rows;
+  a.cols = cols;
+  a.format = format;
+  a.mat_rows = mat_rows;
+  a.dst = dst;
+  a.ld = ld;
+  CUDA_TRY(launch_block8_dequantize(a, dst_f32 != 0, static_cast<cudaStream_t>(stream)), "block dequantizer");
+  return MOE_OK;
+}
+
+moe_status moe_fp8_block_pack(const uint8_t* codes, const float* scales, const int32_t* pos_of, int32_t T, int32_t k,
+                              int32_t cols, int64_t rows, uint8_t* codes_out, float* scales_out, void* workspace,
+                              moe_stream_t stream) {
+  g_msg[0] = 0;
+  if (T < 0 || k < 1 || k > 8) return fail(MOE_ERR_INVALID_ARG, "T=%d must be >= 0, k=%d in 1..8", T, k);
+  if (moe_status s = check_block8(rows, cols); s != MOE_OK) return s;
+  if (cols % 16) return fail(MOE_ERR_UNSUPPORTED, "cols=%d must be a multiple of 16", cols);
+  if (T == 0) return MOE_OK;
+  REQUIRE_PTR(codes);
+  REQUIRE_PTR(scales);
+  REQUIRE_PTR(pos_of);
+  REQUIRE_PTR(codes_out);
+  REQUIRE_PTR(scales_out);
+  if (workspace == nullptr) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return fail(MOE_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+  CUDA_TRY(launch_block8_pack(codes, scales, pos_of, T, k, cols, rows, codes_out, scales_out, static_cast<int*>(workspace),
+                              static_cast<cudaStream_t>(stream)),
+           "block pack");
+  return MOE_OK;
+}
+
+size_t moe_grouped_linear_fp8_workspace_size(const moe_grouped* g) { return check_grouped8(g) == MOE_OK ? linear8_ws_bytes() : 0; }
+
+moe_status moe_grouped_linear_fp8_fwd(const moe_grouped* g, const uint8_t* x, const float* x_scales,
+                                      const int32_t* split_sizes, const uint8_t* w, const float* w_scales, void* y,
+                                      int64_t ldy, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  if (moe_status s = check_grouped8_call(g, ldy, g != nullptr ? g->N : 0, workspace, workspace_bytes); s != MOE_OK) return s;
+  if (g->rows == 0) return MOE_OK;
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(x_scales);
+  REQUIRE_PTR(split_sizes);
+  REQUIRE_PTR(w);
+  REQUIRE_PTR(w_scales);
+  REQUIRE_PTR(y);
+  return run_grouped8(LIN_FWD, g, x, x_scales, w, w_scales, split_sizes, y, ldy, workspace, static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_grouped_linear_fp8_dgrad(const moe_grouped* g, const uint8_t* dy, const float* dy_scales,
+                                        const int32_t* split_sizes, const uint8_t* w, const float* w_scales, void* dx,
+                                        int64_t ldx, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  if (moe_status s = check_grouped8_call(g, ldx, g != nullptr ? g->K : 0, workspace, workspace_bytes); s != MOE_OK) return s;
+  if (g->rows == 0) return MOE_OK;
+  REQUIRE_PTR(dy);
+  REQUIRE_PTR(dy_scales);
+  REQUIRE_PTR(split_sizes);
+  REQUIRE_PTR(w);
+  REQUIRE_PTR(w_scales);
+  REQUIRE_PTR(dx);
+  return run_grouped8(LIN_DGRAD, g, dy, dy_scales, w, w_scales, split_sizes, dx, ldx, workspace,
+                      static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_grouped_linear_fp8_wgrad(const moe_grouped* g, const uint8_t* x, const float* x_scales, const uint8_t* dy,
+                                        const float* dy_scales, const int32_t* split_sizes, void* dw, void* workspace,
+                                        size_t workspace_bytes, moe_stream_t stream) {
+  if (moe_status s = check_grouped8_call(g, g != nullptr ? g->K : 0, g != nullptr ? g->K : 0, workspace, workspace_bytes);
+      s != MOE_OK)
+    return s;
+  REQUIRE_PTR(dw);
+  if (g->rows == 0) {
+    CUDA_TRY(cudaMemsetAsync(dw, 0, size_t(g->E) * g->N * g->K * 2, static_cast<cudaStream_t>(stream)), "grouped linear fp8 wgrad");
+    return MOE_OK;
+  }
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(x_scales);
+  REQUIRE_PTR(dy);
+  REQUIRE_PTR(dy_scales);
+  REQUIRE_PTR(split_sizes);
+  return run_grouped8(LIN_WGRAD, g, dy, dy_scales, x, x_scales, split_sizes, dw, g->K, workspace,
+                      static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_selftest_grouped_linear_fp8_wait(const moe_grouped* g, int32_t op, const uint8_t* a, const float* a_scales,
+                                                const uint8_t* b, const float* b_scales, const int32_t* split_sizes,
+                                                void* out, int32_t loads, int64_t limit_ns, void* workspace,
+                                                size_t workspace_bytes, moe_stream_t stream) {
+  if (op < LIN_FWD || op > LIN_WGRAD) return fail(MOE_ERR_INVALID_ARG, "op=%d must be in 0..2", op);
+  const int ld = g == nullptr ? 0 : op == LIN_FWD ? g->N : g->K;
+  if (moe_status s = check_grouped8_call(g, ld, ld, workspace, workspace_bytes); s != MOE_OK) return s;
+  if (limit_ns < 1000000 || limit_ns > 2000000000) return fail(MOE_ERR_INVALID_ARG, "limit_ns must be in [1 ms, 2 s]");
+  if (g->rows == 0) return fail(MOE_ERR_INVALID_ARG, "rows must be >= 1");
+  REQUIRE_PTR(a);
+  REQUIRE_PTR(a_scales);
+  REQUIRE_PTR(b);
+  REQUIRE_PTR(b_scales);
+  REQUIRE_PTR(split_sizes);
+  REQUIRE_PTR(out);
+  return run_grouped8(op, g, a, a_scales, b, b_scales, split_sizes, out, ld, workspace, static_cast<cudaStream_t>(stream),
+                      uint64_t(limit_ns), loads == 0);
 }
 
 moe_status moe_selftest_wait_timeout(void* scratch, size_t scratch_bytes, int64_t limit_ns, int32_t* code,

@@ -1,0 +1,272 @@
+// The router's balance loss with the experts' counts, its z loss, and their gradient.
+//
+// Page "英伟达开源MoE加速神器", section "三板斧" (tokens are routed to a few experts; a router that is not
+// held to even loads leaves experts idle; the loss itself is an interface addition).  Over the n tokens that
+// the mask leaves, with s = softmax(logits), c_e the choices of expert e and P_e the mean of s_e:
+//   balance = E / (k n) * sum_e c_e P_e,   z = mean (log sum exp logits)^2,   loss = alpha balance + beta z
+//   dlogits = (alpha s_e (f_e - sum_j f_j s_j) + 2 beta lse s_e) / n,   f_e = E c_e / (k n) - 1
+// (the counts are constants; since the softmax sums to one, f may be counted from 1, where even loads do not
+// cancel).  Small and bound by latency: one launch each way.
+#include "kernels.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int BAL_THREADS = 512;
+constexpr int BAL_WARPS = BAL_THREADS / 32;
+
+// Four neighbouring experts' logits from column c on; -Inf past the last.
+template <bool WIDE>
+__device__ __forceinline__ void load4(const float* row, int c, int E, float* x) {
+  if constexpr (WIDE) {
+    float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    if (c < E) q = __ldg(reinterpret_cast<const float4*>(row + c));
+    x[0] = q.x; x[1] = q.y; x[2] = q.z; x[3] = q.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = c + j < E ? __ldg(row + c + j) : -INFINITY;
+  }
+}
+
+// A token's G lanes, each with 4 V of its logits: x -> the softmax, and log sum exp as the result.  A token
+// all of whose logits are -Inf has no softmax: zeros, and 0.
+template <int G, int V>
+__device__ __forceinline__ float softmax(float (*x)[4]) {
+  float m = x[0][0];
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = fmaxf(m, x[v][j]);
+#pragma unroll
+  for (int off = 1; off < G; off *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
+  const bool none = m == -INFINITY;
+  float z = 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[v][j] = none && x[v][j] == -INFINITY ? 0.f : expf(x[v][j] - m);
+      z += x[v][j];
+    }
+#pragma unroll
+  for (int off = 1; off < G; off *= 2) z += __shfl_xor_sync(0xFFFFFFFFu, z, off);
+  if (z == 0.f) return 0.f;
+  const float inv = __fdiv_rn(1.f, z);
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[v][j] *= inv;
+  return m + logf(z);
+}
+
+// A block's sums of the softmax, of the squared lse and its counts go to a row of `partial`
+// [E sums | sum of squares | E counts | tokens]; the block that finishes last adds the rows in order.
+// 32768 tokens, 64 experts: see the launch.
+template <int G, int V, bool WIDE>
+__global__ void __launch_bounds__(BAL_THREADS) balance_fwd_kernel(const __grid_constant__ BalanceArgs a) {
+  extern __shared__ uint32_t sh[];               // [warps][E + 1] f32, then [E + 1] counts
+  __shared__ bool last_s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = lane & (G - 1);
+  const int E = a.E, W = 2 * (E + 1);
+  float* wsum = reinterpret_cast<float*>(sh);
+  int* hist = reinterpret_cast<int*>(sh + BAL_WARPS * (E + 1));
+  for (int e = tid; e <= E; e += BAL_THREADS) hist[e] = 0;
+  __syncthreads();
+  pdl_wait();
+  float acc[V][4], zz = 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[v][j] = 0.f;
+  int tokens = 0;
+  const int64_t step = int64_t(gridDim.x) * (BAL_THREADS / G);
+  // whole warps go round together: a lane past the last token, or at a masked one, adds nothing
+  for (int64_t t0 = (int64_t(blockIdx.x) * BAL_THREADS + warp * 32) / G; t0 < a.T; t0 += step) {
+    const int64_t t = t0 + lane / G;
+    const bool live = t < a.T && (a.mask == nullptr || a.mask[t] != 0);
+    float x[V][4];
+#pragma unroll
+    for (int v = 0; v < V; ++v) load4<WIDE>(a.logits + (live ? t : 0) * E, live ? (v * G + sub) * 4 : E, E, x[v]);
+    const float lse = softmax<G, V>(x);
+    if (!live) continue;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[v][j] += x[v][j];
+    for (int j = sub; j < a.k; j += G) {
+      const int e = a.idx[t * a.k + j];
+      if (e < 0 || e >= E) report_error(a.err, MOE_ERR_DEVICE_BOUNDS, SITE_BALANCE);
+      else atomicAdd(hist + e, 1);
+    }
+    if (sub == 0) {
+      zz = fmaf(lse, lse, zz);
+      ++tokens;
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int off = G; off < 32; off *= 2) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[v][j] += __shfl_xor_sync(0xFFFFFFFFu, acc[v][j], off);
+    zz += __shfl_xor_sync(0xFFFFFFFFu, zz, off);
+  }
+  if (lane < G) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if ((v * G + sub) * 4 + j < E) wsum[warp * (E + 1) + (v * G + sub) * 4 + j] = acc[v][j];
+  }
+  if (lane == 0) wsum[warp * (E + 1) + E] = zz;
+  if (tokens != 0) atomicAdd(hist + E, tokens);
+  __syncthreads();
+  uint32_t* mine = a.partial + int64_t(blockIdx.x) * W;
+  for (int e = tid; e <= E; e += BAL_THREADS) {
+    float s = 0.f;
+    for (int w = 0; w < BAL_WARPS; ++w) s += wsum[w * (E + 1) + e];
+    __stcg(mine + e, __float_as_uint(s));
+    __stcg(mine + E + 1 + e, uint32_t(hist[e]));
+  }
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) {
+    last_s = atomicAdd(a.ticket, 1u) + 1 == gridDim.x;
+    if (last_s) *a.ticket = 0;                   // for the next call
+  }
+  __syncthreads();
+  if (!last_s) return;
+  __threadfence();
+  // every warp adds every 16th row, then the warps' sums are added in order
+  for (int c = lane; c < W; c += 32) {
+    float s = 0.f;
+    int n = 0;
+#pragma unroll 4
+    for (int b = warp; b < int(gridDim.x); b += BAL_WARPS) {
+      const uint32_t p = __ldcg(a.partial + int64_t(b) * W + c);
+      if (c <= E) s += __uint_as_float(p);
+      else n += int(p);
+    }
+    if (c <= E) wsum[warp * (E + 1) + c] = s;
+    else sh[(BAL_WARPS + 1) * (E + 1) + warp * (E + 1) + c - E - 1] = uint32_t(n);
+  }
+  __syncthreads();
+  for (int c = tid; c < W; c += BAL_THREADS) {
+    if (c <= E) {
+      float s = 0.f;
+      for (int w = 0; w < BAL_WARPS; ++w) s += wsum[w * (E + 1) + c];
+      wsum[c] = s;                               // (column c of warp 0's, which nobody else reads)
+    } else {
+      int n = 0;
+      for (int w = 0; w < BAL_WARPS; ++w) n += int(sh[(BAL_WARPS + 1) * (E + 1) + w * (E + 1) + c - E - 1]);
+      hist[c - E - 1] = n;
+      a.counts[c - E - 1] = n;
+    }
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  const double n = hist[E] > 0 ? double(hist[E]) : 1.0;
+  double dot = 0.0;
+  for (int e = lane; e < E; e += 32) {
+    const double p = double(wsum[e]) / n;
+    a.prob[e] = float(p);
+    dot += double(hist[e]) * p;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, off);
+  if (lane == 0) {
+    const double balance = dot * E / (a.k * n), z = double(wsum[E]) / n;
+    a.loss[0] = float(double(a.alpha) * balance + double(a.beta) * z);
+    a.loss[1] = float(balance);
+    a.loss[2] = float(z);
+  }
+}
+
+template <int G, int V, bool WIDE>
+__global__ void __launch_bounds__(BAL_THREADS) balance_bwd_kernel(const __grid_constant__ BalanceArgs a) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & (G - 1);
+  const int E = a.E;
+  pdl_wait();
+  const int64_t n = a.counts[E] > 0 ? a.counts[E] : 1;
+  float f[V][4];
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int e = (v * G + sub) * 4 + j;
+      f[v][j] = e < E ? a.alpha * float(double(int64_t(E) * a.counts[e] - a.k * n) / double(a.k * n)) : 0.f;
+    }
+  const float g = (a.grad != nullptr ? *a.grad : 1.f) / float(n);
+  const int64_t step = int64_t(gridDim.x) * (BAL_THREADS / G);
+  for (int64_t t0 = (int64_t(blockIdx.x) * BAL_THREADS + warp * 32) / G; t0 < a.T; t0 += step) {
+    const int64_t t = t0 + lane / G;
+    const bool in = t < a.T, live = in && (a.mask == nullptr || a.mask[t] != 0);
+    float x[V][4];
+#pragma unroll
+    for (int v = 0; v < V; ++v) load4<WIDE>(a.logits + (live ? t : 0) * E, live ? (v * G + sub) * 4 : E, E, x[v]);
+    const float lse = softmax<G, V>(x);
+    float dot = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dot = fmaf(f[v][j], x[v][j], dot);
+#pragma unroll
+    for (int off = 1; off < G; off *= 2) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, off);
+    if (!in) continue;
+    const float base = 2.f * a.beta * lse - dot;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * G + sub) * 4;
+      float d[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) d[j] = live ? g * x[v][j] * (f[v][j] + base) : 0.f;
+      float* o = a.dlogits + t * E + c;
+      if constexpr (WIDE) {
+        if (c < E) *reinterpret_cast<float4*>(o) = make_float4(d[0], d[1], d[2], d[3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (c + j < E) o[j] = d[j];
+      }
+    }
+  }
+}
+
+template <int G, int V, bool WIDE>
+cudaError_t balance_run(const BalanceArgs& a, bool backward, cudaStream_t st) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int64_t need = (int64_t(a.T) + BAL_THREADS / G - 1) / (BAL_THREADS / G);
+  if (backward) {
+    const int64_t most = int64_t(sms) * 4;
+    return launch_pdl(balance_bwd_kernel<G, V, WIDE>, dim3(unsigned(need < most ? need : most)), dim3(BAL_THREADS), 0, st, a);
+  }
+  int64_t most = sms < kBalanceMaxParts ? sms : kBalanceMaxParts;
+  const size_t smem = size_t(2 * BAL_WARPS + 1) * (a.E + 1) * 4;             // at most 34 KB
+  return launch_pdl(balance_fwd_kernel<G, V, WIDE>, dim3(unsigned(need < most ? need : most)), dim3(BAL_THREADS), smem, st, a);
+}
+
+template <bool WIDE>
+cudaError_t balance_lanes(const BalanceArgs& a, bool backward, cudaStream_t st) {
+  const int fours = (a.E + 3) / 4;               // as few lanes a token as hold its logits, four each
+  if (fours <= 1) return balance_run<1, 1, WIDE>(a, backward, st);
+  if (fours <= 2) return balance_run<2, 1, WIDE>(a, backward, st);
+  if (fours <= 4) return balance_run<4, 1, WIDE>(a, backward, st);
+  if (fours <= 8) return balance_run<8, 1, WIDE>(a, backward, st);
+  if (fours <= 16) return balance_run<16, 1, WIDE>(a, backward, st);
+  if (fours <= 32) return balance_run<32, 1, WIDE>(a, backward, st);
+  return balance_run<32, 2, WIDE>(a, backward, st);
+}
+
+}  // namespace
+
+size_t balance_ws_bytes(int E) { return 256 + size_t(kBalanceMaxParts) * 2 * (E + 1) * 4; }
+
+cudaError_t launch_balance(const BalanceArgs& a, bool backward, cudaStream_t st) {
+  return a.E % 4 == 0 ? balance_lanes<true>(a, backward, st) : balance_lanes<false>(a, backward, st);
+}
+
+}  // namespace moe

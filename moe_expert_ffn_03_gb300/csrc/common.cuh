@@ -27,6 +27,9 @@ enum ErrSite : int {
   SITE_GEMM_DRAIN = 540,
   SITE_ROUTER_DW = 600,
   SITE_LINEAR = 700,
+  SITE_LINEAR8 = 720,
+  SITE_FP8_BLOCK = 740,
+  SITE_BALANCE = 750,
 };
 
 __device__ __forceinline__ void report_error(int* err, int code, int site) {

@@ -1,0 +1,390 @@
+// 8-bit tensors with one f32 scale per block of 128: quantizers of rows, of experts' rows along tokens and of
+// weights, the values back, and rows packed by expert.
+//
+// Page "Efficient MoE Training for Biological Foundation Models", section "MoE训练的瓶颈与TE的对应能力"
+// (8-bit operands with scales of blocks; the block of 128 with an f32 scale is an interface addition).
+//
+//   scale = amax / 448;  code = E4M3(value * (448 / amax))      amax: the block's largest magnitude
+//   rows    blocks of 1 x 128,   scales [ceil(cols/128)][rows]
+//   tokens  blocks of 128 x 1,   scales [blocks][cols]             rows laid out on blocks of 128 per expert
+//   tiles   blocks of 128 x 128, scales [blocks][ceil(cols/128)]   the same, or rows of matrices as they are
+// Scales lie along the index that the product keeps, so that its threads read neighbouring ones.
+#include "fp8_block.cuh"
+#include "kernels.cuh"
+#include "rows.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int Q_THREADS = 256;
+constexpr int Q_MAX_E = 256;
+constexpr int Q_ROWS = 8;                        // rows per thread of a tile of 128 x 128
+
+// A thread's eight neighbouring columns of a row (zeros past `left`), as floats.
+template <typename T, bool WIDE>
+struct Eight {
+  Raw<T, WIDE ? kWide<T> : 1> r[WIDE ? 8 / kWide<T> : 8];
+  __device__ __forceinline__ void load(const T* p, int left) {
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int i = 0; i < 8 / kWide<T>; ++i) {
+        if (left > 0) r[i].load(p + i * kWide<T>);
+        else r[i].zero();
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i < left) r[i].load(p + i);
+        else r[i].zero();
+      }
+    }
+  }
+  __device__ __forceinline__ void get(float* v) const {
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int i = 0; i < 8 / kWide<T>; ++i) r[i].get(v + i * kWide<T>);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r[i].get(v + i);
+    }
+  }
+};
+template <bool WIDE>
+__device__ __forceinline__ void put_codes(uint8_t* p, const uint32_t* q, int left) {
+  if constexpr (WIDE) {
+    if (left > 0) *reinterpret_cast<uint2*>(p) = make_uint2(q[0], q[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) p[i] = uint8_t(q[i >> 2] >> (8 * (i & 3)));
+  }
+}
+
+// Tiles of 128 rows x 128 columns, rows from an expert's first on (matrices of `mat_rows` rows: from the
+// matrix's); 16 lanes hold a row's 128 columns, a thread eight rows in registers, so that a tile is read once
+// for both of its formats.  A persistent grid, tiles of neighbouring columns one after the other.
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(Q_THREADS) block8_quantize_kernel(const __grid_constant__ Block8Args a) {
+  __shared__ uint32_t colmax[Q_THREADS / 32][B8];
+  __shared__ float colup[B8];
+  __shared__ uint32_t colbad[B8];
+  __shared__ int row0[Q_MAX_E + 1], blk0[Q_MAX_E + 1];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int sub = tid >> 4;                      // rows sub, sub + 16, ... of a tile
+  const int c8 = (tid & 15) * 8;
+  pdl_wait();
+  if (a.split_sizes != nullptr) {
+    if (warp == 0) {
+      // prefix sums of rows and blocks, eight experts per lane
+      int rows[8], sum = 0, blocks = 0;
+      int64_t all = 0;
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int e = lane * 8 + i;
+        const int s = e < a.E ? a.split_sizes[e] : 0;
+        const bool wrong = s < 0 || s > a.rows;
+        bad |= wrong;
+        rows[i] = wrong ? 0 : s;
+        all += rows[i];
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, off);
+      bad = __any_sync(0xFFFFFFFFu, bad) || all > a.rows;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (bad) rows[i] = 0;                    // nothing is written then; the products record the error
+        sum += rows[i];
+        blocks += (rows[i] + B8 - 1) / B8;
+      }
+      int rs = sum, bs = blocks;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int r = __shfl_up_sync(0xFFFFFFFFu, rs, off), q = __shfl_up_sync(0xFFFFFFFFu, bs, off);
+        if (lane >= off) {
+          rs += r;
+          bs += q;
+        }
+      }
+      rs -= sum;
+      bs -= blocks;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int e = lane * 8 + i;
+        if (e <= a.E) {
+          row0[e] = rs;
+          blk0[e] = bs;
+        }
+        rs += rows[i];
+        bs += (rows[i] + B8 - 1) / B8;
+      }
+      if (lane == 31 && a.E == Q_MAX_E) {
+        row0[Q_MAX_E] = rs;
+        blk0[Q_MAX_E] = bs;
+      }
+    }
+    __syncthreads();
+  }
+  const int cb = (a.cols + B8 - 1) / B8;
+  const int per = a.mat_rows > 0 ? (a.mat_rows + B8 - 1) / B8 : 0;           // blocks of rows of a matrix
+  const int64_t blocks = a.split_sizes != nullptr ? blk0[a.E]
+                         : a.mat_rows > 0         ? int64_t(a.E) * per
+                                                  : (a.rows + B8 - 1) / B8;
+  for (int64_t t = blockIdx.x; t < blocks * cb; t += gridDim.x) {
+    const int64_t blk = t / cb;
+    const int c0 = int(t - blk * cb) * B8, left = a.cols - c0 - c8;
+    int64_t first;                               // row of the source, and how many the tile has
+    int cnt;
+    if (a.split_sizes != nullptr) {
+      int lo = 0, hi = a.E - 1;                  // largest e with blk0[e] <= blk
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (blk0[mid] <= blk) lo = mid; else hi = mid - 1;
+      }
+      const int off = int(blk - blk0[lo]) * B8;
+      first = row0[lo] + off;
+      cnt = min(B8, row0[lo + 1] - row0[lo] - off);
+    } else if (a.mat_rows > 0) {
+      const int off = int(blk % per) * B8;
+      first = blk / per * a.mat_rows + off;
+      cnt = min(B8, a.mat_rows - off);
+    } else {
+      first = blk * B8;
+      cnt = int(a.rows - first < B8 ? a.rows - first : B8);
+    }
+    const int64_t trow = a.mat_rows > 0 ? first : blk * B8;                  // row of the second format's codes
+    Eight<T, WIDE> raw[Q_ROWS];
+#pragma unroll
+    for (int i = 0; i < Q_ROWS; ++i) {
+      const int r = sub + 16 * i;
+      raw[i].load(static_cast<const T*>(a.src) + (first + r) * a.ld + c0 + c8, r < cnt ? left : 0);
+    }
+    uint32_t cmax[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) cmax[j] = 0;
+#pragma unroll
+    for (int i = 0; i < Q_ROWS; ++i) {
+      float v[8];
+      raw[i].get(v);
+      if (a.tcodes != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) cmax[j] = max(cmax[j], abs_bits(v[j]));
+      }
+      if (a.codes != nullptr) {
+        uint32_t amax = v_amax<8>(v);
+#pragma unroll
+        for (int off = 1; off < 16; off *= 2) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
+        const int r = sub + 16 * i;
+        if (r < cnt) {
+          const Block8 b(amax);
+          const uint32_t q[2] = {b.codes4(v), b.codes4(v + 4)};
+          put_codes<WIDE>(a.codes + (first + r) * a.cols + c0 + c8, q, left);
+          if (c8 == 0) a.scales[int64_t(c0 / B8) * a.rows + first + r] = Block8::scale(amax);
+        }
+      }
+    }
+    if (a.tcodes == nullptr) continue;
+    if (a.tiles) {
+      uint32_t amax = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = max(amax, cmax[j]);
+      amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+      __syncthreads();                           // the tile before has been read
+      if (lane == 0) colmax[warp][0] = amax;
+      __syncthreads();
+      amax = 0;
+#pragma unroll
+      for (int w = 0; w < Q_THREADS / 32; ++w) amax = max(amax, colmax[w][0]);
+      if (tid == 0) a.tscales[blk * cb + c0 / B8] = Block8::scale(amax);
+      const Block8 b(amax);
+#pragma unroll
+      for (int i = 0; i < Q_ROWS; ++i) {
+        const int r = sub + 16 * i;
+        float v[8];
+        raw[i].get(v);
+        // rows past the expert's last are zeros on its last block; a matrix has none
+        const uint32_t q[2] = {r < cnt ? b.codes4(v) : 0u, r < cnt ? b.codes4(v + 4) : 0u};
+        if (r < cnt || a.mat_rows == 0) put_codes<WIDE>(a.tcodes + (trow + r) * a.cols + c0 + c8, q, left);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) cmax[j] = max(cmax[j], __shfl_xor_sync(0xFFFFFFFFu, cmax[j], 16));
+      __syncthreads();                           // the tile before has been read
+      if (lane < 16) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) colmax[warp][c8 + j] = cmax[j];
+      }
+      __syncthreads();
+      if (tid < B8) {
+        uint32_t amax = 0;
+#pragma unroll
+        for (int w = 0; w < Q_THREADS / 32; ++w) amax = max(amax, colmax[w][tid]);
+        const Block8 b(amax);
+        colup[tid] = b.up;
+        colbad[tid] = b.bad;
+        if (c0 + tid < a.cols) a.tscales[blk * a.cols + c0 + tid] = Block8::scale(amax);
+      }
+      __syncthreads();
+      float up[8];
+      uint32_t nan[2] = {0, 0};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        up[j] = colup[c8 + j];
+        if (colbad[c8 + j]) nan[j >> 2] |= 0xFFu << (8 * (j & 3));
+      }
+#pragma unroll
+      for (int i = 0; i < Q_ROWS; ++i) {
+        float v[8];
+        raw[i].get(v);
+        uint32_t q[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          q[k] = cvt_e4m3x2(v[4 * k] * up[4 * k], v[4 * k + 1] * up[4 * k + 1]) |
+                 (cvt_e4m3x2(v[4 * k + 2] * up[4 * k + 2], v[4 * k + 3] * up[4 * k + 3]) << 16);
+          q[k] = sub + 16 * i < cnt ? (q[k] & ~nan[k]) | (0x7F7F7F7Fu & nan[k]) : 0u;
+        }
+        put_codes<WIDE>(a.tcodes + (trow + sub + 16 * i) * a.cols + c0 + c8, q, left);
+      }
+    }
+  }
+}
+
+// Values of codes: a warp takes four rows of 256 columns at a time, eight columns a lane.
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(Q_THREADS) block8_dequantize_kernel(const __grid_constant__ Block8Back a) {
+  const int lane = threadIdx.x & 31;
+  const int chunks = (a.cols + 255) / 256;
+  const int64_t items = (a.rows + 3) / 4 * chunks;
+  pdl_wait();
+  for (int64_t it = (int64_t(blockIdx.x) * Q_THREADS + threadIdx.x) >> 5; it < items; it += (int64_t(gridDim.x) * Q_THREADS) >> 5) {
+    const int64_t r4 = it / chunks;
+    const int col = int(it - r4 * chunks) * 256 + lane * 8, left = a.cols - col;
+    if (left <= 0) continue;
+    uint32_t q[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t row = r4 * 4 + i;
+      q[i][0] = q[i][1] = 0;
+      if (row >= a.rows) continue;
+      const uint8_t* p = a.codes + row * a.cols + col;
+      if constexpr (WIDE) {
+        const uint2 w = __ldcg(reinterpret_cast<const uint2*>(p));
+        q[i][0] = w.x;
+        q[i][1] = w.y;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < left) q[i][j >> 2] |= uint32_t(p[j]) << (8 * (j & 3));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t row = r4 * 4 + i;
+      if (row >= a.rows) continue;
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = e4m3x2_to_float2(q[i][k >> 1] >> (16 * (k & 1)));
+        v[2 * k] = f.x;
+        v[2 * k + 1] = f.y;
+      }
+      const int64_t rb = a.mat_rows > 0 ? row / a.mat_rows * ((a.mat_rows + B8 - 1) / B8) + row % a.mat_rows / B8 : row / B8;
+      if (a.format == MOE_FP8_TOKENS) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < left) v[j] *= __ldg(a.scales + rb * a.cols + col + j);
+      } else {
+        const float s = a.format == MOE_FP8_ROWS ? __ldg(a.scales + int64_t(col / B8) * a.rows + row)
+                                                 : __ldg(a.scales + rb * ((a.cols + B8 - 1) / B8) + col / B8);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= s;
+      }
+      T* o = static_cast<T*>(a.dst) + row * a.ld + col;
+      if constexpr (WIDE) {
+        if constexpr (sizeof(T) == 2) {
+          store_vec<8>(o, v);
+        } else {
+          store_vec<4>(o, v);
+          store_vec<4>(o + 4, v + 4);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < left) store_vec<1>(o + j, v + j);
+      }
+    }
+  }
+}
+
+// Rows of tokens copied to their places by expert: row pos_of[t][j] of the output is token t.  A warp takes a
+// token: its codes once from memory, k times out; then the scales of its blocks.
+__global__ void __launch_bounds__(Q_THREADS) block8_pack_kernel(const uint8_t* codes, const float* scales, const int* pos_of, int T,
+                                                                int k, int cols, int64_t rows, uint8_t* codes_out,
+                                                                float* scales_out, int* err) {
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  for (int64_t t = (int64_t(blockIdx.x) * Q_THREADS + threadIdx.x) >> 5; t < T; t += (int64_t(gridDim.x) * Q_THREADS) >> 5) {
+    for (int c = lane * 16; c < cols; c += 512) {
+      const uint4 v = __ldcg(reinterpret_cast<const uint4*>(codes + t * cols + c));
+      for (int j = 0; j < k; ++j) {
+        const int p = pos_of[t * k + j];
+        if (p >= 0 && p < rows) *reinterpret_cast<uint4*>(codes_out + int64_t(p) * cols + c) = v;
+        else report_error(err, MOE_ERR_DEVICE_BOUNDS, SITE_FP8_BLOCK);
+      }
+    }
+    const int cb = (cols + B8 - 1) / B8;
+    for (int i = lane; i < cb * k; i += 32) {
+      const int j = i % k, b = i / k;
+      const int p = pos_of[t * k + j];
+      if (p >= 0 && p < rows) scales_out[b * rows + p] = __ldg(scales + int64_t(b) * T + t);
+    }
+  }
+}
+
+cudaError_t sm_count(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  return e == cudaSuccess ? cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) : e;
+}
+
+}  // namespace
+
+cudaError_t launch_block8_quantize(const Block8Args& a, bool f32, cudaStream_t st) {
+  int sms = 0;
+  if (const cudaError_t e = sm_count(&sms); e != cudaSuccess) return e;
+  const int64_t cb = (a.cols + B8 - 1) / B8;
+  const int64_t tiles = cb * (a.mat_rows > 0 ? int64_t(a.E) * ((a.mat_rows + B8 - 1) / B8) : a.rows / B8 + (a.split_sizes ? a.E : 1));
+  const int64_t most = int64_t(sms) * 8;
+  const dim3 grid(unsigned(tiles < most ? tiles : most));
+  const bool wide = a.cols % 8 == 0 && a.ld % 8 == 0;
+  if (f32)
+    return wide ? launch_pdl(block8_quantize_kernel<float, true>, grid, dim3(Q_THREADS), 0, st, a)
+                : launch_pdl(block8_quantize_kernel<float, false>, grid, dim3(Q_THREADS), 0, st, a);
+  return wide ? launch_pdl(block8_quantize_kernel<__nv_bfloat16, true>, grid, dim3(Q_THREADS), 0, st, a)
+              : launch_pdl(block8_quantize_kernel<__nv_bfloat16, false>, grid, dim3(Q_THREADS), 0, st, a);
+}
+
+cudaError_t launch_block8_dequantize(const Block8Back& a, bool f32, cudaStream_t st) {
+  int sms = 0;
+  if (const cudaError_t e = sm_count(&sms); e != cudaSuccess) return e;
+  const int64_t items = (a.rows + 3) / 4 * ((a.cols + 255) / 256), blocks = (items + Q_THREADS / 32 - 1) / (Q_THREADS / 32);
+  const int64_t most = int64_t(sms) * 8;
+  const dim3 grid(unsigned(blocks < most ? blocks : most));
+  const bool wide = a.cols % 8 == 0 && a.ld % 8 == 0;
+  if (f32)
+    return wide ? launch_pdl(block8_dequantize_kernel<float, true>, grid, dim3(Q_THREADS), 0, st, a)
+                : launch_pdl(block8_dequantize_kernel<float, false>, grid, dim3(Q_THREADS), 0, st, a);
+  return wide ? launch_pdl(block8_dequantize_kernel<__nv_bfloat16, true>, grid, dim3(Q_THREADS), 0, st, a)
+              : launch_pdl(block8_dequantize_kernel<__nv_bfloat16, false>, grid, dim3(Q_THREADS), 0, st, a);
+}
+
+cudaError_t launch_block8_pack(const uint8_t* codes, const float* scales, const int* pos_of, int T, int k, int cols,
+                               int64_t rows, uint8_t* codes_out, float* scales_out, int* err, cudaStream_t st) {
+  int sms = 0;
+  if (const cudaError_t e = sm_count(&sms); e != cudaSuccess) return e;
+  const int64_t blocks = (int64_t(T) + Q_THREADS / 32 - 1) / (Q_THREADS / 32), most = int64_t(sms) * 8;
+  return launch_pdl(block8_pack_kernel, dim3(unsigned(blocks < most ? blocks : most)), dim3(Q_THREADS), 0, st, codes, scales,
+                    pos_of, T, k, cols, rows, codes_out, scales_out, err);
+}
+
+}  // namespace moe

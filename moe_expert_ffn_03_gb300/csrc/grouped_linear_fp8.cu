@@ -1,0 +1,555 @@
+// Linear layers grouped by expert on dense ragged rows with 8-bit operands: E4M3 codes and one f32
+// scale per block of 128, forward, input gradient and weight gradient on the tensor cores (tcgen05
+// kind::f8f6f4).
+//
+// Page "Efficient MoE Training for Biological Foundation Models", sections "GroupedLinear：把逐专家
+// 循环改成一次分组GEMM" (one grouped call over the experts' rows) and "MoE训练的瓶颈与TE的对应能力"
+// (8-bit operands; the blocks of 128 with f32 scales are an interface addition).
+//
+//   D[m][n] = sum over blocks b of 128 of  sa[b][m] * sb[b][n / 128] * (sum over the block of A * B)
+//   forward   m rows,      n output features, sum over K:      A = x codes,  B = w codes
+//   dgrad     m rows,      n input features,  sum over N:      A = dy codes, B = w codes, MN-major
+//   wgrad     m out. feat. n input features,  sum over tokens: A = dy codes, B = x codes, both MN-major
+//
+// The tensor cores sum codes, so every block of 128 is a product of its own, whose f32 sums are scaled and
+// added to f32 sums in registers.  What that costs decides the layout: with m in the lanes and n in the
+// columns of tensor memory, a thread's row has one scale and its 128 columns (aligned to a block of the B
+// side) another, so a partial sum takes one multiply-add with one factor per thread.  (A scale per
+// column would have to come out of shared memory, 32 bits for every multiply-add.)  256 x 256 x 128 takes
+// the pair's tensor pipes 512 clocks, its epilogue warps 256 of packed multiply-adds and 64 of reads.
+//
+// Persistent CTA pairs (clusters of two, one CTA per SM), tiles of 256 m x 256 n with cta_group::2: each
+// CTA stages its 128 m and its 128 n of a block, 32 KB a stage, six stages.  The 512 columns of tensor
+// memory are two buffers of 256: the tensor pipe fills one with a block's sums while the other is added.
+//   warp 0       TMA producer of the A side, warp 2 of the B side
+//   warp 1       tensor memory; in the leader, the MMAs
+//   warp 3       the experts' prefix sums
+//   warps 4..11  sums: four per lane quarter, 128 columns each, with 224 registers a thread (the other
+//                four warps give up theirs: 128 x 56 + 256 x 224 = 384 x 168)
+// Waits are bounded as everywhere; each lasts as long as a block or a tile's output at most.
+#include <atomic>
+#include <cstdio>
+
+#include "kernels.cuh"
+#include "tcgen05.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int L8_M = 256, L8_N = 256;            // the pair's tile
+constexpr int L8_KT = 128;                       // a block of the contraction: one stage
+constexpr int L8_SIDE = 128 * L8_KT;             // bytes of a CTA's A or B in a stage
+constexpr int L8_STAGE = 2 * L8_SIDE;
+constexpr int L8_STAGES = 6;
+constexpr int L8_EPI_WARPS = 8;
+constexpr int L8_THREADS = 32 * (4 + L8_EPI_WARPS);
+constexpr int L8_REGS = 168, L8_REGS_FEW = 56, L8_REGS_MANY = 224;
+static_assert(128 * L8_REGS_FEW + 32 * L8_EPI_WARPS * L8_REGS_MANY == L8_THREADS * L8_REGS, "register split");
+constexpr int L8_MAX_E = 256;
+constexpr int L8_GROUP = 8;                      // row tiles that share the sweep over the weights
+constexpr int L8_SMALL = 32;                     // rows of the small box of rows
+
+constexpr int L8_OFF_BAR = L8_STAGES * L8_STAGE;
+constexpr int L8_BARS = 2 * L8_STAGES + 5;       // full, empty, tmem_full[2], tmem_empty[2], drain
+constexpr int L8_OFF_MISC = L8_OFF_BAR + L8_BARS * 8;
+constexpr int L8_OFF_SEG = (L8_OFF_MISC + 16 + 15) & ~15;        // row0[E+1], tile0[E+1], order[E]
+constexpr int L8_SMEM = L8_OFF_SEG + 3 * (L8_MAX_E + 1) * 4 + 1024;
+static_assert(L8_SMEM <= 232448, "shared memory budget");
+
+// kind::f8f6f4 instruction descriptor: E4M3 x E4M3 -> f32, M = 256, N columns; a_mn, b_mn: the operand
+// is MN-major.
+__device__ __forceinline__ uint32_t l8_idesc(bool a_mn, bool b_mn, int N) {
+  return (1u << 4) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) | (uint32_t(N >> 3) << 17) |
+         (uint32_t(L8_M >> 4) << 24);
+}
+__device__ __forceinline__ void l8_mma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+struct Ring {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == L8_STAGES) {
+      st = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
+struct Tile8 {
+  int e;
+  int m0, cnt;     // first m (a row of all experts', or an output feature of e) and how many the tile has
+  int n0, n;       // first n, and the MMA's columns: those left rounded up to 32; CTA r holds n0 + r * n/2 ..
+  int c0;          // contraction: first index (wgrad: row of the layout on blocks)
+  int blocks;      // its blocks of 128
+  int last;        // indices in the last block
+};
+
+template <int MODE>
+__device__ __forceinline__ int l8_cols(const Linear8Args& a) { return MODE == LIN_FWD ? a.N : a.K; }
+
+template <int MODE>
+__device__ __forceinline__ int l8_tiles(const Linear8Args& a, const int* tile0) {
+  const int nt = (l8_cols<MODE>(a) + L8_N - 1) / L8_N;
+  return MODE == LIN_WGRAD ? a.E * ((a.N + L8_M - 1) / L8_M) * nt : tile0[a.E] * nt;
+}
+
+// tile0: the experts' first row tiles; wgrad: their first blocks of 128 rows.
+template <int MODE>
+__device__ __forceinline__ void l8_decode(const Linear8Args& a, const int* row0, const int* tile0, const int* order, int t,
+                                          Tile8& tl) {
+  const int cols = l8_cols<MODE>(a), nt = (cols + L8_N - 1) / L8_N;
+  int tn;
+  if (MODE == LIN_WGRAD) {
+    // experts with the most rows first; inside an expert the n tiles of a few m tiles in turn
+    const int mt = (a.N + L8_M - 1) / L8_M;
+    const int slot = t / (mt * nt), rem = t - slot * (mt * nt);
+    const int per = L8_GROUP * nt;
+    const int g = rem / per, first = g * L8_GROUP, gs = min(L8_GROUP, mt - first);
+    const int local = rem - g * per;
+    tl.e = order[slot];
+    tn = local / gs;
+    tl.m0 = (first + local % gs) * L8_M;
+    tl.cnt = min(L8_M, a.N - tl.m0);
+    const int rows = row0[tl.e + 1] - row0[tl.e];
+    tl.c0 = tile0[tl.e] * L8_KT;
+    tl.blocks = (rows + L8_KT - 1) / L8_KT;
+    tl.last = rows - (tl.blocks - 1) * L8_KT;
+  } else {
+    const int total = tile0[a.E];
+    const int per = L8_GROUP * nt;
+    const int g = t / per, first = g * L8_GROUP, gs = min(L8_GROUP, total - first);
+    const int local = t - g * per;
+    const int tt = first + local % gs;
+    int lo = 0, hi = a.E - 1;                    // largest e with tile0[e] <= tt
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (tile0[mid] <= tt) lo = mid; else hi = mid - 1;
+    }
+    tl.e = lo;
+    tn = local / gs;
+    tl.m0 = row0[lo] + (tt - tile0[lo]) * L8_M;
+    tl.cnt = min(L8_M, row0[lo + 1] - tl.m0);
+    const int c = MODE == LIN_FWD ? a.K : a.N;
+    tl.c0 = 0;
+    tl.blocks = (c + L8_KT - 1) / L8_KT;
+    tl.last = c - (tl.blocks - 1) * L8_KT;
+  }
+  tl.n0 = tn * L8_N;
+  tl.n = (min(L8_N, cols - tl.n0) + 31) & ~31;
+}
+
+// The pair's tile after t.  wgrad: there and back, since tiles come longest first: the pair that got the
+// longest of one round gets the shortest of the next.
+template <int MODE>
+__device__ __forceinline__ int l8_after(int t, int num_pairs) {
+  return t + (MODE == LIN_WGRAD ? 2 * (num_pairs - 1 - t % num_pairs) + 1 : num_pairs);
+}
+
+// acc += part * f, two at a time
+__device__ __forceinline__ void l8_add(float* acc, const uint32_t* part, float2 f) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    const float2 r = __ffma2_rn(make_float2(__uint_as_float(part[i]), __uint_as_float(part[i + 1])), f,
+                                make_float2(acc[i], acc[i + 1]));
+    acc[i] = r.x;
+    acc[i + 1] = r.y;
+  }
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(L8_THREADS, 1)
+    grouped_linear_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmAs,
+                              const __grid_constant__ CUtensorMap tmB, const Linear8Args args) {
+  constexpr bool A_MN = MODE == LIN_WGRAD, B_MN = MODE != LIN_FWD;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L8_OFF_BAR);
+  uint64_t* empty = full + L8_STAGES;
+  uint64_t* tmem_full = empty + L8_STAGES;
+  uint64_t* tmem_empty = tmem_full + 2;
+  uint64_t* drain = tmem_empty + 2;
+  uint32_t* tmem_base_s = reinterpret_cast<uint32_t*>(smem + L8_OFF_MISC);
+  volatile int* abort_s = reinterpret_cast<volatile int*>(smem + L8_OFF_MISC + 4);
+  volatile int* bad_s = reinterpret_cast<volatile int*>(smem + L8_OFF_MISC + 8);
+  int* row0 = reinterpret_cast<int*>(smem + L8_OFF_SEG);
+  int* tile0 = row0 + L8_MAX_E + 1;
+  int* order = tile0 + L8_MAX_E + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();       // 0: leader (issues the MMAs), 1: peer
+  const int pair = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L8_STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tmem_full[b], 1);
+      mbar_init(&tmem_empty[b], 2 * L8_EPI_WARPS);
+    }
+    mbar_init(drain, 1);
+    *abort_s = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmAs);
+    prefetch_tmap(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_base_s, 512);                // collectively with the peer CTA
+    tmem_relinquish();
+  }
+  cluster_arrive();                              // this CTA's barriers are initialised
+  // Up to here the kernel touches only its own shared memory, tensor memory and parameters.
+  pdl_wait();
+  if (warp == 3) {
+    // prefix sums of the experts' rows and of their row tiles (wgrad: blocks of 128), eight experts per lane
+    constexpr int PER = MODE == LIN_WGRAD ? L8_KT : L8_M;
+    int rows[8], sum = 0, tiles = 0;
+    int64_t all = 0;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = lane * 8 + i;
+      const int s = e < args.E ? args.split_sizes[e] : 0;
+      const bool wrong = s < 0 || s > args.rows;
+      bad |= wrong;
+      rows[i] = wrong ? 0 : s;
+      all += rows[i];
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, off);
+    bad = __any_sync(0xFFFFFFFFu, bad) || all > args.rows;
+    if (lane == 0) {
+      *bad_s = bad;
+      if (bad) report_error(args.err, MOE_ERR_DEVICE_BOUNDS, SITE_LINEAR8 + 9);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (bad) rows[i] = 0;
+      sum += rows[i];
+      tiles += (rows[i] + PER - 1) / PER;
+    }
+    int rs = sum, ts = tiles;                    // inclusive scans over the lanes
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int r = __shfl_up_sync(0xFFFFFFFFu, rs, off), q = __shfl_up_sync(0xFFFFFFFFu, ts, off);
+      if (lane >= off) {
+        rs += r;
+        ts += q;
+      }
+    }
+    rs -= sum;
+    ts -= tiles;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = lane * 8 + i;
+      if (e <= args.E) {
+        row0[e] = rs;
+        tile0[e] = ts;
+      }
+      rs += rows[i];
+      ts += (rows[i] + PER - 1) / PER;
+    }
+    if (lane == 31 && args.E == L8_MAX_E) {
+      row0[L8_MAX_E] = rs;
+      tile0[L8_MAX_E] = ts;
+    }
+    __syncwarp();
+    if (MODE == LIN_WGRAD) {
+      for (int e = lane; e < args.E; e += 32) {
+        const int me = row0[e + 1] - row0[e];
+        int r = 0;
+        for (int f = 0; f < args.E; ++f) {
+          const int other = row0[f + 1] - row0[f];
+          r += (other > me) || (other == me && f < e);
+        }
+        order[r] = e;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_wait();                                // and the other's, before anything arrives there
+  tc_fence_after();
+  const uint32_t tmem = *tmem_base_s;
+  // inconsistent split_sizes: nothing is computed (the error word says so)
+  const int total = *bad_s ? 0 : l8_tiles<MODE>(args, tile0);
+  const uint64_t lim = args.wait_limit_ns;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L8_REGS_FEW));
+    if (lane == 0 && (warp == 0 || warp == 2) && !args.selftest_no_loads) {
+      // ---------------- TMA producers (both CTAs): warp 0 the A side, warp 2 the B side ----------------
+      const bool a_side = warp == 0;
+      const uint32_t full_c0 = mapa_shared(smem_u32(full), 0);
+      Ring cur;
+      bool ok = true;
+      Tile8 tl;
+      for (int t = pair; ok && t < total; t = l8_after<MODE>(t, num_pairs)) {
+        l8_decode<MODE>(args, row0, tile0, order, t, tl);
+        // A boxes of 128 m, or 32 rows where the CTA has no more; none where it has no m at all (what the
+        // stage holds there instead only meets lanes that nobody stores)
+        const auto a_bytes = [&](int r) {
+          const int left = tl.cnt - r * 128;
+          return left <= 0 ? 0 : !A_MN && left <= L8_SMALL ? L8_SMALL * L8_KT : L8_SIDE;
+        };
+        const int mine = a_bytes(int(rank)), m = tl.m0 + int(rank) * 128, nr = tl.n0 + int(rank) * (tl.n >> 1);
+        for (int kt = 0; kt < tl.blocks; ++kt, cur.next()) {
+          if (!wait_phase_inline(&empty[cur.st], cur.ph ^ 1u, abort_s, args.err, SITE_LINEAR8, lim)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar_c = full_c0 + uint32_t(cur.st) * 8u;
+          uint8_t* pa = smem + cur.st * L8_STAGE;
+          const int c = tl.c0 + kt * L8_KT;
+          if (a_side) {
+            if (rank == 0) mbar_arrive_expect_tx(&full[cur.st], uint32_t(a_bytes(0) + a_bytes(1) + 2 * L8_SIDE));
+            if (mine != 0) tma_load_2d(pa, mine == L8_SIDE ? &tmA : &tmAs, A_MN ? m : c, A_MN ? c : m, bar_c);
+          } else if (MODE == LIN_WGRAD) {
+            tma_load_2d(pa + L8_SIDE, &tmB, nr, c, bar_c);
+          } else {
+            tma_load_3d(pa + L8_SIDE, &tmB, B_MN ? nr : c, B_MN ? c : nr, tl.e, bar_c);
+          }
+        }
+      }
+      pdl_launch_dependents();
+    } else if (warp == 1) {
+      if (lane == 0 && rank == 0) {
+        // ---------------- MMA issuer (leader) ----------------
+        const uint64_t a_desc = A_MN ? desc_sw128_mn(smem_u32(smem), L8_SIDE) : desc_sw128(smem_u32(smem));
+        const uint64_t b_desc = B_MN ? desc_sw128_mn(smem_u32(smem + L8_SIDE), L8_SIDE) : desc_sw128(smem_u32(smem + L8_SIDE));
+        // 32 of the contraction, in the descriptors' 16-byte units: 32 bytes of a K-major row, four
+        // 8-row groups (4 KB) of an MN-major block
+        constexpr uint32_t A_K = A_MN ? 256 : 2, B_K = B_MN ? 256 : 2;
+        Ring cur;
+        uint32_t used = 0;                       // buffers used so far
+        bool ok = true, issued = false;
+        Tile8 tl;
+        for (int t = pair; ok && t < total; t = l8_after<MODE>(t, num_pairs)) {
+          l8_decode<MODE>(args, row0, tile0, order, t, tl);
+          const uint32_t idesc = l8_idesc(A_MN, B_MN, tl.n);
+          for (int kt = 0; kt < tl.blocks; ++kt, cur.next(), ++used) {
+            const uint32_t b = used & 1u;
+            if (!wait_phase_inline(&tmem_empty[b], ((used >> 1) & 1u) ^ 1u, abort_s, args.err, SITE_LINEAR8 + 1, lim) ||
+                !wait_phase_inline(&full[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR8 + 2, lim)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t off = uint64_t(cur.st * (L8_STAGE >> 4));
+            const uint32_t acc = tmem + b * L8_N;
+            const int groups = kt + 1 == tl.blocks ? (tl.last + 31) >> 5 : L8_KT / 32;
+#pragma unroll
+            for (int kk = 0; kk < L8_KT / 32; ++kk)
+              if (kk < groups) l8_mma(acc, a_desc + off + A_K * kk, b_desc + off + B_K * kk, idesc, kk != 0);
+            issued = true;
+            tc_commit(&empty[cur.st]);           // frees the stage in both CTAs
+            tc_commit(&tmem_full[b]);
+          }
+        }
+        if (!ok && issued) {
+          tc_commit(drain);
+          const uint64_t t0 = globaltimer_ns();
+          while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < 20000000ull) {
+          }
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L8_REGS_MANY));
+    // ---------------- sums (both CTAs) ----------------
+    const int q = warp & 3;                      // lane quarter this warp may access
+    const int col0 = ((warp - 4) >> 2) * 128;    // its columns of a buffer: one block of the B side
+    const uint32_t tmem_row = tmem + (uint32_t(q * 32) << 16) + uint32_t(col0);
+    const uint32_t tmem_empty_c0 = mapa_shared(smem_u32(tmem_empty), 0);
+    const int cols = l8_cols<MODE>(args);
+    uint32_t used = 0;
+    bool ok = true;
+    Tile8 tl;
+    for (int t = pair; ok && t < total; t = l8_after<MODE>(t, num_pairs)) {
+      l8_decode<MODE>(args, row0, tile0, order, t, tl);
+      const int at = int(rank) * 128 + q * 32;   // of the tile's m, this warp's first
+      const bool live = at < tl.cnt && col0 < tl.n;
+      const int r = min(at + lane, tl.cnt - 1);
+      // the scales of the lane's m and of the warp's columns, block after block
+      const float* sa = args.sa + (MODE == LIN_WGRAD ? int64_t(tl.c0 / L8_KT) * args.N : 0) + tl.m0 + r;
+      const float* sb = args.sb;
+      const int64_t sa_step = MODE == LIN_WGRAD ? args.N : args.rows;
+      int64_t sb_step;
+      const int nb = (tl.n0 + col0) / 128, kbs = (args.K + 127) / 128, nbs = (args.N + 127) / 128;
+      if (MODE == LIN_FWD) {
+        sb += (int64_t(tl.e) * nbs + nb) * kbs;
+        sb_step = 1;
+      } else {
+        sb += (MODE == LIN_DGRAD ? int64_t(tl.e) * nbs : int64_t(tl.c0 / L8_KT)) * kbs + nb;
+        sb_step = kbs;
+      }
+      float acc[128];
+#pragma unroll
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      // this block's factors, the next one's on their way
+      const bool any = live && tl.blocks > 0;
+      float fa = any ? __ldg(sa) : 0.f, fb = any ? __ldg(sb) : 0.f;
+      for (int kt = 0; kt < tl.blocks; ++kt, ++used) {
+        const float f = fa * fb;
+        if (live && kt + 1 < tl.blocks) {
+          fa = __ldg(sa + (kt + 1) * sa_step);
+          fb = __ldg(sb + (kt + 1) * sb_step);
+        }
+        const uint32_t b = used & 1u;
+        ok = wait_phase_warp_inline(&tmem_full[b], (used >> 1) & 1u, abort_s, args.err, SITE_LINEAR8 + 4, lim);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t src = tmem_row + b * L8_N;
+        const float2 f2 = make_float2(f, f);
+        if (live) {
+          uint32_t p0[32], p1[32];
+          tmem_ld32_async(src, p0);
+          tmem_wait_ld<32>(p0);
+          tmem_ld32_async(src + 32, p1);
+          l8_add(acc, p0, f2);
+          tmem_wait_ld<32>(p1);
+          tmem_ld32_async(src + 64, p0);
+          l8_add(acc + 32, p1, f2);
+          tmem_wait_ld<32>(p0);
+          tmem_ld32_async(src + 96, p1);
+          l8_add(acc + 64, p0, f2);
+          tmem_wait_ld<32>(p1);
+          tc_fence_before();
+          if (lane == 0) mbar_arrive_cluster_relaxed(tmem_empty_c0 + b * 8u);
+          l8_add(acc + 96, p1, f2);
+        } else if (lane == 0) {
+          mbar_arrive_cluster_relaxed(tmem_empty_c0 + b * 8u);
+        }
+      }
+      if (!ok || !live || at + lane >= tl.cnt) continue;
+      // a lane's row: 32 bytes (16 columns) at a time; columns come in multiples of 16
+      __nv_bfloat16* o = args.out + ((MODE == LIN_WGRAD ? int64_t(tl.e) * args.N : 0) + tl.m0 + at + lane) * args.ldo +
+                         tl.n0 + col0;
+#pragma unroll
+      for (int c = 0; c < 128; c += 16) {
+        if (tl.n0 + col0 + c >= cols) break;
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(acc[c + 2 * i], acc[c + 2 * i + 1]);
+        if (args.out_v8) {
+          st_global_v8(o + c, w);
+        } else {
+          reinterpret_cast<uint4*>(o + c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          reinterpret_cast<uint4*>(o + c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0 && *abort_s) {
+    // A wait gave up in this CTA, of whichever warp: copies issued before land before the shared memory
+    // goes (they take microseconds; bounded).
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000ull) {
+    }
+  }
+  cluster_sync();                                // no CTA leaves while the pair's MMAs or arrivals may touch it
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// 8-bit map over row-major [batch][rows][inner] (batch 0: no such dimension), boxes of 128 bytes x box_rows
+// with 128-byte swizzle.
+bool l8_map(CUtensorMap* m, const void* base, int64_t inner, int64_t rows, int64_t batch, int box_rows) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[3] = {cuuint64_t(inner), cuuint64_t(rows), cuuint64_t(batch)};
+  cuuint64_t strides[2] = {cuuint64_t(inner), cuuint64_t(inner) * cuuint64_t(rows)};
+  cuuint32_t box[3] = {128, cuuint32_t(box_rows), 1}, estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, batch > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE>
+cudaError_t l8_launch(const CUtensorMap& ma, const CUtensorMap& mas, const CUtensorMap& mb, const Linear8Args& a, int grid,
+                      cudaStream_t st) {
+  // attributes are per device: set and checked once on each device this process uses
+  constexpr int kMaxDevices = 64;
+  static std::atomic<bool> ready[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices || !ready[dev].load(std::memory_order_acquire)) {
+    cudaFuncAttributes f;
+    e = cudaFuncGetAttributes(&f, grouped_linear_fp8_kernel<MODE>);
+    if (e != cudaSuccess) return e;
+    // the warps' shares have to add up to what the block is launched with, or they would wait for ever
+    if (f.numRegs != L8_REGS) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(grouped_linear_fp8_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, L8_SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < kMaxDevices) ready[dev].store(true, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(L8_THREADS);
+  cfg.dynamicSmemBytes = L8_SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // the kernel calls pdl_wait()
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, grouped_linear_fp8_kernel<MODE>, ma, mas, mb, a);
+}
+
+}  // namespace
+
+size_t linear8_ws_bytes() { return 256; }
+
+cudaError_t launch_grouped_linear_fp8(int mode, const Linear8Args& args, const uint8_t* a_codes, const uint8_t* b_codes,
+                                      cudaStream_t st, char* msg, size_t msg_len) {
+  Linear8Args a = args;
+  CUtensorMap ma, mas, mb;
+  bool ok;
+  if (mode == LIN_WGRAD) {
+    const int64_t rows = (a.rows / L8_KT + a.E) * L8_KT;             // of the layout on blocks
+    ok = l8_map(&ma, a_codes, a.N, rows, 0, 128) && l8_map(&mb, b_codes, a.K, rows, 0, 128);
+    mas = ma;
+  } else {
+    const int64_t inner = mode == LIN_FWD ? a.K : a.N;
+    ok = l8_map(&ma, a_codes, inner, a.rows, 0, 128) && l8_map(&mas, a_codes, inner, a.rows, 0, L8_SMALL) &&
+         l8_map(&mb, b_codes, a.K, a.N, a.E, 128);
+  }
+  if (!ok) {
+    snprintf(msg, msg_len, "cuTensorMapEncodeTiled failed (rows %lld, K %d, N %d, E %d)", (long long)a.rows, a.K, a.N,
+             a.E);
+    return cudaErrorInvalidValue;
+  }
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  a.out_v8 = aligned32(a.out) && a.ldo % 16 == 0;
+  const int64_t pairs = sms / 2 < 1 ? 1 : sms / 2;
+  const int64_t nt = ((mode == LIN_FWD ? a.N : a.K) + L8_N - 1) / L8_N;
+  const int64_t mt = mode == LIN_WGRAD ? int64_t(a.E) * ((a.N + L8_M - 1) / L8_M)
+                                       : (a.rows < a.E ? a.rows : a.E) + a.rows / L8_M;
+  const int64_t tiles = nt * mt;                 // no fewer than there are
+  const int grid = 2 * int(tiles < pairs ? tiles : pairs);
+  switch (mode) {
+    case LIN_FWD: return l8_launch<LIN_FWD>(ma, mas, mb, a, grid, st);
+    case LIN_DGRAD: return l8_launch<LIN_DGRAD>(ma, mas, mb, a, grid, st);
+    default: return l8_launch<LIN_WGRAD>(ma, mas, mb, a, grid, st);
+  }
+}
+
+}  // namespace moe

@@ -104,8 +104,8 @@ cudaError_t launch_router_dw_tc(const void* x, const void* dl_hi, const void* dl
 cudaError_t launch_router_fwd(const void* x, const void* w, int T, int H, int E, float* logits, int* err,
                               cudaStream_t st, char* msg, size_t msg_len);
 cudaError_t launch_router_bwd(const void* x, const void* w, const float* logits, const int* idx, const float* prob,
-                              const float* dprob, int T, int H, int E, int k, int renorm, float* dl, void* dx,
-                              float* dw, void* ws, int* err, cudaStream_t st);
+                              const float* dprob, const float* aux, int T, int H, int E, int k, int renorm,
+                              float* dl, void* dx, float* dw, void* ws, int* err, cudaStream_t st);
 // Top-k routing plus the per-expert scan of the token masks (masks [E][G], bases [E][G],
 // split_sizes [E]).  One launch while E*ceil(T/32) <= 16384 (the last block to finish
 // scans; `ticket` is a zero-initialised counter the launch returns to zero), else two.
@@ -237,6 +237,97 @@ constexpr int kLinearMaxPairs = 76;               // CTA pairs (two SMs each) th
 size_t linear_ws_bytes();
 cudaError_t launch_grouped_linear(int mode, const LinearArgs& a, const void* x, int64_t ldx, const void* dy,
                                   int64_t lddy, const void* w, cudaStream_t st, char* msg, size_t msg_len);
+
+// ---- root-mean-square norm (rmsnorm.cu) ----------------------------------------------------
+struct RmsArgs {
+  int64_t rows;
+  int H;
+  float eps;
+  bool w_f32;                // gamma and dgamma: f32 (else bf16)
+  int64_t ld_in, ld_out;     // row pitch of x, residual, dy, dres and of h, y, dx
+  const void* x;             // forward input; backward: what was normalised
+  const void* residual;      // optional, added to x
+  const void* gamma;
+  void* h;                   // out, optional: x + residual
+  void* y;                   // out, optional where codes is set
+  float* rstd;               // out, optional
+  uint8_t* codes;            // out, optional: y in 8 bits [rows][H]
+  float* scales;             // [ceil(H/128)][rows]
+  const void* dy;
+  const void* dres;          // optional, added to dx
+  void* dx;
+  void* dgamma;
+};
+size_t rms_ws_bytes(int64_t rows, int H);
+cudaError_t launch_rms_fwd(const RmsArgs& a, bool x_f32, cudaStream_t st);
+cudaError_t launch_rms_bwd(const RmsArgs& a, bool x_f32, float* partial, cudaStream_t st);
+
+// ---- the router's balance loss (balance.cu) -------------------------------------------------
+struct BalanceArgs {
+  int T, E, k;
+  float alpha, beta;
+  const float* logits;       // [T][E]
+  const int* idx;            // [T][k]
+  const uint8_t* mask;       // [T], optional: 0 leaves the token out
+  int* counts;               // [E + 1]: out (forward), in (backward)
+  float* prob;               // [E]
+  float* loss;               // [3]
+  uint32_t* partial;         // of the workspace: rows of 2 (E + 1) words
+  unsigned* ticket;
+  int* err;
+  const float* grad;         // [1], optional
+  float* dlogits;            // [T][E]
+};
+constexpr int kBalanceMaxParts = 304;
+size_t balance_ws_bytes(int E);
+cudaError_t launch_balance(const BalanceArgs& a, bool backward, cudaStream_t st);
+
+// ---- 8 bits with one f32 scale per block of 128 (fp8_block.cu) ----------------------------------
+struct Block8Args {
+  const void* src;           // [rows][cols] at pitch ld
+  int64_t rows, ld;
+  int cols;
+  uint8_t* codes;            // rows format: codes [rows][cols], scales [ceil(cols/128)][rows]; optional
+  float* scales;
+  const int* split_sizes;    // device, of E experts; null: one sequence of rows, or matrices
+  int E;
+  int mat_rows;              // E matrices of so many rows (0: none)
+  uint8_t* tcodes;           // tokens or tiles format; optional
+  float* tscales;
+  bool tiles;
+};
+struct Block8Back {
+  const uint8_t* codes;      // [rows][cols]
+  const float* scales;
+  int64_t rows, ld;
+  int cols;
+  int format;                // moe_fp8_format
+  int mat_rows;              // rows of each matrix (0: one)
+  void* dst;
+};
+cudaError_t launch_block8_quantize(const Block8Args& a, bool f32, cudaStream_t st);
+cudaError_t launch_block8_dequantize(const Block8Back& a, bool f32, cudaStream_t st);
+cudaError_t launch_block8_pack(const uint8_t* codes, const float* scales, const int* pos_of, int T, int k, int cols,
+                               int64_t rows, uint8_t* codes_out, float* scales_out, int* err, cudaStream_t st);
+
+// ---- the same on 8-bit operands with a scale per block of 128 (grouped_linear_fp8.cu) --------
+struct Linear8Args {
+  int64_t rows;              // rows of x and dy (the sum of split_sizes, or more)
+  int E, K, N;               // w [E][N][K]
+  const int* split_sizes;    // device
+  const float* sa;           // scales of the A side: FWD x's, DGRAD dy's [blocks of the contraction][rows],
+                             // WGRAD dy's [blocks of the rows][N]
+  const float* sb;           // of the B side: w's [E][ceil(N/128)][ceil(K/128)], WGRAD x's [blocks][ceil(K/128)]
+  __nv_bfloat16* out;        // FWD y [rows][N], DGRAD dx [rows][K], WGRAD dw [E][N][K]
+  int64_t ldo;
+  int* err;
+  uint64_t wait_limit_ns;    // of every bounded wait
+  int selftest_no_loads;     // the producers issue nothing
+  int out_v8;                // set by the launch: 32-byte stores
+};
+size_t linear8_ws_bytes();
+cudaError_t launch_grouped_linear_fp8(int mode, const Linear8Args& a, const uint8_t* a_codes, const uint8_t* b_codes,
+                                      cudaStream_t st, char* msg, size_t msg_len);
 
 // ---- grouped block-scaled MXFP8 GEMM (tcgen05) ------------------------------------
 // C[M][N] = A[M][K] * B[N][K]^T, both operands K-major MX tensors.

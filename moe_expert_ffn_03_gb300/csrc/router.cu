@@ -22,12 +22,14 @@ namespace moe {
 
 // One warp per token.  renormalize: dl[e_j] = p_j (dp_j - sum_i p_i dp_i), 0 elsewhere;
 // plain softmax: dl[e] = s_e (g_e - sum_j p_j dp_j) with g the dprob scattered to idx.
+// aux (optional, [T][E]): a gradient that reaches the logits past the probabilities, added.
 // Also dl as two bf16 terms for the tensor cores, [T][N] with zeros in columns E..N-1:
 // hi = bf16(dl), lo = bf16(dl - hi) (dl - hi is exact in f32).
 __global__ void __launch_bounds__(256) router_dlogits_kernel(const float* __restrict__ logits,
                                                              const int* __restrict__ idx,
                                                              const float* __restrict__ prob,
-                                                             const float* __restrict__ dprob, int T, int E, int k,
+                                                             const float* __restrict__ dprob,
+                                                             const float* __restrict__ aux, int T, int E, int k,
                                                              int renorm, float* __restrict__ dl,
                                                              __nv_bfloat16* __restrict__ dl_hi,
                                                              __nv_bfloat16* __restrict__ dl_lo, int N, int* err) {
@@ -65,6 +67,7 @@ __global__ void __launch_bounds__(256) router_dlogits_kernel(const float* __rest
       }
       if (renorm) v = sel ? pe * (g - pdp) : 0.f;
       else v = expf(lrow[e] - m) / z * (g - pdp);
+      if (aux != nullptr) v += aux[t * E + e];
       dl[t * E + e] = v;
     }
     const __nv_bfloat16 hi = __float2bfloat16_rn(v);
@@ -133,8 +136,8 @@ cudaError_t launch_router_fwd(const void* x, const void* w, int T, int H, int E,
 }
 
 cudaError_t launch_router_bwd(const void* x, const void* w, const float* logits, const int* idx, const float* prob,
-                              const float* dprob, int T, int H, int E, int k, int renorm, float* dl, void* dx,
-                              float* dw, void* ws, int* err, cudaStream_t st) {
+                              const float* dprob, const float* aux, int T, int H, int E, int k, int renorm,
+                              float* dl, void* dx, float* dw, void* ws, int* err, cudaStream_t st) {
   const int N = router_dw_cols(E);
   const int max_chunks = router_dw_max_chunks(H);
   uint8_t* base = static_cast<uint8_t*>(ws);
@@ -143,11 +146,14 @@ cudaError_t launch_router_bwd(const void* x, const void* w, const float* logits,
   __nv_bfloat16* dl_hi = reinterpret_cast<__nv_bfloat16*>(base + off_hi);
   __nv_bfloat16* dl_lo = reinterpret_cast<__nv_bfloat16*>(base + off_hi + al256(size_t(T) * N * 2));
   const unsigned warps_grid = unsigned((int64_t(T) * 32 + 255) / 256);
-  router_dlogits_kernel<<<warps_grid, 256, 0, st>>>(logits, idx, prob, dprob, T, E, k, renorm, dl, dl_hi, dl_lo, N,
+  router_dlogits_kernel<<<warps_grid, 256, 0, st>>>(logits, idx, prob, dprob, aux, T, E, k, renorm, dl, dl_hi,
+                                                   dl_lo, N,
                                                    err);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  router_dx_kernel<<<warps_grid, 256, 0, st>>>(dl, idx, static_cast<const __nv_bfloat16*>(w), T, H, E, k, renorm,
+  // with aux every expert's dl counts, not the selected ones' alone
+  router_dx_kernel<<<warps_grid, 256, 0, st>>>(dl, idx, static_cast<const __nv_bfloat16*>(w), T, H, E, k,
+                                              renorm && aux == nullptr,
                                               static_cast<__nv_bfloat16*>(dx));
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;

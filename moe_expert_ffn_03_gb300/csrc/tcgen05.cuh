@@ -224,6 +224,29 @@ __device__ __forceinline__ bool wait_phase_warp(uint64_t* bar, uint32_t parity, 
                                                 int site, uint64_t limit_ns) {
   return __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, abort_flag, err, site, limit_ns));
 }
+// wait_phase and wait_phase_warp in line: a function that is called has registers of its own, which the
+// split of a block's registers among its warps has no room for.
+__device__ __forceinline__ bool wait_phase_inline(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
+                                                  int site, uint64_t limit_ns) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+    if ((n & 255u) != 0) continue;
+    if (*abort_flag) return false;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > limit_ns) {
+      report_error(err, MOE_ERR_DEVICE_TIMEOUT, site);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait_phase_warp_inline(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
+                                                       int site, uint64_t limit_ns) {
+  return __all_sync(0xFFFFFFFFu, wait_phase_inline(bar, parity, abort_flag, err, site, limit_ns));
+}
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
