@@ -29,6 +29,7 @@
 // Waits are bounded as everywhere; each lasts as long as a block or a tile's output at most.
 #include <atomic>
 #include <cstdio>
+#include <type_traits>
 
 #include "kernels.cuh"
 #include "tcgen05.cuh"
@@ -40,7 +41,7 @@ constexpr int L8_M = 256, L8_N = 256;            // the pair's tile
 constexpr int L8_KT = 128;                       // a block of the contraction: one stage
 constexpr int L8_SIDE = 128 * L8_KT;             // bytes of a CTA's A or B in a stage
 constexpr int L8_STAGE = 2 * L8_SIDE;
-constexpr int L8_STAGES = 6;
+constexpr int L8_STAGES = 6;                     // an even number: a block's buffer is its stage's parity
 constexpr int L8_EPI_WARPS = 8;
 constexpr int L8_THREADS = 32 * (4 + L8_EPI_WARPS);
 constexpr int L8_REGS = 168, L8_REGS_FEW = 56, L8_REGS_MANY = 224;
@@ -50,10 +51,14 @@ constexpr int L8_GROUP = 8;                      // row tiles that share the swe
 constexpr int L8_SMALL = 32;                     // rows of the small box of rows
 
 constexpr int L8_OFF_BAR = L8_STAGES * L8_STAGE;
-constexpr int L8_BARS = 2 * L8_STAGES + 5;       // full, empty, tmem_full[2], tmem_empty[2], drain
+constexpr int L8_BARS = 2 * L8_STAGES + 1;       // full, empty, drain
 constexpr int L8_OFF_MISC = L8_OFF_BAR + L8_BARS * 8;
 constexpr int L8_OFF_SEG = (L8_OFF_MISC + 16 + 15) & ~15;        // row0[E+1], tile0[E+1], order[E]
-constexpr int L8_SMEM = L8_OFF_SEG + 3 * (L8_MAX_E + 1) * 4 + 1024;
+// the scales' rings: [L8_AHEAD][warps][32] of {A side, B side}
+constexpr int L8_AHEAD = 8;                      // blocks whose scales are on their way
+constexpr int L8_SCALE_SLOT = L8_EPI_WARPS * 32 * 2;
+constexpr int L8_OFF_SCALE = (L8_OFF_SEG + 3 * (L8_MAX_E + 1) * 4 + 15) & ~15;
+constexpr int L8_SMEM = L8_OFF_SCALE + L8_AHEAD * L8_SCALE_SLOT * 4 + 1024;
 static_assert(L8_SMEM <= 232448, "shared memory budget");
 
 // kind::f8f6f4 instruction descriptor: E4M3 x E4M3 -> f32, M = 256, N columns; a_mn, b_mn: the operand
@@ -62,14 +67,23 @@ __device__ __forceinline__ uint32_t l8_idesc(bool a_mn, bool b_mn, int N) {
   return (1u << 4) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) | (uint32_t(N >> 3) << 17) |
          (uint32_t(L8_M >> 4) << 24);
 }
-__device__ __forceinline__ void l8_mma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// One tcgen05.mma (E4M3, f32 accumulation).  All descriptors of a kernel differ in the low half only, by a
+// constant from the ring's first, and are made here: as values of their own, all stages' would be kept in
+// registers at once, and there are none for them.
+template <uint32_t A_OFF, uint32_t B_OFF, bool ACCUMULATE>
+__device__ __forceinline__ void l8_mma(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b32 la, lb;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %8, 0;\n\t"
+      "add.u32 la, %1, %6;\n\t"
+      "add.u32 lb, %3, %7;\n\t"
+      "mov.b64 da, {la, %2};\n\t"
+      "mov.b64 db, {lb, %4};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], da, db, %5, p;\n\t}"
+      ::"r"(d), "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "n"(A_OFF), "n"(B_OFF), "n"(int(ACCUMULATE))
       : "memory");
 }
+
 struct Ring {
   int st = 0;
   uint32_t ph = 0;
@@ -151,6 +165,15 @@ __device__ __forceinline__ int l8_after(int t, int num_pairs) {
   return t + (MODE == LIN_WGRAD ? 2 * (num_pairs - 1 - t % num_pairs) + 1 : num_pairs);
 }
 
+// A copy of four bytes on its way to shared memory, and the wait until all but the last N groups of them are
+// there.
+__device__ __forceinline__ void cp_async4(void* smem, const void* gmem) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void cp_async_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_left() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // acc += part * f, two at a time
 __device__ __forceinline__ void l8_add(float* acc, const uint32_t* part, float2 f) {
 #pragma unroll
@@ -162,6 +185,17 @@ __device__ __forceinline__ void l8_add(float* acc, const uint32_t* part, float2 
   }
 }
 
+// A warp's arrival on the leader's barrier of a buffer that it has read (mbar_arrive_cluster_relaxed by lane 0,
+// without a branch).
+__device__ __forceinline__ void l8_hand_back(uint32_t caddr, int lane) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.eq.s32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}"
+      ::"r"(caddr), "r"(lane)
+      : "memory");
+}
+
 template <int MODE>
 __global__ void __launch_bounds__(L8_THREADS, 1)
     grouped_linear_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmAs,
@@ -171,9 +205,7 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L8_OFF_BAR);
   uint64_t* empty = full + L8_STAGES;
-  uint64_t* tmem_full = empty + L8_STAGES;
-  uint64_t* tmem_empty = tmem_full + 2;
-  uint64_t* drain = tmem_empty + 2;
+  uint64_t* drain = empty + L8_STAGES;
   uint32_t* tmem_base_s = reinterpret_cast<uint32_t*>(smem + L8_OFF_MISC);
   volatile int* abort_s = reinterpret_cast<volatile int*>(smem + L8_OFF_MISC + 4);
   volatile int* bad_s = reinterpret_cast<volatile int*>(smem + L8_OFF_MISC + 8);
@@ -187,12 +219,8 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < L8_STAGES; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 1 + 2 * L8_EPI_WARPS); // the operands, and the buffer from both CTAs' warps
       mbar_init(&empty[s], 1);
-    }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&tmem_full[b], 1);
-      mbar_init(&tmem_empty[b], 2 * L8_EPI_WARPS);
     }
     mbar_init(drain, 1);
     *abort_s = 0;
@@ -323,35 +351,55 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
     } else if (warp == 1) {
       if (lane == 0 && rank == 0) {
         // ---------------- MMA issuer (leader) ----------------
+        // An MMA takes its pipe 128 clocks.  Issuing one took this thread 84 with operands computed on the way, and
+        // 50 with constant ones, so the loop is unrolled over the ring's stages (the buffer is the stage's
+        // parity).  A block has one wait (its operands and its buffer share a barrier) and one commit
+        // (the stage is free when the sums are there).
         const uint64_t a_desc = A_MN ? desc_sw128_mn(smem_u32(smem), L8_SIDE) : desc_sw128(smem_u32(smem));
         const uint64_t b_desc = B_MN ? desc_sw128_mn(smem_u32(smem + L8_SIDE), L8_SIDE) : desc_sw128(smem_u32(smem + L8_SIDE));
+        const uint32_t alo = uint32_t(a_desc), ahi = uint32_t(a_desc >> 32), blo = uint32_t(b_desc), bhi = uint32_t(b_desc >> 32);
         // 32 of the contraction, in the descriptors' 16-byte units: 32 bytes of a K-major row, four
         // 8-row groups (4 KB) of an MN-major block
         constexpr uint32_t A_K = A_MN ? 256 : 2, B_K = B_MN ? 256 : 2;
-        Ring cur;
-        uint32_t used = 0;                       // buffers used so far
         bool ok = true, issued = false;
+        uint32_t ph = 0;
+        int at = 0;                              // the next block's stage
         Tile8 tl;
         for (int t = pair; ok && t < total; t = l8_after<MODE>(t, num_pairs)) {
           l8_decode<MODE>(args, row0, tile0, order, t, tl);
           const uint32_t idesc = l8_idesc(A_MN, B_MN, tl.n);
-          for (int kt = 0; kt < tl.blocks; ++kt, cur.next(), ++used) {
-            const uint32_t b = used & 1u;
-            if (!wait_phase_inline(&tmem_empty[b], ((used >> 1) & 1u) ^ 1u, abort_s, args.err, SITE_LINEAR8 + 1, lim) ||
-                !wait_phase_inline(&full[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR8 + 2, lim)) {
+          int left = tl.blocks;
+          // the block in stage ST; false: the tile ends, or a wait gave up
+          const auto block = [&](auto stage) {
+            constexpr uint32_t ST = decltype(stage)::value, OFF = ST * (L8_STAGE >> 4);
+            if (left == 0) return false;
+            if (!wait_phase_inline(&full[ST], ph, abort_s, args.err, SITE_LINEAR8 + 1, lim)) {
               ok = false;
-              break;
+              return false;
             }
             tc_fence_after();
-            const uint64_t off = uint64_t(cur.st * (L8_STAGE >> 4));
-            const uint32_t acc = tmem + b * L8_N;
-            const int groups = kt + 1 == tl.blocks ? (tl.last + 31) >> 5 : L8_KT / 32;
-#pragma unroll
-            for (int kk = 0; kk < L8_KT / 32; ++kk)
-              if (kk < groups) l8_mma(acc, a_desc + off + A_K * kk, b_desc + off + B_K * kk, idesc, kk != 0);
+            const uint32_t acc = tmem + (ST & 1) * L8_N;
+            const int groups = left > 1 ? 4 : (tl.last + 31) >> 5;           // of 32: all but the last are full blocks
+            l8_mma<OFF, OFF, false>(acc, alo, ahi, blo, bhi, idesc);
+            if (groups > 1) l8_mma<OFF + A_K, OFF + B_K, true>(acc, alo, ahi, blo, bhi, idesc);
+            if (groups > 2) l8_mma<OFF + 2 * A_K, OFF + 2 * B_K, true>(acc, alo, ahi, blo, bhi, idesc);
+            if (groups > 3) l8_mma<OFF + 3 * A_K, OFF + 3 * B_K, true>(acc, alo, ahi, blo, bhi, idesc);
             issued = true;
-            tc_commit(&empty[cur.st]);           // frees the stage in both CTAs
-            tc_commit(&tmem_full[b]);
+            tc_commit(&empty[ST]);
+            --left;
+            at = ST + 1 < L8_STAGES ? int(ST) + 1 : 0;
+            ph ^= uint32_t(at == 0);
+            return true;
+          };
+          while (ok && left > 0) {
+            switch (at) {
+              case 0: if (!block(std::integral_constant<uint32_t, 0>{})) break; [[fallthrough]];
+              case 1: if (!block(std::integral_constant<uint32_t, 1>{})) break; [[fallthrough]];
+              case 2: if (!block(std::integral_constant<uint32_t, 2>{})) break; [[fallthrough]];
+              case 3: if (!block(std::integral_constant<uint32_t, 3>{})) break; [[fallthrough]];
+              case 4: if (!block(std::integral_constant<uint32_t, 4>{})) break; [[fallthrough]];
+              default: block(std::integral_constant<uint32_t, 5>{});
+            }
           }
         }
         if (!ok && issued) {
@@ -368,74 +416,112 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
     const int q = warp & 3;                      // lane quarter this warp may access
     const int col0 = ((warp - 4) >> 2) * 128;    // its columns of a buffer: one block of the B side
     const uint32_t tmem_row = tmem + (uint32_t(q * 32) << 16) + uint32_t(col0);
-    const uint32_t tmem_empty_c0 = mapa_shared(smem_u32(tmem_empty), 0);
+    // a block's buffer is handed back on the barrier of the block after the next, which takes it again
+    const uint32_t full_c0 = mapa_shared(smem_u32(full), 0);
+    const auto back = [&](int st) { l8_hand_back(full_c0 + uint32_t(st + 2 < L8_STAGES ? st + 2 : st + 2 - L8_STAGES) * 8u, lane); };
+    l8_hand_back(full_c0, lane);                 // both buffers are free at first
+    l8_hand_back(full_c0 + 8u, lane);
     const int cols = l8_cols<MODE>(args);
-    uint32_t used = 0;
-    bool ok = true;
+    const int kbs = (args.K + 127) / 128, nbs = (args.N + 127) / 128;
+    const int64_t sa_step = MODE == LIN_WGRAD ? args.N : args.rows, sb_step = MODE == LIN_FWD ? 1 : kbs;
+    // A lane's own ring of its scales (its m's, its warp's columns'), L8_AHEAD blocks on their way: what a
+    // lane copies it alone reads, so a wait for its own copies is enough.
+    float* const mine = reinterpret_cast<float*>(smem + L8_OFF_SCALE) + ((warp - 4) * 32 + lane) * 2;
+    int slot = 0;
+    const float *sa = nullptr, *sb = nullptr;    // the next block's
+    int coming = 0;                              // blocks of the tile not yet asked for
+    const auto ask = [&]() {
+      if (coming > 0) {
+        cp_async4(mine + slot * L8_SCALE_SLOT, sa);
+        cp_async4(mine + slot * L8_SCALE_SLOT + 1, sb);
+        sa += sa_step;
+        sb += sb_step;
+        --coming;
+      }
+      cp_async_group();
+      slot = slot + 1 == L8_AHEAD ? 0 : slot + 1;
+    };
+    Ring cur;                                    // a block's sums are there when its stage is free
+    bool ok = true, live = false;
     Tile8 tl;
-    for (int t = pair; ok && t < total; t = l8_after<MODE>(t, num_pairs)) {
+    const int at = int(rank) * 128 + q * 32;     // this warp's first of a tile's m
+    // takes tile t up, and asks for its first blocks' scales
+    const auto take = [&](int t) {
+      if (t >= total) return;
       l8_decode<MODE>(args, row0, tile0, order, t, tl);
-      const int at = int(rank) * 128 + q * 32;   // of the tile's m, this warp's first
-      const bool live = at < tl.cnt && col0 < tl.n;
-      const int r = min(at + lane, tl.cnt - 1);
-      // the scales of the lane's m and of the warp's columns, block after block
-      const float* sa = args.sa + (MODE == LIN_WGRAD ? int64_t(tl.c0 / L8_KT) * args.N : 0) + tl.m0 + r;
-      const float* sb = args.sb;
-      const int64_t sa_step = MODE == LIN_WGRAD ? args.N : args.rows;
-      int64_t sb_step;
-      const int nb = (tl.n0 + col0) / 128, kbs = (args.K + 127) / 128, nbs = (args.N + 127) / 128;
-      if (MODE == LIN_FWD) {
-        sb += (int64_t(tl.e) * nbs + nb) * kbs;
-        sb_step = 1;
-      } else {
-        sb += (MODE == LIN_DGRAD ? int64_t(tl.e) * nbs : int64_t(tl.c0 / L8_KT)) * kbs + nb;
-        sb_step = kbs;
+      live = at < tl.cnt && col0 < tl.n;
+      const int64_t blk = tl.c0 / L8_KT, e = tl.e;
+      sa = args.sa + (MODE == LIN_WGRAD ? blk * args.N : 0) + tl.m0 + min(at + lane, tl.cnt - 1);
+      const int nb = (tl.n0 + col0) / 128;
+      sb = args.sb + (MODE == LIN_FWD ? (e * nbs + nb) * kbs : (MODE == LIN_DGRAD ? e * nbs : blk) * kbs + nb);
+      coming = live ? tl.blocks : 0;
+#pragma unroll 1
+      for (int i = 0; i < L8_AHEAD; ++i) ask();
+    };
+    int t = pair;
+    take(t);
+    while (ok && t < total) {
+      if (!live) {
+        // nobody's m or n: the buffers are handed back as they come
+        for (int kt = 0; ok && kt < tl.blocks; ++kt, cur.next()) {
+          ok = wait_phase_warp_inline(&empty[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR8 + 5, lim);
+          if (ok) back(cur.st);
+        }
+        t = l8_after<MODE>(t, num_pairs);
+        take(t);
+        continue;
       }
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-      // this block's factors, the next one's on their way
-      const bool any = live && tl.blocks > 0;
-      float fa = any ? __ldg(sa) : 0.f, fb = any ? __ldg(sb) : 0.f;
-      for (int kt = 0; kt < tl.blocks; ++kt, ++used) {
-        const float f = fa * fb;
-        if (live && kt + 1 < tl.blocks) {
-          fa = __ldg(sa + (kt + 1) * sa_step);
-          fb = __ldg(sb + (kt + 1) * sb_step);
-        }
-        const uint32_t b = used & 1u;
-        ok = wait_phase_warp_inline(&tmem_full[b], (used >> 1) & 1u, abort_s, args.err, SITE_LINEAR8 + 4, lim);
+      // Columns come 32 at a time, the next 32 on their way while these are added; the last ones of a block are
+      // added after the next block's first have been asked for, so that neither a wait nor a load's latency
+      // stands between two blocks.
+      uint32_t p0[32], p1[32];
+      if (tl.blocks > 0) {
+        ok = wait_phase_warp_inline(&empty[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR8 + 4, lim);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t src = tmem_row + b * L8_N;
-        const float2 f2 = make_float2(f, f);
-        if (live) {
-          uint32_t p0[32], p1[32];
-          tmem_ld32_async(src, p0);
-          tmem_wait_ld<32>(p0);
-          tmem_ld32_async(src + 32, p1);
-          l8_add(acc, p0, f2);
-          tmem_wait_ld<32>(p1);
-          tmem_ld32_async(src + 64, p0);
-          l8_add(acc + 32, p1, f2);
-          tmem_wait_ld<32>(p0);
-          tmem_ld32_async(src + 96, p1);
-          l8_add(acc + 64, p0, f2);
-          tmem_wait_ld<32>(p1);
-          tc_fence_before();
-          if (lane == 0) mbar_arrive_cluster_relaxed(tmem_empty_c0 + b * 8u);
-          l8_add(acc + 96, p1, f2);
-        } else if (lane == 0) {
-          mbar_arrive_cluster_relaxed(tmem_empty_c0 + b * 8u);
-        }
+        tmem_ld32_async(tmem_row + (cur.st & 1) * L8_N, p0);
       }
-      if (!ok || !live || at + lane >= tl.cnt) continue;
+      for (int left = tl.blocks; left > 0; --left) {
+        const uint32_t src = tmem_row + (cur.st & 1) * L8_N;
+        cp_async_left<L8_AHEAD - 1>();
+        const float2 s2 = *reinterpret_cast<const float2*>(mine + slot * L8_SCALE_SLOT);
+        const float2 f2 = make_float2(s2.x * s2.y, s2.x * s2.y);
+        ask();                                   // into the same place: what was there has been read
+        tmem_wait_ld<32>(p0);
+        tmem_ld32_async(src + 32, p1);
+        l8_add(acc, p0, f2);
+        tmem_wait_ld<32>(p1);
+        tmem_ld32_async(src + 64, p0);
+        l8_add(acc + 32, p1, f2);
+        tmem_wait_ld<32>(p0);
+        tmem_ld32_async(src + 96, p1);
+        l8_add(acc + 64, p0, f2);
+        tmem_wait_ld<32>(p1);
+        tc_fence_before();
+        back(cur.st);
+        cur.next();
+        if (left > 1) {
+          ok = wait_phase_warp_inline(&empty[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR8 + 4, lim);
+          if (!ok) break;
+          tc_fence_after();
+          tmem_ld32_async(tmem_row + (cur.st & 1) * L8_N, p0);
+        }
+        l8_add(acc + 96, p1, f2);
+      }
+      if (!ok) break;
       // a lane's row: 32 bytes (16 columns) at a time; columns come in multiples of 16
+      const bool in = at + lane < tl.cnt;
+      const int columns = min(128, cols - tl.n0 - col0);
       __nv_bfloat16* o = args.out + ((MODE == LIN_WGRAD ? int64_t(tl.e) * args.N : 0) + tl.m0 + at + lane) * args.ldo +
                          tl.n0 + col0;
+      t = l8_after<MODE>(t, num_pairs);
+      take(t);                                   // its first scales are on their way while this tile goes out
 #pragma unroll
       for (int c = 0; c < 128; c += 16) {
-        if (tl.n0 + col0 + c >= cols) break;
+        if (!in || c >= columns) break;
         uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(acc[c + 2 * i], acc[c + 2 * i + 1]);
@@ -447,6 +533,7 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
         }
       }
     }
+    cp_async_left<0>();
   }
   tc_fence_before();
   __syncthreads();
