@@ -31,14 +31,12 @@
 #include <cstdio>
 #include <type_traits>
 
-#include "kernels.cuh"
-#include "tcgen05.cuh"
+#include "linear8.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int L8_M = 256, L8_N = 256;            // the pair's tile
-constexpr int L8_KT = 128;                       // a block of the contraction: one stage
 constexpr int L8_SIDE = 128 * L8_KT;             // bytes of a CTA's A or B in a stage
 constexpr int L8_STAGE = 2 * L8_SIDE;
 constexpr int L8_STAGES = 6;                     // an even number: a block's buffer is its stage's parity
@@ -46,7 +44,6 @@ constexpr int L8_EPI_WARPS = 8;
 constexpr int L8_THREADS = 32 * (4 + L8_EPI_WARPS);
 constexpr int L8_REGS = 168, L8_REGS_FEW = 56, L8_REGS_MANY = 224;
 static_assert(128 * L8_REGS_FEW + 32 * L8_EPI_WARPS * L8_REGS_MANY == L8_THREADS * L8_REGS, "register split");
-constexpr int L8_MAX_E = 256;
 constexpr int L8_GROUP = 8;                      // row tiles that share the sweep over the weights
 constexpr int L8_SMALL = 32;                     // rows of the small box of rows
 
@@ -165,15 +162,6 @@ __device__ __forceinline__ int l8_after(int t, int num_pairs) {
   return t + (MODE == LIN_WGRAD ? 2 * (num_pairs - 1 - t % num_pairs) + 1 : num_pairs);
 }
 
-// A copy of four bytes on its way to shared memory, and the wait until all but the last N groups of them are
-// there.
-__device__ __forceinline__ void cp_async4(void* smem, const void* gmem) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
-}
-__device__ __forceinline__ void cp_async_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_left() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 // acc += part * f, two at a time
 __device__ __forceinline__ void l8_add(float* acc, const uint32_t* part, float2 f) {
 #pragma unroll
@@ -237,58 +225,8 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
   // Up to here the kernel touches only its own shared memory, tensor memory and parameters.
   pdl_wait();
   if (warp == 3) {
-    // prefix sums of the experts' rows and of their row tiles (wgrad: blocks of 128), eight experts per lane
-    constexpr int PER = MODE == LIN_WGRAD ? L8_KT : L8_M;
-    int rows[8], sum = 0, tiles = 0;
-    int64_t all = 0;
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = lane * 8 + i;
-      const int s = e < args.E ? args.split_sizes[e] : 0;
-      const bool wrong = s < 0 || s > args.rows;
-      bad |= wrong;
-      rows[i] = wrong ? 0 : s;
-      all += rows[i];
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, off);
-    bad = __any_sync(0xFFFFFFFFu, bad) || all > args.rows;
-    if (lane == 0) {
-      *bad_s = bad;
-      if (bad) report_error(args.err, MOE_ERR_DEVICE_BOUNDS, SITE_LINEAR8 + 9);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (bad) rows[i] = 0;
-      sum += rows[i];
-      tiles += (rows[i] + PER - 1) / PER;
-    }
-    int rs = sum, ts = tiles;                    // inclusive scans over the lanes
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int r = __shfl_up_sync(0xFFFFFFFFu, rs, off), q = __shfl_up_sync(0xFFFFFFFFu, ts, off);
-      if (lane >= off) {
-        rs += r;
-        ts += q;
-      }
-    }
-    rs -= sum;
-    ts -= tiles;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = lane * 8 + i;
-      if (e <= args.E) {
-        row0[e] = rs;
-        tile0[e] = ts;
-      }
-      rs += rows[i];
-      ts += (rows[i] + PER - 1) / PER;
-    }
-    if (lane == 31 && args.E == L8_MAX_E) {
-      row0[L8_MAX_E] = rs;
-      tile0[L8_MAX_E] = ts;
-    }
+    const bool bad = l8_prefix<MODE == LIN_WGRAD ? L8_KT : L8_M>(args, lane, row0, tile0);
+    if (lane == 0) *bad_s = bad;
     __syncwarp();
     if (MODE == LIN_WGRAD) {
       for (int e = lane; e < args.E; e += 32) {
@@ -549,19 +487,6 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// 8-bit map over row-major [batch][rows][inner] (batch 0: no such dimension), boxes of 128 bytes x box_rows
-// with 128-byte swizzle.
-bool l8_map(CUtensorMap* m, const void* base, int64_t inner, int64_t rows, int64_t batch, int box_rows) {
-  EncodeTiledFn fn = get_encode_fn();
-  if (fn == nullptr) return false;
-  cuuint64_t dims[3] = {cuuint64_t(inner), cuuint64_t(rows), cuuint64_t(batch)};
-  cuuint64_t strides[2] = {cuuint64_t(inner), cuuint64_t(inner) * cuuint64_t(rows)};
-  cuuint32_t box[3] = {128, cuuint32_t(box_rows), 1}, estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, batch > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int MODE>
 cudaError_t l8_launch(const CUtensorMap& ma, const CUtensorMap& mas, const CUtensorMap& mb, const Linear8Args& a, int grid,
                       cudaStream_t st) {
@@ -600,11 +525,23 @@ cudaError_t l8_launch(const CUtensorMap& ma, const CUtensorMap& mas, const CUten
 
 }  // namespace
 
-size_t linear8_ws_bytes() { return 256; }
-
 cudaError_t launch_grouped_linear_fp8(int mode, const Linear8Args& args, const uint8_t* a_codes, const uint8_t* b_codes,
                                       cudaStream_t st, char* msg, size_t msg_len) {
   Linear8Args a = args;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int64_t pairs = sms / 2 < 1 ? 1 : sms / 2;
+  const int64_t nt = ((mode == LIN_FWD ? a.N : a.K) + L8_N - 1) / L8_N;
+  const int64_t mt = mode == LIN_WGRAD ? int64_t(a.E) * ((a.N + L8_M - 1) / L8_M)
+                                       : (a.rows < a.E ? a.rows : a.E) + a.rows / L8_M;
+  const int64_t tiles = nt * mt;                 // no fewer than there are
+  // Few rows, and so few tiles that half the pairs would have none: the kernel for few rows.  (16 rows,
+  // 4096 -> 28672, six of eight experts: 128 us there, 155 here; one row, 14336 -> 4096: 26 and 55; but 64 rows,
+  // 4096 -> 28672: 61 and 46.)
+  if (mode != LIN_WGRAD && (a.rows <= int64_t(16) * a.E || (a.rows <= int64_t(64) * a.E && 2 * tiles <= pairs)))
+    return launch_grouped_linear_fp8_few(mode, a, a_codes, b_codes, sms, st, msg, msg_len);
   CUtensorMap ma, mas, mb;
   bool ok;
   if (mode == LIN_WGRAD) {
@@ -621,16 +558,7 @@ cudaError_t launch_grouped_linear_fp8(int mode, const Linear8Args& args, const u
              a.E);
     return cudaErrorInvalidValue;
   }
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
   a.out_v8 = aligned32(a.out) && a.ldo % 16 == 0;
-  const int64_t pairs = sms / 2 < 1 ? 1 : sms / 2;
-  const int64_t nt = ((mode == LIN_FWD ? a.N : a.K) + L8_N - 1) / L8_N;
-  const int64_t mt = mode == LIN_WGRAD ? int64_t(a.E) * ((a.N + L8_M - 1) / L8_M)
-                                       : (a.rows < a.E ? a.rows : a.E) + a.rows / L8_M;
-  const int64_t tiles = nt * mt;                 // no fewer than there are
   const int grid = 2 * int(tiles < pairs ? tiles : pairs);
   switch (mode) {
     case LIN_FWD: return l8_launch<LIN_FWD>(ma, mas, mb, a, grid, st);

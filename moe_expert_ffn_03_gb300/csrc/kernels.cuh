@@ -323,9 +323,15 @@ struct Linear8Args {
   int* err;
   uint64_t wait_limit_ns;    // of every bounded wait
   int selftest_no_loads;     // the producers issue nothing
-  int out_v8;                // set by the launch: 32-byte stores
+  int out_v8;                // set by the launch: 32-byte stores and,
+  unsigned* arrived;         // of the workspace, the arrivals and partial sums of cut tiles
+  float* pieces;
 };
+constexpr int F8_MAX_PIECES = 608;                // pieces of tiles that are cut along the contraction
 size_t linear8_ws_bytes();
+// forward and dgrad where the experts have few rows (grouped_linear_fp8_few.cu)
+cudaError_t launch_grouped_linear_fp8_few(int mode, const Linear8Args& a, const uint8_t* rows_codes, const uint8_t* w_codes,
+                                          int sms, cudaStream_t st, char* msg, size_t msg_len);
 cudaError_t launch_grouped_linear_fp8(int mode, const Linear8Args& a, const uint8_t* a_codes, const uint8_t* b_codes,
                                       cudaStream_t st, char* msg, size_t msg_len);
 

@@ -132,6 +132,19 @@ def test_many_tiles_per_pair():
     check_whole([900, 1, 2100], 784, 4624, seed=4)
 
 
+@pytest.mark.parametrize("split,K,N", [([5, 0, 3], 2064, 272), ([1], 8192, 16), ([2, 1], 272, 4112), ([64], 1008, 1008),
+                                       ([1, 0, 0, 1], 528, 528), ([30, 2] * 16, 336, 1040), ([1], 14336, 4096), ([17], 4096, 2048),
+                                       ([48, 33, 16], 640, 400), ([0, 65, 0, 130], 1024, 272)])
+def test_few_rows(split, K, N):
+    """Tiles of 64 rows, cut along the contraction.  The later calls on the same workspace find the arrival counts
+    as the first did."""
+    c = Case(split, K, N, sum(split), K, True)
+    ref = [bf16(v) for v in c.exact()]
+    for _ in range(3):
+        for name, got, want in zip(("y", "dx", "dw"), c.run(), ref):
+            assert np.array_equal(f64(got), want), name
+
+
 def test_rows_past_the_sum_and_pitches():
     check_whole([40, 0, 9], 96, 112, rows=300, seed=4, pad=24)
     check_whole([40, 0, 9], 96, 112, rows=300, seed=5, pad=16)
