@@ -757,8 +757,8 @@ size_t moe_balance_loss_workspace_size(const moe_balance* b);
  *   logits        f32 [T][E]
  *   idx           int32 [T][k], the choices (moe_route's); one outside 0..E-1 is recorded in the error
  *                 word (MOE_ERR_DEVICE_BOUNDS) and not counted
- *   mask          uint8 [T] or NULL: tokens with 0 are padding.  They are not read, count nothing and have
- *                 dlogits of zero
+ *   mask          uint8 [T] or NULL: tokens with 0 are padding.  They count nothing, whatever their logits
+ *                 and choices hold, and have dlogits of zero
  *   counts        int32 [E + 1]: the choices of every expert, then n.  Out (forward), in (backward)
  *   prob          out f32 [E]: P
  *   loss          out f32 [3]: loss, balance, z.  Zeros where no token is left

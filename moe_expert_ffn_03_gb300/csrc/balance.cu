@@ -14,6 +14,7 @@ namespace {
 
 constexpr int BAL_THREADS = 512;
 constexpr int BAL_WARPS = BAL_THREADS / 32;
+constexpr int BAL_UN = 4;                        // tokens a lane group has on their way at once
 
 // Four neighbouring experts' logits from column c on; -Inf past the last.
 template <bool WIDE>
@@ -79,28 +80,39 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_fwd_kernel(const __grid_c
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[v][j] = 0.f;
   int tokens = 0;
-  const int64_t step = int64_t(gridDim.x) * (BAL_THREADS / G);
+  constexpr int PER = 32 / G;                    // tokens a warp works on side by side
+  const int64_t step = int64_t(gridDim.x) * BAL_WARPS * PER * BAL_UN;
   // whole warps go round together: a lane past the last token, or at a masked one, adds nothing
-  for (int64_t t0 = (int64_t(blockIdx.x) * BAL_THREADS + warp * 32) / G; t0 < a.T; t0 += step) {
-    const int64_t t = t0 + lane / G;
-    const bool live = t < a.T && (a.mask == nullptr || a.mask[t] != 0);
-    float x[V][4];
+  for (int64_t t0 = (int64_t(blockIdx.x) * BAL_WARPS + warp) * PER * BAL_UN + lane / G; t0 - lane / G < a.T; t0 += step) {
+    float x[BAL_UN][V][4];
+    bool live[BAL_UN];
+    int choice[BAL_UN];
 #pragma unroll
-    for (int v = 0; v < V; ++v) load4<WIDE>(a.logits + (live ? t : 0) * E, live ? (v * G + sub) * 4 : E, E, x[v]);
-    const float lse = softmax<G, V>(x);
-    if (!live) continue;
+    for (int u = 0; u < BAL_UN; ++u) {
+      const int64_t t = t0 + u * PER;
+      const bool in = t < a.T;
+      live[u] = in && (a.mask == nullptr || a.mask[t] != 0);
+      choice[u] = in && sub < a.k ? a.idx[t * a.k + sub] : 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[v][j] += x[v][j];
-    for (int j = sub; j < a.k; j += G) {
-      const int e = a.idx[t * a.k + j];
-      if (e < 0 || e >= E) report_error(a.err, MOE_ERR_DEVICE_BOUNDS, SITE_BALANCE);
-      else atomicAdd(hist + e, 1);
+      for (int v = 0; v < V; ++v) load4<WIDE>(a.logits + (in ? t : 0) * E, in ? (v * G + sub) * 4 : E, E, x[u][v]);
     }
-    if (sub == 0) {
-      zz = fmaf(lse, lse, zz);
-      ++tokens;
+#pragma unroll
+    for (int u = 0; u < BAL_UN; ++u) {
+      const float lse = softmax<G, V>(x[u]);
+      if (!live[u]) continue;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[v][j] += x[u][v][j];
+      for (int j = sub; j < a.k; j += G) {
+        const int e = j == sub ? choice[u] : a.idx[(t0 + u * PER) * a.k + j];
+        if (e < 0 || e >= E) report_error(a.err, MOE_ERR_DEVICE_BOUNDS, SITE_BALANCE);
+        else atomicAdd(hist + e, 1);
+      }
+      if (sub == 0) {
+        zz = fmaf(lse, lse, zz);
+        ++tokens;
+      }
     }
   }
   __syncwarp();
@@ -139,17 +151,31 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_fwd_kernel(const __grid_c
   if (!last_s) return;
   __threadfence();
   // every warp adds every 16th row, then the warps' sums are added in order
-  for (int c = lane; c < W; c += 32) {
-    float s = 0.f;
-    int n = 0;
+  constexpr int CH = 5;                          // columns of a lane on their way at once: 64 experts' two kinds
+  for (int c0 = lane; c0 < W; c0 += 32 * CH) {
+    float sum[CH];
+    int n[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      sum[i] = 0.f;
+      n[i] = 0;
+    }
 #pragma unroll 4
     for (int b = warp; b < int(gridDim.x); b += BAL_WARPS) {
-      const uint32_t p = __ldcg(a.partial + int64_t(b) * W + c);
-      if (c <= E) s += __uint_as_float(p);
-      else n += int(p);
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int c = c0 + 32 * i;
+        const uint32_t p = c < W ? __ldcg(a.partial + int64_t(b) * W + c) : 0u;
+        if (c <= E) sum[i] += __uint_as_float(p);
+        else n[i] += int(p);
+      }
     }
-    if (c <= E) wsum[warp * (E + 1) + c] = s;
-    else sh[(BAL_WARPS + 1) * (E + 1) + warp * (E + 1) + c - E - 1] = uint32_t(n);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = c0 + 32 * i;
+      if (c <= E) wsum[warp * (E + 1) + c] = sum[i];
+      else if (c < W) sh[(BAL_WARPS + 1) * (E + 1) + warp * (E + 1) + c - E - 1] = uint32_t(n[i]);
+    }
   }
   __syncthreads();
   for (int c = tid; c < W; c += BAL_THREADS) {
@@ -166,68 +192,80 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_fwd_kernel(const __grid_c
   }
   __syncthreads();
   if (warp != 0) return;
-  const double n = hist[E] > 0 ? double(hist[E]) : 1.0;
-  double dot = 0.0;
+  const float n = float(hist[E] > 0 ? hist[E] : 1);
+  float dot = 0.f;
   for (int e = lane; e < E; e += 32) {
-    const double p = double(wsum[e]) / n;
-    a.prob[e] = float(p);
-    dot += double(hist[e]) * p;
+    const float p = __fdiv_rn(wsum[e], n);
+    a.prob[e] = p;
+    dot = fmaf(float(hist[e]), p, dot);
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, off);
   if (lane == 0) {
-    const double balance = dot * E / (a.k * n), z = double(wsum[E]) / n;
-    a.loss[0] = float(double(a.alpha) * balance + double(a.beta) * z);
-    a.loss[1] = float(balance);
-    a.loss[2] = float(z);
+    const float balance = __fdiv_rn(dot * float(E), float(a.k) * n), z = __fdiv_rn(wsum[E], n);
+    a.loss[0] = fmaf(a.alpha, balance, a.beta * z);
+    a.loss[1] = balance;
+    a.loss[2] = z;
   }
 }
 
 template <int G, int V, bool WIDE>
 __global__ void __launch_bounds__(BAL_THREADS) balance_bwd_kernel(const __grid_constant__ BalanceArgs a) {
+  __shared__ float load_s[4 * 32 * 2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & (G - 1);
   const int E = a.E;
   pdl_wait();
   const int64_t n = a.counts[E] > 0 ? a.counts[E] : 1;
+  // alpha f, from whole numbers: E c - k n has no rounding that even loads would be left with
+  for (int e = threadIdx.x; e < 4 * 32 * 2; e += BAL_THREADS)
+    load_s[e] = e < E ? a.alpha * __fdiv_rn(float(int64_t(E) * a.counts[e] - a.k * n), float(a.k * n)) : 0.f;
+  __syncthreads();
   float f[V][4];
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int e = (v * G + sub) * 4 + j;
-      f[v][j] = e < E ? a.alpha * float(double(int64_t(E) * a.counts[e] - a.k * n) / double(a.k * n)) : 0.f;
+    for (int j = 0; j < 4; ++j) f[v][j] = load_s[(v * G + sub) * 4 + j];
+  const float g = __fdiv_rn(a.grad != nullptr ? *a.grad : 1.f, float(n));
+  constexpr int PER = 32 / G;
+  const int64_t step = int64_t(gridDim.x) * BAL_WARPS * PER * BAL_UN;
+  for (int64_t t0 = (int64_t(blockIdx.x) * BAL_WARPS + warp) * PER * BAL_UN + lane / G; t0 - lane / G < a.T; t0 += step) {
+    float x[BAL_UN][V][4];
+    bool live[BAL_UN];
+#pragma unroll
+    for (int u = 0; u < BAL_UN; ++u) {
+      const int64_t t = t0 + u * PER;
+      const bool in = t < a.T;
+      live[u] = in && (a.mask == nullptr || a.mask[t] != 0);
+#pragma unroll
+      for (int v = 0; v < V; ++v) load4<WIDE>(a.logits + (in ? t : 0) * E, in ? (v * G + sub) * 4 : E, E, x[u][v]);
     }
-  const float g = (a.grad != nullptr ? *a.grad : 1.f) / float(n);
-  const int64_t step = int64_t(gridDim.x) * (BAL_THREADS / G);
-  for (int64_t t0 = (int64_t(blockIdx.x) * BAL_THREADS + warp * 32) / G; t0 < a.T; t0 += step) {
-    const int64_t t = t0 + lane / G;
-    const bool in = t < a.T, live = in && (a.mask == nullptr || a.mask[t] != 0);
-    float x[V][4];
 #pragma unroll
-    for (int v = 0; v < V; ++v) load4<WIDE>(a.logits + (live ? t : 0) * E, live ? (v * G + sub) * 4 : E, E, x[v]);
-    const float lse = softmax<G, V>(x);
-    float dot = 0.f;
+    for (int u = 0; u < BAL_UN; ++u) {
+      const int64_t t = t0 + u * PER;
+      const float lse = softmax<G, V>(x[u]);
+      float dot = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+      for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) dot = fmaf(f[v][j], x[v][j], dot);
+        for (int j = 0; j < 4; ++j) dot = fmaf(f[v][j], x[u][v][j], dot);
 #pragma unroll
-    for (int off = 1; off < G; off *= 2) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, off);
-    if (!in) continue;
-    const float base = 2.f * a.beta * lse - dot;
+      for (int off = 1; off < G; off *= 2) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, off);
+      if (t >= a.T) continue;
+      const float base = 2.f * a.beta * lse - dot;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (v * G + sub) * 4;
-      float d[4];
+      for (int v = 0; v < V; ++v) {
+        const int c = (v * G + sub) * 4;
+        float d[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) d[j] = live ? g * x[v][j] * (f[v][j] + base) : 0.f;
-      float* o = a.dlogits + t * E + c;
-      if constexpr (WIDE) {
-        if (c < E) *reinterpret_cast<float4*>(o) = make_float4(d[0], d[1], d[2], d[3]);
-      } else {
+        for (int j = 0; j < 4; ++j) d[j] = live[u] ? g * x[u][v][j] * (f[v][j] + base) : 0.f;
+        float* o = a.dlogits + t * E + c;
+        if constexpr (WIDE) {
+          if (c < E) *reinterpret_cast<float4*>(o) = make_float4(d[0], d[1], d[2], d[3]);
+        } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (c + j < E) o[j] = d[j];
+          for (int j = 0; j < 4; ++j)
+            if (c + j < E) o[j] = d[j];
+        }
       }
     }
   }
@@ -239,7 +277,8 @@ cudaError_t balance_run(const BalanceArgs& a, bool backward, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int64_t need = (int64_t(a.T) + BAL_THREADS / G - 1) / (BAL_THREADS / G);
+  constexpr int64_t TOKENS = BAL_WARPS * (32 / G) * BAL_UN;       // of a block's round
+  const int64_t need = (a.T + TOKENS - 1) / TOKENS;
   if (backward) {
     const int64_t most = int64_t(sms) * 4;
     return launch_pdl(balance_bwd_kernel<G, V, WIDE>, dim3(unsigned(need < most ? need : most)), dim3(BAL_THREADS), 0, st, a);

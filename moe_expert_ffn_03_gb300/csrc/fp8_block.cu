@@ -60,11 +60,43 @@ __device__ __forceinline__ void put_codes(uint8_t* p, const uint32_t* q, int lef
   }
 }
 
+// The largest magnitudes of a thread's eight columns over its rows (float bits): of bf16 two columns at a time, on
+// the bits of their magnitudes, which order like them with NaN and Inf above all others.
+template <typename T, bool WIDE>
+__device__ __forceinline__ void column_max(const Eight<T, WIDE>* raw, uint32_t* cmax) {
+  if constexpr (WIDE && sizeof(T) == 2) {
+    uint32_t m[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < Q_ROWS; ++i) {
+      const uint4 q = raw[i].r[0].q;
+      m[0] = __vmaxu2(m[0], q.x & 0x7FFF7FFFu);
+      m[1] = __vmaxu2(m[1], q.y & 0x7FFF7FFFu);
+      m[2] = __vmaxu2(m[2], q.z & 0x7FFF7FFFu);
+      m[3] = __vmaxu2(m[3], q.w & 0x7FFF7FFFu);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      cmax[2 * j] = m[j] << 16;
+      cmax[2 * j + 1] = m[j] & 0xFFFF0000u;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) cmax[j] = 0;
+#pragma unroll
+    for (int i = 0; i < Q_ROWS; ++i) {
+      float v[8];
+      raw[i].get(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) cmax[j] = max(cmax[j], abs_bits(v[j]));
+    }
+  }
+}
+
 // Tiles of 128 rows x 128 columns, rows from an expert's first on (matrices of `mat_rows` rows: from the
 // matrix's); 16 lanes hold a row's 128 columns, a thread eight rows in registers, so that a tile is read once
 // for both of its formats.  A persistent grid, tiles of neighbouring columns one after the other.
 template <typename T, bool WIDE>
-__global__ void __launch_bounds__(Q_THREADS) block8_quantize_kernel(const __grid_constant__ Block8Args a) {
+__global__ void __launch_bounds__(Q_THREADS, WIDE && sizeof(T) == 2 ? 3 : 2) block8_quantize_kernel(const __grid_constant__ Block8Args a) {
   __shared__ uint32_t colmax[Q_THREADS / 32][B8];
   __shared__ float colup[B8];
   __shared__ uint32_t colbad[B8];
@@ -130,9 +162,20 @@ __global__ void __launch_bounds__(Q_THREADS) block8_quantize_kernel(const __grid
   const int64_t blocks = a.split_sizes != nullptr ? blk0[a.E]
                          : a.mat_rows > 0         ? int64_t(a.E) * per
                                                   : (a.rows + B8 - 1) / B8;
-  for (int64_t t = blockIdx.x; t < blocks * cb; t += gridDim.x) {
-    const int64_t blk = t / cb;
-    const int c0 = int(t - blk * cb) * B8, left = a.cols - c0 - c8;
+  // tile t is column block t % cb of row block t / cb, counted along without divisions
+  int64_t blk = blockIdx.x / cb;
+  int col_blk = int(blockIdx.x - blk * cb);
+  const int step_blk = int(gridDim.x) / cb, step_col = int(gridDim.x) - step_blk * cb;
+  const auto next = [&]() {
+    blk += step_blk;
+    col_blk += step_col;
+    if (col_blk >= cb) {
+      col_blk -= cb;
+      ++blk;
+    }
+  };
+  for (; blk < blocks; next()) {
+    const int c0 = col_blk * B8, left = a.cols - c0 - c8;
     int64_t first;                               // row of the source, and how many the tile has
     int cnt;
     if (a.split_sizes != nullptr) {
@@ -145,8 +188,8 @@ __global__ void __launch_bounds__(Q_THREADS) block8_quantize_kernel(const __grid
       first = row0[lo] + off;
       cnt = min(B8, row0[lo + 1] - row0[lo] - off);
     } else if (a.mat_rows > 0) {
-      const int off = int(blk % per) * B8;
-      first = blk / per * a.mat_rows + off;
+      const int mat = int(blk) / per, off = (int(blk) - mat * per) * B8;
+      first = int64_t(mat) * a.mat_rows + off;
       cnt = min(B8, a.mat_rows - off);
     } else {
       first = blk * B8;
@@ -154,33 +197,43 @@ __global__ void __launch_bounds__(Q_THREADS) block8_quantize_kernel(const __grid
     }
     const int64_t trow = a.mat_rows > 0 ? first : blk * B8;                  // row of the second format's codes
     Eight<T, WIDE> raw[Q_ROWS];
+    {
+      const T* p = static_cast<const T*>(a.src) + (first + sub) * a.ld + c0 + c8;
 #pragma unroll
-    for (int i = 0; i < Q_ROWS; ++i) {
-      const int r = sub + 16 * i;
-      raw[i].load(static_cast<const T*>(a.src) + (first + r) * a.ld + c0 + c8, r < cnt ? left : 0);
+      for (int i = 0; i < Q_ROWS; ++i) raw[i].load(p + i * 16 * a.ld, sub + 16 * i < cnt ? left : 0);
     }
     uint32_t cmax[8];
+    if (a.tcodes != nullptr) {
+      column_max<T, WIDE>(raw, cmax);
+    }
+    if (a.codes != nullptr) {
+      uint32_t rmax[Q_ROWS];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) cmax[j] = 0;
-#pragma unroll
-    for (int i = 0; i < Q_ROWS; ++i) {
-      float v[8];
-      raw[i].get(v);
-      if (a.tcodes != nullptr) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) cmax[j] = max(cmax[j], abs_bits(v[j]));
+      for (int i = 0; i < Q_ROWS; ++i) {
+        float v[8];
+        raw[i].get(v);
+        rmax[i] = v_amax<8>(v);
       }
-      if (a.codes != nullptr) {
-        uint32_t amax = v_amax<8>(v);
 #pragma unroll
-        for (int off = 1; off < 16; off *= 2) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
-        const int r = sub + 16 * i;
-        if (r < cnt) {
-          const Block8 b(amax);
-          const uint32_t q[2] = {b.codes4(v), b.codes4(v + 4)};
-          put_codes<WIDE>(a.codes + (first + r) * a.cols + c0 + c8, q, left);
-          if (c8 == 0) a.scales[int64_t(c0 / B8) * a.rows + first + r] = Block8::scale(amax);
-        }
+      for (int off = 1; off < 16; off *= 2)
+#pragma unroll
+        for (int i = 0; i < Q_ROWS; ++i) rmax[i] = max(rmax[i], __shfl_xor_sync(0xFFFFFFFFu, rmax[i], off));
+      // The row's 16 lanes share its eight pairs of divisions: lane j takes row j's, the others read it.
+      uint32_t mine = rmax[0];
+#pragma unroll
+      for (int i = 1; i < Q_ROWS; ++i) mine = (lane & 7) == i ? rmax[i] : mine;
+      const float my_up = Block8(mine).up;
+      const int my_row = sub + 16 * (lane & 7);
+      if ((lane & 8) == 0 && my_row < cnt) a.scales[int64_t(c0 / B8) * a.rows + first + my_row] = Block8::scale(mine);
+      uint8_t* out = a.codes + (first + sub) * a.cols + c0 + c8;
+#pragma unroll
+      for (int i = 0; i < Q_ROWS; ++i) {
+        const float up = __shfl_sync(0xFFFFFFFFu, my_up, (lane & 16) | i);
+        float v[8];
+        raw[i].get(v);
+        const Block8 b(up, rmax[i] >= 0x7F800000u);
+        const uint32_t q[2] = {b.codes4(v), b.codes4(v + 4)};
+        if (sub + 16 * i < cnt) put_codes<WIDE>(out + int64_t(i) * 16 * a.cols, q, left);
       }
     }
     if (a.tcodes == nullptr) continue;
@@ -253,64 +306,76 @@ __global__ void __launch_bounds__(Q_THREADS) block8_quantize_kernel(const __grid
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(Q_THREADS) block8_dequantize_kernel(const __grid_constant__ Block8Back a) {
   const int lane = threadIdx.x & 31;
-  const int chunks = (a.cols + 255) / 256;
-  const int64_t items = (a.rows + 3) / 4 * chunks;
+  const int cb = (a.cols + B8 - 1) / B8;
+  const int64_t fours = (a.rows + 3) / 4;
   pdl_wait();
-  for (int64_t it = (int64_t(blockIdx.x) * Q_THREADS + threadIdx.x) >> 5; it < items; it += (int64_t(gridDim.x) * Q_THREADS) >> 5) {
-    const int64_t r4 = it / chunks;
-    const int col = int(it - r4 * chunks) * 256 + lane * 8, left = a.cols - col;
+  for (int col = blockIdx.y * 256 + lane * 8; col - lane * 8 < a.cols; col += gridDim.y * 256) {
+    const int left = a.cols - col;
     if (left <= 0) continue;
-    uint32_t q[4][2];
+    for (int64_t r4 = (int64_t(blockIdx.x) * Q_THREADS + threadIdx.x) >> 5; r4 < fours; r4 += (int64_t(gridDim.x) * Q_THREADS) >> 5) {
+      const int64_t first = r4 * 4;
+      uint32_t q[4][2];
+      float s[8];                                // tokens: the columns', of all four rows (blocks begin on 128s); else rows'
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t row = r4 * 4 + i;
-      q[i][0] = q[i][1] = 0;
-      if (row >= a.rows) continue;
-      const uint8_t* p = a.codes + row * a.cols + col;
-      if constexpr (WIDE) {
-        const uint2 w = __ldcg(reinterpret_cast<const uint2*>(p));
-        q[i][0] = w.x;
-        q[i][1] = w.y;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < left) q[i][j >> 2] |= uint32_t(p[j]) << (8 * (j & 3));
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t row = r4 * 4 + i;
-      if (row >= a.rows) continue;
-      float v[8];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 f = e4m3x2_to_float2(q[i][k >> 1] >> (16 * (k & 1)));
-        v[2 * k] = f.x;
-        v[2 * k + 1] = f.y;
-      }
-      const int64_t rb = a.mat_rows > 0 ? row / a.mat_rows * ((a.mat_rows + B8 - 1) / B8) + row % a.mat_rows / B8 : row / B8;
-      if (a.format == MOE_FP8_TOKENS) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < left) v[j] *= __ldg(a.scales + rb * a.cols + col + j);
-      } else {
-        const float s = a.format == MOE_FP8_ROWS ? __ldg(a.scales + int64_t(col / B8) * a.rows + row)
-                                                 : __ldg(a.scales + rb * ((a.cols + B8 - 1) / B8) + col / B8);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= s;
-      }
-      T* o = static_cast<T*>(a.dst) + row * a.ld + col;
-      if constexpr (WIDE) {
-        if constexpr (sizeof(T) == 2) {
-          store_vec<8>(o, v);
+      for (int i = 0; i < 4; ++i) {
+        const bool in = first + i < a.rows;
+        q[i][0] = q[i][1] = 0;
+        const uint8_t* p = a.codes + (first + i) * a.cols + col;
+        if constexpr (WIDE) {
+          if (in) {
+            const uint2 w = __ldcg(reinterpret_cast<const uint2*>(p));
+            q[i][0] = w.x;
+            q[i][1] = w.y;
+          }
         } else {
-          store_vec<4>(o, v);
-          store_vec<4>(o + 4, v + 4);
-        }
-      } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < left) store_vec<1>(o + j, v + j);
+          for (int j = 0; j < 8; ++j)
+            if (in && j < left) q[i][j >> 2] |= uint32_t(p[j]) << (8 * (j & 3));
+        }
+        if (a.format == MOE_FP8_ROWS) {
+          s[i] = in ? __ldg(a.scales + int64_t(col / B8) * a.rows + first + i) : 0.f;
+        } else if (a.format == MOE_FP8_TILES) {
+          int64_t rb = first / B8;
+          if (a.mat_rows > 0 && in) {            // rows below 2^31
+            const uint32_t row = uint32_t(first + i), mat = row / uint32_t(a.mat_rows);
+            rb = int64_t(mat) * ((a.mat_rows + B8 - 1) / B8) + (row - mat * uint32_t(a.mat_rows)) / B8;
+          }
+          s[i] = in ? __ldg(a.scales + rb * cb + col / B8) : 0.f;
+        }
+      }
+      if (a.format == MOE_FP8_TOKENS) {
+        const float* p = a.scales + first / B8 * a.cols + col;
+        if constexpr (WIDE) {
+          *reinterpret_cast<float4*>(s) = __ldg(reinterpret_cast<const float4*>(p));
+          *reinterpret_cast<float4*>(s + 4) = __ldg(reinterpret_cast<const float4*>(p + 4));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s[j] = j < left ? __ldg(p + j) : 0.f;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (first + i >= a.rows) continue;
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = e4m3x2_to_float2(q[i][k >> 1] >> (16 * (k & 1)));
+          v[2 * k] = f.x * (a.format == MOE_FP8_TOKENS ? s[2 * k] : s[i]);
+          v[2 * k + 1] = f.y * (a.format == MOE_FP8_TOKENS ? s[2 * k + 1] : s[i]);
+        }
+        T* o = static_cast<T*>(a.dst) + (first + i) * a.ld + col;
+        if constexpr (WIDE) {
+          if constexpr (sizeof(T) == 2) {
+            store_vec<8>(o, v);
+          } else {
+            store_vec<4>(o, v);
+            store_vec<4>(o + 4, v + 4);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < left) store_vec<1>(o + j, v + j);
+        }
       }
     }
   }
@@ -367,9 +432,10 @@ cudaError_t launch_block8_quantize(const Block8Args& a, bool f32, cudaStream_t s
 cudaError_t launch_block8_dequantize(const Block8Back& a, bool f32, cudaStream_t st) {
   int sms = 0;
   if (const cudaError_t e = sm_count(&sms); e != cudaSuccess) return e;
-  const int64_t items = (a.rows + 3) / 4 * ((a.cols + 255) / 256), blocks = (items + Q_THREADS / 32 - 1) / (Q_THREADS / 32);
-  const int64_t most = int64_t(sms) * 8;
-  const dim3 grid(unsigned(blocks < most ? blocks : most));
+  const int64_t across = (a.cols + 255) / 256, gy = across < 1024 ? across : 1024;
+  const int64_t need = ((a.rows + 3) / 4 + Q_THREADS / 32 - 1) / (Q_THREADS / 32);
+  const int64_t most = (int64_t(sms) * 8 + gy - 1) / gy;
+  const dim3 grid(unsigned(need < most ? need : most), unsigned(gy));
   const bool wide = a.cols % 8 == 0 && a.ld % 8 == 0;
   if (f32)
     return wide ? launch_pdl(block8_dequantize_kernel<float, true>, grid, dim3(Q_THREADS), 0, st, a)

@@ -18,6 +18,7 @@ struct Block8 {
     bad = amax_bits >= 0x7F800000u;
     up = __fdiv_rn(448.f, fmaxf(__uint_as_float(amax_bits), B8_TINY));
   }
+  __device__ __forceinline__ Block8(float up_, bool bad_) : up(up_), bad(bad_) {}
   static __device__ __forceinline__ float scale(uint32_t amax_bits) {
     return amax_bits >= 0x7F800000u ? 1.f : __fdiv_rn(fmaxf(__uint_as_float(amax_bits), B8_TINY), 448.f);
   }
