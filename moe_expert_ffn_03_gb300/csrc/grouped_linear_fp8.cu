@@ -36,10 +36,23 @@
 namespace moe {
 namespace {
 
+struct alignas(16) Tile8 {
+  int e;
+  int m0, cnt;     // first m (a row of all experts', or an output feature of e) and how many the tile has
+  int n0;          // first n
+  int n;           // the MMA's columns: those left rounded up to 32; CTA r holds n0 + r * n/2 ..
+  int c0;          // contraction: first index (wgrad: row of the layout on blocks)
+  int blocks;      // its blocks of 128; -1 behind the last tile
+  int last;        // indices in the last block
+  int64_t sa, sb;  // offsets of the scales of m0 and n0 of the first block
+  int64_t out;     // of the output's element (m0, n0)
+  int64_t unused;
+};
+
 constexpr int L8_M = 256, L8_N = 256;            // the pair's tile
 constexpr int L8_SIDE = 128 * L8_KT;             // bytes of a CTA's A or B in a stage
 constexpr int L8_STAGE = 2 * L8_SIDE;
-constexpr int L8_STAGES = 6;                     // an even number: a block's buffer is its stage's parity
+constexpr int L8_STAGES = 4;                     // an even number: a block's buffer is its stage's parity
 constexpr int L8_EPI_WARPS = 8;
 constexpr int L8_THREADS = 32 * (4 + L8_EPI_WARPS);
 constexpr int L8_REGS = 168, L8_REGS_FEW = 56, L8_REGS_MANY = 224;
@@ -47,15 +60,20 @@ static_assert(128 * L8_REGS_FEW + 32 * L8_EPI_WARPS * L8_REGS_MANY == L8_THREADS
 constexpr int L8_GROUP = 8;                      // row tiles that share the sweep over the weights
 constexpr int L8_SMALL = 32;                     // rows of the small box of rows
 
-constexpr int L8_OFF_BAR = L8_STAGES * L8_STAGE;
-constexpr int L8_BARS = 2 * L8_STAGES + 1;       // full, empty, drain
+// a warp's output on its way: two boxes of 32 rows of 64 bf16, swizzled in 128 bytes
+constexpr int L8_BOX = 32 * 128;
+constexpr int L8_OFF_OUT = L8_STAGES * L8_STAGE;
+constexpr int L8_OFF_BAR = L8_OFF_OUT + L8_EPI_WARPS * 2 * L8_BOX;
+constexpr int L8_TILES = 4;                      // tiles laid out ahead
+constexpr int L8_BARS = 2 * L8_STAGES + 1 + 2 * L8_TILES;        // full, empty, drain, laid, taken
 constexpr int L8_OFF_MISC = L8_OFF_BAR + L8_BARS * 8;
 constexpr int L8_OFF_SEG = (L8_OFF_MISC + 16 + 15) & ~15;        // row0[E+1], tile0[E+1], order[E]
 // the scales' rings: [L8_AHEAD][warps][32] of {A side, B side}
-constexpr int L8_AHEAD = 8;                      // blocks whose scales are on their way
+constexpr int L8_AHEAD = 4;                      // blocks whose scales are on their way
 constexpr int L8_SCALE_SLOT = L8_EPI_WARPS * 32 * 2;
 constexpr int L8_OFF_SCALE = (L8_OFF_SEG + 3 * (L8_MAX_E + 1) * 4 + 15) & ~15;
-constexpr int L8_SMEM = L8_OFF_SCALE + L8_AHEAD * L8_SCALE_SLOT * 4 + 1024;
+constexpr int L8_OFF_TILES = L8_OFF_SCALE + L8_AHEAD * L8_SCALE_SLOT * 4;
+constexpr int L8_SMEM = L8_OFF_TILES + L8_TILES * int(sizeof(Tile8)) + 1024;
 static_assert(L8_SMEM <= 232448, "shared memory budget");
 
 // kind::f8f6f4 instruction descriptor: E4M3 x E4M3 -> f32, M = 256, N columns; a_mn, b_mn: the operand
@@ -92,14 +110,6 @@ struct Ring {
   }
 };
 
-struct Tile8 {
-  int e;
-  int m0, cnt;     // first m (a row of all experts', or an output feature of e) and how many the tile has
-  int n0, n;       // first n, and the MMA's columns: those left rounded up to 32; CTA r holds n0 + r * n/2 ..
-  int c0;          // contraction: first index (wgrad: row of the layout on blocks)
-  int blocks;      // its blocks of 128
-  int last;        // indices in the last block
-};
 
 template <int MODE>
 __device__ __forceinline__ int l8_cols(const Linear8Args& a) { return MODE == LIN_FWD ? a.N : a.K; }
@@ -153,6 +163,10 @@ __device__ __forceinline__ void l8_decode(const Linear8Args& a, const int* row0,
   }
   tl.n0 = tn * L8_N;
   tl.n = (min(L8_N, cols - tl.n0) + 31) & ~31;
+  const int64_t kbs = (a.K + 127) / 128, nbs = (a.N + 127) / 128, nb = tl.n0 / 128, blk = tl.c0 / L8_KT;
+  tl.sa = (MODE == LIN_WGRAD ? blk * a.N : 0) + tl.m0;
+  tl.sb = MODE == LIN_FWD ? (tl.e * nbs + nb) * kbs : (MODE == LIN_DGRAD ? tl.e * nbs : blk) * kbs + nb;
+  tl.out = ((MODE == LIN_WGRAD ? int64_t(tl.e) * a.N : 0) + tl.m0) * a.ldo + tl.n0;
 }
 
 // The pair's tile after t.  wgrad: there and back, since tiles come longest first: the pair that got the
@@ -161,6 +175,22 @@ template <int MODE>
 __device__ __forceinline__ int l8_after(int t, int num_pairs) {
   return t + (MODE == LIN_WGRAD ? 2 * (num_pairs - 1 - t % num_pairs) + 1 : num_pairs);
 }
+
+// The pair's tiles in turn, as warp 3 of each CTA lays them out in a small ring of shared memory: finding a tile (a
+// search among the experts, divisions) took the warps that add 4000 clocks, a quarter of a tile of 2048.
+struct Tiles8 {
+  const Tile8* ring;
+  uint64_t *laid, *taken;
+  int slot = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ Tiles8(const Tile8* r, uint64_t* l, uint64_t* t) : ring(r), laid(l), taken(t) {}
+  __device__ __forceinline__ void advance() {
+    if (++slot == L8_TILES) {
+      slot = 0;
+      ph ^= 1u;
+    }
+  }
+};
 
 // acc += part * f, two at a time
 __device__ __forceinline__ void l8_add(float* acc, const uint32_t* part, float2 f) {
@@ -184,16 +214,31 @@ __device__ __forceinline__ void l8_hand_back(uint32_t caddr, int lane) {
       : "memory");
 }
 
+// A box of the output from shared memory; what is past the output's end is left out.
+template <int MODE>
+__device__ __forceinline__ void l8_store(const CUtensorMap* map, const void* src, int n, int m, int e) {
+  if constexpr (MODE == LIN_WGRAD)
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(n), "r"(m), "r"(e) : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(n), "r"(m) : "memory");
+}
+
 template <int MODE>
 __global__ void __launch_bounds__(L8_THREADS, 1)
     grouped_linear_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmAs,
-                              const __grid_constant__ CUtensorMap tmB, const Linear8Args args) {
+                              const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmO,
+                              const Linear8Args args) {
   constexpr bool A_MN = MODE == LIN_WGRAD, B_MN = MODE != LIN_FWD;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L8_OFF_BAR);
   uint64_t* empty = full + L8_STAGES;
   uint64_t* drain = empty + L8_STAGES;
+  uint64_t* laid = drain + 1;
+  uint64_t* taken = laid + L8_TILES;
+  Tile8* const tile_ring = reinterpret_cast<Tile8*>(smem + L8_OFF_TILES);
   uint32_t* tmem_base_s = reinterpret_cast<uint32_t*>(smem + L8_OFF_MISC);
   volatile int* abort_s = reinterpret_cast<volatile int*>(smem + L8_OFF_MISC + 4);
   volatile int* bad_s = reinterpret_cast<volatile int*>(smem + L8_OFF_MISC + 8);
@@ -211,11 +256,17 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
       mbar_init(&empty[s], 1);
     }
     mbar_init(drain, 1);
+    for (int i = 0; i < L8_TILES; ++i) {
+      mbar_init(&laid[i], 1);
+      // by the warps that add, the producers and, in the leader, the MMA issuer
+      mbar_init(&taken[i], L8_EPI_WARPS + (args.selftest_no_loads ? 0 : 2) + (rank == 0 ? 1 : 0));
+    }
     *abort_s = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmAs);
     prefetch_tmap(&tmB);
+    prefetch_tmap(&tmO);
   }
   if (warp == 1) {
     tmem_alloc(tmem_base_s, 512);                // collectively with the peer CTA
@@ -256,10 +307,15 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
       const bool a_side = warp == 0;
       const uint32_t full_c0 = mapa_shared(smem_u32(full), 0);
       Ring cur;
+      Tiles8 tiles(tile_ring, laid, taken);
       bool ok = true;
-      Tile8 tl;
-      for (int t = pair; ok && t < total; t = l8_after<MODE>(t, num_pairs)) {
-        l8_decode<MODE>(args, row0, tile0, order, t, tl);
+      for (;;) {
+        ok = ok && wait_phase_inline(&laid[tiles.slot], tiles.ph, abort_s, args.err, SITE_LINEAR8 + 6, lim);
+        if (!ok) break;
+        const Tile8 tl = tile_ring[tiles.slot];
+        mbar_arrive(&taken[tiles.slot]);
+        tiles.advance();
+        if (tl.blocks < 0) break;
         // A boxes of 128 m, or 32 rows where the CTA has no more; none where it has no m at all (what the
         // stage holds there instead only meets lanes that nobody stores)
         const auto a_bytes = [&](int r) {
@@ -302,11 +358,16 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
         bool ok = true, issued = false;
         uint32_t ph = 0;
         int at = 0;                              // the next block's stage
-        Tile8 tl;
-        for (int t = pair; ok && t < total; t = l8_after<MODE>(t, num_pairs)) {
-          l8_decode<MODE>(args, row0, tile0, order, t, tl);
-          const uint32_t idesc = l8_idesc(A_MN, B_MN, tl.n);
-          int left = tl.blocks;
+        Tiles8 tiles(tile_ring, laid, taken);
+        for (;;) {
+          ok = ok && wait_phase_inline(&laid[tiles.slot], tiles.ph, abort_s, args.err, SITE_LINEAR8 + 7, lim);
+          if (!ok) break;
+          int left = tile_ring[tiles.slot].blocks;
+          const int last = tile_ring[tiles.slot].last;
+          const uint32_t idesc = l8_idesc(A_MN, B_MN, tile_ring[tiles.slot].n);
+          mbar_arrive(&taken[tiles.slot]);
+          tiles.advance();
+          if (left < 0) break;
           // the block in stage ST; false: the tile ends, or a wait gave up
           const auto block = [&](auto stage) {
             constexpr uint32_t ST = decltype(stage)::value, OFF = ST * (L8_STAGE >> 4);
@@ -317,7 +378,7 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
             }
             tc_fence_after();
             const uint32_t acc = tmem + (ST & 1) * L8_N;
-            const int groups = left > 1 ? 4 : (tl.last + 31) >> 5;           // of 32: all but the last are full blocks
+            const int groups = left > 1 ? 4 : (last + 31) >> 5;           // of 32: all but the last are full blocks
             l8_mma<OFF, OFF, false>(acc, alo, ahi, blo, bhi, idesc);
             if (groups > 1) l8_mma<OFF + A_K, OFF + B_K, true>(acc, alo, ahi, blo, bhi, idesc);
             if (groups > 2) l8_mma<OFF + 2 * A_K, OFF + 2 * B_K, true>(acc, alo, ahi, blo, bhi, idesc);
@@ -334,9 +395,7 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
               case 0: if (!block(std::integral_constant<uint32_t, 0>{})) break; [[fallthrough]];
               case 1: if (!block(std::integral_constant<uint32_t, 1>{})) break; [[fallthrough]];
               case 2: if (!block(std::integral_constant<uint32_t, 2>{})) break; [[fallthrough]];
-              case 3: if (!block(std::integral_constant<uint32_t, 3>{})) break; [[fallthrough]];
-              case 4: if (!block(std::integral_constant<uint32_t, 4>{})) break; [[fallthrough]];
-              default: block(std::integral_constant<uint32_t, 5>{});
+              default: block(std::integral_constant<uint32_t, 3>{});
             }
           }
         }
@@ -345,6 +404,21 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
           const uint64_t t0 = globaltimer_ns();
           while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < 20000000ull) {
           }
+        }
+      }
+    } else if (warp == 3) {
+      if (lane == 0) {
+        // ---------------- the pair's tiles, laid out for the others ----------------
+        Tiles8 tiles(tile_ring, laid, taken);
+        for (int t = pair;; t = l8_after<MODE>(t, num_pairs)) {
+          if (!wait_phase_inline(&taken[tiles.slot], tiles.ph ^ 1u, abort_s, args.err, SITE_LINEAR8 + 8, lim)) break;
+          Tile8 tl;
+          if (t < total) l8_decode<MODE>(args, row0, tile0, order, t, tl);
+          else tl.blocks = -1;
+          tile_ring[tiles.slot] = tl;
+          mbar_arrive(&laid[tiles.slot]);
+          tiles.advance();
+          if (t >= total) break;
         }
       }
     }
@@ -360,8 +434,8 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
     l8_hand_back(full_c0, lane);                 // both buffers are free at first
     l8_hand_back(full_c0 + 8u, lane);
     const int cols = l8_cols<MODE>(args);
-    const int kbs = (args.K + 127) / 128, nbs = (args.N + 127) / 128;
-    const int64_t sa_step = MODE == LIN_WGRAD ? args.N : args.rows, sb_step = MODE == LIN_FWD ? 1 : kbs;
+    const int64_t sa_step = MODE == LIN_WGRAD ? args.N : args.rows;
+    const int64_t kbs = (args.K + 127) / 128, sb_step = MODE == LIN_FWD ? 1 : kbs, sb_half = MODE == LIN_FWD ? kbs : 1;
     // A lane's own ring of its scales (its m's, its warp's columns'), L8_AHEAD blocks on their way: what a
     // lane copies it alone reads, so a wait for its own copies is enough.
     float* const mine = reinterpret_cast<float*>(smem + L8_OFF_SCALE) + ((warp - 4) * 32 + lane) * 2;
@@ -380,33 +454,44 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
       slot = slot + 1 == L8_AHEAD ? 0 : slot + 1;
     };
     Ring cur;                                    // a block's sums are there when its stage is free
-    bool ok = true, live = false;
-    Tile8 tl;
+    bool ok = true, live = false, end = false;
+    Tiles8 tiles(tile_ring, laid, taken);
     const int at = int(rank) * 128 + q * 32;     // this warp's first of a tile's m
-    // takes tile t up, and asks for its first blocks' scales
-    const auto take = [&](int t) {
-      if (t >= total) return;
-      l8_decode<MODE>(args, row0, tile0, order, t, tl);
-      live = at < tl.cnt && col0 < tl.n;
-      const int64_t blk = tl.c0 / L8_KT, e = tl.e;
-      sa = args.sa + (MODE == LIN_WGRAD ? blk * args.N : 0) + tl.m0 + min(at + lane, tl.cnt - 1);
-      const int nb = (tl.n0 + col0) / 128;
-      sb = args.sb + (MODE == LIN_FWD ? (e * nbs + nb) * kbs : (MODE == LIN_DGRAD ? e * nbs : blk) * kbs + nb);
-      coming = live ? tl.blocks : 0;
-#pragma unroll 1
+    int e = 0, m0 = 0, n0 = 0, blocks = 0;       // the tile's
+    int m_left = 0, n_left = 0;                  // its m and n from the warp's first on
+    __nv_bfloat16* out = nullptr;                // the lane's row, the warp's first n
+    // takes the next tile up, and asks for its first blocks' scales
+    const auto take = [&]() {
+      ok = wait_phase_warp_inline(&laid[tiles.slot], tiles.ph, abort_s, args.err, SITE_LINEAR8 + 6, lim);
+      if (!ok) return;
+      const Tile8* tl = &tile_ring[tiles.slot];
+      e = tl->e;
+      m0 = tl->m0;
+      n0 = tl->n0;
+      blocks = tl->blocks;
+      m_left = tl->cnt - at;
+      n_left = cols - n0 - col0;
+      sa = args.sa + tl->sa + min(at + lane, tl->cnt - 1);
+      sb = args.sb + tl->sb + (col0 != 0 ? sb_half : 0);
+      out = args.out + tl->out + (at + lane) * args.ldo + col0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&taken[tiles.slot]);
+      tiles.advance();
+      end = blocks < 0;
+      live = m_left > 0 && n_left > 0 && !end;
+      coming = live ? blocks : 0;
+#pragma unroll
       for (int i = 0; i < L8_AHEAD; ++i) ask();
     };
-    int t = pair;
-    take(t);
-    while (ok && t < total) {
+    take();
+    while (ok && !end) {
       if (!live) {
         // nobody's m or n: the buffers are handed back as they come
-        for (int kt = 0; ok && kt < tl.blocks; ++kt, cur.next()) {
+        for (int kt = 0; ok && kt < blocks; ++kt, cur.next()) {
           ok = wait_phase_warp_inline(&empty[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR8 + 5, lim);
           if (ok) back(cur.st);
         }
-        t = l8_after<MODE>(t, num_pairs);
-        take(t);
+        if (ok) take();
         continue;
       }
       float acc[128];
@@ -416,13 +501,13 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
       // added after the next block's first have been asked for, so that neither a wait nor a load's latency
       // stands between two blocks.
       uint32_t p0[32], p1[32];
-      if (tl.blocks > 0) {
+      if (blocks > 0) {
         ok = wait_phase_warp_inline(&empty[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR8 + 4, lim);
         if (!ok) break;
         tc_fence_after();
         tmem_ld32_async(tmem_row + (cur.st & 1) * L8_N, p0);
       }
-      for (int left = tl.blocks; left > 0; --left) {
+      for (int left = blocks; left > 0; --left) {
         const uint32_t src = tmem_row + (cur.st & 1) * L8_N;
         cp_async_left<L8_AHEAD - 1>();
         const float2 s2 = *reinterpret_cast<const float2*>(mine + slot * L8_SCALE_SLOT);
@@ -451,26 +536,38 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
       }
       if (!ok) break;
       // a lane's row: 32 bytes (16 columns) at a time; columns come in multiples of 16
-      const bool in = at + lane < tl.cnt;
-      const int columns = min(128, cols - tl.n0 - col0);
-      __nv_bfloat16* o = args.out + ((MODE == LIN_WGRAD ? int64_t(tl.e) * args.N : 0) + tl.m0 + at + lane) * args.ldo +
-                         tl.n0 + col0;
-      t = l8_after<MODE>(t, num_pairs);
-      take(t);                                   // its first scales are on their way while this tile goes out
+      const int rows = min(m_left, 32), columns = n_left, e_out = e, m_out = m0 + at, n_out = n0 + col0;
+      __nv_bfloat16* o = out;
+      take();                                    // its first scales are on their way while this tile goes out
+      if (MODE == LIN_WGRAD || rows == 32) {
+        // Through shared memory and TMA, which is out of the warp's way.  (Stores of 32 bytes a lane to 32 rows
+        // took 5000 clocks a tile, a third of a tile of 2048.)
+        uint8_t* const box = smem + L8_OFF_OUT + (warp - 4) * 2 * L8_BOX;
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");          // the last tile's has been read
+        __syncwarp();
 #pragma unroll
-      for (int c = 0; c < 128; c += 16) {
-        if (!in || c >= columns) break;
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(acc[c + 2 * i], acc[c + 2 * i + 1]);
-        if (args.out_v8) {
-          st_global_v8(o + c, w);
-        } else {
-          reinterpret_cast<uint4*>(o + c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          reinterpret_cast<uint4*>(o + c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        for (int c = 0; c < 128; c += 8) {
+          const uint4 w = make_uint4(pack_bf16x2(acc[c], acc[c + 1]), pack_bf16x2(acc[c + 2], acc[c + 3]),
+                                     pack_bf16x2(acc[c + 4], acc[c + 5]), pack_bf16x2(acc[c + 6], acc[c + 7]));
+          *reinterpret_cast<uint4*>(box + (c >> 6) * L8_BOX + lane * 128 + ((((c >> 3) & 7) ^ (lane & 7)) << 4)) = w;
         }
+        asm volatile("fence.proxy.async;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          l8_store<MODE>(&tmO, box, n_out, m_out, e_out);
+          if (columns > 64) l8_store<MODE>(&tmO, box + L8_BOX, n_out + 64, m_out, e_out);
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+        continue;
       }
+      // the last rows of an expert: a lane's row, 16 bytes at a time (behind them are the next expert's)
+#pragma unroll
+      for (int c = 0; c < 128; c += 8)
+        if (lane < rows && c < columns)
+          *reinterpret_cast<uint4*>(o + c) = make_uint4(pack_bf16x2(acc[c], acc[c + 1]), pack_bf16x2(acc[c + 2], acc[c + 3]),
+                                                        pack_bf16x2(acc[c + 4], acc[c + 5]), pack_bf16x2(acc[c + 6], acc[c + 7]));
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     cp_async_left<0>();
   }
   tc_fence_before();
@@ -487,9 +584,21 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
+// bf16 map of the output [batch][rows][inner] (batch 0: no such dimension) at pitch ld, boxes of 64 x 32.
+bool l8_out_map(CUtensorMap* m, void* base, int64_t inner, int64_t rows, int64_t ld, int64_t batch) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[3] = {cuuint64_t(inner), cuuint64_t(rows), cuuint64_t(batch)};
+  cuuint64_t strides[2] = {cuuint64_t(ld) * 2, cuuint64_t(ld) * cuuint64_t(rows) * 2};
+  cuuint32_t box[3] = {64, 32, 1}, estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, batch > 0 ? 3 : 2, base, dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int MODE>
-cudaError_t l8_launch(const CUtensorMap& ma, const CUtensorMap& mas, const CUtensorMap& mb, const Linear8Args& a, int grid,
-                      cudaStream_t st) {
+cudaError_t l8_launch(const CUtensorMap& ma, const CUtensorMap& mas, const CUtensorMap& mb, const CUtensorMap& mo,
+                      const Linear8Args& a, int grid, cudaStream_t st) {
   // attributes are per device: set and checked once on each device this process uses
   constexpr int kMaxDevices = 64;
   static std::atomic<bool> ready[kMaxDevices];
@@ -520,7 +629,7 @@ cudaError_t l8_launch(const CUtensorMap& ma, const CUtensorMap& mas, const CUten
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, grouped_linear_fp8_kernel<MODE>, ma, mas, mb, a);
+  return cudaLaunchKernelEx(&cfg, grouped_linear_fp8_kernel<MODE>, ma, mas, mb, mo, a);
 }
 
 }  // namespace
@@ -542,7 +651,7 @@ cudaError_t launch_grouped_linear_fp8(int mode, const Linear8Args& args, const u
   // 4096 -> 28672: 61 and 46.)
   if (mode != LIN_WGRAD && (a.rows <= int64_t(16) * a.E || (a.rows <= int64_t(64) * a.E && 2 * tiles <= pairs)))
     return launch_grouped_linear_fp8_few(mode, a, a_codes, b_codes, sms, st, msg, msg_len);
-  CUtensorMap ma, mas, mb;
+  CUtensorMap ma, mas, mb, mo;
   bool ok;
   if (mode == LIN_WGRAD) {
     const int64_t rows = (a.rows / L8_KT + a.E) * L8_KT;             // of the layout on blocks
@@ -553,17 +662,18 @@ cudaError_t launch_grouped_linear_fp8(int mode, const Linear8Args& args, const u
     ok = l8_map(&ma, a_codes, inner, a.rows, 0, 128) && l8_map(&mas, a_codes, inner, a.rows, 0, L8_SMALL) &&
          l8_map(&mb, b_codes, a.K, a.N, a.E, 128);
   }
+  ok = ok && (mode == LIN_WGRAD ? l8_out_map(&mo, a.out, a.K, a.N, a.ldo, a.E)
+                                : l8_out_map(&mo, a.out, mode == LIN_FWD ? a.N : a.K, a.rows, a.ldo, 0));
   if (!ok) {
     snprintf(msg, msg_len, "cuTensorMapEncodeTiled failed (rows %lld, K %d, N %d, E %d)", (long long)a.rows, a.K, a.N,
              a.E);
     return cudaErrorInvalidValue;
   }
-  a.out_v8 = aligned32(a.out) && a.ldo % 16 == 0;
   const int grid = 2 * int(tiles < pairs ? tiles : pairs);
   switch (mode) {
-    case LIN_FWD: return l8_launch<LIN_FWD>(ma, mas, mb, a, grid, st);
-    case LIN_DGRAD: return l8_launch<LIN_DGRAD>(ma, mas, mb, a, grid, st);
-    default: return l8_launch<LIN_WGRAD>(ma, mas, mb, a, grid, st);
+    case LIN_FWD: return l8_launch<LIN_FWD>(ma, mas, mb, mo, a, grid, st);
+    case LIN_DGRAD: return l8_launch<LIN_DGRAD>(ma, mas, mb, mo, a, grid, st);
+    default: return l8_launch<LIN_WGRAD>(ma, mas, mb, mo, a, grid, st);
   }
 }
 

@@ -323,8 +323,7 @@ struct Linear8Args {
   int* err;
   uint64_t wait_limit_ns;    // of every bounded wait
   int selftest_no_loads;     // the producers issue nothing
-  int out_v8;                // set by the launch: 32-byte stores and,
-  unsigned* arrived;         // of the workspace, the arrivals and partial sums of cut tiles
+  unsigned* arrived;         // set by the launch: of the workspace, the arrivals and partial sums of cut tiles
   float* pieces;
 };
 constexpr int F8_MAX_PIECES = 608;                // pieces of tiles that are cut along the contraction
