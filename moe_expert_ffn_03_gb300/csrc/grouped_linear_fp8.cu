@@ -25,7 +25,7 @@
 //   warp 1       tensor memory; in the leader, the MMAs
 //   warp 3       the experts' prefix sums
 //   warps 4..11  sums: four per lane quarter, 128 columns each, with 224 registers a thread (the other
-//                four warps give up theirs: 128 x 56 + 256 x 224 = 384 x 168)
+//                four warps give up theirs: 128 x 40 + 256 x 232 = 384 x 168)
 // Waits are bounded as everywhere; each lasts as long as a block or a tile's output at most.
 #include <atomic>
 #include <cstdio>
@@ -55,7 +55,7 @@ constexpr int L8_STAGE = 2 * L8_SIDE;
 constexpr int L8_STAGES = 4;                     // an even number: a block's buffer is its stage's parity
 constexpr int L8_EPI_WARPS = 8;
 constexpr int L8_THREADS = 32 * (4 + L8_EPI_WARPS);
-constexpr int L8_REGS = 168, L8_REGS_FEW = 56, L8_REGS_MANY = 224;
+constexpr int L8_REGS = 168, L8_REGS_FEW = 40, L8_REGS_MANY = 232;
 static_assert(128 * L8_REGS_FEW + 32 * L8_EPI_WARPS * L8_REGS_MANY == L8_THREADS * L8_REGS, "register split");
 constexpr int L8_GROUP = 8;                      // row tiles that share the sweep over the weights
 constexpr int L8_SMALL = 32;                     // rows of the small box of rows
@@ -502,8 +502,7 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
       // stands between two blocks.
       uint32_t p0[32], p1[32];
       if (blocks > 0) {
-        ok = wait_phase_warp_inline(&empty[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR8 + 4, lim);
-        if (!ok) break;
+        wait_phase_warp_later(&empty[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR8 + 4, lim, ok);
         tc_fence_after();
         tmem_ld32_async(tmem_row + (cur.st & 1) * L8_N, p0);
       }
@@ -512,9 +511,9 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
         cp_async_left<L8_AHEAD - 1>();
         const float2 s2 = *reinterpret_cast<const float2*>(mine + slot * L8_SCALE_SLOT);
         const float2 f2 = make_float2(s2.x * s2.y, s2.x * s2.y);
-        ask();                                   // into the same place: what was there has been read
         tmem_wait_ld<32>(p0);
         tmem_ld32_async(src + 32, p1);
+        ask();                                   // into the same place: what was there has been read
         l8_add(acc, p0, f2);
         tmem_wait_ld<32>(p1);
         tmem_ld32_async(src + 64, p0);
@@ -525,10 +524,13 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
         tmem_wait_ld<32>(p1);
         tc_fence_before();
         back(cur.st);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          ok = false;
+          break;
+        }
         cur.next();
         if (left > 1) {
-          ok = wait_phase_warp_inline(&empty[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR8 + 4, lim);
-          if (!ok) break;
+          wait_phase_warp_later(&empty[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR8 + 4, lim, ok);
           tc_fence_after();
           tmem_ld32_async(tmem_row + (cur.st & 1) * L8_N, p0);
         }

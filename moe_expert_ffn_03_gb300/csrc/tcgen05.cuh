@@ -247,6 +247,17 @@ __device__ __forceinline__ bool wait_phase_warp_inline(uint64_t* bar, uint32_t p
   return __all_sync(0xFFFFFFFFu, wait_phase_inline(bar, parity, abort_flag, err, site, limit_ns));
 }
 
+// The same for a wait that other warps wait for in turn: lanes whose wait gave up clear their `ok` and go on with the
+// others, so that the warp stays together without a vote here; it has to vote on `ok` (__all_sync) before
+// long, and what it computes in between must be harmless.
+__device__ __forceinline__ void wait_phase_warp_later(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
+                                                      int site, uint64_t limit_ns, bool& ok) {
+  if (!mbar_try_wait(bar, parity)) {
+    if (!wait_phase_inline(bar, parity, abort_flag, err, site, limit_ns)) ok = false;
+  }
+  __syncwarp();
+}
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
