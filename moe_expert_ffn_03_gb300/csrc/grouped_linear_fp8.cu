@@ -60,10 +60,9 @@ static_assert(128 * L8_REGS_FEW + 32 * L8_EPI_WARPS * L8_REGS_MANY == L8_THREADS
 constexpr int L8_GROUP = 8;                      // row tiles that share the sweep over the weights
 constexpr int L8_SMALL = 32;                     // rows of the small box of rows
 
-// a warp's output on its way: two boxes of 32 rows of 64 bf16, swizzled in 128 bytes
-constexpr int L8_BOX = 32 * 128;
+constexpr int L8_BOX = 32 * 256;                 // a warp's output on its way: 32 rows of 128 bf16
 constexpr int L8_OFF_OUT = L8_STAGES * L8_STAGE;
-constexpr int L8_OFF_BAR = L8_OFF_OUT + L8_EPI_WARPS * 2 * L8_BOX;
+constexpr int L8_OFF_BAR = L8_OFF_OUT + L8_EPI_WARPS * L8_BOX;
 constexpr int L8_TILES = 4;                      // tiles laid out ahead
 constexpr int L8_BARS = 2 * L8_STAGES + 1 + 2 * L8_TILES;        // full, empty, drain, laid, taken
 constexpr int L8_OFF_MISC = L8_OFF_BAR + L8_BARS * 8;
@@ -214,22 +213,10 @@ __device__ __forceinline__ void l8_hand_back(uint32_t caddr, int lane) {
       : "memory");
 }
 
-// A box of the output from shared memory; what is past the output's end is left out.
-template <int MODE>
-__device__ __forceinline__ void l8_store(const CUtensorMap* map, const void* src, int n, int m, int e) {
-  if constexpr (MODE == LIN_WGRAD)
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
-                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(n), "r"(m), "r"(e) : "memory");
-  else
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];"
-                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(n), "r"(m) : "memory");
-}
-
 template <int MODE>
 __global__ void __launch_bounds__(L8_THREADS, 1)
     grouped_linear_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmAs,
-                              const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmO,
-                              const Linear8Args args) {
+                              const __grid_constant__ CUtensorMap tmB, const Linear8Args args) {
   constexpr bool A_MN = MODE == LIN_WGRAD, B_MN = MODE != LIN_FWD;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -266,7 +253,6 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmAs);
     prefetch_tmap(&tmB);
-    prefetch_tmap(&tmO);
   }
   if (warp == 1) {
     tmem_alloc(tmem_base_s, 512);                // collectively with the peer CTA
@@ -457,23 +443,19 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
     bool ok = true, live = false, end = false;
     Tiles8 tiles(tile_ring, laid, taken);
     const int at = int(rank) * 128 + q * 32;     // this warp's first of a tile's m
-    int e = 0, m0 = 0, n0 = 0, blocks = 0;       // the tile's
-    int m_left = 0, n_left = 0;                  // its m and n from the warp's first on
-    __nv_bfloat16* out = nullptr;                // the lane's row, the warp's first n
+    int blocks = 0, m_left = 0, n_left = 0;      // of the tile: blocks; m and n from the warp's first on
+    __nv_bfloat16* out = nullptr;                // the warp's first row and n
     // takes the next tile up, and asks for its first blocks' scales
     const auto take = [&]() {
       ok = wait_phase_warp_inline(&laid[tiles.slot], tiles.ph, abort_s, args.err, SITE_LINEAR8 + 6, lim);
       if (!ok) return;
       const Tile8* tl = &tile_ring[tiles.slot];
-      e = tl->e;
-      m0 = tl->m0;
-      n0 = tl->n0;
       blocks = tl->blocks;
       m_left = tl->cnt - at;
-      n_left = cols - n0 - col0;
+      n_left = cols - tl->n0 - col0;
       sa = args.sa + tl->sa + min(at + lane, tl->cnt - 1);
       sb = args.sb + tl->sb + (col0 != 0 ? sb_half : 0);
-      out = args.out + tl->out + (at + lane) * args.ldo + col0;
+      out = args.out + tl->out + at * args.ldo + col0;
       __syncwarp();
       if (lane == 0) mbar_arrive(&taken[tiles.slot]);
       tiles.advance();
@@ -537,39 +519,31 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
         l8_add(acc + 96, p1, f2);
       }
       if (!ok) break;
-      // a lane's row: 32 bytes (16 columns) at a time; columns come in multiples of 16
-      const int rows = min(m_left, 32), columns = n_left, e_out = e, m_out = m0 + at, n_out = n0 + col0;
-      __nv_bfloat16* o = out;
+      const int rows = min(m_left, 32), columns = n_left;
+      __nv_bfloat16* const o = out;
       take();                                    // its first scales are on their way while this tile goes out
-      if (MODE == LIN_WGRAD || rows == 32) {
-        // Through shared memory and TMA, which is out of the warp's way.  (Stores of 32 bytes a lane to 32 rows
-        // took 5000 clocks a tile, a third of a tile of 2048.)
-        uint8_t* const box = smem + L8_OFF_OUT + (warp - 4) * 2 * L8_BOX;
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");          // the last tile's has been read
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < 128; c += 8) {
-          const uint4 w = make_uint4(pack_bf16x2(acc[c], acc[c + 1]), pack_bf16x2(acc[c + 2], acc[c + 3]),
-                                     pack_bf16x2(acc[c + 4], acc[c + 5]), pack_bf16x2(acc[c + 6], acc[c + 7]));
-          *reinterpret_cast<uint4*>(box + (c >> 6) * L8_BOX + lane * 128 + ((((c >> 3) & 7) ^ (lane & 7)) << 4)) = w;
-        }
-        asm volatile("fence.proxy.async;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-          l8_store<MODE>(&tmO, box, n_out, m_out, e_out);
-          if (columns > 64) l8_store<MODE>(&tmO, box + L8_BOX, n_out + 64, m_out, e_out);
-          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        }
-        continue;
-      }
-      // the last rows of an expert: a lane's row, 16 bytes at a time (behind them are the next expert's)
+      // Through the warp's own shared memory, so that 16 lanes store a row's 256 bytes.  (32 bytes a lane to 32
+      // rows took 5000 clocks a tile, a third of a tile of 2048; TMA stores 2000, most of it the wait for the
+      // last ones and the fence before them.)
+      uint8_t* const box = smem + L8_OFF_OUT + (warp - 4) * L8_BOX;
+      __syncwarp();                              // the last tile's has been read
 #pragma unroll
       for (int c = 0; c < 128; c += 8)
-        if (lane < rows && c < columns)
-          *reinterpret_cast<uint4*>(o + c) = make_uint4(pack_bf16x2(acc[c], acc[c + 1]), pack_bf16x2(acc[c + 2], acc[c + 3]),
-                                                        pack_bf16x2(acc[c + 4], acc[c + 5]), pack_bf16x2(acc[c + 6], acc[c + 7]));
+        *reinterpret_cast<uint4*>(box + lane * 256 + (((c >> 3) ^ (lane & 7)) << 4)) =
+            make_uint4(pack_bf16x2(acc[c], acc[c + 1]), pack_bf16x2(acc[c + 2], acc[c + 3]),
+                       pack_bf16x2(acc[c + 4], acc[c + 5]), pack_bf16x2(acc[c + 6], acc[c + 7]));
+      __syncwarp();
+      const int chunk = lane & 15;
+      if (chunk * 8 < columns) {                 // columns come in multiples of 16
+        __nv_bfloat16* to = o + chunk * 8;
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += 2) {
+          const int r = r0 + (lane >> 4);
+          const uint4 w = *reinterpret_cast<const uint4*>(box + r * 256 + ((chunk ^ (r & 7)) << 4));
+          if (r < rows) *reinterpret_cast<uint4*>(to + r * args.ldo) = w;
+        }
+      }
     }
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     cp_async_left<0>();
   }
   tc_fence_before();
@@ -586,21 +560,9 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// bf16 map of the output [batch][rows][inner] (batch 0: no such dimension) at pitch ld, boxes of 64 x 32.
-bool l8_out_map(CUtensorMap* m, void* base, int64_t inner, int64_t rows, int64_t ld, int64_t batch) {
-  EncodeTiledFn fn = get_encode_fn();
-  if (fn == nullptr) return false;
-  cuuint64_t dims[3] = {cuuint64_t(inner), cuuint64_t(rows), cuuint64_t(batch)};
-  cuuint64_t strides[2] = {cuuint64_t(ld) * 2, cuuint64_t(ld) * cuuint64_t(rows) * 2};
-  cuuint32_t box[3] = {64, 32, 1}, estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, batch > 0 ? 3 : 2, base, dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int MODE>
-cudaError_t l8_launch(const CUtensorMap& ma, const CUtensorMap& mas, const CUtensorMap& mb, const CUtensorMap& mo,
-                      const Linear8Args& a, int grid, cudaStream_t st) {
+cudaError_t l8_launch(const CUtensorMap& ma, const CUtensorMap& mas, const CUtensorMap& mb, const Linear8Args& a, int grid,
+                      cudaStream_t st) {
   // attributes are per device: set and checked once on each device this process uses
   constexpr int kMaxDevices = 64;
   static std::atomic<bool> ready[kMaxDevices];
@@ -631,7 +593,7 @@ cudaError_t l8_launch(const CUtensorMap& ma, const CUtensorMap& mas, const CUten
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, grouped_linear_fp8_kernel<MODE>, ma, mas, mb, mo, a);
+  return cudaLaunchKernelEx(&cfg, grouped_linear_fp8_kernel<MODE>, ma, mas, mb, a);
 }
 
 }  // namespace
@@ -653,7 +615,7 @@ cudaError_t launch_grouped_linear_fp8(int mode, const Linear8Args& args, const u
   // 4096 -> 28672: 61 and 46.)
   if (mode != LIN_WGRAD && (a.rows <= int64_t(16) * a.E || (a.rows <= int64_t(64) * a.E && 2 * tiles <= pairs)))
     return launch_grouped_linear_fp8_few(mode, a, a_codes, b_codes, sms, st, msg, msg_len);
-  CUtensorMap ma, mas, mb, mo;
+  CUtensorMap ma, mas, mb;
   bool ok;
   if (mode == LIN_WGRAD) {
     const int64_t rows = (a.rows / L8_KT + a.E) * L8_KT;             // of the layout on blocks
@@ -664,8 +626,6 @@ cudaError_t launch_grouped_linear_fp8(int mode, const Linear8Args& args, const u
     ok = l8_map(&ma, a_codes, inner, a.rows, 0, 128) && l8_map(&mas, a_codes, inner, a.rows, 0, L8_SMALL) &&
          l8_map(&mb, b_codes, a.K, a.N, a.E, 128);
   }
-  ok = ok && (mode == LIN_WGRAD ? l8_out_map(&mo, a.out, a.K, a.N, a.ldo, a.E)
-                                : l8_out_map(&mo, a.out, mode == LIN_FWD ? a.N : a.K, a.rows, a.ldo, 0));
   if (!ok) {
     snprintf(msg, msg_len, "cuTensorMapEncodeTiled failed (rows %lld, K %d, N %d, E %d)", (long long)a.rows, a.K, a.N,
              a.E);
@@ -673,9 +633,9 @@ cudaError_t launch_grouped_linear_fp8(int mode, const Linear8Args& args, const u
   }
   const int grid = 2 * int(tiles < pairs ? tiles : pairs);
   switch (mode) {
-    case LIN_FWD: return l8_launch<LIN_FWD>(ma, mas, mb, mo, a, grid, st);
-    case LIN_DGRAD: return l8_launch<LIN_DGRAD>(ma, mas, mb, mo, a, grid, st);
-    default: return l8_launch<LIN_WGRAD>(ma, mas, mb, mo, a, grid, st);
+    case LIN_FWD: return l8_launch<LIN_FWD>(ma, mas, mb, a, grid, st);
+    case LIN_DGRAD: return l8_launch<LIN_DGRAD>(ma, mas, mb, a, grid, st);
+    default: return l8_launch<LIN_WGRAD>(ma, mas, mb, a, grid, st);
   }
 }
 
