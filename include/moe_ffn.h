@@ -808,12 +808,16 @@ moe_status moe_fp8_block_quantize_weights(const void* w, int32_t w_f32, int32_t 
  * ld; mat_rows: the rows of each matrix of weights (tiles), else 0. */
 moe_status moe_fp8_block_dequantize(const uint8_t* codes, const float* scales, int32_t format, int64_t rows, int32_t mat_rows,
                                     int32_t cols, void* dst, int32_t dst_f32, int64_t ld, moe_stream_t stream);
-/* Rows (MOE_FP8_ROWS) of T tokens copied to their places by expert: row pos_of[t][j] of the output is token
- * t (moe_ep_pack's pos_of); cols a multiple of 16.  A place outside 0..rows-1 is recorded in the workspace's
- * error word (256 bytes, zero-filled once) and skipped. */
-moe_status moe_fp8_block_pack(const uint8_t* codes, const float* scales, const int32_t* pos_of, int32_t T, int32_t k,
-                              int32_t cols, int64_t rows, uint8_t* codes_out, float* scales_out, void* workspace,
-                              moe_stream_t stream);
+/* moe_fp8_block_pack -- moe_ep_pack (world 1) for rows that are in 8 bits already (MOE_FP8_ROWS, moe_rmsnorm_fwd's): the
+ * (token, slot) rows of T tokens in expert order without padding.  idx, prob, row_of [T][k] and split_sizes [E]
+ * are moe_route's; codes [T][cols], cols a multiple of 16.  Out: codes_out [T*k][cols] and scales_out
+ * [ceil(cols/128)][T*k], prob_rows f32 [T*k], and pos_of int32 [T][k], every (token, slot)'s row.  One whose
+ * expert or row does not fit is recorded in the workspace's error word (256 bytes, zero-filled once), marked -1
+ * in pos_of and skipped. */
+moe_status moe_fp8_block_pack(const uint8_t* codes, const float* scales, const int32_t* idx, const float* prob,
+                              const int32_t* row_of, const int32_t* split_sizes, int32_t T, int32_t k, int32_t E,
+                              int32_t cols, uint8_t* codes_out, float* scales_out, float* prob_rows, int32_t* pos_of,
+                              void* workspace, moe_stream_t stream);
 
 /* Bytes of workspace of the calls below (256-byte aligned, zero-filled once before first use); later calls
  * on the same stream may reuse it, for any sizes; calls running at the same time on other streams need

@@ -162,7 +162,7 @@ def lib() -> ctypes.CDLL:
             "moe_fp8_block_quantize": ([P, c_int32, I64, c_int32, I64, P, P, P, c_int32, P, P, c_int32, P], c_int32),
             "moe_fp8_block_quantize_weights": ([P, c_int32, c_int32, c_int32, c_int32, P, P, P], c_int32),
             "moe_fp8_block_dequantize": ([P, P, c_int32, I64, c_int32, c_int32, P, c_int32, I64, P], c_int32),
-            "moe_fp8_block_pack": ([P, P, P, c_int32, c_int32, c_int32, I64, P, P, P, P], c_int32),
+            "moe_fp8_block_pack": ([P] * 6 + [c_int32] * 4 + [P] * 6, c_int32),
             "moe_grouped_linear_fp8_workspace_size": ([G], c_size_t),
             "moe_grouped_linear_fp8_fwd": ([G] + [P] * 6 + [I64, P, c_size_t, P], c_int32),
             "moe_grouped_linear_fp8_dgrad": ([G] + [P] * 6 + [I64, P, c_size_t, P], c_int32),
@@ -663,14 +663,18 @@ def moe_fp8_block_dequantize(codes, scales, kind, dst, stream=None):
                                           _on(stream, codes, scales, dst)))
 
 
-def moe_fp8_block_pack(codes, scales, pos_of, codes_out, scales_out, workspace, stream=None):
-    """Rows of tokens (codes [T][cols], scales [ceil(cols/128)][T]) copied to their places pos_of [T][k] in codes_out."""
-    (T, cols), k, rows = codes.shape, pos_of.shape[1], codes_out.shape[0]
+def moe_fp8_block_pack(codes, scales, idx, prob, row_of, split_sizes, codes_out, scales_out, prob_rows, pos_of, workspace,
+                       stream=None):
+    """The (token, slot) rows of tokens in 8 bits (codes [T][cols], scales [ceil(cols/128)][T]) in expert order."""
+    (T, cols), k, E = codes.shape, idx.shape[1], split_sizes.numel()
+    R = T * k
     _dense(workspace, _U8, 256)
-    _check(lib().moe_fp8_block_pack(_dense(codes, _U8, T * cols), _dense(scales, _F32, T * _cuts(cols)),
-                                    _dense(pos_of, _I32, T * k), T, k, cols, rows, _dense(codes_out, _U8, rows * cols),
-                                    _dense(scales_out, _F32, rows * _cuts(cols)), _p(workspace),
-                                    _on(stream, codes, scales, pos_of, codes_out, scales_out, workspace)))
+    _check(lib().moe_fp8_block_pack(_dense(codes, _U8, T * cols), _dense(scales, _F32, T * _cuts(cols)), _dense(idx, _I32, R),
+                                    _dense(prob, _F32, R), _dense(row_of, _I32, R), _dense(split_sizes, _I32, E), T, k, E, cols,
+                                    _dense(codes_out, _U8, R * cols), _dense(scales_out, _F32, R * _cuts(cols)),
+                                    _dense(prob_rows, _F32, R), _dense(pos_of, _I32, R), _p(workspace),
+                                    _on(stream, codes, scales, idx, prob, row_of, split_sizes, codes_out, scales_out, prob_rows,
+                                        pos_of, workspace)))
 
 
 def moe_grouped_linear_fp8_workspace_size(g: MoeGrouped) -> int:

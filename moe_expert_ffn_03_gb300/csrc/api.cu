@@ -1828,24 +1828,32 @@ moe_status moe_fp8_block_dequantize(const uint8_t* codes, const float* scales, i
   return MOE_OK;
 }
 
-moe_status moe_fp8_block_pack(const uint8_t* codes, const float* scales, const int32_t* pos_of, int32_t T, int32_t k,
-                              int32_t cols, int64_t rows, uint8_t* codes_out, float* scales_out, void* workspace,
-                              moe_stream_t stream) {
-  g_msg[0] = 0;
-  if (T < 0 || k < 1 || k > 8) return fail(MOE_ERR_INVALID_ARG, "T=%d must be >= 0, k=%d in 1..8", T, k);
-  if (moe_status s = check_block8(rows, cols); s != MOE_OK) return s;
+moe_status moe_fp8_block_pack(const uint8_t* codes, const float* scales, const int32_t* idx, const float* prob,
+                              const int32_t* row_of, const int32_t* split_sizes, int32_t T, int32_t k, int32_t E,
+                              int32_t cols, uint8_t* codes_out, float* scales_out, float* prob_rows, int32_t* pos_of,
+                              void* workspace, moe_stream_t stream) {
+  if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T=%d must be >= 0", T);
+  if (E < 1 || E > 256) return fail(MOE_ERR_UNSUPPORTED, "E=%d must be in 1..256", E);
+  if (k < 1 || k > 8 || k > E) return fail(MOE_ERR_UNSUPPORTED, "k=%d must be in 1..min(E,8)", k);
+  if (int64_t(T) * k > (int64_t(1) << 30)) return fail(MOE_ERR_UNSUPPORTED, "T*k must be <= 2^30");
+  if (moe_status s = check_block8(T, cols); s != MOE_OK) return s;
   if (cols % 16) return fail(MOE_ERR_UNSUPPORTED, "cols=%d must be a multiple of 16", cols);
   if (T == 0) return MOE_OK;
   REQUIRE_PTR(codes);
   REQUIRE_PTR(scales);
-  REQUIRE_PTR(pos_of);
+  REQUIRE_PTR(idx);
+  REQUIRE_PTR(prob);
+  REQUIRE_PTR(row_of);
+  REQUIRE_PTR(split_sizes);
   REQUIRE_PTR(codes_out);
   REQUIRE_PTR(scales_out);
+  REQUIRE_PTR(prob_rows);
+  REQUIRE_PTR(pos_of);
   if (workspace == nullptr) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return fail(MOE_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
-  CUDA_TRY(launch_block8_pack(codes, scales, pos_of, T, k, cols, rows, codes_out, scales_out, static_cast<int*>(workspace),
-                              static_cast<cudaStream_t>(stream)),
-           "block pack");
+  Block8Pack a{codes, scales, idx, prob, row_of, split_sizes, T, k, E, cols, codes_out, scales_out, prob_rows, pos_of,
+               static_cast<int*>(workspace)};
+  CUDA_TRY(launch_block8_pack(a, static_cast<cudaStream_t>(stream)), "block pack");
   return MOE_OK;
 }
 

@@ -381,27 +381,73 @@ __global__ void __launch_bounds__(Q_THREADS) block8_dequantize_kernel(const __gr
   }
 }
 
-// Rows of tokens copied to their places by expert: row pos_of[t][j] of the output is token t.  A warp takes a
-// token: its codes once from memory, k times out; then the scales of its blocks.
-__global__ void __launch_bounds__(Q_THREADS) block8_pack_kernel(const uint8_t* codes, const float* scales, const int* pos_of, int T,
-                                                                int k, int cols, int64_t rows, uint8_t* codes_out,
-                                                                float* scales_out, int* err) {
+// Rows of tokens copied to their places by expert, dense (row_of has every expert's rows on multiples of 128).  A
+// warp takes a token: its codes once from memory, k times out; then the scales of its blocks.
+__global__ void __launch_bounds__(Q_THREADS) block8_pack_kernel(const __grid_constant__ Block8Pack a) {
+  __shared__ int start[Q_MAX_E], pad_start[Q_MAX_E], size[Q_MAX_E];
   const int lane = threadIdx.x & 31;
   pdl_wait();
-  for (int64_t t = (int64_t(blockIdx.x) * Q_THREADS + threadIdx.x) >> 5; t < T; t += (int64_t(gridDim.x) * Q_THREADS) >> 5) {
-    for (int c = lane * 16; c < cols; c += 512) {
-      const uint4 v = __ldcg(reinterpret_cast<const uint4*>(codes + t * cols + c));
-      for (int j = 0; j < k; ++j) {
-        const int p = pos_of[t * k + j];
-        if (p >= 0 && p < rows) *reinterpret_cast<uint4*>(codes_out + int64_t(p) * cols + c) = v;
-        else report_error(err, MOE_ERR_DEVICE_BOUNDS, SITE_FP8_BLOCK);
+  if (threadIdx.x < 32) {
+    int rows[8], sum = 0, padded = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = lane * 8 + i;
+      rows[i] = e < a.E ? a.split_sizes[e] : 0;
+      sum += rows[i];
+      padded += (rows[i] + B8 - 1) / B8 * B8;
+    }
+    int rs = sum, ps = padded;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int r = __shfl_up_sync(0xFFFFFFFFu, rs, off), q = __shfl_up_sync(0xFFFFFFFFu, ps, off);
+      if (lane >= off) {
+        rs += r;
+        ps += q;
       }
     }
-    const int cb = (cols + B8 - 1) / B8;
-    for (int i = lane; i < cb * k; i += 32) {
-      const int j = i % k, b = i / k;
-      const int p = pos_of[t * k + j];
-      if (p >= 0 && p < rows) scales_out[b * rows + p] = __ldg(scales + int64_t(b) * T + t);
+    rs -= sum;
+    ps -= padded;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = lane * 8 + i;
+      start[e] = rs;
+      pad_start[e] = ps;
+      size[e] = rows[i];
+      rs += rows[i];
+      ps += (rows[i] + B8 - 1) / B8 * B8;
+    }
+  }
+  __syncthreads();
+  const int64_t rows = int64_t(a.T) * a.k;
+  const int cb = (a.cols + B8 - 1) / B8;
+  for (int64_t t = (int64_t(blockIdx.x) * Q_THREADS + threadIdx.x) >> 5; t < a.T; t += (int64_t(gridDim.x) * Q_THREADS) >> 5) {
+    int pos = -1;
+    if (lane < a.k) {
+      const int64_t pair = t * a.k + lane;
+      const int e = a.idx[pair], r = a.row_of[pair];
+      if (e >= 0 && e < a.E && r >= pad_start[e] && r - pad_start[e] < size[e]) pos = start[e] + (r - pad_start[e]);
+      if (pos < 0 || pos >= rows) {
+        report_error(a.err, MOE_ERR_DEVICE_BOUNDS, SITE_FP8_BLOCK);
+        pos = -1;
+      } else {
+        a.prob_rows[pos] = a.prob[pair];
+      }
+      a.pos_of[pair] = pos;
+    }
+    int to[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) to[j] = __shfl_sync(0xFFFFFFFFu, pos, j);
+    for (int c = lane * 16; c < a.cols; c += 512) {
+      const uint4 v = __ldcg(reinterpret_cast<const uint4*>(a.codes + t * a.cols + c));
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (to[j] >= 0) *reinterpret_cast<uint4*>(a.codes_out + int64_t(to[j]) * a.cols + c) = v;
+    }
+    for (int b = lane; b < cb; b += 32) {
+      const float s = __ldg(a.scales + int64_t(b) * a.T + t);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (to[j] >= 0) a.scales_out[b * rows + to[j]] = s;
     }
   }
 }
@@ -444,13 +490,11 @@ cudaError_t launch_block8_dequantize(const Block8Back& a, bool f32, cudaStream_t
               : launch_pdl(block8_dequantize_kernel<__nv_bfloat16, false>, grid, dim3(Q_THREADS), 0, st, a);
 }
 
-cudaError_t launch_block8_pack(const uint8_t* codes, const float* scales, const int* pos_of, int T, int k, int cols,
-                               int64_t rows, uint8_t* codes_out, float* scales_out, int* err, cudaStream_t st) {
+cudaError_t launch_block8_pack(const Block8Pack& a, cudaStream_t st) {
   int sms = 0;
   if (const cudaError_t e = sm_count(&sms); e != cudaSuccess) return e;
-  const int64_t blocks = (int64_t(T) + Q_THREADS / 32 - 1) / (Q_THREADS / 32), most = int64_t(sms) * 8;
-  return launch_pdl(block8_pack_kernel, dim3(unsigned(blocks < most ? blocks : most)), dim3(Q_THREADS), 0, st, codes, scales,
-                    pos_of, T, k, cols, rows, codes_out, scales_out, err);
+  const int64_t blocks = (int64_t(a.T) + Q_THREADS / 32 - 1) / (Q_THREADS / 32), most = int64_t(sms) * 8;
+  return launch_pdl(block8_pack_kernel, dim3(unsigned(blocks < most ? blocks : most)), dim3(Q_THREADS), 0, st, a);
 }
 
 }  // namespace moe

@@ -305,10 +305,23 @@ struct Block8Back {
   int mat_rows;              // rows of each matrix (0: one)
   void* dst;
 };
+struct Block8Pack {
+  const uint8_t* codes;      // rows format of T tokens
+  const float* scales;
+  const int* idx;            // [T][k], prob and row_of alike
+  const float* prob;
+  const int* row_of;
+  const int* split_sizes;    // [E]
+  int T, k, E, cols;
+  uint8_t* codes_out;        // rows format of T * k rows
+  float* scales_out;
+  float* prob_rows;          // [T * k]
+  int* pos_of;               // [T][k]
+  int* err;
+};
 cudaError_t launch_block8_quantize(const Block8Args& a, bool f32, cudaStream_t st);
 cudaError_t launch_block8_dequantize(const Block8Back& a, bool f32, cudaStream_t st);
-cudaError_t launch_block8_pack(const uint8_t* codes, const float* scales, const int* pos_of, int T, int k, int cols,
-                               int64_t rows, uint8_t* codes_out, float* scales_out, int* err, cudaStream_t st);
+cudaError_t launch_block8_pack(const Block8Pack& a, cudaStream_t st);
 
 // ---- the same on 8-bit operands with a scale per block of 128 (grouped_linear_fp8.cu) --------
 struct Linear8Args {

@@ -132,27 +132,41 @@ def test_inconsistent_sizes_write_nothing(split):
         assert bool((t == 77).all())
 
 
-@pytest.mark.parametrize("T,k,cols", [(1, 1, 16), (5, 2, 128), (300, 8, 144), (70, 3, 1040)])
-def test_pack(T, k, cols):
+@pytest.mark.parametrize("T,k,E,cols", [(1, 1, 1, 16), (5, 2, 8, 128), (300, 8, 256, 144), (700, 3, 40, 1040)])
+def test_pack(T, k, E, cols):
     g = torch.Generator(device="cuda").manual_seed(T)
     c = torch.randint(0, 255, (T, cols), generator=g, device="cuda").to(U8)
     s = torch.rand(-(-cols // 128), T, generator=g, device="cuda")
-    rows = T * k + 3
-    pos = torch.randperm(rows, generator=g, device="cuda")[: T * k].to(torch.int32).view(T, k)
-    co, so = torch.full((rows, cols), 77, dtype=U8, device="cuda"), torch.full((s.shape[0], rows), 77.0, device="cuda")
+    idx = torch.rand(T, E, generator=g, device="cuda").topk(k, 1).indices.to(torch.int32)
+    prob = torch.rand(T, k, generator=g, device="cuda")
+    flat = idx.flatten().long()
+    split = torch.bincount(flat, minlength=E).to(torch.int32)
+    order = torch.argsort(flat, stable=True)                 # rows by expert, tokens in order
+    pos = torch.empty_like(order)
+    pos[order] = torch.arange(T * k, device="cuda")
+    pad = torch.cumsum((split + 127) // 128 * 128, 0) - (split + 127) // 128 * 128
+    first = torch.cumsum(split, 0) - split
+    row_of = (pos + (pad - first)[flat]).to(torch.int32).view(T, k)
     ws = torch.zeros(256, dtype=U8, device="cuda")
-    B.moe_fp8_block_pack(c, s, pos, co, so, ws)
-    flat = pos.flatten().long()
-    ref_c, ref_s = torch.full_like(co, 77), torch.full_like(so, 77)
-    ref_c[flat] = c.repeat_interleave(k, 0)
-    ref_s[:, flat] = s.repeat_interleave(k, 1)
-    assert torch.equal(co, ref_c) and torch.equal(so, ref_s) and B.moe_get_device_error(ws) == (0, 0)
-    # a place that is none is recorded and skipped
-    pos[0, 0] = rows
-    co2, so2 = torch.full_like(co, 77), torch.full_like(so, 77)
-    B.moe_fp8_block_pack(c, s, pos, co2, so2, ws)
-    ref_c[flat[0]], ref_s[:, flat[0]] = 77, 77
-    assert torch.equal(co2, ref_c) and torch.equal(so2, ref_s) and B.moe_get_device_error(ws)[0] == 7
+
+    def run():
+        out = [torch.full((T * k, cols), 77, dtype=U8, device="cuda"), torch.full((s.shape[0], T * k), 77.0, device="cuda"),
+               torch.full((T * k,), 77.0, device="cuda"), torch.full((T, k), 77, dtype=torch.int32, device="cuda")]
+        B.moe_fp8_block_pack(c, s, idx, prob, row_of, split, *out, ws)
+        return out
+
+    co, so, pr, po = run()
+    assert B.moe_get_device_error(ws) == (0, 0) and torch.equal(po.flatten().long(), pos)
+    tok = order // k
+    assert torch.equal(co, c[tok]) and torch.equal(so, s[:, tok]) and torch.equal(pr, prob.flatten()[order])
+    # a row that is none of its expert's is recorded and skipped
+    lost = int(pos[0])
+    row_of[0, 0] += 1000000
+    co2, so2, pr2, po2 = run()
+    assert B.moe_get_device_error(ws)[0] == 7 and int(po2[0, 0]) == -1
+    keep = [i for i in range(T * k) if i != lost]
+    assert torch.equal(co2[keep], co[keep]) and torch.equal(so2[:, keep], so[:, keep]) and torch.equal(pr2[keep], pr[keep])
+    assert bool((co2[lost] == 77).all()) and float(pr2[lost]) == 77.0 and bool((so2[:, lost] == 77).all())
 
 
 def test_values_are_exact_products():
