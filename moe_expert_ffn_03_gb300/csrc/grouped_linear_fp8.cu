@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
       // stands between two blocks.
       uint32_t p0[32], p1[32];
       if (blocks > 0) {
-        wait_phase_warp_later(&empty[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR8 + 4, lim, ok);
+        wait_phase_warp_later(false, &empty[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR8 + 4, lim, ok);
         tc_fence_after();
         tmem_ld32_async(tmem_row + (cur.st & 1) * L8_N, p0);
       }
@@ -502,22 +502,21 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
         l8_add(acc + 32, p1, f2);
         tmem_wait_ld<32>(p0);
         tmem_ld32_async(src + 96, p1);
+        const int freed = cur.st;
+        cur.next();
+        const bool seen = mbar_look(&empty[cur.st], cur.ph);
         l8_add(acc + 64, p0, f2);
         tmem_wait_ld<32>(p1);
         tc_fence_before();
-        back(cur.st);
-        if (!__all_sync(0xFFFFFFFFu, ok)) {
-          ok = false;
-          break;
-        }
-        cur.next();
+        back(freed);
         if (left > 1) {
-          wait_phase_warp_later(&empty[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR8 + 4, lim, ok);
+          wait_phase_warp_later(seen, &empty[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR8 + 4, lim, ok);
           tc_fence_after();
           tmem_ld32_async(tmem_row + (cur.st & 1) * L8_N, p0);
         }
         l8_add(acc + 96, p1, f2);
       }
+      ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       const int rows = min(m_left, 32), columns = n_left;
       __nv_bfloat16* const o = out;

@@ -247,15 +247,25 @@ __device__ __forceinline__ bool wait_phase_warp_inline(uint64_t* bar, uint32_t p
   return __all_sync(0xFFFFFFFFu, wait_phase_inline(bar, parity, abort_flag, err, site, limit_ns));
 }
 
-// The same for a wait that other warps wait for in turn: lanes whose wait gave up clear their `ok` and go on with the
-// others, so that the warp stays together without a vote here; it has to vote on `ok` (__all_sync) before
-// long, and what it computes in between must be harmless.
-__device__ __forceinline__ void wait_phase_warp_later(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
-                                                      int site, uint64_t limit_ns, bool& ok) {
-  if (!mbar_try_wait(bar, parity)) {
-    if (!wait_phase_inline(bar, parity, abort_flag, err, site, limit_ns)) ok = false;
-  }
+// The same where the warp has looked at the phase before (`seen`): lanes whose wait gives up clear their `ok` and go on
+// with the others, so that the warp stays together without a vote here; it has to vote on `ok` (__all_sync)
+// in the end, and what it computes in between must be harmless.
+__device__ __forceinline__ void wait_phase_warp_later(bool seen, uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                      int* err, int site, uint64_t limit_ns, bool& ok) {
+  if (!seen && !wait_phase_inline(bar, parity, abort_flag, err, site, limit_ns)) ok = false;
   __syncwarp();
+}
+// Whether a phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_look(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
