@@ -16,17 +16,28 @@
 // columns of tensor memory, a thread's row has one scale and its 128 columns (aligned to a block of the B
 // side) another, so a partial sum takes one multiply-add with one factor per thread.  (A scale per
 // column would have to come out of shared memory, 32 bits for every multiply-add.)  256 x 256 x 128 takes
-// the pair's tensor pipes 512 clocks, its epilogue warps 256 of packed multiply-adds and 64 of reads.
+// the pair's tensor pipes 512 clocks, an SM's quarter 256 of packed multiply-adds and 136 of reads.
 //
 // Persistent CTA pairs (clusters of two, one CTA per SM), tiles of 256 m x 256 n with cta_group::2: each
-// CTA stages its 128 m and its 128 n of a block, 32 KB a stage, six stages.  The 512 columns of tensor
+// CTA stages its 128 m and its 128 n of a block, 32 KB a stage, four stages.  The 512 columns of tensor
 // memory are two buffers of 256: the tensor pipe fills one with a block's sums while the other is added.
 //   warp 0       TMA producer of the A side, warp 2 of the B side
 //   warp 1       tensor memory; in the leader, the MMAs
-//   warp 3       the experts' prefix sums
-//   warps 4..11  sums: four per lane quarter, 128 columns each, with 224 registers a thread (the other
+//   warp 3       the experts' prefix sums, then the tiles, laid out ahead for the others
+//   warps 4..11  sums: four per lane quarter, 128 columns each, with 232 registers a thread (the other
 //                four warps give up theirs: 128 x 40 + 256 x 232 = 384 x 168)
 // Waits are bounded as everywhere; each lasts as long as a block or a tile's output at most.
+//
+// What holds the tensor pipe up is the way round of a buffer: sums there, seen, read, added, handed back, seen,
+// filled again, with single threads and two warps a quarter on it.  So a block has one wait and one commit
+// for the MMA's thread, constant descriptors, scales asked for two blocks ahead (one ahead, 8192 rows,
+// 4096 -> 16384: 490 us, two: 414; from a ring in shared memory 412, but 32768 rows 5% longer), the next
+// barrier looked at before the last additions; measured the same or worse: sixteen warps of 64 columns (494),
+// halves of 128 columns with four buffers (558; an MMA of 128 columns takes 104 clocks, not 64), single CTAs of
+// 128 x 256 (490), a second thread that issues (478).  Measured, on its own: 32768 rows, 4096 -> 28672, E = 8,
+// forward 2.89 ms (2.66 PFLOP/s), under the power limit of calls in a row 3.2 ms; 8192 rows, 4096 -> 16384,
+// E = 2: 414 us (2.65); 65536 rows, 2048 -> 2816, E = 16: 350 us forward (2.16: a tile's output takes a quarter of
+// its time there), 315 weight gradient (2.40).
 #include <atomic>
 #include <cstdio>
 #include <type_traits>
@@ -67,11 +78,7 @@ constexpr int L8_TILES = 4;                      // tiles laid out ahead
 constexpr int L8_BARS = 2 * L8_STAGES + 1 + 2 * L8_TILES;        // full, empty, drain, laid, taken
 constexpr int L8_OFF_MISC = L8_OFF_BAR + L8_BARS * 8;
 constexpr int L8_OFF_SEG = (L8_OFF_MISC + 16 + 15) & ~15;        // row0[E+1], tile0[E+1], order[E]
-// the scales' rings: [L8_AHEAD][warps][32] of {A side, B side}
-constexpr int L8_AHEAD = 4;                      // blocks whose scales are on their way
-constexpr int L8_SCALE_SLOT = L8_EPI_WARPS * 32 * 2;
-constexpr int L8_OFF_SCALE = (L8_OFF_SEG + 3 * (L8_MAX_E + 1) * 4 + 15) & ~15;
-constexpr int L8_OFF_TILES = L8_OFF_SCALE + L8_AHEAD * L8_SCALE_SLOT * 4;
+constexpr int L8_OFF_TILES = (L8_OFF_SEG + 3 * (L8_MAX_E + 1) * 4 + 15) & ~15;
 constexpr int L8_SMEM = L8_OFF_TILES + L8_TILES * int(sizeof(Tile8)) + 1024;
 static_assert(L8_SMEM <= 232448, "shared memory budget");
 
@@ -422,22 +429,17 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
     const int cols = l8_cols<MODE>(args);
     const int64_t sa_step = MODE == LIN_WGRAD ? args.N : args.rows;
     const int64_t kbs = (args.K + 127) / 128, sb_step = MODE == LIN_FWD ? 1 : kbs, sb_half = MODE == LIN_FWD ? kbs : 1;
-    // A lane's own ring of its scales (its m's, its warp's columns'), L8_AHEAD blocks on their way: what a
-    // lane copies it alone reads, so a wait for its own copies is enough.
-    float* const mine = reinterpret_cast<float*>(smem + L8_OFF_SCALE) + ((warp - 4) * 32 + lane) * 2;
-    int slot = 0;
-    const float *sa = nullptr, *sb = nullptr;    // the next block's
+    const float *sa = nullptr, *sb = nullptr;    // scales of the next block's: the lane's m, the warp's columns
+    float fa0 = 0.f, fb0 = 0.f, fa1 = 0.f, fb1 = 0.f;        // asked for two blocks ahead, by turns
     int coming = 0;                              // blocks of the tile not yet asked for
-    const auto ask = [&]() {
+    const auto ask = [&](float& fa, float& fb) {
       if (coming > 0) {
-        cp_async4(mine + slot * L8_SCALE_SLOT, sa);
-        cp_async4(mine + slot * L8_SCALE_SLOT + 1, sb);
+        fa = __ldg(sa);
+        fb = __ldg(sb);
         sa += sa_step;
         sb += sb_step;
         --coming;
       }
-      cp_async_group();
-      slot = slot + 1 == L8_AHEAD ? 0 : slot + 1;
     };
     Ring cur;                                    // a block's sums are there when its stage is free
     bool ok = true, live = false, end = false;
@@ -462,8 +464,8 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
       end = blocks < 0;
       live = m_left > 0 && n_left > 0 && !end;
       coming = live ? blocks : 0;
-#pragma unroll
-      for (int i = 0; i < L8_AHEAD; ++i) ask();
+      ask(fa0, fb0);
+      ask(fa1, fb1);
     };
     take();
     while (ok && !end) {
@@ -488,14 +490,13 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
         tc_fence_after();
         tmem_ld32_async(tmem_row + (cur.st & 1) * L8_N, p0);
       }
-      for (int left = blocks; left > 0; --left) {
+      const auto block = [&](int left, float& fa, float& fb) {
         const uint32_t src = tmem_row + (cur.st & 1) * L8_N;
-        cp_async_left<L8_AHEAD - 1>();
-        const float2 s2 = *reinterpret_cast<const float2*>(mine + slot * L8_SCALE_SLOT);
-        const float2 f2 = make_float2(s2.x * s2.y, s2.x * s2.y);
+        const float f = fa * fb;
+        const float2 f2 = make_float2(f, f);
         tmem_wait_ld<32>(p0);
         tmem_ld32_async(src + 32, p1);
-        ask();                                   // into the same place: what was there has been read
+        ask(fa, fb);
         l8_add(acc, p0, f2);
         tmem_wait_ld<32>(p1);
         tmem_ld32_async(src + 64, p0);
@@ -515,6 +516,11 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
           tmem_ld32_async(tmem_row + (cur.st & 1) * L8_N, p0);
         }
         l8_add(acc + 96, p1, f2);
+      };
+      for (int left = blocks; left > 0; left -= 2) {
+        block(left, fa0, fb0);
+        if (left == 1) break;
+        block(left - 1, fa1, fb1);
       }
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
@@ -543,7 +549,6 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
         }
       }
     }
-    cp_async_left<0>();
   }
   tc_fence_before();
   __syncthreads();
