@@ -60,19 +60,23 @@ __device__ __forceinline__ void put_codes(uint8_t* p, const uint32_t* q, int lef
   }
 }
 
-// The largest magnitudes of a thread's eight columns over its rows (float bits): of bf16 two columns at a time, on
-// the bits of their magnitudes, which order like them with NaN and Inf above all others.
+// The largest magnitudes (float bits) of a thread's rows over its eight columns, and of its columns over its rows.
+// Of bf16 two values at a time, on the bits of their magnitudes, which order like them with NaN and Inf above
+// all others.
 template <typename T, bool WIDE>
-__device__ __forceinline__ void column_max(const Eight<T, WIDE>* raw, uint32_t* cmax) {
+__device__ __forceinline__ void maxima(const Eight<T, WIDE>* raw, uint32_t* rmax, uint32_t* cmax) {
   if constexpr (WIDE && sizeof(T) == 2) {
     uint32_t m[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < Q_ROWS; ++i) {
       const uint4 q = raw[i].r[0].q;
-      m[0] = __vmaxu2(m[0], q.x & 0x7FFF7FFFu);
-      m[1] = __vmaxu2(m[1], q.y & 0x7FFF7FFFu);
-      m[2] = __vmaxu2(m[2], q.z & 0x7FFF7FFFu);
-      m[3] = __vmaxu2(m[3], q.w & 0x7FFF7FFFu);
+      const uint32_t a = q.x & 0x7FFF7FFFu, b = q.y & 0x7FFF7FFFu, c = q.z & 0x7FFF7FFFu, d = q.w & 0x7FFF7FFFu;
+      m[0] = __vmaxu2(m[0], a);
+      m[1] = __vmaxu2(m[1], b);
+      m[2] = __vmaxu2(m[2], c);
+      m[3] = __vmaxu2(m[3], d);
+      const uint32_t r = __vmaxu2(__vmaxu2(a, b), __vmaxu2(c, d));
+      rmax[i] = max(r << 16, r & 0xFFFF0000u);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -86,8 +90,13 @@ __device__ __forceinline__ void column_max(const Eight<T, WIDE>* raw, uint32_t* 
     for (int i = 0; i < Q_ROWS; ++i) {
       float v[8];
       raw[i].get(v);
+      rmax[i] = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) cmax[j] = max(cmax[j], abs_bits(v[j]));
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t a = abs_bits(v[j]);
+        cmax[j] = max(cmax[j], a);
+        rmax[i] = max(rmax[i], a);
+      }
     }
   }
 }
@@ -98,8 +107,7 @@ __device__ __forceinline__ void column_max(const Eight<T, WIDE>* raw, uint32_t* 
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(Q_THREADS, WIDE && sizeof(T) == 2 ? 3 : 2) block8_quantize_kernel(const __grid_constant__ Block8Args a) {
   __shared__ uint32_t colmax[Q_THREADS / 32][B8];
-  __shared__ float colup[B8];
-  __shared__ uint32_t colbad[B8];
+  __shared__ __align__(16) float colup[B8];
   __shared__ int row0[Q_MAX_E + 1], blk0[Q_MAX_E + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int sub = tid >> 4;                      // rows sub, sub + 16, ... of a tile
@@ -202,18 +210,9 @@ __global__ void __launch_bounds__(Q_THREADS, WIDE && sizeof(T) == 2 ? 3 : 2) blo
 #pragma unroll
       for (int i = 0; i < Q_ROWS; ++i) raw[i].load(p + i * 16 * a.ld, sub + 16 * i < cnt ? left : 0);
     }
-    uint32_t cmax[8];
-    if (a.tcodes != nullptr) {
-      column_max<T, WIDE>(raw, cmax);
-    }
+    uint32_t rmax[Q_ROWS], cmax[8];
+    maxima<T, WIDE>(raw, rmax, cmax);
     if (a.codes != nullptr) {
-      uint32_t rmax[Q_ROWS];
-#pragma unroll
-      for (int i = 0; i < Q_ROWS; ++i) {
-        float v[8];
-        raw[i].get(v);
-        rmax[i] = v_amax<8>(v);
-      }
 #pragma unroll
       for (int off = 1; off < 16; off *= 2)
 #pragma unroll
@@ -231,12 +230,13 @@ __global__ void __launch_bounds__(Q_THREADS, WIDE && sizeof(T) == 2 ? 3 : 2) blo
         const float up = __shfl_sync(0xFFFFFFFFu, my_up, (lane & 16) | i);
         float v[8];
         raw[i].get(v);
-        const Block8 b(up, rmax[i] >= 0x7F800000u);
+        const Block8 b(up);
         const uint32_t q[2] = {b.codes4(v), b.codes4(v + 4)};
         if (sub + 16 * i < cnt) put_codes<WIDE>(out + int64_t(i) * 16 * a.cols, q, left);
       }
     }
     if (a.tcodes == nullptr) continue;
+    float ups[8];                                // the columns' factors
     if (a.tiles) {
       uint32_t amax = 0;
 #pragma unroll
@@ -249,16 +249,9 @@ __global__ void __launch_bounds__(Q_THREADS, WIDE && sizeof(T) == 2 ? 3 : 2) blo
 #pragma unroll
       for (int w = 0; w < Q_THREADS / 32; ++w) amax = max(amax, colmax[w][0]);
       if (tid == 0) a.tscales[blk * cb + c0 / B8] = Block8::scale(amax);
-      const Block8 b(amax);
+      const float up = Block8(amax).up;
 #pragma unroll
-      for (int i = 0; i < Q_ROWS; ++i) {
-        const int r = sub + 16 * i;
-        float v[8];
-        raw[i].get(v);
-        // rows past the expert's last are zeros on its last block; a matrix has none
-        const uint32_t q[2] = {r < cnt ? b.codes4(v) : 0u, r < cnt ? b.codes4(v + 4) : 0u};
-        if (r < cnt || a.mat_rows == 0) put_codes<WIDE>(a.tcodes + (trow + r) * a.cols + c0 + c8, q, left);
-      }
+      for (int j = 0; j < 8; ++j) ups[j] = up;
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) cmax[j] = max(cmax[j], __shfl_xor_sync(0xFFFFFFFFu, cmax[j], 16));
@@ -272,32 +265,27 @@ __global__ void __launch_bounds__(Q_THREADS, WIDE && sizeof(T) == 2 ? 3 : 2) blo
         uint32_t amax = 0;
 #pragma unroll
         for (int w = 0; w < Q_THREADS / 32; ++w) amax = max(amax, colmax[w][tid]);
-        const Block8 b(amax);
-        colup[tid] = b.up;
-        colbad[tid] = b.bad;
+        colup[tid] = Block8(amax).up;
         if (c0 + tid < a.cols) a.tscales[blk * a.cols + c0 + tid] = Block8::scale(amax);
       }
       __syncthreads();
-      float up[8];
-      uint32_t nan[2] = {0, 0};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        up[j] = colup[c8 + j];
-        if (colbad[c8 + j]) nan[j >> 2] |= 0xFFu << (8 * (j & 3));
-      }
+      for (int j = 0; j < 8; j += 4) *reinterpret_cast<float4*>(ups + j) = *reinterpret_cast<const float4*>(colup + c8 + j);
+    }
+    // rows past the expert's last are zeros on its last block; a matrix has none
+    const int out_rows = a.mat_rows > 0 ? cnt : B8;
+    uint8_t* out = a.tcodes + (trow + sub) * a.cols + c0 + c8;
 #pragma unroll
-      for (int i = 0; i < Q_ROWS; ++i) {
-        float v[8];
-        raw[i].get(v);
-        uint32_t q[2];
+    for (int i = 0; i < Q_ROWS; ++i) {
+      float v[8];
+      raw[i].get(v);
+      uint32_t q[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          q[k] = cvt_e4m3x2(v[4 * k] * up[4 * k], v[4 * k + 1] * up[4 * k + 1]) |
-                 (cvt_e4m3x2(v[4 * k + 2] * up[4 * k + 2], v[4 * k + 3] * up[4 * k + 3]) << 16);
-          q[k] = sub + 16 * i < cnt ? (q[k] & ~nan[k]) | (0x7F7F7F7Fu & nan[k]) : 0u;
-        }
-        put_codes<WIDE>(a.tcodes + (trow + sub + 16 * i) * a.cols + c0 + c8, q, left);
-      }
+      for (int k = 0; k < 2; ++k)
+        q[k] = cvt_e4m3x2(v[4 * k] * ups[4 * k], v[4 * k + 1] * ups[4 * k + 1]) |
+               (cvt_e4m3x2(v[4 * k + 2] * ups[4 * k + 2], v[4 * k + 3] * ups[4 * k + 3]) << 16);
+      if (cnt < B8 && sub + 16 * i >= cnt) q[0] = q[1] = 0;      // (0 times a NaN factor is none)
+      if (sub + 16 * i < out_rows) put_codes<WIDE>(out + int64_t(i) * 16 * a.cols, q, left);
     }
   }
 }
