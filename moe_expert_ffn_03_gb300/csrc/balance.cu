@@ -289,7 +289,7 @@ cudaError_t balance_run(const BalanceArgs& a, bool backward, cudaStream_t st) {
     const int64_t most = int64_t(sms) * 4;
     return launch_pdl(balance_bwd_kernel<G, V, WIDE>, dim3(unsigned(need < most ? need : most)), dim3(BAL_THREADS), 0, st, a);
   }
-  int64_t most = sms < kBalanceMaxParts ? sms : kBalanceMaxParts;
+  const int64_t most = 2 * sms < kBalanceMaxParts ? 2 * sms : kBalanceMaxParts;     // two blocks an SM
   const size_t smem = size_t(2 * BAL_WARPS + 1) * (a.E + 1) * 4;             // at most 34 KB
   return launch_pdl(balance_fwd_kernel<G, V, WIDE>, dim3(unsigned(need < most ? need : most)), dim3(BAL_THREADS), smem, st, a);
 }
