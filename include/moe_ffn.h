@@ -713,8 +713,8 @@ moe_status moe_grouped_linear_wgrad(const moe_grouped* g, const void* x, int64_t
  *   codes,scales  both set or both NULL: out y in 8 bits, made before y is rounded ("rows" below): codes
  *                 [rows][H], scales f32 [ceil(H/128)][rows]
  * Types and sizes are those of moe_norm.  Finite rows have the norm of its definition also where float32
- * cannot hold their squares' sum; what passes the output's range there is Inf.  A row with a NaN or an Inf
- * gives NaN.  h and y must not overlap x and residual, except that h may be x or residual itself when
+ * cannot hold their squares' sum; what passes the output's range there is Inf.  A row with a NaN gives NaN;
+ * one with an Inf gives NaN there and 0 elsewhere (rstd is 0), as the formula does.  h and y must not overlap x and residual, except that h may be x or residual itself when
  * ld_in = ld_out (a bf16 row whose mean square float32 cannot hold, or only just, is then normalised as
  * stored in h).
  */

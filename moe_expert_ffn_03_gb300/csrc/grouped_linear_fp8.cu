@@ -614,10 +614,13 @@ cudaError_t launch_grouped_linear_fp8(int mode, const Linear8Args& args, const u
   const int64_t mt = mode == LIN_WGRAD ? int64_t(a.E) * ((a.N + L8_M - 1) / L8_M)
                                        : (a.rows < a.E ? a.rows : a.E) + a.rows / L8_M;
   const int64_t tiles = nt * mt;                 // no fewer than there are
-  // Few rows, and so few tiles that half the pairs would have none: the kernel for few rows.  (16 rows,
-  // 4096 -> 28672, six of eight experts: 128 us there, 155 here; one row, 14336 -> 4096: 26 and 55; but 64 rows,
-  // 4096 -> 28672: 61 and 46.)
-  if (mode != LIN_WGRAD && (a.rows <= int64_t(16) * a.E || (a.rows <= int64_t(64) * a.E && 2 * tiles <= pairs)))
+  // The kernel for few rows: up to 16 an expert, and up to 64 where half the pairs would have no tile of a long
+  // contraction.  (Both measured, that one first.  16 rows, 4096 -> 28672, six of eight experts: 128 and 155 us;
+  // 32 rows, 2048 -> 1024, E = 8: 9.1 and 11.1, 128 rows 10.4 and 11.2, 256 rows 12.5 and 11.3; one row,
+  // 14336 -> 4096: 26 and 55, 48 rows 40 and 55; but 64 rows, 4096 -> 4096: 22 and 18.)
+  const int64_t blocks = ((mode == LIN_FWD ? a.K : a.N) + L8_KT - 1) / L8_KT;
+  if (mode != LIN_WGRAD && (a.rows <= int64_t(16) * a.E ||
+                            (a.rows <= int64_t(64) * a.E && 2 * tiles <= pairs && blocks >= 64)))
     return launch_grouped_linear_fp8_few(mode, a, a_codes, b_codes, sms, st, msg, msg_len);
   CUtensorMap ma, mas, mb;
   bool ok;
