@@ -55,8 +55,7 @@ struct alignas(16) Tile8 {
   int c0;          // contraction: first index (wgrad: row of the layout on blocks)
   int blocks;      // its blocks of 128; -1 behind the last tile
   int last;        // indices in the last block
-  int64_t sa, sb;  // offsets of the scales of m0 and n0 of the first block
-  int64_t out;     // of the output's element (m0, n0)
+  const float *sa, *sb[2];  // scales of the first block: m0's, and those of n0 and n0 + 128
   int64_t unused;
 };
 
@@ -71,9 +70,10 @@ static_assert(128 * L8_REGS_FEW + 32 * L8_EPI_WARPS * L8_REGS_MANY == L8_THREADS
 constexpr int L8_GROUP = 8;                      // row tiles that share the sweep over the weights
 constexpr int L8_SMALL = 32;                     // rows of the small box of rows
 
-constexpr int L8_BOX = 32 * 256;                 // a warp's output on its way: 32 rows of 128 bf16
+// a warp's output on its way: two boxes of 32 rows of 64 bf16, swizzled in 128 bytes
+constexpr int L8_BOX = 32 * 128;
 constexpr int L8_OFF_OUT = L8_STAGES * L8_STAGE;
-constexpr int L8_OFF_BAR = L8_OFF_OUT + L8_EPI_WARPS * L8_BOX;
+constexpr int L8_OFF_BAR = L8_OFF_OUT + L8_EPI_WARPS * 2 * L8_BOX;
 constexpr int L8_TILES = 4;                      // tiles laid out ahead
 constexpr int L8_BARS = 2 * L8_STAGES + 1 + 2 * L8_TILES;        // full, empty, drain, laid, taken
 constexpr int L8_OFF_MISC = L8_OFF_BAR + L8_BARS * 8;
@@ -170,9 +170,9 @@ __device__ __forceinline__ void l8_decode(const Linear8Args& a, const int* row0,
   tl.n0 = tn * L8_N;
   tl.n = (min(L8_N, cols - tl.n0) + 31) & ~31;
   const int64_t kbs = (a.K + 127) / 128, nbs = (a.N + 127) / 128, nb = tl.n0 / 128, blk = tl.c0 / L8_KT;
-  tl.sa = (MODE == LIN_WGRAD ? blk * a.N : 0) + tl.m0;
-  tl.sb = MODE == LIN_FWD ? (tl.e * nbs + nb) * kbs : (MODE == LIN_DGRAD ? tl.e * nbs : blk) * kbs + nb;
-  tl.out = ((MODE == LIN_WGRAD ? int64_t(tl.e) * a.N : 0) + tl.m0) * a.ldo + tl.n0;
+  tl.sa = a.sa + (MODE == LIN_WGRAD ? blk * a.N : 0) + tl.m0;
+  tl.sb[0] = a.sb + (MODE == LIN_FWD ? (tl.e * nbs + nb) * kbs : (MODE == LIN_DGRAD ? tl.e * nbs : blk) * kbs + nb);
+  tl.sb[1] = tl.sb[0] + (MODE == LIN_FWD ? kbs : 1);
 }
 
 // The pair's tile after t.  wgrad: there and back, since tiles come longest first: the pair that got the
@@ -220,10 +220,22 @@ __device__ __forceinline__ void l8_hand_back(uint32_t caddr, int lane) {
       : "memory");
 }
 
+// A box of the output from shared memory; what is past the output's end is left out.
+template <int MODE>
+__device__ __forceinline__ void l8_store(const CUtensorMap* map, const void* src, int n, int m, int e) {
+  if constexpr (MODE == LIN_WGRAD)
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(n), "r"(m), "r"(e) : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(n), "r"(m) : "memory");
+}
+
 template <int MODE>
 __global__ void __launch_bounds__(L8_THREADS, 1)
     grouped_linear_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmAs,
-                              const __grid_constant__ CUtensorMap tmB, const Linear8Args args) {
+                              const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmO,
+                              const Linear8Args args) {
   constexpr bool A_MN = MODE == LIN_WGRAD, B_MN = MODE != LIN_FWD;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -260,6 +272,7 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmAs);
     prefetch_tmap(&tmB);
+    prefetch_tmap(&tmO);
   }
   if (warp == 1) {
     tmem_alloc(tmem_base_s, 512);                // collectively with the peer CTA
@@ -428,7 +441,7 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
     l8_hand_back(full_c0 + 8u, lane);
     const int cols = l8_cols<MODE>(args);
     const int64_t sa_step = MODE == LIN_WGRAD ? args.N : args.rows;
-    const int64_t kbs = (args.K + 127) / 128, sb_step = MODE == LIN_FWD ? 1 : kbs, sb_half = MODE == LIN_FWD ? kbs : 1;
+    const int64_t kbs = (args.K + 127) / 128, sb_step = MODE == LIN_FWD ? 1 : kbs;
     const float *sa = nullptr, *sb = nullptr;    // scales of the next block's: the lane's m, the warp's columns
     float fa0 = 0.f, fb0 = 0.f, fa1 = 0.f, fb1 = 0.f;        // asked for two blocks ahead, by turns
     int coming = 0;                              // blocks of the tile not yet asked for
@@ -445,24 +458,24 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
     bool ok = true, live = false, end = false;
     Tiles8 tiles(tile_ring, laid, taken);
     const int at = int(rank) * 128 + q * 32;     // this warp's first of a tile's m
-    int blocks = 0, m_left = 0, n_left = 0;      // of the tile: blocks; m and n from the warp's first on
-    __nv_bfloat16* out = nullptr;                // the warp's first row and n
+    int blocks = 0, e = 0, m = 0, n = 0, m_left = 0;         // the tile's, m and n from the warp's first on
     // takes the next tile up, and asks for its first blocks' scales
     const auto take = [&]() {
       ok = wait_phase_warp_inline(&laid[tiles.slot], tiles.ph, abort_s, args.err, SITE_LINEAR8 + 6, lim);
       if (!ok) return;
       const Tile8* tl = &tile_ring[tiles.slot];
       blocks = tl->blocks;
+      if (MODE == LIN_WGRAD) e = tl->e;
+      m = tl->m0 + at;
+      n = tl->n0 + col0;
       m_left = tl->cnt - at;
-      n_left = cols - tl->n0 - col0;
-      sa = args.sa + tl->sa + min(at + lane, tl->cnt - 1);
-      sb = args.sb + tl->sb + (col0 != 0 ? sb_half : 0);
-      out = args.out + tl->out + at * args.ldo + col0;
+      sa = tl->sa + min(at + lane, tl->cnt - 1);
+      sb = tl->sb[col0 >> 7];
       __syncwarp();
       if (lane == 0) mbar_arrive(&taken[tiles.slot]);
       tiles.advance();
       end = blocks < 0;
-      live = m_left > 0 && n_left > 0 && !end;
+      live = m_left > 0 && n < cols && !end;
       coming = live ? blocks : 0;
       ask(fa0, fb0);
       ask(fa1, fb1);
@@ -481,41 +494,41 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-      // Columns come 32 at a time, the next 32 on their way while these are added; the last ones of a block are
-      // added after the next block's first have been asked for, so that neither a wait nor a load's latency
-      // stands between two blocks.
+      // A block's columns come 64 at a time, and its buffer is handed back before the last 64 are added: the time
+      // from the sums' arrival to that is on the buffer's way round, what comes after is not.  (32 at a time, the
+      // last 32 added behind the next block's first load: 8192 rows, 4096 -> 16384, 416 us; this 404.)
       uint32_t p0[32], p1[32];
       if (blocks > 0) {
         wait_phase_warp_later(false, &empty[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR8 + 4, lim, ok);
         tc_fence_after();
         tmem_ld32_async(tmem_row + (cur.st & 1) * L8_N, p0);
+        tmem_ld32_async(tmem_row + (cur.st & 1) * L8_N + 32, p1);
       }
       const auto block = [&](int left, float& fa, float& fb) {
         const uint32_t src = tmem_row + (cur.st & 1) * L8_N;
         const float f = fa * fb;
         const float2 f2 = make_float2(f, f);
         tmem_wait_ld<32>(p0);
-        tmem_ld32_async(src + 32, p1);
-        ask(fa, fb);
-        l8_add(acc, p0, f2);
         tmem_wait_ld<32>(p1);
+        l8_add(acc, p0, f2);
         tmem_ld32_async(src + 64, p0);
         l8_add(acc + 32, p1, f2);
-        tmem_wait_ld<32>(p0);
         tmem_ld32_async(src + 96, p1);
+        ask(fa, fb);
         const int freed = cur.st;
         cur.next();
-        const bool seen = mbar_look(&empty[cur.st], cur.ph);
-        l8_add(acc + 64, p0, f2);
+        tmem_wait_ld<32>(p0);
         tmem_wait_ld<32>(p1);
         tc_fence_before();
         back(freed);
+        l8_add(acc + 64, p0, f2);
+        l8_add(acc + 96, p1, f2);
         if (left > 1) {
-          wait_phase_warp_later(seen, &empty[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR8 + 4, lim, ok);
+          wait_phase_warp_later(false, &empty[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR8 + 4, lim, ok);
           tc_fence_after();
           tmem_ld32_async(tmem_row + (cur.st & 1) * L8_N, p0);
+          tmem_ld32_async(tmem_row + (cur.st & 1) * L8_N + 32, p1);
         }
-        l8_add(acc + 96, p1, f2);
       };
       for (int left = blocks; left > 0; left -= 2) {
         block(left, fa0, fb0);
@@ -524,31 +537,43 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
       }
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
-      const int rows = min(m_left, 32), columns = n_left;
-      __nv_bfloat16* const o = out;
-      take();                                    // its first scales are on their way while this tile goes out
-      // Through the warp's own shared memory, so that 16 lanes store a row's 256 bytes.  (32 bytes a lane to 32
-      // rows took 5000 clocks a tile, a third of a tile of 2048; TMA stores 2000, most of it the wait for the
-      // last ones and the fence before them.)
-      uint8_t* const box = smem + L8_OFF_OUT + (warp - 4) * L8_BOX;
-      __syncwarp();                              // the last tile's has been read
+      const int rows = min(m_left, 32), columns = cols - n, e_out = e, m_out = m, n_out = n;
+      // Through the warp's own shared memory and TMA: meanwhile the tensor pipe fills the two buffers and stops, so
+      // what counts is the warps' own time.  (2000 clocks a tile of it: taking the next tile up 600, these stores
+      // 650, the fence 350, two boxes 420; rows read back and stored by 16 lanes each 3300, 32 bytes a lane to 32
+      // rows 5000, a bulk copy a row 3300.  65536 rows, 2048 -> 2816: 316 and 334 us.)
+      uint8_t* const box = smem + L8_OFF_OUT + (warp - 4) * 2 * L8_BOX;
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");      // the last tile's has been read
+      __syncwarp();
 #pragma unroll
       for (int c = 0; c < 128; c += 8)
-        *reinterpret_cast<uint4*>(box + lane * 256 + (((c >> 3) ^ (lane & 7)) << 4)) =
+        *reinterpret_cast<uint4*>(box + (c >> 6) * L8_BOX + lane * 128 + ((((c >> 3) & 7) ^ (lane & 7)) << 4)) =
             make_uint4(pack_bf16x2(acc[c], acc[c + 1]), pack_bf16x2(acc[c + 2], acc[c + 3]),
                        pack_bf16x2(acc[c + 4], acc[c + 5]), pack_bf16x2(acc[c + 6], acc[c + 7]));
+      take();                                    // while those land; its first scales are on their way
+      if (MODE == LIN_WGRAD || rows == 32) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          l8_store<MODE>(&tmO, box, n_out, m_out, e_out);
+          if (columns > 64) l8_store<MODE>(&tmO, box + L8_BOX, n_out + 64, m_out, e_out);
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+        continue;
+      }
+      // the last rows of an expert (behind them are the next one's): 16 lanes store a row's 256 bytes
       __syncwarp();
       const int chunk = lane & 15;
       if (chunk * 8 < columns) {                 // columns come in multiples of 16
-        __nv_bfloat16* to = o + chunk * 8;
-#pragma unroll
-        for (int r0 = 0; r0 < 32; r0 += 2) {
-          const int r = r0 + (lane >> 4);
-          const uint4 w = *reinterpret_cast<const uint4*>(box + r * 256 + ((chunk ^ (r & 7)) << 4));
-          if (r < rows) *reinterpret_cast<uint4*>(to + r * args.ldo) = w;
-        }
+        const uint8_t* from = box + (chunk >> 3) * L8_BOX;
+        __nv_bfloat16* to = args.out + m_out * args.ldo + n_out + chunk * 8;
+#pragma unroll 4
+        for (int r = lane >> 4; r < rows; r += 2)
+          *reinterpret_cast<uint4*>(to + r * args.ldo) =
+              *reinterpret_cast<const uint4*>(from + r * 128 + (((chunk & 7) ^ (r & 7)) << 4));
       }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
@@ -564,9 +589,21 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
+// bf16 map of the output [batch][rows][inner] (batch 0: no such dimension) at pitch ld, boxes of 64 x 32.
+bool l8_out_map(CUtensorMap* m, void* base, int64_t inner, int64_t rows, int64_t ld, int64_t batch) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[3] = {cuuint64_t(inner), cuuint64_t(rows), cuuint64_t(batch)};
+  cuuint64_t strides[2] = {cuuint64_t(ld) * 2, cuuint64_t(ld) * cuuint64_t(rows) * 2};
+  cuuint32_t box[3] = {64, 32, 1}, estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, batch > 0 ? 3 : 2, base, dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int MODE>
-cudaError_t l8_launch(const CUtensorMap& ma, const CUtensorMap& mas, const CUtensorMap& mb, const Linear8Args& a, int grid,
-                      cudaStream_t st) {
+cudaError_t l8_launch(const CUtensorMap& ma, const CUtensorMap& mas, const CUtensorMap& mb, const CUtensorMap& mo,
+                      const Linear8Args& a, int grid, cudaStream_t st) {
   // attributes are per device: set and checked once on each device this process uses
   constexpr int kMaxDevices = 64;
   static std::atomic<bool> ready[kMaxDevices];
@@ -597,7 +634,7 @@ cudaError_t l8_launch(const CUtensorMap& ma, const CUtensorMap& mas, const CUten
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, grouped_linear_fp8_kernel<MODE>, ma, mas, mb, a);
+  return cudaLaunchKernelEx(&cfg, grouped_linear_fp8_kernel<MODE>, ma, mas, mb, mo, a);
 }
 
 }  // namespace
@@ -622,7 +659,7 @@ cudaError_t launch_grouped_linear_fp8(int mode, const Linear8Args& args, const u
   if (mode != LIN_WGRAD && (a.rows <= int64_t(16) * a.E ||
                             (a.rows <= int64_t(64) * a.E && 2 * tiles <= pairs && blocks >= 64)))
     return launch_grouped_linear_fp8_few(mode, a, a_codes, b_codes, sms, st, msg, msg_len);
-  CUtensorMap ma, mas, mb;
+  CUtensorMap ma, mas, mb, mo;
   bool ok;
   if (mode == LIN_WGRAD) {
     const int64_t rows = (a.rows / L8_KT + a.E) * L8_KT;             // of the layout on blocks
@@ -633,6 +670,8 @@ cudaError_t launch_grouped_linear_fp8(int mode, const Linear8Args& args, const u
     ok = l8_map(&ma, a_codes, inner, a.rows, 0, 128) && l8_map(&mas, a_codes, inner, a.rows, 0, L8_SMALL) &&
          l8_map(&mb, b_codes, a.K, a.N, a.E, 128);
   }
+  ok = ok && (mode == LIN_WGRAD ? l8_out_map(&mo, a.out, a.K, a.N, a.ldo, a.E)
+                                : l8_out_map(&mo, a.out, mode == LIN_FWD ? a.N : a.K, a.rows, a.ldo, 0));
   if (!ok) {
     snprintf(msg, msg_len, "cuTensorMapEncodeTiled failed (rows %lld, K %d, N %d, E %d)", (long long)a.rows, a.K, a.N,
              a.E);
@@ -640,9 +679,9 @@ cudaError_t launch_grouped_linear_fp8(int mode, const Linear8Args& args, const u
   }
   const int grid = 2 * int(tiles < pairs ? tiles : pairs);
   switch (mode) {
-    case LIN_FWD: return l8_launch<LIN_FWD>(ma, mas, mb, a, grid, st);
-    case LIN_DGRAD: return l8_launch<LIN_DGRAD>(ma, mas, mb, a, grid, st);
-    default: return l8_launch<LIN_WGRAD>(ma, mas, mb, a, grid, st);
+    case LIN_FWD: return l8_launch<LIN_FWD>(ma, mas, mb, mo, a, grid, st);
+    case LIN_DGRAD: return l8_launch<LIN_DGRAD>(ma, mas, mb, mo, a, grid, st);
+    default: return l8_launch<LIN_WGRAD>(ma, mas, mb, mo, a, grid, st);
   }
 }
 
