@@ -104,9 +104,12 @@ __device__ __forceinline__ void maxima(const Eight<T, WIDE>* raw, uint32_t* rmax
 // Tiles of 128 rows x 128 columns, rows from an expert's first on (matrices of `mat_rows` rows: from the
 // matrix's); 16 lanes hold a row's 128 columns, a thread eight rows in registers, so that a tile is read once
 // for both of its formats.  A persistent grid, tiles of neighbouring columns one after the other.
+// Memory and instructions bound it together (1000 a thread and tile): 65536 x 2048 bf16 into rows and tokens 97 us,
+// 5.5 TB/s, with 32 warps an SM (24 warps and maxima by full butterflies 111; 40 warps 105, they spill; the next
+// tile on its way to shared memory meanwhile 110: loads are not what it waits for).
 template <typename T, bool WIDE>
-__global__ void __launch_bounds__(Q_THREADS, WIDE && sizeof(T) == 2 ? 3 : 2) block8_quantize_kernel(const __grid_constant__ Block8Args a) {
-  __shared__ uint32_t colmax[Q_THREADS / 32][B8];
+__global__ void __launch_bounds__(Q_THREADS, WIDE && sizeof(T) == 2 ? 4 : 2) block8_quantize_kernel(const __grid_constant__ Block8Args a) {
+  __shared__ uint32_t colmaxes[2][Q_THREADS / 32][B8];       // by turns: the tile before may still be read
   __shared__ __align__(16) float colup[B8];
   __shared__ int row0[Q_MAX_E + 1], blk0[Q_MAX_E + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -182,6 +185,7 @@ __global__ void __launch_bounds__(Q_THREADS, WIDE && sizeof(T) == 2 ? 3 : 2) blo
       ++blk;
     }
   };
+  int turn = 0;
   for (; blk < blocks; next()) {
     const int c0 = col_blk * B8, left = a.cols - c0 - c8;
     int64_t first;                               // row of the source, and how many the tile has
@@ -213,14 +217,23 @@ __global__ void __launch_bounds__(Q_THREADS, WIDE && sizeof(T) == 2 ? 3 : 2) blo
     uint32_t rmax[Q_ROWS], cmax[8];
     maxima<T, WIDE>(raw, rmax, cmax);
     if (a.codes != nullptr) {
+      // The row's 16 lanes share its eight pairs of divisions: lane j takes row j's, the others read it.  Maxima are
+      // exchanged by halves, so that each step leaves a lane with half as many rows, in the end its own.
+      uint32_t half[4], pair[2];
 #pragma unroll
-      for (int off = 1; off < 16; off *= 2)
+      for (int i = 0; i < 4; ++i) {
+        const bool up = lane & 4;
+        const uint32_t give = __shfl_xor_sync(0xFFFFFFFFu, up ? rmax[i] : rmax[i + 4], 4);
+        half[i] = max(up ? rmax[i + 4] : rmax[i], give);
+      }
 #pragma unroll
-        for (int i = 0; i < Q_ROWS; ++i) rmax[i] = max(rmax[i], __shfl_xor_sync(0xFFFFFFFFu, rmax[i], off));
-      // The row's 16 lanes share its eight pairs of divisions: lane j takes row j's, the others read it.
-      uint32_t mine = rmax[0];
-#pragma unroll
-      for (int i = 1; i < Q_ROWS; ++i) mine = (lane & 7) == i ? rmax[i] : mine;
+      for (int i = 0; i < 2; ++i) {
+        const bool up = lane & 2;
+        const uint32_t give = __shfl_xor_sync(0xFFFFFFFFu, up ? half[i] : half[i + 2], 2);
+        pair[i] = max(up ? half[i + 2] : half[i], give);
+      }
+      uint32_t mine = max((lane & 1) ? pair[1] : pair[0], __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? pair[0] : pair[1], 1));
+      mine = max(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, 8));
       const float my_up = Block8(mine).up;
       const int my_row = sub + 16 * (lane & 7);
       if ((lane & 8) == 0 && my_row < cnt) a.scales[int64_t(c0 / B8) * a.rows + first + my_row] = Block8::scale(mine);
@@ -236,13 +249,14 @@ __global__ void __launch_bounds__(Q_THREADS, WIDE && sizeof(T) == 2 ? 3 : 2) blo
       }
     }
     if (a.tcodes == nullptr) continue;
+    uint32_t (*const colmax)[B8] = colmaxes[turn];
+    turn ^= 1;
     float ups[8];                                // the columns' factors
     if (a.tiles) {
       uint32_t amax = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) amax = max(amax, cmax[j]);
       amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-      __syncthreads();                           // the tile before has been read
       if (lane == 0) colmax[warp][0] = amax;
       __syncthreads();
       amax = 0;
@@ -255,7 +269,6 @@ __global__ void __launch_bounds__(Q_THREADS, WIDE && sizeof(T) == 2 ? 3 : 2) blo
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) cmax[j] = max(cmax[j], __shfl_xor_sync(0xFFFFFFFFu, cmax[j], 16));
-      __syncthreads();                           // the tile before has been read
       if (lane < 16) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) colmax[warp][c8 + j] = cmax[j];
@@ -281,9 +294,7 @@ __global__ void __launch_bounds__(Q_THREADS, WIDE && sizeof(T) == 2 ? 3 : 2) blo
       raw[i].get(v);
       uint32_t q[2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        q[k] = cvt_e4m3x2(v[4 * k] * ups[4 * k], v[4 * k + 1] * ups[4 * k + 1]) |
-               (cvt_e4m3x2(v[4 * k + 2] * ups[4 * k + 2], v[4 * k + 3] * ups[4 * k + 3]) << 16);
+      for (int k = 0; k < 8; k += 4) q[k >> 2] = block8_codes4(v + k, ups + k);
       if (cnt < B8 && sub + 16 * i >= cnt) q[0] = q[1] = 0;      // (0 times a NaN factor is none)
       if (sub + 16 * i < out_rows) put_codes<WIDE>(out + int64_t(i) * 16 * a.cols, q, left);
     }

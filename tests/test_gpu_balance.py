@@ -180,3 +180,12 @@ def test_router_backward_takes_it_along(E, k, renorm):
     # dlogits as two bf16 terms: 2^-16 of each, and float32 sums
     size = total.abs().t() @ x.double().abs()
     assert bool(((out[1][2].double() - ref_dw).abs() <= size * (2.0 ** -16 + 200 * 2.0 ** -23)).all())
+
+
+def test_the_same_expert_twice():
+    """A choice counts as often as it stands there."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x = torch.randn(70, 6, generator=g, device="cuda")
+    idx = torch.randint(0, 6, (70, 3), generator=g, device="cuda", dtype=torch.int32)
+    idx[:, 2] = idx[:, 0]
+    check(x, idx, None)

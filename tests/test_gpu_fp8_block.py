@@ -39,7 +39,7 @@ def fresh(rows, cols, blocks, tiles):
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("split,cols,pad", [([1], 1, 0), ([1], 128, 0), ([5, 0, 3], 8, 0), ([129, 128, 127], 136, 8),
-                                            ([0, 40, 300], 130, 3), ([1, 0, 2, 3], 264, 0), ([700], 1003, 0), ([64] * 20, 392, 0)])
+                                            ([0, 40, 300], 130, 3), ([1, 0, 2, 3], 264, 0), ([700], 1003, 0), ([64] * 20, 392, 0), ([0] * 199 + [2] * 57, 72, 0)])
 def test_quantize(split, cols, pad, dtype):
     rows = sum(split)
     extra = 5                                                # rows of no expert
