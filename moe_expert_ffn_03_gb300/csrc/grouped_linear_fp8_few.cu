@@ -18,6 +18,7 @@
 // so results do not depend on timing; nobody waits for anybody.
 #include <atomic>
 #include <cstdio>
+#include <type_traits>
 
 #include "linear8.cuh"
 
@@ -106,8 +107,9 @@ __device__ __forceinline__ int f8_parts(int tiles, int all, int ctas, int lane) 
   const int most = min(all / F8_MIN_PIECE, tiles > 0 ? F8_MAX_PIECES / tiles : 1);
   uint32_t best = 0xFFFFFFFFu;                   // blocks of the longest SM, then pieces (fewest win)
   for (int p = lane + 1; p <= max(most, 1); p += 32) {
-    const int64_t cost = int64_t((int64_t(tiles) * p + ctas - 1) / ctas) * ((all + p - 1) / p + (p > 1 ? 2 : 0));
-    const uint32_t key = uint32_t(cost < (1 << 21) ? cost : (1 << 21) - 1) << 10 | uint32_t(p);
+    // below 2^32: tiles * p is at most F8_MAX_PIECES, or p is 1 and tiles below 2^22
+    const uint32_t rounds = (uint32_t(tiles) * p + ctas - 1) / uint32_t(ctas), cost = rounds * ((uint32_t(all) + p - 1) / p + (p > 1 ? 2 : 0));
+    const uint32_t key = (cost < (1u << 21) ? cost : (1u << 21) - 1) << 10 | uint32_t(p);
     best = min(best, key);
   }
   return int(__reduce_min_sync(0xFFFFFFFFu, best) & 1023u);
@@ -339,14 +341,25 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         if (before + 1 != unsigned(parts)) continue;
         __threadfence();
         if (lane == 0) args.arrived[w.tile * 4 + q] = 0;           // for the next call
+        // few rows: four pieces at a time are on their way
+        const auto join = [&](auto most) {
+          constexpr int ROWS = decltype(most)::value, BATCH = F8_ROWS / ROWS;
 #pragma unroll
-        for (int c = 0; c < F8_ROWS; ++c) acc[c] = c < cnt ? __ldcg(piece(0) + c * 32) : 0.f;
-        for (int p = 1; p < parts; ++p) {
-          const float* s = piece(p);
+          for (int c = 0; c < ROWS; ++c) acc[c] = 0.f;
+          for (int p = 0; p < parts; p += BATCH) {
+            float v[BATCH][ROWS];
 #pragma unroll
-          for (int c = 0; c < F8_ROWS; ++c)
-            if (c < cnt) acc[c] += __ldcg(s + c * 32);
-        }
+            for (int i = 0; i < BATCH; ++i)
+#pragma unroll
+              for (int c = 0; c < ROWS; ++c) v[i][c] = c < cnt && p + i < parts ? __ldcg(piece(p + i) + c * 32) : 0.f;
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i)
+#pragma unroll
+              for (int c = 0; c < ROWS; ++c) acc[c] += v[i][c];
+          }
+        };
+        if (cnt <= F8_SMALL) join(std::integral_constant<int, F8_SMALL>{});
+        else join(std::integral_constant<int, F8_ROWS>{});
       }
       // lanes hold neighbouring m of a row: 64 bytes a warp and row
       const int m = w.m0 + q * 32 + lane;
