@@ -24,9 +24,10 @@
 //   warp 0       TMA producer of the A side, warp 2 of the B side
 //   warp 1       tensor memory; in the leader, the MMAs
 //   warp 3       the experts' prefix sums, then the tiles, laid out ahead for the others
-//   warps 4..11  sums: four per lane quarter, 128 columns each, with 232 registers a thread (the other
+//   warps 4..11  sums: two per lane quarter, 128 columns each, with 232 registers a thread (the other
 //                four warps give up theirs: 128 x 40 + 256 x 232 = 384 x 168)
-// Waits are bounded as everywhere; each lasts as long as a block or a tile's output at most.
+// Waits are bounded as everywhere; each lasts as long as a block or a tile's output at most, warp 3's as long as a
+// tile.
 //
 // What holds the tensor pipe up is the way round of a buffer: sums there, seen, read, added, handed back, seen,
 // filled again, with single threads and two warps a quarter on it.  So a block has one wait and one commit
@@ -415,9 +416,13 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
     } else if (warp == 3) {
       if (lane == 0) {
         // ---------------- the pair's tiles, laid out for the others ----------------
+        // A slot comes free when the tile before is done, which in the weight gradient may be all rows' (2^30 take
+        // seconds); a block takes 400 ns.
+        const int c = MODE == LIN_FWD ? args.K : MODE == LIN_DGRAD ? args.N : row0[order[0] + 1] - row0[order[0]];
+        const uint64_t tile_lim = lim + uint64_t((c + L8_KT - 1) / L8_KT) * 4096u;
         Tiles8 tiles(tile_ring, laid, taken);
         for (int t = pair;; t = l8_after<MODE>(t, num_pairs)) {
-          if (!wait_phase_inline(&taken[tiles.slot], tiles.ph ^ 1u, abort_s, args.err, SITE_LINEAR8 + 8, lim)) break;
+          if (!wait_phase_inline(&taken[tiles.slot], tiles.ph ^ 1u, abort_s, args.err, SITE_LINEAR8 + 8, tile_lim)) break;
           Tile8 tl;
           if (t < total) l8_decode<MODE>(args, row0, tile0, order, t, tl);
           else tl.blocks = -1;
