@@ -30,15 +30,16 @@
 // tile.
 //
 // What holds the tensor pipe up is the way round of a buffer: sums there, seen, read, added, handed back, seen,
-// filled again, with single threads and two warps a quarter on it.  So a block has one wait and one commit
-// for the MMA's thread, constant descriptors, scales asked for two blocks ahead (one ahead, 8192 rows,
-// 4096 -> 16384: 490 us, two: 414; from a ring in shared memory 412, but 32768 rows 5% longer), the next
-// barrier looked at before the last additions; measured the same or worse: sixteen warps of 64 columns (494),
-// halves of 128 columns with four buffers (558; an MMA of 128 columns takes 104 clocks, not 64), single CTAs of
-// 128 x 256 (490), a second thread that issues (478).  Measured, on its own: 32768 rows, 4096 -> 28672, E = 8,
-// forward 2.89 ms (2.66 PFLOP/s), under the power limit of calls in a row 3.2 ms; 8192 rows, 4096 -> 16384,
-// E = 2: 414 us (2.65); 65536 rows, 2048 -> 2816, E = 16: 350 us forward (2.16: a tile's output takes a quarter of
-// its time there), 315 weight gradient (2.40).
+// filled again, with single threads and two warps a quarter on it: 750 clocks a block, 613 without any sums.  So a
+// block has one wait and one commit for the MMA's thread, constant descriptors, scales asked for two
+// blocks ahead (8192 rows, 4096 -> 16384, before the steps below: one ahead 490 us, two 414; from a ring in shared
+// memory 412, but 32768 rows 5% longer), and goes back before its last half is added (416 -> 404); measured the
+// same or worse: sixteen warps of 64 columns (494 against 490), halves of 128 columns with four buffers (558; an
+// MMA of 128 columns takes 104 clocks, not 64), single CTAs of 128 x 256 (490), a second thread that issues
+// (478), test_wait in place of try_wait where the sums are waited for (425 against 396).  Measured, on its own:
+// 32768 rows, 4096 -> 28672, E = 8, forward 2.78 ms (2.77 PFLOP/s), under the power limit of calls in a row 3.2 ms;
+// 8192 rows, 4096 -> 16384, E = 2: 396 us (2.78); 65536 rows, 2048 -> 2816, E = 16: 304 us forward (2.49: a tile's output
+// is a tenth of its time there), 300 input gradient, 278 weight gradient (2.72).
 #include <atomic>
 #include <cstdio>
 #include <type_traits>
