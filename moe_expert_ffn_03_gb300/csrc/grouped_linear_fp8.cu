@@ -58,7 +58,8 @@ struct alignas(16) Tile8 {
   int blocks;      // its blocks of 128; -1 behind the last tile
   int last;        // indices in the last block
   const float *sa, *sb[2];  // scales of the first block: m0's, and those of n0 and n0 + 128
-  int64_t unused;
+  int piece;       // of a tile that is cut: where its partial sums go; else -1
+  int unused;
 };
 
 constexpr int L8_M = 256, L8_N = 256;            // the pair's tile
@@ -71,6 +72,8 @@ constexpr int L8_REGS = 168, L8_REGS_FEW = 40, L8_REGS_MANY = 232;
 static_assert(128 * L8_REGS_FEW + 32 * L8_EPI_WARPS * L8_REGS_MANY == L8_THREADS * L8_REGS, "register split");
 constexpr int L8_GROUP = 8;                      // row tiles that share the sweep over the weights
 constexpr int L8_SMALL = 32;                     // rows of the small box of rows
+constexpr int L8_SHARES = 2 * L8_EPI_WARPS;      // of a tile: 32 m x 128 n each
+constexpr int L8_MIN_CUT = 8;                    // blocks up to which a tile is not cut
 
 // a warp's output on its way: two boxes of 32 rows of 64 bf16, swizzled in 128 bytes
 constexpr int L8_BOX = 32 * 128;
@@ -79,8 +82,8 @@ constexpr int L8_OFF_BAR = L8_OFF_OUT + L8_EPI_WARPS * 2 * L8_BOX;
 constexpr int L8_TILES = 4;                      // tiles laid out ahead
 constexpr int L8_BARS = 2 * L8_STAGES + 1 + 2 * L8_TILES;        // full, empty, drain, laid, taken
 constexpr int L8_OFF_MISC = L8_OFF_BAR + L8_BARS * 8;
-constexpr int L8_OFF_SEG = (L8_OFF_MISC + 16 + 15) & ~15;        // row0[E+1], tile0[E+1], order[E]
-constexpr int L8_OFF_TILES = (L8_OFF_SEG + 3 * (L8_MAX_E + 1) * 4 + 15) & ~15;
+constexpr int L8_OFF_SEG = (L8_OFF_MISC + 16 + 15) & ~15;        // row0[E+1], tile0[E+1], order[E], unit0[E+1]
+constexpr int L8_OFF_TILES = (L8_OFF_SEG + 4 * (L8_MAX_E + 1) * 4 + 15) & ~15;
 constexpr int L8_SMEM = L8_OFF_TILES + L8_TILES * int(sizeof(Tile8)) + 1024;
 static_assert(L8_SMEM <= 232448, "shared memory budget");
 
@@ -128,27 +131,140 @@ __device__ __forceinline__ int l8_tiles(const Linear8Args& a, const int* tile0) 
   return MODE == LIN_WGRAD ? a.E * ((a.N + L8_M - 1) / L8_M) * nt : tile0[a.E] * nt;
 }
 
+// An expert's tile i of the weight gradient: the n tiles of a few m tiles in turn.
+__device__ __forceinline__ void l8_wgrad_tile(const Linear8Args& a, int i, int& m0, int& n0) {
+  const int mt = (a.N + L8_M - 1) / L8_M, nt = (a.K + L8_N - 1) / L8_N, per = L8_GROUP * nt;
+  const int g = i / per, first = g * L8_GROUP, gs = min(L8_GROUP, mt - first);
+  const int local = i - g * per;
+  m0 = (first + local % gs) * L8_M;
+  n0 = local / gs * L8_N;
+}
+
+// Warps (their logarithm) that share a cut tile's sums: with few pieces they are quick for one.
+__device__ __forceinline__ int l8_team(int parts) { return parts <= 4 ? 0 : parts <= 8 ? 1 : parts <= 16 ? 2 : 3; }
+
+// One warp: into how many pieces the weight gradient's tiles are cut along their rows, where an expert's are few and
+// long.  unit0: of every expert in `order` (most rows first) the first of its tiles' pieces, those of one
+// place side by side.  A piece has `len` blocks at most: of 31 lengths from an even share of the pairs up, and
+// of the longest tile's, the one that is done first by this measure in blocks (400 ns): the pairs' rounds, or an even
+// share and one piece more if that is less; four for an output; if anything is cut, 8 for the second launch
+// and a fifth for writing and reading each piece.  Cut tiles are longer than a share, so that their pieces are less than
+// twice as many as the pairs.  The cut experts are written to `plan`.
+__device__ __forceinline__ void l8_cut(const Linear8Args& a, const int* row0, const int* order, int* unit0, int pairs, int lane,
+                                       bool writes) {
+  const int tiles = ((a.N + L8_M - 1) / L8_M) * ((a.K + L8_N - 1) / L8_N);            // an expert's
+  const auto blocks_of = [&](int slot) { return (row0[order[slot] + 1] - row0[order[slot]] + L8_KT - 1) / L8_KT; };
+  int64_t sum = 0;
+  for (int s = lane; s < a.E; s += 32) sum += blocks_of(s);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+  const int share = int((sum * tiles + pairs - 1) / pairs), longest = blocks_of(0);
+  const int base = max(L8_MIN_CUT, share);
+  int len = lane < 31 ? base + int(int64_t(base) * lane / 8) : max(base, longest);
+  const float per = 1.f / float(len);
+  float units = 0.f, cut = 0.f;
+  int s = 0;
+  for (; s < a.E; ++s) {
+    const int b = blocks_of(s);
+    if (b <= base) break;                        // nor are those behind it cut
+    const float parts = b <= len ? 1.f : ceilf(float(b) * per);
+    units += parts;
+    cut += b <= len ? 0.f : parts;
+  }
+  units = (units + float(a.E - s)) * float(tiles);
+  const float piece = float(min(len, longest));
+  const float cost = fminf(ceilf(units / float(pairs)) * piece, float(share) + piece) + 4.f +
+                     (cut > 0.f ? 8.f + 0.2f * cut * float(tiles) : 0.f);
+  const uint32_t best = __reduce_min_sync(0xFFFFFFFFu, __float_as_uint(cost));        // not negative: ordered as integers
+  len = __shfl_sync(0xFFFFFFFFu, len, __ffs(__ballot_sync(0xFFFFFFFFu, __float_as_uint(cost) == best)) - 1);
+  // eight experts a lane
+  for (;;) {
+    int mine[8], all = 0, cut = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int slot = lane * 8 + i;
+      const int parts = slot < a.E ? max(1, (blocks_of(slot) + len - 1) / len) : 0;
+      mine[i] = parts * tiles;
+      all += mine[i];
+      cut += parts > 1 ? mine[i] : 0;
+    }
+    int before = all;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int u = __shfl_up_sync(0xFFFFFFFFu, before, off);
+      if (lane >= off) before += u;
+    }
+    before -= all;
+    if (__reduce_add_sync(0xFFFFFFFFu, unsigned(cut)) > unsigned(L8_MAX_PIECES)) {
+      len += len;
+      continue;
+    }
+    int joins = 0;                               // units of the second launch
+#pragma unroll
+    for (int i = 0; i < 8; ++i) joins += mine[i] > tiles ? tiles * L8_SHARES << l8_team(mine[i] / tiles) : 0;
+    int join0 = joins;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int u = __shfl_up_sync(0xFFFFFFFFu, join0, off);
+      if (lane >= off) join0 += u;
+    }
+    const int all_joins = __shfl_sync(0xFFFFFFFFu, join0, 31);
+    join0 -= joins;
+    int cuts = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int slot = lane * 8 + i;
+      if (slot <= a.E) unit0[slot] = before;
+      if (mine[i] > tiles) {
+        const int parts = mine[i] / tiles;
+        ++cuts;
+        if (writes) reinterpret_cast<int4*>(a.plan)[1 + slot] = make_int4(order[slot], before, parts, join0);
+        join0 += tiles * L8_SHARES << l8_team(parts);
+      }
+      before += mine[i];
+    }
+    if (lane == 31 && a.E == L8_MAX_E) unit0[L8_MAX_E] = before;
+    cuts = int(__reduce_add_sync(0xFFFFFFFFu, unsigned(cuts)));
+    if (writes && lane == 0) reinterpret_cast<int4*>(a.plan)[0] = make_int4(cuts, all_joins, 0, 0);
+    __syncwarp();
+    return;
+  }
+}
+
 // tile0: the experts' first row tiles; wgrad: their first blocks of 128 rows.
-template <int MODE>
-__device__ __forceinline__ void l8_decode(const Linear8Args& a, const int* row0, const int* tile0, const int* order, int t,
-                                          Tile8& tl) {
+template <int MODE, bool CUT>
+__device__ __forceinline__ void l8_decode(const Linear8Args& a, const int* row0, const int* tile0, const int* order,
+                                          const int* unit0, int t, Tile8& tl) {
   const int cols = l8_cols<MODE>(a), nt = (cols + L8_N - 1) / L8_N;
-  int tn;
+  tl.piece = -1;
   if (MODE == LIN_WGRAD) {
-    // experts with the most rows first; inside an expert the n tiles of a few m tiles in turn
-    const int mt = (a.N + L8_M - 1) / L8_M;
-    const int slot = t / (mt * nt), rem = t - slot * (mt * nt);
-    const int per = L8_GROUP * nt;
-    const int g = rem / per, first = g * L8_GROUP, gs = min(L8_GROUP, mt - first);
-    const int local = rem - g * per;
+    // experts with the most rows first
+    const int tiles = (a.N + L8_M - 1) / L8_M * nt;
+    int slot, rem, part = 0, parts = 1;
+    if constexpr (CUT) {
+      int lo = 0, hi = a.E - 1;                  // largest slot with unit0[slot] <= t
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (unit0[mid] <= t) lo = mid; else hi = mid - 1;
+      }
+      slot = lo;
+      rem = t - unit0[slot];
+      parts = (unit0[slot + 1] - unit0[slot]) / tiles;
+      part = rem / tiles;
+      rem -= part * tiles;
+      if (parts > 1) tl.piece = t;
+    } else {
+      slot = t / tiles;
+      rem = t - slot * tiles;
+    }
     tl.e = order[slot];
-    tn = local / gs;
-    tl.m0 = (first + local % gs) * L8_M;
+    l8_wgrad_tile(a, rem, tl.m0, tl.n0);
     tl.cnt = min(L8_M, a.N - tl.m0);
-    const int rows = row0[tl.e + 1] - row0[tl.e];
-    tl.c0 = tile0[tl.e] * L8_KT;
-    tl.blocks = (rows + L8_KT - 1) / L8_KT;
-    tl.last = rows - (tl.blocks - 1) * L8_KT;
+    const int rows = row0[tl.e + 1] - row0[tl.e], all = (rows + L8_KT - 1) / L8_KT;
+    const int from = CUT ? int(int64_t(part) * all / parts) : 0, to = CUT ? int(int64_t(part + 1) * all / parts) : all;
+    tl.c0 = (tile0[tl.e] + from) * L8_KT;
+    tl.blocks = to - from;
+    tl.last = to == all ? rows - (all - 1) * L8_KT : L8_KT;
   } else {
     const int total = tile0[a.E];
     const int per = L8_GROUP * nt;
@@ -161,7 +277,7 @@ __device__ __forceinline__ void l8_decode(const Linear8Args& a, const int* row0,
       if (tile0[mid] <= tt) lo = mid; else hi = mid - 1;
     }
     tl.e = lo;
-    tn = local / gs;
+    tl.n0 = local / gs * L8_N;
     tl.m0 = row0[lo] + (tt - tile0[lo]) * L8_M;
     tl.cnt = min(L8_M, row0[lo + 1] - tl.m0);
     const int c = MODE == LIN_FWD ? a.K : a.N;
@@ -169,7 +285,6 @@ __device__ __forceinline__ void l8_decode(const Linear8Args& a, const int* row0,
     tl.blocks = (c + L8_KT - 1) / L8_KT;
     tl.last = c - (tl.blocks - 1) * L8_KT;
   }
-  tl.n0 = tn * L8_N;
   tl.n = (min(L8_N, cols - tl.n0) + 31) & ~31;
   const int64_t kbs = (a.K + 127) / 128, nbs = (a.N + 127) / 128, nb = tl.n0 / 128, blk = tl.c0 / L8_KT;
   tl.sa = a.sa + (MODE == LIN_WGRAD ? blk * a.N : 0) + tl.m0;
@@ -233,7 +348,7 @@ __device__ __forceinline__ void l8_store(const CUtensorMap* map, const void* src
                  ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(n), "r"(m) : "memory");
 }
 
-template <int MODE>
+template <int MODE, bool CUT>
 __global__ void __launch_bounds__(L8_THREADS, 1)
     grouped_linear_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmAs,
                               const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmO,
@@ -253,6 +368,7 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
   int* row0 = reinterpret_cast<int*>(smem + L8_OFF_SEG);
   int* tile0 = row0 + L8_MAX_E + 1;
   int* order = tile0 + L8_MAX_E + 1;
+  int* unit0 = order + L8_MAX_E + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();       // 0: leader (issues the MMAs), 1: peer
@@ -297,6 +413,8 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
         }
         order[r] = e;
       }
+      __syncwarp();
+      if constexpr (CUT) l8_cut(args, row0, order, unit0, num_pairs, lane, blockIdx.x == 0);
     }
   }
   tc_fence_before();
@@ -305,7 +423,7 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_base_s;
   // inconsistent split_sizes: nothing is computed (the error word says so)
-  const int total = *bad_s ? 0 : l8_tiles<MODE>(args, tile0);
+  const int total = *bad_s ? 0 : CUT ? unit0[args.E] : l8_tiles<MODE>(args, tile0);
   const uint64_t lim = args.wait_limit_ns;
 
   if (warp < 4) {
@@ -417,15 +535,13 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
     } else if (warp == 3) {
       if (lane == 0) {
         // ---------------- the pair's tiles, laid out for the others ----------------
-        // A slot comes free when the tile before is done, which in the weight gradient may be all rows' (2^30 take
-        // seconds); a block takes 400 ns.
-        const int c = MODE == LIN_FWD ? args.K : MODE == LIN_DGRAD ? args.N : row0[order[0] + 1] - row0[order[0]];
-        const uint64_t tile_lim = lim + uint64_t((c + L8_KT - 1) / L8_KT) * 4096u;
+        // A slot comes free when the tile before is done.  In the weight gradient that is far below the limit, too:
+        // an expert of few tiles has them cut, one of many has no room for rows that take a tenth of a second.
         Tiles8 tiles(tile_ring, laid, taken);
         for (int t = pair;; t = l8_after<MODE>(t, num_pairs)) {
-          if (!wait_phase_inline(&taken[tiles.slot], tiles.ph ^ 1u, abort_s, args.err, SITE_LINEAR8 + 8, tile_lim)) break;
+          if (!wait_phase_inline(&taken[tiles.slot], tiles.ph ^ 1u, abort_s, args.err, SITE_LINEAR8 + 8, lim)) break;
           Tile8 tl;
-          if (t < total) l8_decode<MODE>(args, row0, tile0, order, t, tl);
+          if (t < total) l8_decode<MODE, CUT>(args, row0, tile0, order, unit0, t, tl);
           else tl.blocks = -1;
           tile_ring[tiles.slot] = tl;
           mbar_arrive(&laid[tiles.slot]);
@@ -465,6 +581,7 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
     Tiles8 tiles(tile_ring, laid, taken);
     const int at = int(rank) * 128 + q * 32;     // this warp's first of a tile's m
     int blocks = 0, e = 0, m = 0, n = 0, m_left = 0;         // the tile's, m and n from the warp's first on
+    int piece = -1;
     // takes the next tile up, and asks for its first blocks' scales
     const auto take = [&]() {
       ok = wait_phase_warp_inline(&laid[tiles.slot], tiles.ph, abort_s, args.err, SITE_LINEAR8 + 6, lim);
@@ -472,6 +589,7 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
       const Tile8* tl = &tile_ring[tiles.slot];
       blocks = tl->blocks;
       if (MODE == LIN_WGRAD) e = tl->e;
+      if (CUT) piece = tl->piece;
       m = tl->m0 + at;
       n = tl->n0 + col0;
       m_left = tl->cnt - at;
@@ -544,6 +662,16 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       const int rows = min(m_left, 32), columns = cols - n, e_out = e, m_out = m, n_out = n;
+      if constexpr (CUT) {
+        if (piece >= 0) {
+          // partial sums, [n][the warp's 32 m]
+          float* mine = args.pieces + int64_t(piece) * L8_PIECE + (int(rank) * L8_EPI_WARPS + warp - 4) * (32 * 128) + lane;
+#pragma unroll
+          for (int c = 0; c < 128; ++c) __stcg(mine + c * 32, acc[c]);
+          take();
+          continue;
+        }
+      }
       // Through the warp's own shared memory and TMA: meanwhile the tensor pipe fills the two buffers and stops, so
       // what counts is the warps' own time.  (2000 clocks a tile of it: taking the next tile up 600, these stores
       // 650, the fence 350, two boxes 420; rows read back and stored by 16 lanes each 3300, 32 bytes a lane to 32
@@ -607,7 +735,60 @@ bool l8_out_map(CUtensorMap* m, void* base, int64_t inner, int64_t rows, int64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE>
+// The cut tiles' partial sums, added in the order of the rows.  A warp takes 16 n of 32 m; where a tile has many pieces,
+// two, four or eight warps share them, every second, fourth or eighth each.
+__global__ void __launch_bounds__(256) grouped_linear_fp8_join_kernel(const __grid_constant__ Linear8Args a) {
+  __shared__ float red[8][16][33];
+  __shared__ int4 plan[1 + L8_MAX_PIECES / 2];   // a cut tile has two pieces at least
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tiles = ((a.N + L8_M - 1) / L8_M) * ((a.K + L8_N - 1) / L8_N);
+  pdl_wait();
+  if (tid <= L8_MAX_PIECES / 2) plan[tid] = __ldcg(reinterpret_cast<const int4*>(a.plan) + tid);
+  __syncthreads();
+  const int cuts = plan[0].x, units = plan[0].y;
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    int lo = 0, hi = cuts - 1;                   // largest slot whose units begin up to u
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (plan[1 + mid].w <= u) lo = mid; else hi = mid - 1;
+    }
+    const int4 slot = plan[1 + lo];
+    const int parts = slot.z, lg = l8_team(parts), team = 1 << lg, rem = u - slot.w;
+    const int i = rem / (L8_SHARES << lg), share = rem & (L8_SHARES - 1), sub = (rem / L8_SHARES) & (team - 1);
+    int m, n;
+    l8_wgrad_tile(a, i, m, n);
+    m += (share >> 3) * 128 + (share & 3) * 32;  // CTA, lane quarter
+    n += ((share >> 2) & 1) * 128 + sub * (128 >> lg);
+    if (m >= a.N || n >= a.K) continue;
+    const int c0 = sub * (128 >> lg) + (warp >> lg) * 16;
+    const float* from = a.pieces + int64_t(slot.y + i) * L8_PIECE + share * (32 * 128) + c0 * 32 + lane;
+    float acc[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) acc[c] = 0.f;
+#pragma unroll 4
+    for (int p = warp & (team - 1); p < parts; p += team) {
+      const float* s = from + int64_t(p) * tiles * L8_PIECE;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) acc[c] += __ldcg(s + c * 32);
+    }
+    __syncthreads();                             // the sums before have been read
+#pragma unroll
+    for (int c = 0; c < 16; ++c) red[warp][c][lane] = acc[c];
+    __syncthreads();
+    const int row = tid >> 3, c = (tid & 7) * 2;
+    for (int g = 0; g < 8 >> lg; ++g) {
+      float x = 0.f, y = 0.f;
+      for (int w = g << lg; w < (g + 1) << lg; ++w) {
+        x += red[w][c][row];
+        y += red[w][c + 1][row];
+      }
+      if (m + row < a.N && n + g * 16 < a.K)     // K comes in multiples of 16
+        *reinterpret_cast<uint32_t*>(a.out + (int64_t(slot.x) * a.N + m + row) * a.ldo + n + g * 16 + c) = pack_bf16x2(x, y);
+    }
+  }
+}
+
+template <int MODE, bool CUT = false>
 cudaError_t l8_launch(const CUtensorMap& ma, const CUtensorMap& mas, const CUtensorMap& mb, const CUtensorMap& mo,
                       const Linear8Args& a, int grid, cudaStream_t st) {
   // attributes are per device: set and checked once on each device this process uses
@@ -618,11 +799,11 @@ cudaError_t l8_launch(const CUtensorMap& ma, const CUtensorMap& mas, const CUten
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices || !ready[dev].load(std::memory_order_acquire)) {
     cudaFuncAttributes f;
-    e = cudaFuncGetAttributes(&f, grouped_linear_fp8_kernel<MODE>);
+    e = cudaFuncGetAttributes(&f, grouped_linear_fp8_kernel<MODE, CUT>);
     if (e != cudaSuccess) return e;
     // the warps' shares have to add up to what the block is launched with, or they would wait for ever
     if (f.numRegs != L8_REGS) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(grouped_linear_fp8_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, L8_SMEM);
+    e = cudaFuncSetAttribute(grouped_linear_fp8_kernel<MODE, CUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L8_SMEM);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices) ready[dev].store(true, std::memory_order_release);
   }
@@ -640,14 +821,30 @@ cudaError_t l8_launch(const CUtensorMap& ma, const CUtensorMap& mas, const CUten
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, grouped_linear_fp8_kernel<MODE>, ma, mas, mb, mo, a);
+  return cudaLaunchKernelEx(&cfg, grouped_linear_fp8_kernel<MODE, CUT>, ma, mas, mb, mo, a);
 }
 
 }  // namespace
 
+// The workspace: error word, arrivals of the four warps of the tiles of few rows, plan, pieces.
+constexpr size_t kPlanBytes = 1280;
+static_assert(kPlanBytes >= (1 + L8_MAX_PIECES / 2) * sizeof(int4), "a cut tile has two pieces at least");
+constexpr size_t kPiecesAt = 256 + size_t(F8_MAX_PIECES) * 4 * sizeof(unsigned) + kPlanBytes;
+static_assert(kPiecesAt % 256 == 0, "pieces start on whole lines");
+size_t linear8_ws_bytes() {
+  const size_t few = size_t(F8_MAX_PIECES) * F8_PIECE, wide = size_t(L8_MAX_PIECES) * L8_PIECE;
+  return kPiecesAt + (few > wide ? few : wide) * sizeof(float);
+}
+void linear8_ws_parts(Linear8Args* a) {
+  a->arrived = reinterpret_cast<unsigned*>(reinterpret_cast<uint8_t*>(a->err) + 256);
+  a->plan = reinterpret_cast<int*>(a->arrived + F8_MAX_PIECES * 4);
+  a->pieces = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a->err) + kPiecesAt);
+}
+
 cudaError_t launch_grouped_linear_fp8(int mode, const Linear8Args& args, const uint8_t* a_codes, const uint8_t* b_codes,
                                       cudaStream_t st, char* msg, size_t msg_len) {
   Linear8Args a = args;
+  linear8_ws_parts(&a);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -687,8 +884,17 @@ cudaError_t launch_grouped_linear_fp8(int mode, const Linear8Args& args, const u
   switch (mode) {
     case LIN_FWD: return l8_launch<LIN_FWD>(ma, mas, mb, mo, a, grid, st);
     case LIN_DGRAD: return l8_launch<LIN_DGRAD>(ma, mas, mb, mo, a, grid, st);
-    default: return l8_launch<LIN_WGRAD>(ma, mas, mb, mo, a, grid, st);
+    default: break;
   }
+  // Tiles may be cut where an expert has fewer than there are pairs, and rows enough to keep one busy long after the
+  // others; whether they are, the kernel finds out.  (Both measured, that one first.  65000 rows, 256 -> 256, E = 1:
+  // 31 and 214 us; 40000 rows, 1024 -> 512, E = 1: 40 and 134; 60000 rows, 512 -> 512, E = 4: 43 and 62; 4000 rows,
+  // 256 -> 256: 22 and 25, 2048 rows 21 and 17; nothing to cut in 8000 rows, 1024 -> 2048, E = 8: 34 and 29.)
+  const int64_t tiles_e = nt * ((a.N + L8_M - 1) / L8_M);
+  if (tiles_e >= pairs || a.rows / L8_KT < 4 * L8_MIN_CUT) return l8_launch<LIN_WGRAD>(ma, mas, mb, mo, a, grid, st);
+  e = l8_launch<LIN_WGRAD, true>(ma, mas, mb, mo, a, 2 * int(pairs), st);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(grouped_linear_fp8_join_kernel, dim3(unsigned(sms) * 6), dim3(256), 0, st, a);
 }
 
 }  // namespace moe

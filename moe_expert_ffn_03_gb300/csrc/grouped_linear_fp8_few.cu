@@ -32,7 +32,7 @@ constexpr int F8_SMALL = 16;                     // rows of the small box of row
 constexpr int F8_THREADS = 256;
 constexpr int F8_AHEAD = 8;                      // blocks whose scales are on their way
 constexpr int F8_SLOT = F8_ROWS + 4;             // a block's: the rows', then the weights'
-constexpr int F8_PIECE = F8_M * F8_ROWS;         // f32 of a piece
+static_assert(F8_PIECE == F8_M * F8_ROWS, "f32 of a piece");
 constexpr int F8_MIN_PIECE = 4;                  // blocks a piece has at least
 
 constexpr int F8_OFF_BAR = F8_STAGES * F8_STAGE;
@@ -404,14 +404,9 @@ cudaError_t f8_launch(const CUtensorMap& mw, const CUtensorMap& mx, const CUtens
 
 }  // namespace
 
-// The workspace: error word, arrivals of every tile's four warps, pieces.
-size_t linear8_ws_bytes() { return 256 + size_t(F8_MAX_PIECES) * (4 * sizeof(unsigned) + F8_PIECE * sizeof(float)); }
-
 cudaError_t launch_grouped_linear_fp8_few(int mode, const Linear8Args& args, const uint8_t* rows_codes, const uint8_t* w_codes,
                                           int sms, cudaStream_t st, char* msg, size_t msg_len) {
-  Linear8Args a = args;
-  a.arrived = reinterpret_cast<unsigned*>(reinterpret_cast<uint8_t*>(a.err) + 256);
-  a.pieces = reinterpret_cast<float*>(a.arrived + F8_MAX_PIECES * 4);
+  const Linear8Args& a = args;
   CUtensorMap mw, mx, mxs;
   const int64_t inner = mode == LIN_FWD ? a.K : a.N;
   if (!l8_map(&mw, w_codes, a.K, a.N, a.E, 128) || !l8_map(&mx, rows_codes, inner, a.rows, 0, F8_ROWS) ||

@@ -337,10 +337,11 @@ struct Linear8Args {
   uint64_t wait_limit_ns;    // of every bounded wait
   int selftest_no_loads;     // the producers issue nothing
   unsigned* arrived;         // set by the launch: of the workspace, the arrivals and partial sums of cut tiles
+  int* plan;                 // which tiles of the weight gradient are cut
   float* pieces;
 };
-constexpr int F8_MAX_PIECES = 608;                // pieces of tiles that are cut along the contraction
 size_t linear8_ws_bytes();
+void linear8_ws_parts(Linear8Args* a);           // arrived, plan and pieces from err, the workspace's first word
 // forward and dgrad where the experts have few rows (grouped_linear_fp8_few.cu)
 cudaError_t launch_grouped_linear_fp8_few(int mode, const Linear8Args& a, const uint8_t* rows_codes, const uint8_t* w_codes,
                                           int sms, cudaStream_t st, char* msg, size_t msg_len);

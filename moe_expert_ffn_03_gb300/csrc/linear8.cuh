@@ -10,6 +10,10 @@ namespace {
 
 constexpr int L8_KT = 128;                       // a block of the contraction: one stage
 constexpr int L8_MAX_E = 256;
+// Partial sums of tiles that are cut along the contraction: pieces of the kernel for few rows (128 x 64), and
+// of the weight gradient's (256 x 256).
+constexpr int F8_MAX_PIECES = 608, F8_PIECE = 128 * 64;
+constexpr int L8_MAX_PIECES = 152, L8_PIECE = 256 * 256;
 
 // One warp: the experts' first rows and first tiles of PER rows, eight experts per lane.  Sizes that do not fit
 // in the rows are recorded (true) and taken as zeros.

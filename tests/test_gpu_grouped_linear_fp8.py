@@ -145,6 +145,34 @@ def test_few_rows(split, K, N):
             assert np.array_equal(f64(got), want), name
 
 
+@pytest.mark.parametrize("split,K,N", [([40000], 48, 32), ([9000, 0, 4100, 1, 130], 272, 256), ([30000] + [1] * 40, 64, 144),
+                                       ([6000, 6000, 5999], 528, 784), ([4097], 16, 16), ([4096 + 128 * 77, 5], 32, 16), ([20000, 900], 1040, 2064)])
+def test_weight_gradient_of_few_long_tiles(split, K, N):
+    """Tiles that are cut along the rows: several experts, ends of every kind, and a workspace used again.  Codes of -1,
+    0 and 1: sums of up to 40000 such products, of variance 0.44, stay below 2^24, and scales of one keep them whole."""
+    R, E = sum(split), len(split)
+    g, nb = B.grouped(R, K, N, E), B.fp8_blocks(R, E)
+    ss = torch.tensor(split, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(B.moe_grouped_linear_fp8_workspace_size(g), dtype=torch.uint8, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(R)
+    pick = torch.tensor([0xB8, 0x00, 0x38], dtype=torch.uint8, device="cuda")
+    xt, dyt = (pick[torch.randint(0, 3, (nb * 128, c), generator=gen, device="cuda")] for c in (K, N))
+    at, ref = 0, torch.zeros(E, N, K, dtype=torch.float64, device="cuda")
+    for e, n in enumerate(split):
+        end = at + -(-n // 128) * 128
+        dyt[at + n: end] = 0                                 # as the quantizer leaves them
+        xt[at + n: end] = 0
+        x, dy = (t[at:end].view(torch.float8_e4m3fn).double() for t in (xt, dyt))
+        ref[e] = dy.T @ x
+        at = end
+    one = lambda *s: torch.ones(*s, device="cuda")  # noqa: E731
+    for _ in range(2):
+        dw = torch.full((E, N, K), 77.0, dtype=torch.bfloat16, device="cuda")
+        B.moe_grouped_linear_fp8_wgrad(g, xt, one(nb, -(-K // 128)), dyt, one(nb, N), ss, dw, ws)
+        assert B.moe_get_device_error(ws) == (0, 0)
+        assert torch.equal(dw, ref.to(torch.bfloat16))
+
+
 def test_rows_past_the_sum_and_pitches():
     check_whole([40, 0, 9], 96, 112, rows=300, seed=4, pad=24)
     check_whole([40, 0, 9], 96, 112, rows=300, seed=5, pad=16)
