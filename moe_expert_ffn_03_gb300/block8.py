@@ -132,7 +132,7 @@ class Fp8MoEBlock:
     def forward(self, x, weights, residual=None, mask=None, stream=None):
         """(h, out) of x bf16 [T][H] (and residual); weights: gamma bf16 [H], w_r bf16 [E][H], w_gu and w_d Weights8.
         mask uint8 [T]: tokens with 0 are padding, which the balance loss leaves out.  Without a residual h is x
-        itself, which the backward pass reads again.  counts, prob_mean and loss are the balance loss's."""
+        itself, which the backward pass reads again, as it does mask.  counts, prob_mean and loss are the balance loss's."""
         s, w = self.s, weights
         self._weights(w)
         h = self.h if residual is not None else None

@@ -173,6 +173,49 @@ def test_weight_gradient_of_few_long_tiles(split, K, N):
         assert torch.equal(dw, ref.to(torch.bfloat16))
 
 
+def test_weight_gradient_of_many_rows_that_no_expert_has():
+    """The path that cuts tiles, with nothing to cut: zeros where no expert has rows, nothing at all where the sizes do
+    not fit."""
+    R, K, N, E = 6000, 32, 48, 3
+    g, nb = B.grouped(R, K, N, E), B.fp8_blocks(R, E)
+    u8 = lambda *s: torch.full(s, 0x38, dtype=torch.uint8, device="cuda")  # noqa: E731
+    one = lambda *s: torch.ones(*s, device="cuda")  # noqa: E731
+    for split, want, code in (([0, 0, 0], 0.0, 0), ([6000, 1, 0], 77.0, 7), ([-1, 5000, 0], 77.0, 7)):
+        ws = torch.zeros(B.moe_grouped_linear_fp8_workspace_size(g), dtype=torch.uint8, device="cuda")
+        dw = torch.full((E, N, K), 77.0, dtype=torch.bfloat16, device="cuda")
+        B.moe_grouped_linear_fp8_wgrad(g, u8(nb * 128, K), one(nb, 1), u8(nb * 128, N), one(nb, N),
+                                       torch.tensor(split, dtype=torch.int32, device="cuda"), dw, ws)
+        assert B.moe_get_device_error(ws)[0] == code and bool((dw == want).all())
+
+
+def test_cut_weight_gradients_in_two_graphs():
+    """Two graphs that share a workspace, replayed in turn with other rows: each gives what its eager call gives."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    cases = []
+    for split, K, N in (([9000, 100], 256, 144), ([50, 5000, 3], 64, 528)):
+        R, E = sum(split), len(split)
+        g, nb = B.grouped(R, K, N, E), B.fp8_blocks(R, E)
+        code = lambda c: torch.randint(0, 100, (nb * 128, c), generator=gen, device="cuda").to(torch.uint8)  # noqa: B023,E731
+        cases.append([g, code(K), torch.rand(nb, -(-K // 128), generator=gen, device="cuda"), code(N),
+                      torch.rand(nb, N, generator=gen, device="cuda"), torch.tensor(split, dtype=torch.int32, device="cuda"),
+                      torch.empty(E, N, K, dtype=torch.bfloat16, device="cuda")])
+    ws = torch.zeros(max(B.moe_grouped_linear_fp8_workspace_size(c[0]) for c in cases), dtype=torch.uint8, device="cuda")
+    want, graphs = [], []
+    for c in cases:
+        B.moe_grouped_linear_fp8_wgrad(*c, ws)
+        want.append(c[-1].clone())
+    for c in cases:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            B.moe_grouped_linear_fp8_wgrad(*c, ws)
+    for i in (0, 1, 1, 0, 1):
+        cases[i][-1].zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(cases[i][-1], want[i])
+    assert B.moe_get_device_error(ws) == (0, 0)
+
+
 def test_rows_past_the_sum_and_pitches():
     check_whole([40, 0, 9], 96, 112, rows=300, seed=4, pad=24)
     check_whole([40, 0, 9], 96, 112, rows=300, seed=5, pad=16)
