@@ -745,7 +745,7 @@ typedef struct moe_balance {
 } moe_balance;
 
 /* Bytes of workspace of moe_balance_loss_fwd (256-byte aligned, zero-filled once before first use: a
- * device error word, then a counter that every call leaves at zero).  Calls that run at the same time
+ * device error word, then counters that every call leaves at zero).  Calls that run at the same time
  * need one each.  0 for invalid sizes.  Host only. */
 size_t moe_balance_loss_workspace_size(const moe_balance* b);
 
