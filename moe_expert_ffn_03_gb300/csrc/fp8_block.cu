@@ -20,9 +20,12 @@ constexpr int Q_THREADS = 256;
 constexpr int Q_MAX_E = 256;
 constexpr int Q_ROWS = 8;                        // rows per thread of a tile of 128 x 128
 
-// A thread's eight neighbouring columns of a row (zeros past `left`), as floats.
+// A thread's eight columns of a row (zeros past `left`), as floats: neighbours, or, where rows do not start on whole
+// vectors, 16 apart, so that 16 lanes read and write neighbouring values.  (65536 x 2047 bf16 into rows and
+// tokens: 203 us, with neighbours 400.)
 template <typename T, bool WIDE>
 struct Eight {
+  static constexpr int STEP = WIDE ? 1 : 16;
   Raw<T, WIDE ? kWide<T> : 1> r[WIDE ? 8 / kWide<T> : 8];
   __device__ __forceinline__ void load(const T* p, int left) {
     if constexpr (WIDE) {
@@ -34,7 +37,7 @@ struct Eight {
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (i < left) r[i].load(p + i);
+        if (i * STEP < left) r[i].load(p + i * STEP);
         else r[i].zero();
       }
     }
@@ -49,14 +52,14 @@ struct Eight {
     }
   }
 };
-template <bool WIDE>
+template <bool WIDE, int STEP>
 __device__ __forceinline__ void put_codes(uint8_t* p, const uint32_t* q, int left) {
   if constexpr (WIDE) {
     if (left > 0) *reinterpret_cast<uint2*>(p) = make_uint2(q[0], q[1]);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < left) p[i] = uint8_t(q[i >> 2] >> (8 * (i & 3)));
+      if (i * STEP < left) p[i * STEP] = uint8_t(q[i >> 2] >> (8 * (i & 3)));
   }
 }
 
@@ -114,7 +117,8 @@ __global__ void __launch_bounds__(Q_THREADS, WIDE && sizeof(T) == 2 ? 4 : 2) blo
   __shared__ int row0[Q_MAX_E + 1], blk0[Q_MAX_E + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int sub = tid >> 4;                      // rows sub, sub + 16, ... of a tile
-  const int c8 = (tid & 15) * 8;
+  constexpr int STEP = Eight<T, WIDE>::STEP;     // between a thread's columns
+  const int c8 = WIDE ? (tid & 15) * 8 : tid & 15;           // and the first of them
   pdl_wait();
   if (a.split_sizes != nullptr) {
     if (warp == 0) {
@@ -245,7 +249,7 @@ __global__ void __launch_bounds__(Q_THREADS, WIDE && sizeof(T) == 2 ? 4 : 2) blo
         raw[i].get(v);
         const Block8 b(up);
         const uint32_t q[2] = {b.codes4(v), b.codes4(v + 4)};
-        if (sub + 16 * i < cnt) put_codes<WIDE>(out + int64_t(i) * 16 * a.cols, q, left);
+        if (sub + 16 * i < cnt) put_codes<WIDE, STEP>(out + int64_t(i) * 16 * a.cols, q, left);
       }
     }
     if (a.tcodes == nullptr) continue;
@@ -271,7 +275,7 @@ __global__ void __launch_bounds__(Q_THREADS, WIDE && sizeof(T) == 2 ? 4 : 2) blo
       for (int j = 0; j < 8; ++j) cmax[j] = max(cmax[j], __shfl_xor_sync(0xFFFFFFFFu, cmax[j], 16));
       if (lane < 16) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) colmax[warp][c8 + j] = cmax[j];
+        for (int j = 0; j < 8; ++j) colmax[warp][c8 + j * STEP] = cmax[j];
       }
       __syncthreads();
       if (tid < B8) {
@@ -282,8 +286,13 @@ __global__ void __launch_bounds__(Q_THREADS, WIDE && sizeof(T) == 2 ? 4 : 2) blo
         if (c0 + tid < a.cols) a.tscales[blk * a.cols + c0 + tid] = Block8::scale(amax);
       }
       __syncthreads();
+      if constexpr (WIDE) {
 #pragma unroll
-      for (int j = 0; j < 8; j += 4) *reinterpret_cast<float4*>(ups + j) = *reinterpret_cast<const float4*>(colup + c8 + j);
+        for (int j = 0; j < 8; j += 4) *reinterpret_cast<float4*>(ups + j) = *reinterpret_cast<const float4*>(colup + c8 + j);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ups[j] = colup[c8 + j * STEP];
+      }
     }
     // rows past the expert's last are zeros on its last block; a matrix has none
     const int out_rows = a.mat_rows > 0 ? cnt : B8;
@@ -296,25 +305,27 @@ __global__ void __launch_bounds__(Q_THREADS, WIDE && sizeof(T) == 2 ? 4 : 2) blo
 #pragma unroll
       for (int k = 0; k < 8; k += 4) q[k >> 2] = block8_codes4(v + k, ups + k);
       if (cnt < B8 && sub + 16 * i >= cnt) q[0] = q[1] = 0;      // (0 times a NaN factor is none)
-      if (sub + 16 * i < out_rows) put_codes<WIDE>(out + int64_t(i) * 16 * a.cols, q, left);
+      if (sub + 16 * i < out_rows) put_codes<WIDE, STEP>(out + int64_t(i) * 16 * a.cols, q, left);
     }
   }
 }
 
-// Values of codes: a warp takes four rows of 256 columns at a time, eight columns a lane.
+// Values of codes: a warp takes four rows of 256 columns at a time, eight columns a lane: neighbours, or, where rows
+// do not start on whole vectors, 32 apart.
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(Q_THREADS) block8_dequantize_kernel(const __grid_constant__ Block8Back a) {
-  const int lane = threadIdx.x & 31;
+  constexpr int STEP = WIDE ? 1 : 32, HALVES = WIDE ? 1 : 2;     // blocks of 128 that a lane's columns lie in
+  const int lane = threadIdx.x & 31, c8 = WIDE ? lane * 8 : lane;
   const int cb = (a.cols + B8 - 1) / B8;
   const int64_t fours = (a.rows + 3) / 4;
   pdl_wait();
-  for (int col = blockIdx.y * 256 + lane * 8; col - lane * 8 < a.cols; col += gridDim.y * 256) {
+  for (int col = blockIdx.y * 256 + c8; col - c8 < a.cols; col += gridDim.y * 256) {
     const int left = a.cols - col;
     if (left <= 0) continue;
     for (int64_t r4 = (int64_t(blockIdx.x) * Q_THREADS + threadIdx.x) >> 5; r4 < fours; r4 += (int64_t(gridDim.x) * Q_THREADS) >> 5) {
       const int64_t first = r4 * 4;
       uint32_t q[4][2];
-      float s[8];                                // tokens: the columns', of all four rows (blocks begin on 128s); else rows'
+      float s[8];                                // tokens: the columns', of all four rows (blocks begin on 128s); else [row][half]
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const bool in = first + i < a.rows;
@@ -329,17 +340,22 @@ __global__ void __launch_bounds__(Q_THREADS) block8_dequantize_kernel(const __gr
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (in && j < left) q[i][j >> 2] |= uint32_t(p[j]) << (8 * (j & 3));
+            if (in && j * STEP < left) q[i][j >> 2] |= uint32_t(p[j * STEP]) << (8 * (j & 3));
         }
-        if (a.format == MOE_FP8_ROWS) {
-          s[i] = in ? __ldg(a.scales + int64_t(col / B8) * a.rows + first + i) : 0.f;
-        } else if (a.format == MOE_FP8_TILES) {
-          int64_t rb = first / B8;
-          if (a.mat_rows > 0 && in) {            // rows below 2^31
-            const uint32_t row = uint32_t(first + i), mat = row / uint32_t(a.mat_rows);
-            rb = int64_t(mat) * ((a.mat_rows + B8 - 1) / B8) + (row - mat * uint32_t(a.mat_rows)) / B8;
+        if (a.format != MOE_FP8_TOKENS) {
+          int64_t at = first + i, step = a.rows; // rows: of the first half, and to the second
+          if (a.format == MOE_FP8_TILES) {
+            int64_t rb = first / B8;
+            if (a.mat_rows > 0 && in) {          // rows below 2^31
+              const uint32_t row = uint32_t(first + i), mat = row / uint32_t(a.mat_rows);
+              rb = int64_t(mat) * ((a.mat_rows + B8 - 1) / B8) + (row - mat * uint32_t(a.mat_rows)) / B8;
+            }
+            at = rb * cb;
+            step = 1;
           }
-          s[i] = in ? __ldg(a.scales + rb * cb + col / B8) : 0.f;
+          at += col / B8 * step;
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h) s[i * HALVES + h] = in && h * B8 < left ? __ldg(a.scales + at + h * step) : 0.f;
         }
       }
       if (a.format == MOE_FP8_TOKENS) {
@@ -349,7 +365,7 @@ __global__ void __launch_bounds__(Q_THREADS) block8_dequantize_kernel(const __gr
           *reinterpret_cast<float4*>(s + 4) = __ldg(reinterpret_cast<const float4*>(p + 4));
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) s[j] = j < left ? __ldg(p + j) : 0.f;
+          for (int j = 0; j < 8; ++j) s[j] = j * STEP < left ? __ldg(p + j * STEP) : 0.f;
         }
       }
 #pragma unroll
@@ -357,10 +373,11 @@ __global__ void __launch_bounds__(Q_THREADS) block8_dequantize_kernel(const __gr
         if (first + i >= a.rows) continue;
         float v[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f = e4m3x2_to_float2(q[i][k >> 1] >> (16 * (k & 1)));
-          v[2 * k] = f.x * (a.format == MOE_FP8_TOKENS ? s[2 * k] : s[i]);
-          v[2 * k + 1] = f.y * (a.format == MOE_FP8_TOKENS ? s[2 * k + 1] : s[i]);
+        for (int k = 0; k < 8; k += 2) {
+          const float2 f = e4m3x2_to_float2(q[i][k >> 2] >> (8 * (k & 3)));
+          const float other = s[i * HALVES + (WIDE ? 0 : k >> 2)];
+          v[k] = f.x * (a.format == MOE_FP8_TOKENS ? s[k] : other);
+          v[k + 1] = f.y * (a.format == MOE_FP8_TOKENS ? s[k + 1] : other);
         }
         T* o = static_cast<T*>(a.dst) + (first + i) * a.ld + col;
         if constexpr (WIDE) {
@@ -373,8 +390,87 @@ __global__ void __launch_bounds__(Q_THREADS) block8_dequantize_kernel(const __gr
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (j < left) store_vec<1>(o + j, v + j);
+            if (j * STEP < left) store_vec<1>(o + j * STEP, v + j);
         }
+      }
+    }
+  }
+}
+
+// The same for rows that are dense but do not start on whole vectors: a thread takes a few times eight neighbouring
+// values, whichever rows they are of.  (65536 x 2047 to bf16: rows 111 us, value by value 212; tokens, which have a
+// scale a column, 187 and 232.)
+template <typename T, bool TOKENS>
+__global__ void __launch_bounds__(Q_THREADS) block8_dequantize_flat_kernel(const __grid_constant__ Block8Back a) {
+  constexpr int UN = TOKENS ? 2 : 4, SCALES = TOKENS ? 8 : 2;
+  const int64_t total = a.rows * a.cols, eights = (total + 7) / 8, step = int64_t(gridDim.x) * Q_THREADS;
+  const int cb = (a.cols + B8 - 1) / B8;
+  const auto scale = [&](int64_t row, int col) {
+    if (a.format == MOE_FP8_ROWS) return __ldg(a.scales + int64_t(col / B8) * a.rows + row);
+    int64_t rb = row / B8;
+    if (a.mat_rows > 0) {                        // rows below 2^31
+      const uint32_t r = uint32_t(row), mat = r / uint32_t(a.mat_rows);
+      rb = int64_t(mat) * ((a.mat_rows + B8 - 1) / B8) + (r - mat * uint32_t(a.mat_rows)) / B8;
+    }
+    return __ldg(a.scales + rb * cb + col / B8);
+  };
+  pdl_wait();
+  for (int64_t t = int64_t(blockIdx.x) * Q_THREADS + threadIdx.x; t < eights; t += UN * step) {
+    uint2 q[UN];
+    float s[UN][SCALES];                         // of every value (tokens); of the first, and from the next block or row on
+    int turn[UN];                                // where that begins
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int64_t at = (t + u * step) * 8;
+      q[u] = make_uint2(0, 0);
+      turn[u] = 8;
+#pragma unroll
+      for (int j = 0; j < SCALES; ++j) s[u][j] = 0.f;
+      if (at >= total) continue;
+      if (at + 8 <= total) {
+        q[u] = __ldcg(reinterpret_cast<const uint2*>(a.codes + at));
+      } else {
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+          if (at + j < total) w[j >> 2] |= uint32_t(a.codes[at + j]) << (8 * (j & 3));
+        q[u] = make_uint2(w[0], w[1]);
+      }
+      const int64_t row = total < (int64_t(1) << 32) ? int64_t(uint32_t(at) / uint32_t(a.cols)) : at / a.cols;
+      const int col = int(at - row * a.cols);
+      if constexpr (TOKENS) {
+        const float* p = a.scales + row / B8 * a.cols + col;
+        const float* next = a.scales + (row + 1) / B8 * a.cols + (col - a.cols);     // the same of the next row's
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (at + j < total) s[u][j] = __ldg((col + j < a.cols ? p : next) + j);
+        continue;
+      }
+      s[u][0] = scale(row, col);
+      turn[u] = min(a.cols - col, B8 - (col & (B8 - 1)));
+      if (turn[u] < 8 && at + turn[u] < total) s[u][1] = col + turn[u] < a.cols ? scale(row, col + turn[u]) : scale(row + 1, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int64_t at = (t + u * step) * 8;
+      if (at >= total) continue;
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; k += 2) {
+        const float2 f = e4m3x2_to_float2((k < 4 ? q[u].x : q[u].y) >> (8 * (k & 3)));
+        v[k] = f.x * (TOKENS ? s[u][k % SCALES] : k < turn[u] ? s[u][0] : s[u][1]);
+        v[k + 1] = f.y * (TOKENS ? s[u][(k + 1) % SCALES] : k + 1 < turn[u] ? s[u][0] : s[u][1]);
+      }
+      T* o = static_cast<T*>(a.dst) + at;
+      if (at + 8 > total) {
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+          if (at + j < total) store_vec<1>(o + j, v + j);
+      } else if constexpr (sizeof(T) == 2) {
+        store_vec<8>(o, v);
+      } else {
+        store_vec<4>(o, v);
+        store_vec<4>(o + 4, v + 4);
       }
     }
   }
@@ -482,6 +578,16 @@ cudaError_t launch_block8_dequantize(const Block8Back& a, bool f32, cudaStream_t
   const int64_t most = (int64_t(sms) * 8 + gy - 1) / gy;
   const dim3 grid(unsigned(need < most ? need : most), unsigned(gy));
   const bool wide = a.cols % 8 == 0 && a.ld % 8 == 0;
+  // Eight values lie in two rows at most, and in two blocks where a row's last block has eight or more.
+  if (!wide && a.ld == a.cols && a.cols >= 8 && (a.format == MOE_FP8_TOKENS || (a.cols - 1) % B8 >= 7)) {
+    const int64_t blocks = (a.rows * a.cols + 8 * Q_THREADS - 1) / (8 * Q_THREADS), cap = int64_t(sms) * 6;
+    const dim3 flat(unsigned(blocks < cap ? blocks : cap));
+    if (a.format == MOE_FP8_TOKENS)
+      return f32 ? launch_pdl(block8_dequantize_flat_kernel<float, true>, flat, dim3(Q_THREADS), 0, st, a)
+                 : launch_pdl(block8_dequantize_flat_kernel<__nv_bfloat16, true>, flat, dim3(Q_THREADS), 0, st, a);
+    return f32 ? launch_pdl(block8_dequantize_flat_kernel<float, false>, flat, dim3(Q_THREADS), 0, st, a)
+               : launch_pdl(block8_dequantize_flat_kernel<__nv_bfloat16, false>, flat, dim3(Q_THREADS), 0, st, a);
+  }
   if (f32)
     return wide ? launch_pdl(block8_dequantize_kernel<float, true>, grid, dim3(Q_THREADS), 0, st, a)
                 : launch_pdl(block8_dequantize_kernel<float, false>, grid, dim3(Q_THREADS), 0, st, a);

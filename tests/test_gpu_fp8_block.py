@@ -177,3 +177,25 @@ def test_values_are_exact_products():
     B.moe_fp8_block_dequantize(c, s, "rows", out)
     ref = fb.E4M3[c.cpu().numpy()].astype(np.float32) * np.repeat(s.t().cpu().numpy(), 128, axis=1)
     assert np.array_equal(f64(out), ref.astype(np.float64), equal_nan=True)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("rows,cols", [(1, 9), (3, 11), (700, 129), (301, 134), (37, 135), (301, 137), (64, 1003), (5, 3829), (9000, 255)])
+def test_values_of_rows_of_any_length(rows, cols, dt):
+    """Rows and tiles that start anywhere, blocks of one value, of seven, of eight, several rows in a vector's eight values."""
+    g = torch.Generator(device="cuda").manual_seed(rows + cols)
+    c = torch.randint(0, 127, (rows, cols), generator=g, device="cuda").to(U8) | (torch.randint(0, 2, (rows, cols), generator=g, device="cuda") << 7).to(U8)
+    cb, host = -(-cols // 128), c.cpu().numpy()
+    s = torch.rand(cb, rows, generator=g, device="cuda") + 0.5
+    out = torch.full((rows, cols), 77.0, dtype=dt, device="cuda")
+    B.moe_fp8_block_dequantize(c, s, "rows", out)
+    values = fb.E4M3[host].astype(np.float32)
+    wide = np.repeat(s.cpu().numpy().T, 128, 1)[:, :cols]
+    assert torch.equal(out.cpu(), torch.tensor(values * wide).to(dt))
+    mats = next(n for n in (3, 2, 1) if rows % n == 0)       # weights: every matrix on blocks of its own
+    m = rows // mats
+    s = torch.rand(mats, -(-m // 128), cb, generator=g, device="cuda") + 0.5
+    out = torch.full((mats, m, cols), 77.0, dtype=dt, device="cuda")
+    B.moe_fp8_block_dequantize(c.view(mats, m, cols), s, "tiles", out)
+    wide = np.repeat(np.repeat(s.cpu().numpy(), 128, 2)[:, :, :cols], 128, 1)[:, :m]
+    assert torch.equal(out.cpu(), torch.tensor(values.reshape(mats, m, cols) * wide).to(dt))
