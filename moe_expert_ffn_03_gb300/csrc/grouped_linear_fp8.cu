@@ -855,14 +855,14 @@ cudaError_t launch_grouped_linear_fp8(int mode, const Linear8Args& args, const u
                                        : (a.rows < a.E ? a.rows : a.E) + a.rows / L8_M;
   const int64_t tiles = nt * mt;                 // no fewer than there are
   // The kernel for few rows: up to 16 an expert, and where a long contraction has so few tiles that cutting them
-  // leaves an SM 16 blocks at most.  (Both measured, that one first.  16 rows, 4096 -> 28672, six of eight experts: 128
+  // leaves an SM 24 blocks at most.  (Both measured, that one first.  16 rows, 4096 -> 28672, six of eight experts: 128
   // and 155 us; 32 rows, 2048 -> 1024, E = 8: 9.1 and 11.1, 128 rows 10.4 and 11.2, 256 rows 12.5 and 11.3; one row,
   // 14336 -> 4096: 26 and 55, 48 rows 33 and 55; with L2 emptied, 9 us of each: 512 rows, input gradient 8192 -> 512: 27
   // and 37, 200 rows, 4096 -> 1024, E = 4: 21 and 23, 64 rows, 4096 -> 4096: 23 and 23, 4000 rows, input gradient
   // 8192 -> 128: 37 and 35, 69 rows, 1952 -> 1584: 19 and 17.)
   const int64_t blocks = ((mode == LIN_FWD ? a.K : a.N) + L8_KT - 1) / L8_KT;
   const int64_t small = (((mode == LIN_FWD ? a.N : a.K) + 127) / 128) * ((a.rows < a.E ? a.rows : a.E) + a.rows / 64);
-  if (mode != LIN_WGRAD && (a.rows <= int64_t(16) * a.E || (blocks >= 32 && small * blocks <= int64_t(16) * sms)))
+  if (mode != LIN_WGRAD && (a.rows <= int64_t(16) * a.E || (blocks >= 32 && small * blocks <= int64_t(24) * sms)))
     return launch_grouped_linear_fp8_few(mode, a, a_codes, b_codes, sms, st, msg, msg_len);
   CUtensorMap ma, mas, mb, mo;
   bool ok;
