@@ -102,13 +102,14 @@ __device__ __forceinline__ void f8_decode(const Linear8Args& a, const int* row0,
 }
 
 // Pieces of a tile: what makes the SMs' last round the fullest, each piece at least F8_MIN_PIECE blocks; a
-// piece's own cost (its sums through memory) is taken as two blocks.  One warp, a number of pieces per lane.
+// piece's own cost (its sums through memory, behind a fence) is taken as eight blocks (as two: 64 rows, 2048 -> 2816,
+// E = 8: 22.1 us, 17.6; 100 rows, 1024 -> 1024, E = 8: 9.2, 7.8).  One warp, a number of pieces per lane.
 __device__ __forceinline__ int f8_parts(int tiles, int all, int ctas, int lane) {
   const int most = min(all / F8_MIN_PIECE, tiles > 0 ? F8_MAX_PIECES / tiles : 1);
   uint32_t best = 0xFFFFFFFFu;                   // blocks of the longest SM, then pieces (fewest win)
   for (int p = lane + 1; p <= max(most, 1); p += 32) {
     // below 2^32: tiles * p is at most F8_MAX_PIECES, or p is 1 and tiles below 2^22
-    const uint32_t rounds = (uint32_t(tiles) * p + ctas - 1) / uint32_t(ctas), cost = rounds * ((uint32_t(all) + p - 1) / p + (p > 1 ? 2 : 0));
+    const uint32_t rounds = (uint32_t(tiles) * p + ctas - 1) / uint32_t(ctas), cost = rounds * ((uint32_t(all) + p - 1) / p + (p > 1 ? 8 : 0));
     const uint32_t key = (cost < (1u << 21) ? cost : (1u << 21) - 1) << 10 | uint32_t(p);
     best = min(best, key);
   }
