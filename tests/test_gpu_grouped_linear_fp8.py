@@ -146,7 +146,7 @@ def test_few_rows(split, K, N):
 
 
 @pytest.mark.parametrize("split,K,N", [([40000], 48, 32), ([9000, 0, 4100, 1, 130], 272, 256), ([30000] + [1] * 40, 64, 144),
-                                       ([6000, 6000, 5999], 528, 784), ([4097], 16, 16), ([4096 + 128 * 77, 5], 32, 16), ([20000, 900], 1040, 2064)])
+                                       ([6000, 6000, 5999], 528, 784), ([4097], 16, 16), ([4096 + 128 * 77, 5], 32, 16), ([3] * 100 + [5000] + [2] * 155, 16, 32), ([20] * 255 + [9000], 48, 16), ([20000, 900], 1040, 2064)])
 def test_weight_gradient_of_few_long_tiles(split, K, N):
     """Tiles that are cut along the rows: several experts, ends of every kind, and a workspace used again.  Codes of -1,
     0 and 1: sums of up to 40000 such products, of variance 0.44, stay below 2^24, and scales of one keep them whole."""
