@@ -73,9 +73,10 @@ __device__ __forceinline__ void rms_outputs(const RmsArgs& a, const P& at, int64
 
 // The rows of this thread's row group whose mean square (with eps) is above float32's range or below 2^-120,
 // once more, on times a power of two: a loop of its own behind the kernel's.  Where h has taken the place
-// of x or the residual by then, the row is h as stored.
+// of x or the residual by then, the row is h as stored.  sums[flip] is the buffer that the kernel's last sum has
+// not used; from there on they take turns, also where a row turns out to be within range.
 template <typename T, int VEC, int NV>
-__device__ __noinline__ void rms_fwd_rescaled(const RmsArgs& a, int tpr, float* buf0, float* buf1) {
+__device__ __noinline__ void rms_fwd_rescaled(const RmsArgs& a, int tpr, float (*sums)[32], int flip) {
   const Place<VEC, NV, 2, 0> at(tpr, nullptr);
   const Weight<VEC, NV> gamma(a.gamma, a.w_f32, at.col0, a.H);
   const float inv_H = 1.f / float(a.H);
@@ -84,7 +85,7 @@ __device__ __noinline__ void rms_fwd_rescaled(const RmsArgs& a, int tpr, float* 
   const T* res = static_cast<const T*>(summed ? nullptr : a.residual);
   float h[NV][VEC];
   // the row, and its mean square times f^2
-  const auto load = [&](int64_t row, float f, float* buf) {
+  const auto load = [&](int64_t row, float f) {
     float w[VEC], sum[VEC];
     v_fill<VEC>(w, f);
     v_fill<VEC>(sum, 0.f);
@@ -107,15 +108,16 @@ __device__ __noinline__ void rms_fwd_rescaled(const RmsArgs& a, int tpr, float* 
     float s[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < VEC; ++j) s[0] += sum[j];
-    row_sum<1>(s, tpr, at.group, buf);
+    row_sum<1>(s, tpr, at.group, sums[flip]);
+    flip ^= 1;
     return s[0] * inv_H;
   };
   for (int64_t row = int64_t(blockIdx.x) * at.groups + at.group; row < a.rows; row += int64_t(gridDim.x) * at.groups) {
-    const float var = load(row, 1.f, buf0) + a.eps;
+    const float var = load(row, 1.f) + a.eps;
     // bf16 rows as stored are not quite the sums: those near the bounds are taken along
     if (summed ? var >= 0x1p-119f && var <= 0x1p127f : rms_in_range(var)) continue;
     const float f = var < 1.f ? RMS_SMALL : RMS_LARGE;
-    const float ms = load(row, f, buf1);
+    const float ms = load(row, f);
     float rstd = inv_sqrt(ms + a.eps * f * f);   // of the row as it is held
     if (at.t == 0 && a.rstd != nullptr) a.rstd[row] = ms == 0.f ? inv_sqrt(a.eps) : rstd * f;
     if (ms == 0.f && a.eps > 0.f) rstd = 0.f;    // eps * f * f may have gone under
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(max_block(VEC), 1) rms_fwd_kernel(const __grid
     for (int i = 0; i < NV; ++i) v_mul<VEC>(h[i], rs);
     rms_outputs<T, VEC, NV>(a, at, row, h, gamma);
   }
-  if (odd) rms_fwd_rescaled<T, VEC, NV>(a, tpr, sums[0], sums[1]);
+  if (odd) rms_fwd_rescaled<T, VEC, NV>(a, tpr, sums, flip);
 }
 
 // A persistent grid and a ring as in the forward pass.  A thread keeps its columns' sums of dgamma in
