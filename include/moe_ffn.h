@@ -801,11 +801,13 @@ enum moe_fp8_format { MOE_FP8_ROWS = 0, MOE_FP8_TOKENS = 1, MOE_FP8_TILES = 2 };
 moe_status moe_fp8_block_quantize(const void* src, int32_t src_f32, int64_t rows, int32_t cols, int64_t ld, uint8_t* codes,
                                   float* scales, const int32_t* split_sizes, int32_t E, uint8_t* tcodes, float* tscales,
                                   int32_t format, moe_stream_t stream);
-/* Weights [E][N][K], dense, in tiles; both of the products that read them take these codes. */
+/* Weights [E][N][K], dense, in tiles; both of the products that read them take these codes.  E <= 65536, N and K
+ * <= 2^20, E*N < 2^31. */
 moe_status moe_fp8_block_quantize_weights(const void* w, int32_t w_f32, int32_t E, int32_t N, int32_t K, uint8_t* codes,
                                           float* scales, moe_stream_t stream);
 /* The values of codes [rows][cols] (rows = B*128 for tokens and tiles) in bf16, or f32 with dst_f32, at pitch
- * ld; mat_rows: the rows of each matrix of weights (tiles), else 0. */
+ * ld; mat_rows: the rows of each matrix of weights (tiles), else 0.  rows < 2^31: longer layouts of tokens or tiles are
+ * taken in parts of whole blocks. */
 moe_status moe_fp8_block_dequantize(const uint8_t* codes, const float* scales, int32_t format, int64_t rows, int32_t mat_rows,
                                     int32_t cols, void* dst, int32_t dst_f32, int64_t ld, moe_stream_t stream);
 /* moe_fp8_block_pack -- moe_ep_pack (world 1) for rows that are in 8 bits already (MOE_FP8_ROWS, moe_rmsnorm_fwd's): the

@@ -1786,6 +1786,8 @@ moe_status moe_fp8_block_quantize_weights(const void* w, int32_t w_f32, int32_t 
   if ((w_f32 & ~1) != 0) return fail(MOE_ERR_INVALID_ARG, "w_f32 must be 0 or 1");
   if (E < 1 || N < 1 || K < 1) return fail(MOE_ERR_INVALID_ARG, "E=%d, N=%d and K=%d must be >= 1", E, N, K);
   if (E > 65536 || N > (1 << 20) || K > (1 << 20)) return fail(MOE_ERR_UNSUPPORTED, "E must be <= 65536, N and K <= 2^20");
+  // as many rows as moe_fp8_block_dequantize takes
+  if (int64_t(E) * N >= (int64_t(1) << 31)) return fail(MOE_ERR_UNSUPPORTED, "E*N=%lld must be below 2^31", (long long)E * N);
   REQUIRE_PTR(w);
   REQUIRE_PTR(codes);
   REQUIRE_PTR(scales);
