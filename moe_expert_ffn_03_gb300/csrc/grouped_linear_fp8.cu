@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
       // last 32 added behind the next block's first load: 8192 rows, 4096 -> 16384, 416 us; this 404.)
       uint32_t p0[32], p1[32];
       if (blocks > 0) {
-        wait_phase_warp_later(false, &empty[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR8 + 4, lim, ok);
+        wait_phase_warp_later(&empty[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR8 + 4, lim, ok);
         tc_fence_after();
         tmem_ld32_async(tmem_row + (cur.st & 1) * L8_N, p0);
         tmem_ld32_async(tmem_row + (cur.st & 1) * L8_N + 32, p1);
@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
         l8_add(acc + 64, p0, f2);
         l8_add(acc + 96, p1, f2);
         if (left > 1) {
-          wait_phase_warp_later(false, &empty[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR8 + 4, lim, ok);
+          wait_phase_warp_later(&empty[cur.st], cur.ph, abort_s, args.err, SITE_LINEAR8 + 4, lim, ok);
           tc_fence_after();
           tmem_ld32_async(tmem_row + (cur.st & 1) * L8_N, p0);
           tmem_ld32_async(tmem_row + (cur.st & 1) * L8_N + 32, p1);

@@ -247,12 +247,12 @@ __device__ __forceinline__ bool wait_phase_warp_inline(uint64_t* bar, uint32_t p
   return __all_sync(0xFFFFFFFFu, wait_phase_inline(bar, parity, abort_flag, err, site, limit_ns));
 }
 
-// The same where the warp has looked at the phase before (`seen`): lanes whose wait gives up clear their `ok` and go on
-// with the others, so that the warp stays together without a vote here; it has to vote on `ok` (__all_sync)
-// in the end, and what it computes in between must be harmless.
-__device__ __forceinline__ void wait_phase_warp_later(bool seen, uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                                      int* err, int site, uint64_t limit_ns, bool& ok) {
-  if (!seen && !wait_phase_inline(bar, parity, abort_flag, err, site, limit_ns)) ok = false;
+// The same without a vote: lanes whose wait gives up clear their `ok` and go on with the others, so that the warp
+// stays together; it has to vote on `ok` (__all_sync) in the end, and what it computes in between must be
+// harmless.  A lane that has given up waits no more, so the rest of its work is done in no time.
+__device__ __forceinline__ void wait_phase_warp_later(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err, int site,
+                                                      uint64_t limit_ns, bool& ok) {
+  if (ok && !wait_phase_inline(bar, parity, abort_flag, err, site, limit_ns)) ok = false;
   __syncwarp();
 }
 // Whether a phase has completed, without waiting.

@@ -1,0 +1,58 @@
+"""What the kernels of the grouped linear layers on 8-bit operands have to keep to where they begin early and where a
+wait gives up, read off the CUDA sources: it matters only in an unlucky moment."""
+import os
+import re
+
+from test_pdl_waits import CSRC, kernel_body, sources
+
+KERNELS = (("grouped_linear_fp8.cu", "grouped_linear_fp8_kernel"), ("grouped_linear_fp8_few.cu", "grouped_linear_fp8_few_kernel"))
+
+
+def plain(text):
+    return re.sub(r"//[^\n]*", "", text)
+
+
+def test_kernels_with_a_launch_of_their_own_wait_too():
+    """A launch that sets the programmatic-serialization attribute itself is found in its file: all kernels there wait."""
+    files = [n for n, t in sources().items() if "cudaLaunchAttributeProgrammaticStreamSerialization" in plain(t)]
+    assert {"gemm.cu", "grouped_linear.cu", "grouped_linear_fp8.cu"} <= set(files)
+    text = plain(sources()["grouped_linear_fp8.cu"])
+    for name in ("grouped_linear_fp8_kernel", "grouped_linear_fp8_join_kernel"):
+        assert "pdl_wait();" in kernel_body(text, name), name
+
+
+def test_nothing_of_earlier_kernels_is_read_before_the_wait():
+    for file, kernel in KERNELS:
+        body = plain(kernel_body(sources()[file], kernel))
+        before, after = body.split("pdl_wait();")
+        for name in ("args.split_sizes", "args.sa", "args.sb", "args.out", "args.arrived", "args.pieces", "args.plan", "l8_prefix", "l8_cut",
+                     "tma_load", "f8_load", "report_error", "wait_phase"):
+            assert name not in before, (kernel, name)
+        assert "l8_prefix" in after
+        assert before.count("{") == before.count("}") + 1, f"{kernel}: not all threads wait"
+    body = plain(kernel_body(sources()["grouped_linear_fp8.cu"], "grouped_linear_fp8_join_kernel"))
+    assert "a.plan" not in body.split("pdl_wait();")[0] and "a.pieces" not in body.split("pdl_wait();")[0]
+
+
+def test_copies_land_after_any_wait_gave_up():
+    """Behind the block's last barrier, whichever warp gave up, and before tensor memory and shared memory go."""
+    for file, kernel in KERNELS:
+        body = plain(kernel_body(sources()[file], kernel))
+        at = body.rindex("if (warp == 0 && *abort_s) {")
+        assert "__syncthreads();" in body[:at][-60:], kernel              # all warps are through
+        end = body[at:]
+        assert re.match(r"if \(warp == 0 && \*abort_s\) \{[^}]*globaltimer_ns\(\)", end), kernel
+        together = "cluster_sync();" if "cluster_sync();" in end else "__syncthreads();"
+        assert 0 < end.index(together) < end.index("dealloc"), kernel
+
+
+def test_a_lane_that_has_given_up_waits_no_more():
+    text = plain(open(os.path.join(CSRC, "tcgen05.cuh")).read())
+    later = text[text.index("void wait_phase_warp_later("):]
+    later = later[:later.index("\n}")]
+    assert re.search(r"if \(ok && !wait_phase_inline\(", later) and "ok = false;" in later and "__syncwarp();" in later
+    # its kernel votes before the sums go anywhere
+    body = plain(kernel_body(sources()["grouped_linear_fp8.cu"], "grouped_linear_fp8_kernel"))
+    last = body.rindex("wait_phase_warp_later(")
+    vote = body.index("ok = __all_sync(0xFFFFFFFFu, ok);", last)
+    assert all(body.index(s, last) > vote for s in ("__stcg(mine", "l8_store<MODE>(&tmO", "args.out"))
