@@ -255,18 +255,6 @@ __device__ __forceinline__ void wait_phase_warp_later(uint64_t* bar, uint32_t pa
   if (ok && !wait_phase_inline(bar, parity, abort_flag, err, site, limit_ns)) ok = false;
   __syncwarp();
 }
-// Whether a phase has completed, without waiting.
-__device__ __forceinline__ bool mbar_look(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,

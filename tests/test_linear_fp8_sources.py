@@ -56,3 +56,13 @@ def test_a_lane_that_has_given_up_waits_no_more():
     last = body.rindex("wait_phase_warp_later(")
     vote = body.index("ok = __all_sync(0xFFFFFFFFu, ok);", last)
     assert all(body.index(s, last) > vote for s in ("__stcg(mine", "l8_store<MODE>(&tmO", "args.out"))
+
+
+def test_waits_are_all_called():
+    """Every form of a bounded wait has a caller."""
+    text = plain(open(os.path.join(CSRC, "tcgen05.cuh")).read())
+    names = set(re.findall(r"\b(wait_phase\w*|mbar_\w+)\([^;]*\) \{", text))
+    everything = "".join(plain(t) for t in sources().values()) + "".join(
+        plain(open(os.path.join(CSRC, f)).read()) for f in os.listdir(CSRC) if f.endswith(".cuh"))
+    for name in sorted(names):
+        assert len(re.findall(rf"\b{name}\(", everything)) >= 2, f"{name} is called nowhere"
