@@ -50,7 +50,11 @@ def test_a_lane_that_has_given_up_waits_no_more():
     text = plain(open(os.path.join(CSRC, "tcgen05.cuh")).read())
     later = text[text.index("void wait_phase_warp_later("):]
     later = later[:later.index("\n}")]
-    assert re.search(r"if \(ok && !wait_phase_inline\(", later) and "ok = false;" in later and "__syncwarp();" in later
+    # polls counted from 256: the first that fails looks at the flag, which whoever gave up has found or left set
+    assert re.search(r"if \(!wait_phase_inline\([^;]*, ok \? 1u : 256u\)\) ok = false;", later) and "__syncwarp();" in later
+    wait = text[text.index("bool wait_phase_inline("):]
+    wait = wait[:wait.index("\n}")]
+    assert re.search(r"n = first; !mbar_try_wait\(bar, parity\); \+\+n\) \{\s*if \(\(n & 255u\) != 0\) continue;\s*if \(\*abort_flag\) return false;", wait)
     # its kernel votes before the sums go anywhere
     body = plain(kernel_body(sources()["grouped_linear_fp8.cu"], "grouped_linear_fp8_kernel"))
     last = body.rindex("wait_phase_warp_later(")
