@@ -13,7 +13,8 @@ Forward:  moe_rmsnorm_fwd (n for the router, and in 8 bits) -> moe_router_fwd ->
           -> moe_fp8_block_quantize -> moe_grouped_linear_fp8_fwd -> moe_unpermute_combine
 Backward: the same in reverse.  A weight gradient's operands are quantized along tokens; its x is what the
           product has read, the values of n in 8 bits, and the activation is computed again from its
-          8-bit checkpoint.
+          8-bit checkpoint.  The router's weight gradient takes n from the same codes, E4M3 (2^-4 of a value at most)
+          where the forward pass gave the router bf16: n is not kept a second time.
 """
 from __future__ import annotations
 

@@ -36,10 +36,12 @@
 // memory 412, but 32768 rows 5% longer), and goes back before its last half is added (416 -> 404); measured the
 // same or worse: sixteen warps of 64 columns (494 against 490), halves of 128 columns with four buffers (558; an
 // MMA of 128 columns takes 104 clocks, not 64), single CTAs of 128 x 256 (490), a second thread that issues
-// (478), test_wait in place of try_wait where the sums are waited for (425 against 396).  Measured, on its own:
-// 32768 rows, 4096 -> 28672, E = 8, forward 2.78 ms (2.77 PFLOP/s), under the power limit of calls in a row 3.2 ms;
-// 8192 rows, 4096 -> 16384, E = 2: 396 us (2.78); 65536 rows, 2048 -> 2816, E = 16: 304 us forward (2.49: a tile's output
-// is a tenth of its time there), 300 input gradient, 278 weight gradient (2.72).
+// (478), test_wait in place of try_wait where the sums are waited for (425 against 396).  All of these on one card with
+// even splits, random codes and a memory fill between calls, and so: 32768 rows, 4096 -> 28672, E = 8, forward
+// 2.78 ms (2.77 PFLOP/s; on other cards 2.89 to 3.12); 8192 rows, 4096 -> 16384, E = 2: 396 us (2.78; 451 to 463);
+// 65536 rows, 2048 -> 2816, E = 16: 304 us forward (2.49: a tile's output is a tenth of its time there; 316 to 359), 300
+// input gradient (302 to 306), 278 weight gradient (2.72; 287 to 297).  Calls in a row meet the power limit, and loads that
+// are uneven leave pairs without work: the first with such loads 3.17 to 3.28 ms (2.4).
 #include <atomic>
 #include <cstdio>
 #include <type_traits>
@@ -535,8 +537,10 @@ __global__ void __launch_bounds__(L8_THREADS, 1)
     } else if (warp == 3) {
       if (lane == 0) {
         // ---------------- the pair's tiles, laid out for the others ----------------
-        // A slot comes free when the tile before is done.  In the weight gradient that is far below the limit, too:
-        // an expert of few tiles has them cut, one of many has no room for rows that take a tenth of a second.
+        // A slot comes free when the tile before is done.  In the weight gradient that is below the limit, too: what
+        // l8_cut weighs leaves no piece longer than two even shares, which is tiles / 38 of all rows on 76 pairs, and
+        // tiles enough for that to be long want K + N above 2500, so that memory has room for some 110 million
+        // rows: 0.3 s a tile (750 clocks a block of 128).
         Tiles8 tiles(tile_ring, laid, taken);
         for (int t = pair;; t = l8_after<MODE>(t, num_pairs)) {
           if (!wait_phase_inline(&taken[tiles.slot], tiles.ph ^ 1u, abort_s, args.err, SITE_LINEAR8 + 8, lim)) break;
@@ -858,8 +862,12 @@ cudaError_t launch_grouped_linear_fp8(int mode, const Linear8Args& args, const u
   // leaves an SM 24 blocks at most.  (Both measured, that one first.  16 rows, 4096 -> 28672, six of eight experts: 128
   // and 155 us; 32 rows, 2048 -> 1024, E = 8: 9.1 and 11.1, 128 rows 10.4 and 11.2, 256 rows 12.5 and 11.3; one row,
   // 14336 -> 4096: 26 and 55, 48 rows 33 and 55; with L2 emptied, 9 us of each: 512 rows, input gradient 8192 -> 512: 27
-  // and 37, 200 rows, 4096 -> 1024, E = 4: 21 and 23, 64 rows, 4096 -> 4096: 23 and 23, 4000 rows, input gradient
-  // 8192 -> 128: 37 and 35, 69 rows, 1952 -> 1584: 19 and 17.)
+  // and 37, 200 rows, 4096 -> 1024, E = 4: 21 and 23, 64 rows, 4096 -> 4096: 23 and 23.  Near the rule's edge it takes
+  // the slower one by a little: 4000 rows, input gradient 8192 -> 128: 37 and 35; 69 rows, 1952 -> 1584: 19 and 17; and
+  // 48 rows, 3968 -> 4096 go to the other kernel, 17.7 us, where 4096 -> 4096 take 14.2 in a row.)  How the rows are split
+  // only the device knows: 4096 rows, 2048 -> 2816, E = 256, all of one expert, whose weights are then read once for every 64
+  // rows, take 149 us here, 16 rows more 29 in the other kernel; with 1 row to each of the other experts 353 and
+  // 305; split evenly 289 and 297.
   const int64_t blocks = ((mode == LIN_FWD ? a.K : a.N) + L8_KT - 1) / L8_KT;
   const int64_t small = (((mode == LIN_FWD ? a.N : a.K) + 127) / 128) * ((a.rows < a.E ? a.rows : a.E) + a.rows / 64);
   if (mode != LIN_WGRAD && (a.rows <= int64_t(16) * a.E || (blocks >= 32 && small * blocks <= int64_t(24) * sms)))

@@ -70,3 +70,21 @@ def test_waits_are_all_called():
         plain(open(os.path.join(CSRC, f)).read()) for f in os.listdir(CSRC) if f.endswith(".cuh"))
     for name in sorted(names):
         assert len(re.findall(rf"\b{name}\(", everything)) >= 2, f"{name} is called nowhere"
+
+
+def test_longest_tile_is_far_below_the_limit_of_the_waits():
+    """The wait for a free slot of the ring of tiles lasts a tile.  A weight gradient's is the longest: its plan weighs a
+    piece of one even share of the pairs, which costs two shares at most (a share and a piece), so the piece it picks
+    is no longer than that; nor is any longer than all rows that fit in memory.  750 clocks a block at 2.07 GHz."""
+    pairs, memory = 76, 284_208 << 20
+    longest = 0.0
+    for a in range(1, 200):
+        for b in range(1, 200):
+            K, N = 256 * (a - 1) + 16, 256 * (b - 1) + 16             # the smallest sizes with a x b tiles of 256 x 256
+            blocks = min(1 << 30, memory // (K + N)) / 128
+            longest = max(longest, blocks * min(1.0, 2 * a * b / pairs) * 750 / 2.07e9)
+    assert 0.25 < longest < 0.32
+    text = plain(sources()["grouped_linear_fp8.cu"])
+    assert "fminf(ceilf(units / float(pairs)) * piece, float(share) + piece)" in text        # the plan's measure
+    assert 2_000_000_000 == int(re.search(r"kWaitLimitNs = (\d+)", "".join(
+        open(os.path.join(CSRC, f)).read() for f in os.listdir(CSRC)).replace("ull", "").replace("'", "")).group(1))
