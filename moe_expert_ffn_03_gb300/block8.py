@@ -91,8 +91,8 @@ class Scratch8:
 class Fp8MoEBlock:
     """One block for fixed sizes (H and I multiples of 128, as the routing's entry points have them).
 
-    alpha and beta weigh the balance loss and the z loss; both 0 leaves them out.  Without `training` nothing is
-    kept for a backward pass."""
+    alpha and beta weigh the balance loss and the z loss; both 0 leaves them out, and counts, prob_mean and loss stay
+    zeros (split_sizes has the experts' rows).  Without `training` nothing is kept for a backward pass."""
 
     def __init__(self, T, H, I, E, k, device="cuda", scratch=None, eps=1e-5, alpha=0.0, beta=0.0, training=True):
         self.T, self.H, self.I, self.E, self.k = T, H, I, E, k
@@ -116,7 +116,8 @@ class Fp8MoEBlock:
         self.gu_codes = e(R, 2 * I, dt=U8) if training else None
         self.gu_scales = e(R, 2 * ((I + 31) // 32), dt=U8) if training else None
         # results
-        self.counts, self.prob_mean, self.loss = e(E + 1, dt=I32), e(E, dt=F32), torch.zeros(3, device=dev)
+        self.counts, self.prob_mean = torch.zeros(E + 1, dtype=I32, device=dev), torch.zeros(E, device=dev)
+        self.loss = torch.zeros(3, device=dev)
         self.h, self.out = e(T, H), e(T, H)
         if training:
             self.dx, self.dgamma, self.dw_r = e(T, H), e(H), e(E, H, dt=F32)
