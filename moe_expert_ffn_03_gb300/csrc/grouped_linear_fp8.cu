@@ -41,7 +41,7 @@
 // 2.78 ms (2.77 PFLOP/s; on other cards 2.89 to 3.12); 8192 rows, 4096 -> 16384, E = 2: 396 us (2.78; 451 to 463);
 // 65536 rows, 2048 -> 2816, E = 16: 304 us forward (2.49: a tile's output is a tenth of its time there; 316 to 359), 300
 // input gradient (302 to 306), 278 weight gradient (2.72; 287 to 297).  Calls in a row meet the power limit, and loads that
-// are uneven leave pairs without work: the first with such loads 3.17 to 3.28 ms (2.4).
+// are uneven leave pairs without work: the first with such loads 3.12 to 3.32 ms (2.4).
 #include <atomic>
 #include <cstdio>
 #include <type_traits>
